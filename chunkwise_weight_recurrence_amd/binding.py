@@ -20,7 +20,9 @@ EXPORTS = ("ttt_workspace_size", "ttt_saved_size", "ttt_chunk_fwd", "ttt_chunk_b
            "inplace_ttt_bwd_guarded", "ttt_mlp_workspace_size", "ttt_mlp_chunk_fwd",
            "ttt_mlp_bwd_workspace_size", "ttt_mlp_chunk_bwd", "ttt_mlp_saved_size",
            "ttt_last_error", "ttt_version", "ttt_timing_enable", "ttt_timing_read", "ttt_chunk_bwd_noalloc",
-           "ttt_noalloc_scratch_bytes")
+           "ttt_noalloc_scratch_bytes", "ttt_recurrence_workspace_size", "ttt_recurrence_saved_size",
+           "ttt_recurrence_fwd", "ttt_recurrence_bwd", "ttt_recurrence_step", "ttt_layernorm_fwd",
+           "ttt_layernorm_workspace_size", "ttt_layernorm_bwd")
 
 
 class Status(IntEnum):
@@ -56,6 +58,16 @@ class Decay(IntEnum):
     VECTOR = 2
 
 
+class Gate(IntEnum):
+    SIGMOID = 0
+    LOG = 1
+
+
+class RecInput(IntEnum):
+    PLAIN = 0
+    CONVEX = 1
+
+
 class Kernel(IntEnum):
     """Mirror of ``ttt_kernel`` (per-kernel timing ids)."""
     FWD = 0
@@ -84,6 +96,12 @@ class Kernel(IntEnum):
     NORM_BWD_PRE = 23
     MLP_QUERY = 24
     MLP_BWD_PRE = 25
+    REC_FWD = 26
+    REC_BWD = 27
+    REC_STEP = 28
+    LN_FWD = 29
+    LN_BWD = 30
+    LN_REDUCE = 31
 
 
 ENTRY_FWD = 0
@@ -104,6 +122,20 @@ class TTTMlpDesc(ctypes.Structure):
                 ("dk", ctypes.c_int32), ("dh", ctypes.c_int32), ("dv", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("loss", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("decay", ctypes.c_int32), ("lr_bias", ctypes.c_float)]
+
+
+class TTTRecDesc(ctypes.Structure):
+    """Mirror of ``ttt_rec_desc``."""
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("input", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldg", ctypes.c_int64)]
+
+
+class TTTLnDesc(ctypes.Structure):
+    """Mirror of ``ttt_ln_desc``."""
+    _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("D", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("period", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 class TTTError(RuntimeError):
@@ -167,6 +199,17 @@ def lib():
     L.ttt_mlp_bwd_workspace_size.restype = i32
     L.ttt_mlp_chunk_bwd.argtypes = [mptr] + [vp] * 18 + [vp, sz, vp]
     L.ttt_mlp_chunk_bwd.restype = i32
+    rptr, nptr = ctypes.POINTER(TTTRecDesc), ctypes.POINTER(TTTLnDesc)
+    L.ttt_recurrence_workspace_size.argtypes = [rptr, i32, ctypes.POINTER(sz)]
+    L.ttt_recurrence_saved_size.argtypes = [rptr, ctypes.POINTER(sz)]
+    L.ttt_recurrence_fwd.argtypes = [rptr] + [vp] * 8 + [sz, vp]
+    L.ttt_recurrence_bwd.argtypes = [rptr] + [vp] * 11 + [sz, vp]
+    L.ttt_recurrence_step.argtypes = [rptr] + [vp] * 3 + [i32] + [vp] * 3
+    L.ttt_layernorm_fwd.argtypes = [nptr] + [vp] * 9
+    L.ttt_layernorm_workspace_size.argtypes = [nptr, ctypes.POINTER(sz)]
+    L.ttt_layernorm_bwd.argtypes = [nptr] + [vp] * 10 + [sz, vp]
+    for name in EXPORTS[-8:]:
+        getattr(L, name).restype = i32
     L.ttt_last_error.argtypes = []
     L.ttt_last_error.restype = ctypes.c_char_p
     L.ttt_version.argtypes = []
@@ -225,6 +268,19 @@ def make_mlp_desc(B, H, T, dk, dh, dv, C, dtype="bf16", loss="mse", act="gelu", 
         return int(cls[x.upper()]) if isinstance(x, str) else int(x)
     return TTTMlpDesc(B, H, T, dk, dh, dv, C, enum(DType, dtype), enum(Loss, loss), enum(Act, act),
                       enum(Decay, decay), float(lr_bias))
+
+
+def make_rec_desc(B, T, D, dtype="bf16", gate="sigmoid", input="convex", packed=False, ldx=0, ldg=0):
+    """Build a TTTRecDesc from names ("bf16"/"f32", "sigmoid"/"log", "plain"/"convex")."""
+    def enum(cls, x):
+        return int(cls[x.upper()]) if isinstance(x, str) else int(x)
+    return TTTRecDesc(B, T, D, int(packed), enum(DType, dtype), enum(Gate, gate), enum(RecInput, input), 0, ldx, ldg)
+
+
+def make_ln_desc(rows, D, dtype="bf16", groups=1, period=1, eps=1e-5, ldx=0):
+    """Build a TTTLnDesc; ``dtype`` by name ("bf16"/"f32")."""
+    return TTTLnDesc(rows, ldx, D, groups, period, int(DType[dtype.upper()]) if isinstance(dtype, str) else int(dtype),
+                     float(eps), 0)
 
 
 def ttt_last_error() -> str:
@@ -372,6 +428,140 @@ def inplace_ttt_bwd_guarded(B, T, d_model, d_ff, C, eta, clip_tau, doc_starts, z
                                          float(clip_tau), arr, len(starts), _p(z), _p(vhat), _p(w0), _p(w_init),
                                          _p(w_final), _p(d_o), _p(d_wfinal), _p(dz), _p(dvhat), _p(dw0),
                                          _p(dw_init), _p(ws), int(ws_bytes), _stream(stream)))
+
+
+_TORCH_DTYPE = {DType.F32: "torch.float32", DType.BF16: "torch.bfloat16"}
+
+
+class _Call:
+    """Checks the torch tensors of one call against its desc and collects their device.
+
+    A tensor on the host, on another device than the call's first, of another
+    type or with fewer elements than the kernels touch would fault the GPU; it
+    raises ValueError here.  Integers are device pointers and are taken as they are."""
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, name, x, dtype, rows, cols, ld=0):
+        """``rows`` rows of ``cols`` elements, ``ld`` elements apart (0: dense); returns the pointer."""
+        if x is None or isinstance(x, int):
+            return x
+        if not hasattr(x, "data_ptr"):
+            raise TypeError(f"cannot pass {type(x)!r} as a device pointer")
+        if x.device != self.device:
+            if self.device is not None:
+                raise ValueError(f"{name} is on {x.device}, the tensors before it on {self.device}")
+            if x.device.type != "cuda":
+                raise ValueError(f"{name} must be on the GPU, not on {x.device}")
+            self.device = x.device
+        if str(x.dtype) != dtype:
+            raise ValueError(f"{name} must be {dtype[6:]}, not {str(x.dtype)[6:]}")
+        if ld and ld != cols:
+            st = x.stride()
+            if x.dim() < 2 or st[-1] != 1 or x.shape[-1] != cols or st[-2] != ld or \
+                    any(st[i] != st[i + 1] * x.shape[i + 1] for i in range(x.dim() - 2)):
+                raise ValueError(f"{name} must have rows of {cols} elements, {ld} apart (got shape {tuple(x.shape)}, "
+                                 f"strides {st})")
+        elif not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if x.numel() < rows * cols:
+            raise ValueError(f"{name} has {x.numel()} elements, {rows * cols} are needed")
+        return x.data_ptr()
+
+    def run(self, f, *args, ws=None, ws_bytes=None, stream=None):
+        """Call ``f`` with the device of the tensors current, on ``stream`` (None: that device's current stream)."""
+        if ws_bytes is not None or ws is not None:
+            if hasattr(ws, "data_ptr"):
+                size = ws.numel() * ws.element_size()
+                ws_bytes = size if ws_bytes is None else min(size, int(ws_bytes))
+                ws = self("ws", ws, str(ws.dtype), 0, 0)
+            args = (*args, ws, ws_bytes or 0)
+        elif f.argtypes[-2] is ctypes.c_size_t:
+            args = (*args, None, 0)
+        if self.device is None:
+            _check(f(*args, _stream(stream)))
+            return
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                self.device = None
+                _check(f(*args, _stream(stream)))
+            return
+        _check(f(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+
+
+def ttt_recurrence_workspace_size(desc: TTTRecDesc, entry: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_recurrence_workspace_size(ctypes.byref(desc), int(entry), ctypes.byref(n)))
+    return n.value
+
+
+def ttt_recurrence_saved_size(desc: TTTRecDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_recurrence_saved_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def _rec_tokens(desc):
+    return desc.T if desc.packed else desc.B * desc.T
+
+
+def ttt_recurrence_fwd(desc, x, gate, h0, seq_starts, o, h_final, saved, ws, ws_bytes=None, stream=None):
+    """``seq_starts``: int32 device tensor of B + 1 positions for a packed desc, else None."""
+    L, c = lib(), _Call()
+    dt, n, D = _TORCH_DTYPE.get(desc.dtype), _rec_tokens(desc), desc.D
+    c.run(L.ttt_recurrence_fwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
+          c("h0", h0, "torch.float32", desc.B, D), c("seq_starts", seq_starts, "torch.int32", 1, desc.B + 1),
+          c("o", o, dt, n, D), c("h_final", h_final, "torch.float32", desc.B, D),
+          c("saved", saved, "torch.uint8", 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
+          ws=ws, ws_bytes=ws_bytes, stream=stream)
+
+
+def ttt_recurrence_bwd(desc, x, gate, h0, seq_starts, saved, d_o, d_hfinal, dx, dgate, dh0, ws, ws_bytes=None,
+                       stream=None):
+    L, c = lib(), _Call()
+    dt, n, D = _TORCH_DTYPE.get(desc.dtype), _rec_tokens(desc), desc.D
+    c.run(L.ttt_recurrence_bwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
+          c("h0", h0, "torch.float32", desc.B, D), c("seq_starts", seq_starts, "torch.int32", 1, desc.B + 1),
+          c("saved", saved, "torch.uint8", 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
+          c("d_o", d_o, dt, n, D), c("d_hfinal", d_hfinal, "torch.float32", desc.B, D),
+          c("dx", dx, dt, n, D, desc.ldx), c("dgate", dgate, dt, n, D, desc.ldg),
+          c("dh0", dh0, "torch.float32", desc.B, D), ws=ws, ws_bytes=ws_bytes, stream=stream)
+
+
+def ttt_recurrence_step(desc, x, gate, slots, h, o, n_states=None, stream=None):
+    """``h``: [n_states, D] float32, updated in place; ``n_states`` is only needed where h is a raw pointer."""
+    L, c = lib(), _Call()
+    dt, n, D = _TORCH_DTYPE.get(desc.dtype), desc.B, desc.D
+    if n_states is None:
+        n_states = h.numel() // D if hasattr(h, "numel") and D > 0 else 0
+    c.run(L.ttt_recurrence_step, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
+          c("slots", slots, "torch.int32", 1, n), n_states, c("h", h, "torch.float32", n_states, D), c("o", o, dt, n, D),
+          stream=stream)
+
+
+def ttt_layernorm_workspace_size(desc: TTTLnDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_layernorm_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def ttt_layernorm_fwd(desc, x, res, w, b, y, r, mean, rstd, stream=None):
+    L, c = lib(), _Call()
+    dt, n, D, G, f32 = _TORCH_DTYPE.get(desc.dtype), desc.rows, desc.D, desc.groups, "torch.float32"
+    c.run(L.ttt_layernorm_fwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("res", res, dt, n, D),
+          c("w", w, f32, G, D), c("b", b, f32, G, D), c("y", y, dt, n, D), c("r", r, dt, n, D),
+          c("mean", mean, f32, n, 1), c("rstd", rstd, f32, n, 1), stream=stream)
+
+
+def ttt_layernorm_bwd(desc, x, w, mean, rstd, dy, dr, dx, dw, db, ws, ws_bytes=None, stream=None):
+    L, c = lib(), _Call()
+    dt, n, D, G, f32 = _TORCH_DTYPE.get(desc.dtype), desc.rows, desc.D, desc.groups, "torch.float32"
+    c.run(L.ttt_layernorm_bwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("w", w, f32, G, D),
+          c("mean", mean, f32, n, 1), c("rstd", rstd, f32, n, 1), c("dy", dy, dt, n, D), c("dr", dr, dt, n, D),
+          c("dx", dx, dt, n, D, desc.ldx), c("dw", dw, f32, G, D), c("db", db, f32, G, D), ws=ws, ws_bytes=ws_bytes,
+          stream=stream)
 
 
 def ttt_timing_enable(on: bool) -> None:

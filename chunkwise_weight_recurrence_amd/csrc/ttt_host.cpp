@@ -567,4 +567,192 @@ int ttt_mlp_chunk_bwd(const ttt_mlp_desc* desc, const void* q, const void* k, co
   return ok();
 }
 
+namespace {
+
+int check_rec_desc(const ttt_rec_desc* d) {
+  if (!d) return fail(TTT_ERR_INVALID_ARG, "desc is NULL");
+  if (d->B < 0 || d->T < 0) return fail(TTT_ERR_INVALID_ARG, "B, T must be >= 0 (got %d, %d)", d->B, d->T);
+  if (d->D < 1) return fail(TTT_ERR_INVALID_ARG, "D must be >= 1 (got %d)", d->D);
+  if (d->packed != 0 && d->packed != 1) return fail(TTT_ERR_INVALID_ARG, "packed must be 0 or 1 (got %d)", d->packed);
+  if (d->dtype != TTT_F32 && d->dtype != TTT_BF16) return fail(TTT_ERR_INVALID_ARG, "invalid dtype %d", d->dtype);
+  if (d->gate != TTT_GATE_SIGMOID && d->gate != TTT_GATE_LOG) return fail(TTT_ERR_INVALID_ARG, "invalid gate %d", d->gate);
+  if (d->input != TTT_REC_PLAIN && d->input != TTT_REC_CONVEX) return fail(TTT_ERR_INVALID_ARG, "invalid input %d", d->input);
+  if (d->reserved != 0) return fail(TTT_ERR_INVALID_ARG, "reserved must be 0 (got %d)", d->reserved);
+  if ((d->ldx != 0 && d->ldx < d->D) || (d->ldg != 0 && d->ldg < d->D))
+    return fail(TTT_ERR_INVALID_ARG, "ldx, ldg must be 0 or >= D (got %lld, %lld)", static_cast<long long>(d->ldx),
+                static_cast<long long>(d->ldg));
+  const int64_t n = d->packed ? d->T : static_cast<int64_t>(d->B) * d->T;
+  // Token indices are 32-bit, rounded up to whole tiles; a lane's channel offset in bytes too.
+  if (n > (int64_t{1} << 31) - 4096 || d->D > (1 << 24) || !ttt::recurrence_grid_fits(*d))
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens of %d channels)", static_cast<long long>(n), d->D);
+  const int64_t ld = d->ldx > d->ldg ? d->ldx : d->ldg;
+  if (static_cast<double>(n) * static_cast<double>(ld > d->D ? ld : d->D) > 4.0e12)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (rows %lld elements apart)", static_cast<long long>(ld));
+  return TTT_OK;
+}
+
+// Whether two arrays of the same size share a byte.
+bool overlap(const void* p, const void* q, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && (a < b ? b - a : a - b) < bytes;
+}
+
+int check_ln_desc(const ttt_ln_desc* d) {
+  if (!d) return fail(TTT_ERR_INVALID_ARG, "desc is NULL");
+  if (d->rows < 0) return fail(TTT_ERR_INVALID_ARG, "rows must be >= 0 (got %lld)", static_cast<long long>(d->rows));
+  if (d->D < 1) return fail(TTT_ERR_INVALID_ARG, "D must be >= 1 (got %d)", d->D);
+  if (d->groups < 1 || d->period < 1)
+    return fail(TTT_ERR_INVALID_ARG, "groups, period must be >= 1 (got %d, %d)", d->groups, d->period);
+  if (d->groups > 1 && d->rows % (static_cast<int64_t>(d->groups) * d->period) != 0)
+    return fail(TTT_ERR_INVALID_ARG, "rows (%lld) must be a multiple of groups * period (%d * %d)",
+                static_cast<long long>(d->rows), d->groups, d->period);
+  if (d->dtype != TTT_F32 && d->dtype != TTT_BF16) return fail(TTT_ERR_INVALID_ARG, "invalid dtype %d", d->dtype);
+  if (!std::isfinite(d->eps) || d->eps < 0.0f) return fail(TTT_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (d->reserved != 0) return fail(TTT_ERR_INVALID_ARG, "reserved must be 0 (got %d)", d->reserved);
+  if (d->ldx != 0 && d->ldx < d->D)
+    return fail(TTT_ERR_INVALID_ARG, "ldx must be 0 or >= D (got %lld)", static_cast<long long>(d->ldx));
+  if (d->rows > (int64_t{1} << 31) - 1 || d->D > (1 << 24) || d->groups > (1 << 20) ||
+      static_cast<double>(d->rows) * static_cast<double>(d->ldx > d->D ? d->ldx : d->D) > 4.0e12 ||
+      static_cast<double>(d->groups) * d->D > 1.0e9)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld rows of %d)", static_cast<long long>(d->rows), d->D);
+  return TTT_OK;
+}
+
+}  // namespace
+
+int ttt_recurrence_workspace_size(const ttt_rec_desc* desc, int entry, size_t* bytes) {
+  const int st = check_rec_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  if (entry != TTT_ENTRY_FWD && entry != TTT_ENTRY_BWD)
+    return fail(TTT_ERR_INVALID_ARG, "invalid entry %d (0 = forward, 1 = backward)", entry);
+  *bytes = ttt::recurrence_workspace(*desc);
+  return ok();
+}
+
+int ttt_recurrence_saved_size(const ttt_rec_desc* desc, size_t* bytes) {
+  const int st = check_rec_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ttt::recurrence_saved(*desc);
+  return ok();
+}
+
+int ttt_recurrence_fwd(const ttt_rec_desc* desc, const void* x, const void* gate, const float* h0,
+                       const int32_t* seq_starts, void* o, float* h_final, void* saved, void* ws, size_t ws_bytes,
+                       void* stream) {
+  const int st = check_rec_desc(desc);
+  if (st != TTT_OK) return st;
+  const int64_t n = desc->packed ? desc->T : static_cast<int64_t>(desc->B) * desc->T;
+  if (n > 0 && (!x || !gate || !o)) return fail(TTT_ERR_INVALID_ARG, "x, gate and o are required");
+  if (desc->packed ? !seq_starts && desc->B > 0 : seq_starts != nullptr)
+    return fail(TTT_ERR_INVALID_ARG, "seq_starts is required with packed sequences, and NULL without");
+  if (overlap(h0, h_final, sizeof(float) * desc->B * static_cast<size_t>(desc->D)))
+    return fail(TTT_ERR_INVALID_ARG, "h_final must not overlap h0");
+  if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"h0", h0}, {"seq_starts", seq_starts}, {"o", o},
+                                    {"h_final", h_final}, {"saved", saved}, {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const size_t need = ttt::recurrence_workspace(*desc);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  if (desc->B == 0 || (n == 0 && !h_final)) return ok();
+  const hipError_t e = ttt::recurrence_fwd_launch(*desc, x, gate, h0, seq_starts, o, h_final, saved, ws,
+                                                  static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_recurrence_fwd launch");
+  return ok();
+}
+
+int ttt_recurrence_bwd(const ttt_rec_desc* desc, const void* x, const void* gate, const float* h0,
+                       const int32_t* seq_starts, const void* saved, const void* d_o, const float* d_hfinal, void* dx,
+                       void* dgate, float* dh0, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_rec_desc(desc);
+  if (st != TTT_OK) return st;
+  const int64_t n = desc->packed ? desc->T : static_cast<int64_t>(desc->B) * desc->T;
+  if (n > 0 && (!x || !gate || !saved || !d_o || !dx || !dgate))
+    return fail(TTT_ERR_INVALID_ARG, "x, gate, saved, d_o, dx and dgate are required");
+  if (desc->packed ? !seq_starts && desc->B > 0 : seq_starts != nullptr)
+    return fail(TTT_ERR_INVALID_ARG, "seq_starts is required with packed sequences, and NULL without");
+  if (overlap(d_hfinal, dh0, sizeof(float) * desc->B * static_cast<size_t>(desc->D)))
+    return fail(TTT_ERR_INVALID_ARG, "dh0 must not overlap d_hfinal");
+  if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"h0", h0}, {"seq_starts", seq_starts}, {"saved", saved},
+                                    {"d_o", d_o}, {"d_hfinal", d_hfinal}, {"dx", dx}, {"dgate", dgate}, {"dh0", dh0},
+                                    {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const size_t need = ttt::recurrence_workspace(*desc);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  if (desc->B == 0 || (n == 0 && !dh0)) return ok();
+  const hipError_t e = ttt::recurrence_bwd_launch(*desc, x, gate, h0, seq_starts, saved, d_o, d_hfinal, dx, dgate, dh0,
+                                                  ws, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_recurrence_bwd launch");
+  return ok();
+}
+
+int ttt_recurrence_step(const ttt_rec_desc* desc, const void* x, const void* gate, const int32_t* slots, int n_states,
+                        float* h, void* o, void* stream) {
+  const int st = check_rec_desc(desc);
+  if (st != TTT_OK) return st;
+  if (desc->T != 1 || desc->packed) return fail(TTT_ERR_INVALID_ARG, "a step has T = 1 and packed = 0");
+  if (n_states < 0) return fail(TTT_ERR_INVALID_ARG, "n_states must be >= 0 (got %d)", n_states);
+  if (!slots && n_states < desc->B)
+    return fail(TTT_ERR_INVALID_ARG, "without slots n_states must be >= B (got %d, %d)", n_states, desc->B);
+  if (static_cast<double>(n_states) * desc->D > 4.0e12)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d states of %d channels)", n_states, desc->D);
+  if (desc->B == 0) return ok();
+  if (!x || !gate || !h || !o) return fail(TTT_ERR_INVALID_ARG, "x, gate, h and o are required");
+  if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"slots", slots}, {"h", h}, {"o", o}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const hipError_t e =
+      ttt::recurrence_step_launch(*desc, x, gate, slots, n_states, h, o, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_recurrence_step launch");
+  return ok();
+}
+
+int ttt_layernorm_fwd(const ttt_ln_desc* desc, const void* x, const void* res, const float* w, const float* b, void* y,
+                      void* r, float* mean, float* rstd, void* stream) {
+  const int st = check_ln_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!res != !r) return fail(TTT_ERR_INVALID_ARG, "res and r go together");
+  if (const char* bad = misaligned({{"x", x}, {"res", res}, {"w", w}, {"b", b}, {"y", y}, {"r", r}, {"mean", mean},
+                                    {"rstd", rstd}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  if (desc->rows == 0) return ok();
+  if (!x || !y) return fail(TTT_ERR_INVALID_ARG, "x and y are required");
+  const hipError_t e =
+      ttt::layernorm_fwd_launch(*desc, x, res, w, b, y, r, mean, rstd, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_layernorm_fwd launch");
+  return ok();
+}
+
+int ttt_layernorm_workspace_size(const ttt_ln_desc* desc, size_t* bytes) {
+  const int st = check_ln_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ttt::layernorm_workspace(*desc);
+  return ok();
+}
+
+int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const float* w, const float* mean, const float* rstd,
+                      const void* dy, const void* dr, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                      void* stream) {
+  const int st = check_ln_desc(desc);
+  if (st != TTT_OK) return st;
+  if (desc->rows > 0 && (!x || !mean || !rstd || !dy || !dx))
+    return fail(TTT_ERR_INVALID_ARG, "x, mean, rstd, dy and dx are required");
+  if (const char* bad = misaligned({{"x", x}, {"w", w}, {"mean", mean}, {"rstd", rstd}, {"dy", dy}, {"dr", dr},
+                                    {"dx", dx}, {"dw", dw}, {"db", db}, {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  if (dw || db) {
+    const size_t need = ttt::layernorm_workspace(*desc);
+    if (!ws || ws_bytes < need)
+      return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  } else if (desc->rows == 0) {
+    return ok();
+  }
+  const hipError_t e =
+      ttt::layernorm_bwd_launch(*desc, x, w, mean, rstd, dy, dr, dx, dw, db, ws, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_layernorm_bwd launch");
+  return ok();
+}
+
 }  // extern "C"

@@ -158,6 +158,26 @@ hipError_t mlp_bwd_launch(const ttt_mlp_desc& d, const void* q, const void* k, c
                           void* dv, float* dbeta, float* dgamma, float* dw1_0, float* dw2_0, void* ws,
                           hipStream_t s);
 
+// ---- gated linear recurrence (ttt_recurrence.hip) ----
+bool recurrence_grid_fits(const ttt_rec_desc& d);
+size_t recurrence_workspace(const ttt_rec_desc& d);
+size_t recurrence_saved(const ttt_rec_desc& d);
+hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const void* gate, const float* h0,
+                                 const int32_t* starts, void* o, float* h_final, void* saved, void* ws, hipStream_t s);
+hipError_t recurrence_bwd_launch(const ttt_rec_desc& d, const void* x, const void* gate, const float* h0,
+                                 const int32_t* starts, const void* saved, const void* d_o, const float* d_hfinal,
+                                 void* dx, void* dgate, float* dh0, void* ws, hipStream_t s);
+hipError_t recurrence_step_launch(const ttt_rec_desc& d, const void* x, const void* gate, const int32_t* slots,
+                                  int n_states, float* h, void* o, hipStream_t s);
+
+// ---- layer norm (ttt_layernorm.hip) ----
+size_t layernorm_workspace(const ttt_ln_desc& d);
+hipError_t layernorm_fwd_launch(const ttt_ln_desc& d, const void* x, const void* res, const float* w, const float* b,
+                                void* y, void* r, float* mean, float* rstd, hipStream_t s);
+hipError_t layernorm_bwd_launch(const ttt_ln_desc& d, const void* x, const float* w, const float* mean,
+                                const float* rstd, const void* dy, const void* dr, void* dx, float* dw, float* db,
+                                void* ws, hipStream_t s);
+
 // Brackets one kernel launch with HIP events on its stream while per-kernel
 // timing is on; does nothing otherwise.
 class KernelScope {

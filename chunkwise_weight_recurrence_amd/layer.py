@@ -220,3 +220,82 @@ class InplaceBuffers:
         else:
             B.inplace_ttt_fwd(c["B"], c["T"], c["d_model"], c["d_ff"], c["C"], c["eta"], self.z, self.vhat,
                               self.w, self.o, self.ws, self.ws_bytes, stream=stream)
+
+
+class RecurrenceBuffers:
+    """Outputs and workspace of the gated linear recurrence over x and gate ([B,T,D], or packed [T,D]).
+
+    ``x`` and ``gate`` are device tensors whose rows may be strided (two halves
+    of one projection).  ``seq_starts``: int32 device tensor of B + 1 row
+    positions for packed sequences.  ``h0``: [B,D] float32 or None."""
+
+    def __init__(self, x, gate, kind="sigmoid", input="convex", h0=None, seq_starts=None, with_bwd=False):
+        torch = _torch()
+        D = x.shape[-1]
+        packed = seq_starts is not None
+        Bn, T = (seq_starts.numel() - 1, x.shape[0]) if packed else x.shape[:2]
+        self.x, self.gate, self.h0, self.seq_starts = x, gate, h0, seq_starts
+        self.desc = B.make_rec_desc(Bn, T, D, dtype="bf16" if x.dtype == torch.bfloat16 else "f32", gate=kind,
+                                    input=input, packed=packed, ldx=x.stride(-2) if x.shape[-2] > 1 else D,
+                                    ldg=gate.stride(-2) if gate.shape[-2] > 1 else D)
+        d = x.device
+        self.o = torch.empty(x.shape, dtype=x.dtype, device=d)
+        self.h_final = torch.empty((Bn, D), dtype=torch.float32, device=d)
+        size = B.ttt_recurrence_workspace_size(self.desc, B.ENTRY_FWD)
+        self.saved = None
+        if with_bwd:
+            size = max(size, B.ttt_recurrence_workspace_size(self.desc, B.ENTRY_BWD))
+            self.saved = torch.empty(B.ttt_recurrence_saved_size(self.desc), dtype=torch.uint8, device=d)
+            self.dx = torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=d)
+            self.dgate = torch.empty_strided(gate.shape, gate.stride(), dtype=gate.dtype, device=d)
+            self.dh0 = torch.empty((Bn, D), dtype=torch.float32, device=d)
+        self.ws = torch.empty(max(size, 1), dtype=torch.uint8, device=d)
+
+    def forward(self, stream=None):
+        B.ttt_recurrence_fwd(self.desc, self.x, self.gate, self.h0, self.seq_starts, self.o, self.h_final, self.saved,
+                             self.ws, stream=stream)
+
+    def backward(self, d_o, d_hfinal=None, stream=None):
+        """Fills dx, dgate (with the strides of x and gate) and dh0."""
+        B.ttt_recurrence_bwd(self.desc, self.x, self.gate, self.h0, self.seq_starts, self.saved, d_o, d_hfinal, self.dx,
+                             self.dgate, self.dh0, self.ws, stream=stream)
+
+
+class LayerNormBuffers:
+    """Outputs and workspace of the layer norm over the rows of ``x`` ([..., D], rows may be strided).
+
+    ``w``, ``b``: [groups, D] float32 or None; row i has group (i / period) %
+    groups.  ``res``: the residual stream or None; ``self.r`` is then the new one."""
+
+    def __init__(self, x, w=None, b=None, res=None, groups=1, period=1, eps=1e-5, with_bwd=False):
+        torch = _torch()
+        D = x.shape[-1]
+        rows = x.numel() // D
+        f32, d = torch.float32, x.device
+        self.x, self.w, self.b, self.res = x, w, b, res
+        dtype = "bf16" if x.dtype == torch.bfloat16 else "f32"
+        ld = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else D
+        self.desc = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=eps, ldx=ld)
+        # the backward reads the rows that were normalised: the dense r where there is a residual
+        self.desc_bwd = self.desc if res is None else B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period,
+                                                                     eps=eps)
+        self.y = torch.empty(x.shape, dtype=x.dtype, device=d)
+        self.r = torch.empty(x.shape, dtype=x.dtype, device=d) if res is not None else None
+        self.mean = self.rstd = None
+        if with_bwd:
+            self.mean = torch.empty(rows, dtype=f32, device=d)
+            self.rstd = torch.empty(rows, dtype=f32, device=d)
+            self.dx = torch.empty_like(self.r) if res is not None else \
+                torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=d)
+            self.dw = torch.empty((groups, D), dtype=f32, device=d)
+            self.db = torch.empty((groups, D), dtype=f32, device=d)
+            self.ws = torch.empty(B.ttt_layernorm_workspace_size(self.desc_bwd), dtype=torch.uint8, device=d)
+
+    def forward(self, stream=None):
+        B.ttt_layernorm_fwd(self.desc, self.x, self.res, self.w, self.b, self.y, self.r, self.mean, self.rstd,
+                            stream=stream)
+
+    def backward(self, dy, dr=None, stream=None):
+        """Fills dx (also the residual's gradient), dw and db."""
+        B.ttt_layernorm_bwd(self.desc_bwd, self.x if self.r is None else self.r, self.w, self.mean, self.rstd, dy, dr,
+                            self.dx, self.dw, self.db, self.ws, stream=stream)

@@ -448,6 +448,141 @@ TTT_API int ttt_chunk_bwd_noalloc(const ttt_desc* desc, const void* q, const voi
 /* Bytes of the fixed scratch array behind ttt_chunk_bwd_noalloc (per GPU). */
 TTT_API size_t ttt_noalloc_scratch_bytes(void);
 
+/*
+ * Gated linear recurrence, the vector-state mixer that stands beside the
+ * fast-weight layer in a stack: per channel, with h_{-1} = h0 of its sequence,
+ *   a_t = Sigmoid(gate_t) (SIGMOID) or exp(gate_t) (LOG, as log_decay: <= 0);
+ *   h_t = a_t h_{t-1} + x_t (PLAIN)   or   a_t h_{t-1} + (1 - a_t) x_t (CONVEX);
+ *   o_t = h_t rounded to dtype.
+ * A sequence's state is kept in float32 throughout.
+ */
+typedef enum { TTT_GATE_SIGMOID = 0, TTT_GATE_LOG = 1 } ttt_rec_gate;
+typedef enum { TTT_REC_PLAIN = 0, TTT_REC_CONVEX = 1 } ttt_rec_input;
+
+typedef struct {
+  int32_t B;      /* sequences (rows of one token each for ttt_recurrence_step) */
+  int32_t T;      /* tokens of each sequence; packed: token rows of the buffers */
+  int32_t D;      /* channels, >= 1; per-head channels [B,H,T,d] are B*H sequences of d */
+  int32_t packed; /* 0: x is [B,T,D]; 1: x is [T,D], the sequences one behind the other */
+  int32_t dtype;  /* ttt_dtype of x, gate, o and their gradients                */
+  int32_t gate;   /* ttt_rec_gate                                               */
+  int32_t input;  /* ttt_rec_input                                              */
+  int32_t reserved; /* 0                                                        */
+  int64_t ldx;    /* elements from one token's x (and dx) to the next; 0 means D */
+  int64_t ldg;    /* the same for gate (and dgate)                              */
+} ttt_rec_desc;
+
+/*
+ * ttt_recurrence_workspace_size -- bytes of device workspace that
+ * ttt_recurrence_fwd (TTT_ENTRY_FWD) or ttt_recurrence_bwd (TTT_ENTRY_BWD)
+ * needs (0 is possible).  ttt_recurrence_saved_size -- bytes of the saved
+ * context that the forward writes and the backward needs: the float32 state at
+ * the start of every run of 128 tokens.  Both write *bytes and return TTT_OK, or
+ * a negative status for an invalid desc.
+ */
+TTT_API int ttt_recurrence_workspace_size(const ttt_rec_desc* desc, int entry, size_t* bytes);
+TTT_API int ttt_recurrence_saved_size(const ttt_rec_desc* desc, size_t* bytes);
+
+/*
+ * ttt_recurrence_fwd -- the recurrence over whole sequences.
+ *   x, gate    [B,T,D] or [T,D] dtype, rows ldx / ldg apart
+ *   h0         [B,D] f32 or NULL (zero)
+ *   seq_starts DEVICE array [B+1] int32, ascending (packed only, else NULL):
+ *              sequence s holds the rows seq_starts[s] .. seq_starts[s+1] - 1.
+ *              A sequence may be empty.  Rows before the first start or from the
+ *              last entry on belong to none: their outputs are left as they were.
+ *              The contents are not checked (no entry leads to an access outside
+ *              the buffers; entries out of order give unspecified outputs).
+ *   o          [B,T,D] or [T,D] dtype (written)
+ *   h_final    [B,D] f32 or NULL (written: the state after the last token; h0 for
+ *              an empty sequence).  It may not overlap h0.
+ *   saved      ttt_recurrence_saved_size bytes, or NULL (no backward)
+ *   ws, ws_bytes  workspace of at least ttt_recurrence_workspace_size bytes; two
+ *              calls that may run at the same time need one each
+ * Calls may be captured into a graph.
+ */
+TTT_API int ttt_recurrence_fwd(const ttt_rec_desc* desc, const void* x, const void* gate, const float* h0,
+                               const int32_t* seq_starts, void* o, float* h_final, void* saved, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * ttt_recurrence_bwd -- gradients of <d_o, O> + <d_hfinal, h_final>.
+ *   x, gate, h0, seq_starts  as passed to ttt_recurrence_fwd
+ *   saved      what ttt_recurrence_fwd wrote for the same desc and inputs (read,
+ *              not checked)
+ *   d_o        as o;  d_hfinal [B,D] f32 or NULL (zero)
+ *   dx, dgate  as x and gate, rows ldx / ldg apart (written)
+ *   dh0        [B,D] f32 or NULL (written; it may not overlap d_hfinal)
+ */
+TTT_API int ttt_recurrence_bwd(const ttt_rec_desc* desc, const void* x, const void* gate, const float* h0,
+                               const int32_t* seq_starts, const void* saved, const void* d_o, const float* d_hfinal,
+                               void* dx, void* dgate, float* dh0, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ttt_recurrence_step -- one token for each of B running sequences (T must be 1,
+ * packed 0): h[slot] <- a h[slot] + u, o = h[slot].
+ *   x, gate  [B,D] dtype, rows ldx / ldg apart;  o [B,D] dtype (written)
+ *   slots    DEVICE array [B] int32: the row of h that each row of x belongs to,
+ *            or NULL (row b has state b; then n_states >= B).  A row whose slot
+ *            is not in 0 .. n_states - 1 is padding: its o and every state are
+ *            left as they were.  Rows with the same slot are consecutive tokens of
+ *            it, in row order.
+ *   h        [n_states,D] f32, read and updated in place
+ * No workspace.
+ */
+TTT_API int ttt_recurrence_step(const ttt_rec_desc* desc, const void* x, const void* gate, const int32_t* slots,
+                                int n_states, float* h, void* o, void* stream);
+
+/*
+ * Layer norm of the rows of [rows, D], with an affine weight and bias of each
+ * group of rows and an optional residual added before it.  Row i belongs to group
+ * (i / period) % groups: the fast-weight layer's output [B,H,T,d] with one weight
+ * a head is rows = B*H*T, groups = H, period = T.  groups = 1: one weight, period
+ * is ignored.
+ */
+typedef struct {
+  int64_t rows;   /* 0 .. 2^31 - 1; a multiple of groups * period when groups > 1 */
+  int64_t ldx;    /* elements from one row of x (and dx) to the next; 0 means D   */
+  int32_t D;      /* 1 .. 2^24                                                    */
+  int32_t groups; /* >= 1                                                         */
+  int32_t period; /* >= 1                                                         */
+  int32_t dtype;  /* ttt_dtype of x, res, y, r and their gradients                */
+  float eps;      /* added to the variance, >= 0                                  */
+  int32_t reserved; /* 0                                                          */
+} ttt_ln_desc;
+
+/*
+ * ttt_layernorm_fwd -- with r = x, or x + res rounded to dtype:
+ *   y = (r - mean(r)) / sqrt(var(r) + eps) * w_g + b_g    (var over D, biased)
+ *   x       [rows,D] dtype, rows ldx apart
+ *   res     [rows,D] dtype or NULL;  r [rows,D] dtype (written; required with res,
+ *           else NULL).  r may be res: the residual stream is then updated in place
+ *   w, b    [groups,D] f32, each may be NULL (1 and 0)
+ *   y       [rows,D] dtype (written)
+ *   mean, rstd  [rows] f32 or NULL (written: mean(r) and 1 / sqrt(var(r) + eps))
+ */
+TTT_API int ttt_layernorm_fwd(const ttt_ln_desc* desc, const void* x, const void* res, const float* w, const float* b,
+                              void* y, void* r, float* mean, float* rstd, void* stream);
+
+/* Bytes of the workspace of ttt_layernorm_bwd: partial sums of dw and db. */
+TTT_API int ttt_layernorm_workspace_size(const ttt_ln_desc* desc, size_t* bytes);
+
+/*
+ * ttt_layernorm_bwd -- gradients of <dy, Y> + <dr, R>.
+ *   x        the rows that were normalised: r where a residual was added (then
+ *            desc.ldx is r's, D), else x
+ *   w, mean, rstd  as passed to / written by ttt_layernorm_fwd
+ *   dy       [rows,D] dtype;  dr [rows,D] dtype or NULL: the gradient that reaches
+ *            r from its other readers, added to dx
+ *   dx       [rows,D] dtype, rows ldx apart (written; the gradient of res is the same)
+ *   dw, db   [groups,D] f32, each may be NULL (written: sums over the group's rows)
+ *   ws, ws_bytes  at least ttt_layernorm_workspace_size bytes; may be NULL where dw
+ *            and db are
+ */
+TTT_API int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const float* w, const float* mean,
+                              const float* rstd, const void* dy, const void* dr, void* dx, float* dw, float* db,
+                              void* ws, size_t ws_bytes, void* stream);
+
 /* Message for the last non-OK return on this thread ("" if none). */
 TTT_API const char* ttt_last_error(void);
 
@@ -496,7 +631,13 @@ typedef enum {
   TTT_KERNEL_NORM_BWD_PRE = 23,  /* row-path backward: chunk-parallel terms free of the carried dW */
   TTT_KERNEL_MLP_QUERY = 24,     /* two-layer fast net forward: query view of every chunk */
   TTT_KERNEL_MLP_BWD_PRE = 25,   /* two-layer fast net backward: chunk-parallel terms free of the carried dW */
-  TTT_KERNEL_COUNT = 26
+  TTT_KERNEL_REC_FWD = 26,       /* gated linear recurrence forward */
+  TTT_KERNEL_REC_BWD = 27,       /* gated linear recurrence backward */
+  TTT_KERNEL_REC_STEP = 28,      /* gated linear recurrence, one token a sequence */
+  TTT_KERNEL_LN_FWD = 29,        /* layer norm forward */
+  TTT_KERNEL_LN_BWD = 30,        /* layer norm backward: dx and partial dw, db */
+  TTT_KERNEL_LN_REDUCE = 31,     /* layer norm backward: sum of the partial dw, db */
+  TTT_KERNEL_COUNT = 32
 } ttt_kernel;
 
 TTT_API int ttt_timing_enable(int on);

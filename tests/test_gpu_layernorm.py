@@ -1,0 +1,259 @@
+"""GPU tests of the layer norm against the fp64 oracle: every way a row is laid over
+threads, grouped weights, residuals, strides, and rows that are hard to normalise.
+
+Tolerances: the oracle's bound on fp32 arithmetic plus half a step of the output's
+type (``tests/block_utils.py::worst``; above 1 is wrong)."""
+import numpy as np
+import pytest
+
+from chunkwise_weight_recurrence_amd import binding as B
+from oracle import layernorm_oracle as ln
+from tests.block_utils import f64, rounded, torch_dtype, worst
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+def _run(rows, D, dtype, groups=1, period=1, residual=False, affine=True, seed=0, x=None, dr=True, eps=EPS):
+    import torch
+    rng = np.random.default_rng(seed)
+    x = rounded(rng, (rows, D), dtype, mean=0.5, std=2.0) if x is None else x
+    res = rounded(rng, (rows, D), dtype) if residual else None
+    w = rounded(rng, (groups, D), "f32", mean=1.0, std=0.3) if affine else None
+    b = rounded(rng, (groups, D), "f32") if affine else None
+    dy = rounded(rng, (rows, D), dtype)
+    drt = rounded(rng, (rows, D), dtype) if dr else None
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    io = dict(dtype=torch_dtype(dtype), device="cuda")
+    f32 = dict(dtype=torch.float32, device="cuda")
+    nan = float("nan")
+    out = dict(y=torch.full((rows, D), nan, **io), mean=torch.full((rows,), nan, **f32), rstd=torch.full((rows,), nan, **f32),
+               dx=torch.full((rows, D), nan, **io), dw=torch.full((groups, D), nan, **f32), db=torch.full((groups, D), nan, **f32))
+    r = torch.full((rows, D), nan, **io) if residual else None
+    desc = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=eps)
+    ws = torch.full((B.ttt_layernorm_workspace_size(desc),), 255, dtype=torch.uint8, device="cuda")
+    xd = dev(x)
+    B.ttt_layernorm_fwd(desc, xd, dev(res), dev(w), dev(b), out["y"], r, out["mean"], out["rstd"])
+    kept = r if residual else xd
+    B.ttt_layernorm_bwd(desc, kept, dev(w), out["mean"], out["rstd"], dev(dy), dev(drt), out["dx"], out["dw"], out["db"], ws)
+    torch.cuda.synchronize()
+    if residual:
+        assert torch.equal(r.cpu(), (x.float() + res.float()).to(x.dtype))
+    f = ln.forward(f64(kept), None if w is None else f64(w), None if b is None else f64(b), eps, groups, period)
+    g = ln.backward(f64(kept), None if w is None else f64(w), eps, f64(dy), f64(drt) if dr else None, groups, period)
+    errs = dict(y=worst(out["y"], f["y"], f["e_y"], dtype), mean=worst(out["mean"], f["mean"], f["e_mean"], "f32"),
+                rstd=worst(out["rstd"], f["rstd"], f["e_rstd"], "f32"), dx=worst(out["dx"], g["dx"], g["e_dx"], dtype),
+                dw=worst(out["dw"], g["dw"], g["e_dw"], "f32"), db=worst(out["db"], g["db"], g["e_db"], "f32"))
+    assert all(e <= 1.0 for e in errs.values()), ((rows, D, dtype, groups, period), errs)
+    return out
+
+
+# narrow rows (a part of a wave), a whole wave, several waves, two and four pieces a thread
+WIDTHS = [1, 2, 7, 8, 16, 24, 63, 64, 65, 128, 130, 256, 500, 512, 513, 520, 1000, 1001, 1024, 2048, 2560, 4000]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_widths(dtype):
+    for k, D in enumerate(WIDTHS):
+        for rows in (1, 3, 37):
+            _run(rows, D, dtype, residual=k % 2 == 0, affine=k % 3 != 0, seed=k, dr=k % 2 == 1)
+
+
+@pytest.mark.parametrize("D,dtype", [(4104, "bf16"), (8192, "bf16"), (9000, "f32"), (20000, "bf16"), (20001, "f32"),
+                                     (32768, "bf16")])
+def test_wide_rows(D, dtype):
+    _run(5, D, dtype, residual=D % 2 == 0)
+
+
+@pytest.mark.parametrize("rows,D,dtype", [(20000, 24, "bf16"), (9001, 128, "bf16"), (5003, 520, "f32"), (8200, 33, "f32")])
+def test_many_rows(rows, D, dtype):
+    """Several steps of a workgroup, four rows at a time, a ragged last one."""
+    _run(rows, D, dtype, residual=True)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 600), ("f32", 30)])
+def test_grouped_weights(dtype, D):
+    for groups, period, reps in ((2, 1, 5), (3, 7, 1), (16, 5, 3), (5, 300, 2), (700, 1, 2)):
+        _run(groups * period * reps, D, dtype, groups=groups, period=period)
+
+
+def test_wide_grouped_rows():
+    _run(12, 20001, "bf16", groups=2, period=3)
+
+
+def test_means_far_above_the_deviation():
+    """Rows around 1000 with a deviation of 1: the variance must not be a difference of large squares."""
+    import torch
+    rng = np.random.default_rng(3)
+    for D in (96, 1001, 20001):
+        _run(40, D, "f32", x=rounded(rng, (40, D), "f32", mean=1000.0), seed=1)
+        spike = rounded(rng, (40, D), "bf16")
+        spike[:, 0] = 3000.0   # one channel far out
+        _run(40, D, "bf16", x=spike, seed=2)
+    # constant rows: only eps is left under the root
+    x = torch.full((5, 64), 2.0, dtype=torch.bfloat16)
+    out = _run(5, 64, "bf16", x=x, seed=3)
+    assert torch.allclose(out["rstd"].cpu(), torch.full((5,), EPS ** -0.5), rtol=1e-6)
+
+
+def test_bad_rows_stay_alone():
+    import torch
+    rng = np.random.default_rng(4)
+    for D in (64, 1000, 20001):
+        x = rounded(rng, (9, D), "bf16")
+        desc = B.make_ln_desc(9, D)
+        ys = []
+        for bad in (None, float("nan"), float("inf")):
+            v = x.clone()
+            if bad is not None:
+                v[4, D // 2] = bad
+            y = torch.empty_like(v, device="cuda")
+            B.ttt_layernorm_fwd(desc, v.cuda(), None, None, None, y, None, None, None)
+            ys.append(y.cpu())
+        good = [i for i in range(9) if i != 4]
+        for y in ys[1:]:
+            assert torch.equal(y[good], ys[0][good]) and torch.isnan(y[4]).any()
+
+
+def test_no_rows():
+    import torch
+    desc = B.make_ln_desc(0, 64, groups=2)
+    dw, db = (torch.full((2, 64), float("nan"), device="cuda") for _ in range(2))
+    e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    m = torch.empty(0, device="cuda")
+    ws = torch.empty(B.ttt_layernorm_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    B.ttt_layernorm_fwd(desc, e, None, None, None, e, None, m, m)
+    B.ttt_layernorm_bwd(desc, e, None, m, m, e, None, e, dw, db, ws)
+    torch.cuda.synchronize()
+    assert (dw == 0).all() and (db == 0).all()   # a sum over nothing
+
+
+def test_optional_outputs():
+    """dw alone, db alone, neither (then without a workspace); inference without mean and rstd."""
+    import torch
+    out = _run(50, 200, "bf16", seed=5)
+    rng = np.random.default_rng(5)
+    x = rounded(rng, (50, 200), "bf16", mean=0.5, std=2.0).cuda()
+    w = rounded(rng, (1, 200), "f32", mean=1.0, std=0.3).cuda()
+    b = rounded(rng, (1, 200), "f32").cuda()
+    dy, dr = (rounded(rng, (50, 200), "bf16").cuda() for _ in range(2))
+    desc = B.make_ln_desc(50, 200)
+    y = torch.empty_like(x)
+    B.ttt_layernorm_fwd(desc, x, None, w, b, y, None, None, None)
+    assert torch.equal(y, out["y"])
+    ws = torch.empty(B.ttt_layernorm_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    for want_w, want_b in ((True, False), (False, True), (False, False)):
+        dx = torch.empty_like(x)
+        dw, db = (torch.empty_like(w) if q else None for q in (want_w, want_b))
+        B.ttt_layernorm_bwd(desc, x, w, out["mean"], out["rstd"], dy, dr, dx, dw, db, ws if want_w or want_b else None)
+        assert torch.equal(dx, out["dx"])
+        assert dw is None or torch.equal(dw, out["dw"])
+        assert db is None or torch.equal(db, out["db"])
+
+
+def test_strided_rows_and_residual_in_place():
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import LayerNormBuffers
+    rng = np.random.default_rng(6)
+    for D, room in ((64, 200), (33, 47), (600, 1208)):
+        wide = torch.full((4, 10, room), float("nan"), dtype=torch.bfloat16, device="cuda")
+        x = wide[..., :D]
+        x.copy_(rounded(rng, (4, 10, D), "bf16"))
+        w = rounded(rng, (1, D), "f32").cuda()
+        dy = rounded(rng, (4, 10, D), "bf16").cuda()
+        buf = LayerNormBuffers(x, w, with_bwd=True)
+        dwide = torch.full_like(wide, 7.0)
+        buf.dx = dwide[..., :D]
+        buf.forward()
+        buf.backward(dy)
+        dense = LayerNormBuffers(x.contiguous(), w, with_bwd=True)
+        dense.forward()
+        dense.backward(dy)
+        f = ln.forward(f64(x).reshape(40, D), f64(w), None, EPS)
+        g = ln.backward(f64(x).reshape(40, D), f64(w), EPS, f64(dy).reshape(40, D))
+        assert worst(buf.y.reshape(40, D), f["y"], f["e_y"], "bf16") <= 1
+        assert worst(buf.dx.reshape(40, D), g["dx"], g["e_dx"], "bf16") <= 1 and worst(buf.dw, g["dw"], g["e_dw"], "f32") <= 1
+        assert (dwide[..., D:] == 7.0).all()
+        # the residual stream updated in place
+        stream = rounded(rng, (4, 10, D), "bf16").cuda()
+        apart = LayerNormBuffers(x, w, res=stream.clone())
+        apart.forward()
+        same = LayerNormBuffers(x, w, res=stream)
+        same.r = stream
+        same.forward()
+        assert torch.equal(same.y, apart.y) and torch.equal(stream, apart.r)
+
+
+def test_repeats_to_the_bit():
+    import torch
+    a = _run(9000, 128, "bf16", groups=4, period=750, seed=7)
+    for _ in range(3):
+        b = _run(9000, 128, "bf16", groups=4, period=750, seed=7)
+        assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_offsets_past_32_bits():
+    import torch
+    rows, D = 70_000, 32_768   # 2.3e9 elements
+    rng = np.random.default_rng(8)
+    x = torch.zeros((rows, D), dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    tail, dt = rounded(rng, (40, D), "bf16"), rounded(rng, (40, D), "bf16")
+    x[-40:], dy[-40:] = tail.cuda(), dt.cuda()
+    w = rounded(rng, (1, D), "f32")
+    desc = B.make_ln_desc(rows, D)
+    y = torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dw, db = torch.empty(1, D, device="cuda"), torch.empty(1, D, device="cuda")
+    ws = torch.empty(B.ttt_layernorm_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    B.ttt_layernorm_fwd(desc, x, None, w.cuda(), None, y, None, mean, rstd)
+    f = ln.forward(f64(tail), f64(w), None, EPS)
+    assert worst(y[-40:], f["y"], f["e_y"], "bf16") <= 1 and not y[:-40].any()
+    B.ttt_layernorm_bwd(desc, x, w.cuda(), mean, rstd, dy, None, y, dw, db, ws)
+    g = ln.backward(f64(tail), f64(w), EPS, f64(dt))
+    assert worst(y[-40:], g["dx"], g["e_dx"], "bf16") <= 1 and not y[:-40].any()
+    assert worst(dw, g["dw"], g["e_dw"], "f32") <= 1 and worst(db, g["db"], g["e_db"], "f32") <= 1
+
+
+def test_graph_replays():
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import LayerNormBuffers
+    rng = np.random.default_rng(9)
+    probs = []
+    for rows, D, G in ((600, 200, 1), (4800, 64, 4)):
+        x, res, dy, dr = (rounded(rng, (rows, D), "bf16").cuda() for _ in range(4))
+        w, b = (rounded(rng, (G, D), "f32").cuda() for _ in range(2))
+        probs.append((LayerNormBuffers(x, w, b, res=res, groups=G, period=100, with_bwd=True), dy, dr))
+    big = max((p[0].ws for p in probs), key=lambda t: t.numel())
+    for p in probs:
+        p[0].ws = big
+
+    def both(p):
+        p[0].forward()
+        p[0].backward(p[1], p[2])
+
+    def outs(p):
+        return [p[0].y, p[0].r, p[0].dx, p[0].dw, p[0].db]
+
+    eager = []
+    for p in probs:
+        both(p)
+        torch.cuda.synchronize()
+        eager.append([t.clone() for t in outs(p)])
+    side, graphs = torch.cuda.Stream(), []
+    for p in probs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            both(p)
+        graphs.append(g)
+    for r in range(4):
+        for k, p in enumerate(probs):
+            for t in outs(p):
+                t.fill_(float("nan"))
+            graphs[k].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs(p), eager[k])), (r, k)
+            both(probs[1 - k])
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs(probs[1 - k]), eager[1 - k])), (r, k)

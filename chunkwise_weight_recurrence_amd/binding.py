@@ -102,6 +102,7 @@ class Kernel(IntEnum):
     LN_FWD = 29
     LN_BWD = 30
     LN_REDUCE = 31
+    REC_CLEAR = 32
 
 
 ENTRY_FWD = 0

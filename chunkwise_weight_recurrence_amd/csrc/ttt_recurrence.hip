@@ -11,13 +11,28 @@
 // All sequences lie behind one another on one token axis (a dense [B,T,D] is the
 // packed case with a start every T tokens).  A tile is kTile tokens x 64 V
 // channels; a wave holds kLW tokens of it in registers, V channels a lane, and
-// the waves' maps meet in LDS.  Tiles meet through `agg`, the map of every
-// (tile, channel).  A sequence start inside a tile makes its map independent of
-// what enters it, so a tile reads the maps back to the tile where the sequence
-// of its first token starts, and no further.  Starts are the same for every
-// channel, so all control flow on them is wave-uniform.  The state of another
-// sequence is never multiplied in (not even by zero): a NaN or an infinity stays
-// in its sequence.
+// the waves' maps meet in LDS.
+//
+// Tiles meet through memory, in one pass over the data: a tile publishes its map
+// as soon as it has it, then reads the maps of the tiles before it (after it, in
+// the backward), folds them in their order and writes its outputs from the value
+// that enters it.  A sequence start inside a tile makes its map independent of
+// what enters, so a tile reads back to the tile where the sequence of its first
+// token starts, and no further; over long ways it reads the maps of whole groups
+// of kGroup tiles, which each group's last tile publishes.
+// - A map is one 8-byte word (A, B) a channel, stored and loaded whole at agent
+//   scope, so a word that is not all ones is complete: no fence, no flag.
+// - Every wait ends: a workgroup takes its place on the token axis from a counter
+//   (one a channel block) when it starts to run, so the tiles that it waits for
+//   are held by workgroups that run already, and these publish before they wait.
+//   A group's map depends on its tiles' maps alone.  Should a caller break the
+//   rule of one workspace a call all the same, the wait gives up after kPolls
+//   looks and the outputs are NaN.
+// - The fold's order is fixed by the tiles' places, so results repeat to the bit.
+//
+// Starts are the same for every channel, so all control flow on them is
+// wave-uniform.  The state of another sequence is never multiplied in (not even
+// by zero): a NaN or an infinity stays in its sequence.
 
 #include <cstdint>
 #include <type_traits>
@@ -30,8 +45,11 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
-constexpr int kLW = 16;              // tokens a wave holds
+constexpr int kLW = 16;                // tokens a wave holds
 constexpr int kTile = kWaves * kLW;  // tokens of a tile
+constexpr int kGroup = 32;           // tiles of a group
+constexpr int kCounterStride = 32;   // ints between two channel blocks' counters: a cache line each
+constexpr int kPolls = 1 << 20;      // of a wave, together; a look takes about a microsecond
 
 struct RecArgs {
   int B, T, n, D;  // sequences, tokens of each (dense), tokens on the axis, channels
@@ -44,7 +62,9 @@ struct RecArgs {
   void* o;
   float* h_final;
   float* ckpt;  // [nt][Dp]: the state that enters each tile
-  float2* agg;  // [nt][Dp]: each tile's map (A, B)
+  uint64_t* maps;    // [nt][Dp]: each tile's map, all ones until it is there
+  uint64_t* groups;  // [ng][Dp]: each whole group's
+  int* counters;     // [ncb]: tiles taken
   const void* d_o;
   const float* d_hfinal;
   void* dx;
@@ -56,16 +76,19 @@ struct RecArgs {
 template <typename E, int V> struct Io;
 template <> struct Io<float, 1> {
   using Raw = float;
+  static constexpr Raw kInf = __builtin_inff();
   static __device__ __forceinline__ void get(Raw r, float (&f)[1]) { f[0] = r; }
   static __device__ __forceinline__ Raw put(const float (&f)[1]) { return f[0]; }
 };
 template <> struct Io<bf16_t, 1> {
   using Raw = uint16_t;
+  static constexpr Raw kInf = 0x7f80;
   static __device__ __forceinline__ void get(Raw r, float (&f)[1]) { f[0] = bf16_to_f32(r); }
   static __device__ __forceinline__ Raw put(const float (&f)[1]) { return f32_to_bf16(f[0]); }
 };
 template <> struct Io<bf16_t, 2> {
   using Raw = uint32_t;
+  static constexpr Raw kInf = 0x7f807f80u;
   static __device__ __forceinline__ void get(Raw r, float (&f)[2]) {
     f[0] = __uint_as_float(r << 16);
     f[1] = __uint_as_float(r & 0xffff0000u);
@@ -77,6 +100,18 @@ template <> struct Io<bf16_t, 2> {
 // whole wave, the lane adds a 32-bit offset.
 template <typename Raw> __device__ __forceinline__ Raw load_at(const void* base, int64_t row_bytes, uint32_t off) {
   return *reinterpret_cast<const Raw*>(static_cast<const char*>(base) + row_bytes + off);
+}
+// kLW rows from row t on; rows past the last of n read the last.
+template <typename Raw> __device__ __forceinline__ void load_rows(const void* base, int64_t row_bytes, int t, int n, uint32_t off,
+                                                                  Raw (&r)[kLW]) {
+  if (t + kLW <= n) {
+    const char* p = static_cast<const char*>(base) + t * row_bytes;
+#pragma unroll
+    for (int j = 0; j < kLW; ++j, p += row_bytes) r[j] = load_at<Raw>(p, 0, off);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j) r[j] = load_at<Raw>(base, min(t + j, n - 1) * row_bytes, off);
+  }
 }
 template <typename Raw> __device__ __forceinline__ void store_at(void* base, int64_t row_bytes, uint32_t off, Raw v) {
   *reinterpret_cast<Raw*>(static_cast<char*>(base) + row_bytes + off) = v;
@@ -109,6 +144,14 @@ struct Meta {
   int start[kTile], end[kTile];
   int lo, hi, first, last;
 };
+// The same for one wave's tokens: bits of those that belong to a sequence, start
+// one, end one; and the tile's first and last, or first = the tile's first token
+// and last = its last where the tile has no token of a sequence.
+struct Bits {
+  uint32_t ok, start, end;
+  int first, last;
+};
+constexpr uint32_t kAll = static_cast<uint32_t>((uint64_t{1} << kLW) - 1);
 
 // The largest j in 0 .. count - 1 with p[j] <= t, or -1 (p sorted); 64 probes a
 // step, the result uniform over the wave.
@@ -127,10 +170,15 @@ __device__ __forceinline__ int last_not_above(const int32_t* p, int count, int t
   }
 }
 
-__device__ __forceinline__ void tile_meta(const RecArgs& a, int t0, Meta& m) {
+__device__ __forceinline__ Bits tile_meta(const RecArgs& a, int t0, Meta& m) {
   const int tid = threadIdx.x;
   const int tl = t0 + kTile - 1;
   if (!a.starts) {
+    if (tl < a.n) {
+      const int from = t0 - t0 % a.T;
+      // inside one sequence, and neither its start nor its end
+      if (from < t0 && from + a.T - 1 > tl) return Bits{kAll, 0, 0, from, from + a.T - 1};
+    }
     if (tid < kTile) {
       const int t = t0 + tid;
       int s = -1, e = -1;
@@ -168,6 +216,11 @@ __device__ __forceinline__ void tile_meta(const RecArgs& a, int t0, Meta& m) {
     }
   }
   __syncthreads();
+  const int lane = tid & 63, at = (tid >> 6) * kLW + lane % kLW, t = t0 + at;
+  const bool ok = lane < kLW && t >= m.lo && t < m.hi;
+  const bool some = m.lo < m.hi;
+  return Bits{static_cast<uint32_t>(__ballot(ok)), static_cast<uint32_t>(__ballot(ok && m.start[at] >= 0)),
+              static_cast<uint32_t>(__ballot(ok && m.end[at] >= 0)), some ? m.first : t0, some ? m.last : tl};
 }
 
 // Sequences without a token: the state passes through (dst = src, or zero).
@@ -184,54 +237,181 @@ __device__ __forceinline__ void pass_empty(const RecArgs& a, int i, int c, bool 
   }
 }
 
-// The value that enters a tile, folded over the maps of `count` tiles, first ..
-// first + dir (count - 1).  The first tile's map has a reset in it, so only its B
-// counts.  Each wave folds a part, the parts meet in `look`; afterwards every
-// wave returns the whole fold.
+// The map of a run of tokens as one word.  A B of all ones (a NaN that no
+// arithmetic makes) would read as pending and becomes another NaN.
+__device__ __forceinline__ void publish(uint64_t* p, float A, float B) {
+  const uint32_t hi = __float_as_uint(B) == 0xffffffffu ? 0x7fc00000u : __float_as_uint(B);
+  __hip_atomic_store(p, static_cast<uint64_t>(hi) << 32 | __float_as_uint(A), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Folds `count` maps onto (A, B), count <= N: all are loaded at once, and again
+// while one of them is pending (a pending word reads as NaN).  addr(k): the first
+// of the lane's V words.
+template <int V, int N, typename Addr>
+__device__ __forceinline__ void fold_some(int count, Addr addr, bool reset_first, int& polls, float (&A)[V], float (&B)[V]) {
+  uint64_t q[N][V];
+  while (true) {
+    bool pending = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint64_t* p = addr(k < count ? k : 0);
+#pragma unroll
+      for (int v = 0; v < V; ++v) q[k][v] = __hip_atomic_load(p + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) pending |= static_cast<uint32_t>(q[k][v] >> 32) == 0xffffffffu;
+    if (__ballot(pending) == 0 || --polls <= 0) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k < count) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float qa = __uint_as_float(static_cast<uint32_t>(q[k][v])), qb = __uint_as_float(static_cast<uint32_t>(q[k][v] >> 32));
+        const bool reset = k == 0 && reset_first;
+        B[v] = reset ? qb : qa * B[v] + qb;
+        A[v] = reset ? 0.0f : qa * A[v];
+      }
+    }
+  }
+}
+
+// The tiles whose maps enter tile i, from tile `far` on, in their order: far's own
+// group up to its border as tiles, then whole groups, then the tiles of i's group.
+// dir = 1: tiles before i; -1: behind it.  Groups are counted in the direction, so
+// that in the backward a "group" is the same set of tiles read from the end.
+struct Way {
+  int far, n1, group, n2, near, n3, dir;
+  __device__ __forceinline__ Way(int i, int far_, int dir_) : far(far_), dir(dir_) {
+    const int gi = i / kGroup, gf = far / kGroup;
+    if (gi == gf) {
+      n1 = n2 = 0;
+      group = 0;
+      near = far;
+      n3 = dir > 0 ? i - far : far - i;
+    } else if (dir > 0) {
+      n1 = (gf + 1) * kGroup - far;
+      group = gf + 1;
+      n2 = gi - gf - 1;
+      near = gi * kGroup;
+      n3 = i - near;
+    } else {
+      n1 = far - gf * kGroup + 1;
+      group = gf - 1;
+      n2 = gf - gi - 1;
+      near = (gi + 1) * kGroup - 1;
+      n3 = near - i;
+    }
+  }
+  __device__ __forceinline__ int count() const { return n1 + n2 + n3; }
+  __device__ __forceinline__ const uint64_t* at(const RecArgs& a, int k, int c) const {
+    const bool tile1 = k < n1, grp = !tile1 && k < n1 + n2;
+    const int row = tile1 ? far + dir * k : grp ? group + dir * (k - n1) : near + dir * (k - n1 - n2);
+    return (grp ? a.groups : a.maps) + static_cast<int64_t>(row) * a.Dp + c;
+  }
+};
+
+// The value that enters tile i.  The farthest tile's map has a reset in it, so only
+// its B counts.  Each wave folds a part, the parts meet in `look`.
 template <int V>
-__device__ __forceinline__ void fold_tiles(const RecArgs& a, int first, int count, int dir, int c, float (&look)[kWaves][2 * V][64],
-                                           float (&h)[V]) {
+__device__ __forceinline__ void fold_way(const RecArgs& a, const Way& way, int c, float (&look)[kWaves][64][2 * V], float (&h)[V]) {
+  constexpr int N = 4;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int count = way.count();
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = 0.0f;
   if (count <= 0) return;  // the same for the whole workgroup
   const int k0 = static_cast<int>(static_cast<int64_t>(count) * wave / kWaves);
   const int k1 = static_cast<int>(static_cast<int64_t>(count) * (wave + 1) / kWaves);
-  float A[V], Bv[V];
+  int polls = kPolls;
+  float A[V], B[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, Bv[v] = 0.0f;
-  for (int k = k0; k < k1; ++k) {
-    const float2* p = a.agg + static_cast<int64_t>(first + dir * k) * a.Dp + c;
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  for (int k = k0; k < k1; k += N)
+    fold_some<V, N>(min(N, k1 - k), [&](int j) { return way.at(a, k + j, c); }, k == 0, polls, A, B);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 q = p[v];
-      Bv[v] = k == 0 ? q.y : q.x * Bv[v] + q.y;
-      A[v] = k == 0 ? 0.0f : q.x * A[v];
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) look[wave][2 * v][lane] = A[v], look[wave][2 * v + 1][lane] = Bv[v];
+  for (int v = 0; v < V; ++v) look[wave][lane][2 * v] = A[v], look[wave][lane][2 * v + 1] = B[v];
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = look[w][2 * v][lane] * h[v] + look[w][2 * v + 1][lane];
+    for (int v = 0; v < V; ++v) h[v] = look[w][lane][2 * v] * h[v] + look[w][lane][2 * v + 1];
 }
 
-constexpr int kAggregate = 0;  // only the tile's map, to agg
-constexpr int kOutput = 1;     // reads the maps, writes the outputs
+// Tile i's map (A, B) goes out; the last tile of a group (in direction dir) then
+// publishes the group's.  Wave 0 holds the map.
+template <int V>
+__device__ __forceinline__ void publish_tile(const RecArgs& a, int i, int dir, int c, float (&look)[kWaves][64][2 * V],
+                                             const float (&A)[V], const float (&B)[V]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(a.maps + static_cast<int64_t>(i) * a.Dp + c + v, A[v], B[v]);
+  }
+  const int g = i / kGroup, from = dir > 0 ? g * kGroup : g * kGroup + kGroup - 1;
+  // only a whole group has a map, and only its last tile publishes it
+  if (i != (dir > 0 ? g * kGroup + kGroup - 1 : g * kGroup) || (g + 1) * kGroup > a.nt) return;
+  constexpr int N = kGroup / kWaves;
+  float GA[V], GB[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) GA[v] = 1.0f, GB[v] = 0.0f;
+  const int count = wave == kWaves - 1 ? N - 1 : N;  // all but tile i itself
+  int polls = kPolls;
+  fold_some<V, N>(count, [&](int j) { return a.maps + static_cast<int64_t>(from + dir * (wave * N + j)) * a.Dp + c; }, false, polls,
+                  GA, GB);
+#pragma unroll
+  for (int v = 0; v < V; ++v) look[wave][lane][2 * v] = GA[v], look[wave][lane][2 * v + 1] = GB[v];
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float qa = look[w][lane][2 * v], qb = look[w][lane][2 * v + 1];
+        GB[v] = qa * GB[v] + qb;
+        GA[v] = qa * GA[v];
+      }
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(a.groups + static_cast<int64_t>(g) * a.Dp + c + v, A[v] * GA[v], A[v] * GB[v] + B[v]);
+  }
+  __syncthreads();  // `look` is free again
+}
 
-template <typename E, int V, int GATE, int IN, int MODE>
-__global__ __launch_bounds__(kThreads) void rec_fwd_kernel(RecArgs a) {
+// The tile that this workgroup works on: the next one of its channel block (place
+// 0 is the first in the direction of the run).
+__device__ __forceinline__ int take_tile(const RecArgs& a, int cb, int dir) {
+  __shared__ int place;
+  if (threadIdx.x == 0)
+    place = __hip_atomic_fetch_add(a.counters + cb * kCounterStride, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const int p = min(max(__builtin_amdgcn_readfirstlane(place), 0), a.nt - 1);
+  return dir > 0 ? p : a.nt - 1 - p;
+}
+
+// Every map pending, every counter at zero.
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ maps, int64_t n, int* __restrict__ counters, int nc) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) maps[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  if (i < nc) counters[i] = 0;
+}
+
+// LINKED: there is more than one tile.
+template <typename E, int V, int GATE, int IN, bool LINKED>
+__global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(RecArgs a) {
   using IO = Io<E, V>;
   using Raw = typename IO::Raw;
   __shared__ Meta m;
-  __shared__ float part[kWaves][2 * V][64];
-  __shared__ float look[kWaves][2 * V][64];
+  __shared__ __attribute__((aligned(16))) float part[kWaves][64][2 * V];
+  __shared__ __attribute__((aligned(16))) float look[kWaves][64][2 * V];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i = blockIdx.x / a.ncb, cb = blockIdx.x % a.ncb;
+  const int cb = blockIdx.x % a.ncb;
+  const int i = LINKED ? take_tile(a, cb, 1) : 0;
   const int c = (cb * 64 + lane) * V;
   const bool in = c < a.D;
   const uint32_t cl = in ? c : 0;  // lanes past the last channel read the first and store nothing
@@ -242,24 +422,20 @@ __global__ __launch_bounds__(kThreads) void rec_fwd_kernel(RecArgs a) {
 
   Raw xr[kLW], gr[kLW];
   if (a.n > 0) {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      const int t = min(tw + j, a.n - 1);
-      xr[j] = load_at<Raw>(a.x, t * rx, off);
-      gr[j] = load_at<Raw>(a.g, t * rg, off);
-    }
+    load_rows<Raw>(a.x, rx, tw, a.n, off, xr);
+    load_rows<Raw>(a.g, rg, tw, a.n, off, gr);
   } else {
 #pragma unroll
     for (int j = 0; j < kLW; ++j) xr[j] = gr[j] = Raw(0);
   }
-  tile_meta(a, t0, m);
-  const bool mine = lane < kLW;
-  const int t = tw + lane, at = mine ? wave * kLW + lane : 0;
-  const bool ok = mine && t >= m.lo && t < m.hi;
-  const uint32_t okm = static_cast<uint32_t>(__ballot(ok));
-  const uint32_t sm = static_cast<uint32_t>(__ballot(ok && m.start[at] >= 0));
-  const uint32_t em = static_cast<uint32_t>(__ballot(ok && m.end[at] >= 0));
-  const bool simple = okm == (1u << kLW) - 1 && sm == 0;
+  const Bits bits = tile_meta(a, t0, m);
+  const uint32_t okm = bits.ok, sm = bits.start, em = bits.end;
+  if (okm != kAll) {
+    // a token of no sequence: a = 1 and u = 0 leave what passes over it as it is
+#pragma unroll
+    for (int j = 0; j < kLW; ++j)
+      if (!(okm >> j & 1)) xr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+  }
 
   float av[kLW][V], uv[kLW][V];
   float A[V], h[V];
@@ -281,7 +457,7 @@ __global__ __launch_bounds__(kThreads) void rec_fwd_kernel(RecArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) f[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
   };
-  if (simple) {
+  if (sm == 0) {
 #pragma unroll
     for (int j = 0; j < kLW; ++j)
 #pragma unroll
@@ -292,10 +468,6 @@ __global__ __launch_bounds__(kThreads) void rec_fwd_kernel(RecArgs a) {
   } else {
 #pragma unroll
     for (int j = 0; j < kLW; ++j) {
-      if (!(okm >> j & 1)) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) av[j][v] = 1.0f, uv[j][v] = 0.0f;
-      }
       if (sm >> j & 1) initial(j, h);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -305,82 +477,81 @@ __global__ __launch_bounds__(kThreads) void rec_fwd_kernel(RecArgs a) {
     }
     // a start: what enters no longer counts.  The sign of A carries it to the readers of `part`.
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = sm ? -1.0f : A[v];
+    for (int v = 0; v < V; ++v) A[v] = -1.0f;
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) part[wave][2 * v][lane] = A[v], part[wave][2 * v + 1][lane] = h[v];
+  for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
   __syncthreads();
 
   // fold the maps of waves 0 .. upto - 1 onto h; A: the product, dropped at a start
   auto fold_waves = [&](int upto, float (&hh)[V], float (&AA)[V]) {
+    for (int w = 0; w < upto; ++w) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < upto) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float pa = part[w][2 * v][lane], pb = part[w][2 * v + 1][lane];
-          const bool reset = pa < 0.0f;
-          hh[v] = reset ? pb : pa * hh[v] + pb;
-          AA[v] = reset ? 0.0f : pa * AA[v];
-        }
+      for (int v = 0; v < V; ++v) {
+        const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+        const bool reset = pa < 0.0f;
+        hh[v] = reset ? pb : pa * hh[v] + pb;
+        AA[v] = reset ? 0.0f : pa * AA[v];
       }
     }
   };
-  if constexpr (MODE == kAggregate) {
+  if constexpr (LINKED) {
     if (wave == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
       fold_waves(kWaves, h, A);
+    }
+    publish_tile<V>(a, i, 1, c, look, A, h);
+    fold_way<V>(a, Way(i, bits.first / kTile, 1), c, look, h);
+  } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) a.agg[static_cast<int64_t>(i) * a.Dp + c + v] = make_float2(A[v], h[v]);
+    for (int v = 0; v < V; ++v) h[v] = 0.0f;
+  }
+  if (a.ckpt && wave == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v] = h[v];
+  }
+  fold_waves(wave, h, A);
+  if (okm == kAll && (sm | em) == 0) {
+    char* p = static_cast<char*>(a.o) + tw * ro;
+#pragma unroll
+    for (int j = 0; j < kLW; ++j, p += ro) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
+      if (in) store_at<Raw>(p, 0, off, IO::put(h));
     }
   } else {
-    const int ts = m.first / kTile;
-    fold_tiles<V>(a, ts, m.lo < m.hi ? i - ts : 0, 1, c, look, h);
-    if (a.ckpt && wave == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v] = h[v];
-    }
-    fold_waves(wave, h, A);
-    if (simple && em == 0) {
+    for (int j = 0; j < kLW; ++j) {
+      if (sm >> j & 1) initial(j, h);
 #pragma unroll
-      for (int j = 0; j < kLW; ++j) {
+      for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
+      if (in && (okm >> j & 1)) store_at<Raw>(a.o, (tw + j) * ro, off, IO::put(h));
+      if (in && a.h_final && (em >> j & 1)) {
+        const int s = __builtin_amdgcn_readfirstlane(m.end[wave * kLW + j]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
-        if (in) store_at<Raw>(a.o, (tw + j) * ro, off, IO::put(h));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kLW; ++j) {
-        if (sm >> j & 1) initial(j, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
-        if (in && (okm >> j & 1)) store_at<Raw>(a.o, (tw + j) * ro, off, IO::put(h));
-        if (in && a.h_final && (em >> j & 1)) {
-          const int s = __builtin_amdgcn_readfirstlane(m.end[wave * kLW + j]);
-#pragma unroll
-          for (int v = 0; v < V; ++v) a.h_final[static_cast<int64_t>(s) * a.D + c + v] = h[v];
-        }
+        for (int v = 0; v < V; ++v) a.h_final[static_cast<int64_t>(s) * a.D + c + v] = h[v];
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.h0, a.h_final);
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.h0, a.h_final);
 }
 
 // The backward: the same tiles, e running from the end.  The tile's states are
 // formed again from the state that entered it (ckpt) and the waves' forward maps.
-template <typename E, int V, int GATE, int IN, int MODE>
-__global__ __launch_bounds__(kThreads) void rec_bwd_kernel(RecArgs a) {
+template <typename E, int V, int GATE, int IN, bool LINKED>
+__global__ __launch_bounds__(kThreads, 2) void rec_bwd_kernel(RecArgs a) {
   using IO = Io<E, V>;
   using Raw = typename IO::Raw;
   __shared__ Meta m;
-  __shared__ float part[kWaves][2 * V][64];   // forward maps
-  __shared__ float rpart[kWaves][2 * V][64];  // maps of e, from the end
-  __shared__ float look[kWaves][2 * V][64];
+  __shared__ __attribute__((aligned(16))) float part[kWaves][64][2 * V];   // forward maps
+  __shared__ __attribute__((aligned(16))) float rpart[kWaves][64][2 * V];  // maps of e, from the end
+  __shared__ __attribute__((aligned(16))) float look[kWaves][64][2 * V];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i = blockIdx.x / a.ncb, cb = blockIdx.x % a.ncb;
+  const int cb = blockIdx.x % a.ncb;
+  const int i = LINKED ? take_tile(a, cb, -1) : 0;
   const int c = (cb * 64 + lane) * V;
   const bool in = c < a.D;
   const uint32_t cl = in ? c : 0;
@@ -391,25 +562,20 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(RecArgs a) {
 
   Raw xr[kLW], gr[kLW], dr[kLW];
   if (a.n > 0) {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      const int t = min(tw + j, a.n - 1);
-      gr[j] = load_at<Raw>(a.g, t * rg, off);
-      dr[j] = load_at<Raw>(a.d_o, t * ro, off);
-      xr[j] = load_at<Raw>(a.x, t * rx, off);
-    }
+    load_rows<Raw>(a.g, rg, tw, a.n, off, gr);
+    load_rows<Raw>(a.d_o, ro, tw, a.n, off, dr);
+    load_rows<Raw>(a.x, rx, tw, a.n, off, xr);
   } else {
 #pragma unroll
     for (int j = 0; j < kLW; ++j) xr[j] = gr[j] = dr[j] = Raw(0);
   }
-  tile_meta(a, t0, m);
-  const bool mine = lane < kLW;
-  const int t = tw + lane, at = mine ? wave * kLW + lane : 0;
-  const bool ok = mine && t >= m.lo && t < m.hi;
-  const uint32_t okm = static_cast<uint32_t>(__ballot(ok));
-  const uint32_t sm = static_cast<uint32_t>(__ballot(ok && m.start[at] >= 0));
-  const uint32_t em = static_cast<uint32_t>(__ballot(ok && m.end[at] >= 0));
-  const bool simple = okm == (1u << kLW) - 1 && (sm | em) == 0;
+  const Bits bits = tile_meta(a, t0, m);
+  const uint32_t okm = bits.ok, sm = bits.start, em = bits.end;
+  if (okm != kAll) {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j)
+      if (!(okm >> j & 1)) xr[j] = dr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+  }
 
   float av[kLW][V];
 #pragma unroll
@@ -441,135 +607,159 @@ __global__ __launch_bounds__(kThreads) void rec_bwd_kernel(RecArgs a) {
     for (int v = 0; v < V; ++v) f[v] = a.d_hfinal ? a.d_hfinal[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
   };
 
-  // e's map over the wave's tokens
+  // e's map over the wave's tokens, from the end
   float A[V], e[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.0f, e[v] = 0.0f;
-#pragma unroll
-  for (int j = kLW - 1; j >= 0; --j) {
-    if (!simple && (em >> j & 1)) final_grad(j, e);
+  auto back = [&](int j) {
     float d[V];
     IO::get(dr[j], d);
-    if (simple || (okm >> j & 1)) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        e[v] = av[j][v] * (d[v] + e[v]);
-        A[v] *= av[j][v];
-      }
+    for (int v = 0; v < V; ++v) {
+      e[v] = av[j][v] * (d[v] + e[v]);
+      A[v] *= av[j][v];
     }
-  }
+  };
+  if (em == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) rpart[wave][2 * v][lane] = em ? -1.0f : A[v], rpart[wave][2 * v + 1][lane] = e[v];
-
-  if constexpr (MODE == kOutput) {
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      if (!simple && (sm >> j & 1)) initial(j, h);
-      float u[V], rest[V], x[V];
-      input(j, u, rest, x);
-      if (simple || (okm >> j & 1)) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = av[j][v] * h[v] + u[v];
-          A[v] *= av[j][v];
-        }
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) part[wave][2 * v][lane] = sm ? -1.0f : A[v], part[wave][2 * v + 1][lane] = h[v];
-  }
-  __syncthreads();
-
-  if constexpr (MODE == kAggregate) {
-    if (wave == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float AA = 1.0f, ee = 0.0f;
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-          const float pa = rpart[w][2 * v][lane], pb = rpart[w][2 * v + 1][lane];
-          ee = pa < 0.0f ? pb : pa * ee + pb;
-          AA = pa < 0.0f ? 0.0f : pa * AA;
-        }
-        a.agg[static_cast<int64_t>(i) * a.Dp + c + v] = make_float2(AA, ee);
-      }
-    }
+    for (int j = kLW - 1; j >= 0; --j) back(j);
   } else {
-    // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
-    float wv[kLW][V];
-    {
-      float h[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float pa = part[w][2 * v][lane], pb = part[w][2 * v + 1][lane];
-            h[v] = pa < 0.0f ? pb : pa * h[v] + pb;
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kLW; ++j) {
-        if (!simple && (sm >> j & 1)) initial(j, h);
-        float u[V], rest[V], x[V];
-        input(j, u, rest, x);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float da = GATE == TTT_GATE_SIGMOID ? av[j][v] * rest[v] : av[j][v];
-          wv[j][v] = da * (IN == TTT_REC_PLAIN ? h[v] : h[v] - x[v]);
-        }
-        if (simple || (okm >> j & 1)) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + u[v];
-        }
-      }
-    }
-    const int te = m.last / kTile;
-    fold_tiles<V>(a, te, m.lo < m.hi ? te - i : 0, -1, c, look, e);
-#pragma unroll
-    for (int w = kWaves - 1; w >= 0; --w) {
-      if (w > wave) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float pa = rpart[w][2 * v][lane], pb = rpart[w][2 * v + 1][lane];
-          e[v] = pa < 0.0f ? pb : pa * e[v] + pb;
-        }
-      }
-    }
 #pragma unroll
     for (int j = kLW - 1; j >= 0; --j) {
-      if (!simple && (em >> j & 1)) final_grad(j, e);
-      if (simple || (okm >> j & 1)) {
-        float d[V], ox[V], og[V], u[V], rest[V], x[V];
-        IO::get(dr[j], d);
-        if constexpr (IN == TTT_REC_CONVEX) input(j, u, rest, x);
+      if (em >> j & 1) final_grad(j, e);
+      back(j);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = -1.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) rpart[wave][lane][2 * v] = A[v], rpart[wave][lane][2 * v + 1] = e[v];
+
+  // the state's map over them
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+  auto state = [&](int j) {
+    float u[V], rest[V], x[V];
+    input(j, u, rest, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = av[j][v] * h[v] + u[v];
+      A[v] *= av[j][v];
+    }
+  };
+  if (sm == 0) {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j) state(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j) {
+      if (sm >> j & 1) initial(j, h);
+      state(j);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = -1.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
+  __syncthreads();
+
+  if constexpr (LINKED) {
+    if (wave == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) A[v] = 1.0f, e[v] = 0.0f;
+#pragma unroll
+      for (int w = kWaves - 1; w >= 0; --w)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float dh = d[v] + e[v];
-          ox[v] = IN == TTT_REC_PLAIN ? dh : dh * rest[v];
-          og[v] = dh * wv[j][v];
-          e[v] = av[j][v] * dh;
+          const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
+          e[v] = pa < 0.0f ? pb : pa * e[v] + pb;
+          A[v] = pa < 0.0f ? 0.0f : pa * A[v];
         }
-        if (in) {
-          store_at<Raw>(a.dx, (tw + j) * rx, off, IO::put(ox));
-          store_at<Raw>(a.dg, (tw + j) * rg, off, IO::put(og));
-        }
-      }
-      if (!simple && in && a.dh0 && (sm >> j & 1)) {
+    }
+    publish_tile<V>(a, i, -1, c, look, A, e);
+  }
+  // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
+  float wv[kLW][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
+  for (int w = 0; w < wave; ++w) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+      h[v] = pa < 0.0f ? pb : pa * h[v] + pb;
+    }
+  }
+  auto slope = [&](int j) {
+    float u[V], rest[V], x[V];
+    input(j, u, rest, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float da = GATE == TTT_GATE_SIGMOID ? av[j][v] * rest[v] : av[j][v];
+      wv[j][v] = da * (IN == TTT_REC_PLAIN ? h[v] : h[v] - x[v]);
+      h[v] = av[j][v] * h[v] + u[v];
+    }
+  };
+  if (sm == 0) {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j) slope(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kLW; ++j) {
+      if (sm >> j & 1) initial(j, h);
+      slope(j);
+    }
+  }
+  if constexpr (LINKED) {
+    fold_way<V>(a, Way(i, bits.last / kTile, -1), c, look, e);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = 0.0f;
+  }
+  for (int w = kWaves - 1; w > wave; --w) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
+      e[v] = pa < 0.0f ? pb : pa * e[v] + pb;
+    }
+  }
+  char* px = static_cast<char*>(a.dx) + (tw + kLW - 1) * rx;
+  char* pg = static_cast<char*>(a.dg) + (tw + kLW - 1) * rg;
+  auto gradients = [&](int j, bool store) {
+    float d[V], ox[V], og[V], u[V], rest[V], x[V];
+    IO::get(dr[j], d);
+    if constexpr (IN == TTT_REC_CONVEX) input(j, u, rest, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float dh = d[v] + e[v];
+      ox[v] = IN == TTT_REC_PLAIN ? dh : dh * rest[v];
+      og[v] = dh * wv[j][v];
+      e[v] = av[j][v] * dh;
+    }
+    if (store) {
+      store_at<Raw>(px, 0, off, IO::put(ox));
+      store_at<Raw>(pg, 0, off, IO::put(og));
+    }
+    px -= rx;
+    pg -= rg;
+  };
+  if (okm == kAll && (sm | em) == 0) {
+#pragma unroll
+    for (int j = kLW - 1; j >= 0; --j) gradients(j, in);
+  } else {
+#pragma unroll
+    for (int j = kLW - 1; j >= 0; --j) {
+      if (em >> j & 1) final_grad(j, e);
+      gradients(j, in && (okm >> j & 1));
+      if (in && a.dh0 && (sm >> j & 1)) {
         const int s = __builtin_amdgcn_readfirstlane(m.start[wave * kLW + j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a.dh0[static_cast<int64_t>(s) * a.D + c + v] = e[v];
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.d_hfinal, a.dh0);
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.d_hfinal, a.dh0);
 }
 
 // One token for each row: h[slot] <- a h[slot] + u, o = h[slot].  Rows that name
@@ -692,10 +882,33 @@ RecArgs make_args(const ttt_rec_desc& d, int V) {
 
 bool recurrence_grid_fits(const ttt_rec_desc& d) { return tiles(d) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31); }
 
+// The maps of the tiles and of the whole groups, then the counters.
+size_t map_words(const ttt_rec_desc& d) {
+  return static_cast<size_t>(tiles(d) + tiles(d) / kGroup) * padded_channels(d);
+}
+size_t counter_ints(const ttt_rec_desc& d) { return static_cast<size_t>((d.D + 63) / 64) * kCounterStride; }
+
 size_t recurrence_workspace(const ttt_rec_desc& d) {
   if (tiles(d) == 1) return 0;
-  return align256(static_cast<size_t>(tiles(d)) * padded_channels(d) * sizeof(float2));
+  return align256(map_words(d) * sizeof(uint64_t)) + align256(counter_ints(d) * sizeof(int));
 }
+namespace {
+
+// Lays out the workspace and clears it (a kernel, so that a graph can hold it).
+hipError_t link_tiles(const ttt_rec_desc& d, RecArgs& a, void* ws, hipStream_t s) {
+  a.maps = static_cast<uint64_t*>(ws);
+  a.groups = a.maps + static_cast<size_t>(a.nt) * a.Dp;
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + align256(map_words(d) * sizeof(uint64_t)));
+  const int64_t n = static_cast<int64_t>(map_words(d) / 2);  // Dp is even
+  const int nc = static_cast<int>(counter_ints(d));
+  const int64_t work = n > nc ? n : nc;
+  KernelScope scope(TTT_KERNEL_REC_CLEAR, s);
+  rec_clear_kernel<<<static_cast<uint32_t>((work + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint4*>(ws), n, a.counters, nc);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 size_t recurrence_saved(const ttt_rec_desc& d) {
   return align256(static_cast<size_t>(tiles(d)) * padded_channels(d) * sizeof(float));
 }
@@ -705,18 +918,17 @@ hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const voi
   const int V = lane_channels(d.dtype, d.D, d.ldx, d.ldg);
   RecArgs a = make_args(d, V);
   a.x = x; a.g = gate; a.h0 = h0; a.starts = d.packed ? starts : nullptr;
-  a.o = o; a.h_final = h_final; a.ckpt = static_cast<float*>(saved); a.agg = static_cast<float2*>(ws);
+  a.o = o; a.h_final = h_final; a.ckpt = static_cast<float*>(saved);
+  if (a.nt > 1) {
+    const hipError_t e = link_tiles(d, a, ws, s);
+    if (e != hipSuccess) return e;
+  }
   return dispatch(d, V, [&](auto e, auto v, auto gk, auto in) {
     using E = decltype(e);
     const dim3 grid(static_cast<uint32_t>(a.nt) * a.ncb);
-    if (a.nt > 1) {
-      KernelScope scope(TTT_KERNEL_REC_FWD, s);
-      rec_fwd_kernel<E, v(), gk(), in(), kAggregate><<<grid, kThreads, 0, s>>>(a);
-    }
-    {
-      KernelScope scope(TTT_KERNEL_REC_FWD, s);
-      rec_fwd_kernel<E, v(), gk(), in(), kOutput><<<grid, kThreads, 0, s>>>(a);
-    }
+    KernelScope scope(TTT_KERNEL_REC_FWD, s);
+    if (a.nt > 1) rec_fwd_kernel<E, v(), gk(), in(), true><<<grid, kThreads, 0, s>>>(a);
+    else rec_fwd_kernel<E, v(), gk(), in(), false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -727,19 +939,18 @@ hipError_t recurrence_bwd_launch(const ttt_rec_desc& d, const void* x, const voi
   const int V = lane_channels(d.dtype, d.D, d.ldx, d.ldg);
   RecArgs a = make_args(d, V);
   a.x = x; a.g = gate; a.h0 = h0; a.starts = d.packed ? starts : nullptr;
-  a.ckpt = const_cast<float*>(static_cast<const float*>(saved)); a.agg = static_cast<float2*>(ws);
+  a.ckpt = const_cast<float*>(static_cast<const float*>(saved));
   a.d_o = d_o; a.d_hfinal = d_hfinal; a.dx = dx; a.dg = dgate; a.dh0 = dh0;
+  if (a.nt > 1) {
+    const hipError_t e = link_tiles(d, a, ws, s);
+    if (e != hipSuccess) return e;
+  }
   return dispatch(d, V, [&](auto e, auto v, auto gk, auto in) {
     using E = decltype(e);
     const dim3 grid(static_cast<uint32_t>(a.nt) * a.ncb);
-    if (a.nt > 1) {
-      KernelScope scope(TTT_KERNEL_REC_BWD, s);
-      rec_bwd_kernel<E, v(), gk(), in(), kAggregate><<<grid, kThreads, 0, s>>>(a);
-    }
-    {
-      KernelScope scope(TTT_KERNEL_REC_BWD, s);
-      rec_bwd_kernel<E, v(), gk(), in(), kOutput><<<grid, kThreads, 0, s>>>(a);
-    }
+    KernelScope scope(TTT_KERNEL_REC_BWD, s);
+    if (a.nt > 1) rec_bwd_kernel<E, v(), gk(), in(), true><<<grid, kThreads, 0, s>>>(a);
+    else rec_bwd_kernel<E, v(), gk(), in(), false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }

@@ -637,7 +637,8 @@ typedef enum {
   TTT_KERNEL_LN_FWD = 29,        /* layer norm forward */
   TTT_KERNEL_LN_BWD = 30,        /* layer norm backward: dx and partial dw, db */
   TTT_KERNEL_LN_REDUCE = 31,     /* layer norm backward: sum of the partial dw, db */
-  TTT_KERNEL_COUNT = 32
+  TTT_KERNEL_REC_CLEAR = 32,     /* gated linear recurrence: workspace cleared */
+  TTT_KERNEL_COUNT = 33
 } ttt_kernel;
 
 TTT_API int ttt_timing_enable(int on);

@@ -582,11 +582,11 @@ int check_rec_desc(const ttt_rec_desc* d) {
     return fail(TTT_ERR_INVALID_ARG, "ldx, ldg must be 0 or >= D (got %lld, %lld)", static_cast<long long>(d->ldx),
                 static_cast<long long>(d->ldg));
   const int64_t n = d->packed ? d->T : static_cast<int64_t>(d->B) * d->T;
-  // Token indices are 32-bit, rounded up to whole tiles; a lane's channel offset in bytes too.
-  if (n > (int64_t{1} << 31) - 4096 || d->D > (1 << 24) || !ttt::recurrence_grid_fits(*d))
+  // Token indices are 32-bit, rounded up to whole tiles; a wave's 32 rows lie within 2^30 bytes.
+  if (n > (int64_t{1} << 31) - 4096 || d->D > (1 << 23) || !ttt::recurrence_grid_fits(*d))
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens of %d channels)", static_cast<long long>(n), d->D);
   const int64_t ld = d->ldx > d->ldg ? d->ldx : d->ldg;
-  if (static_cast<double>(n) * static_cast<double>(ld > d->D ? ld : d->D) > 4.0e12)
+  if (ld > (1 << 23) || static_cast<double>(n) * static_cast<double>(ld > d->D ? ld : d->D) > 4.0e12)
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (rows %lld elements apart)", static_cast<long long>(ld));
   return TTT_OK;
 }
@@ -626,7 +626,7 @@ int ttt_recurrence_workspace_size(const ttt_rec_desc* desc, int entry, size_t* b
   if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
   if (entry != TTT_ENTRY_FWD && entry != TTT_ENTRY_BWD)
     return fail(TTT_ERR_INVALID_ARG, "invalid entry %d (0 = forward, 1 = backward)", entry);
-  *bytes = ttt::recurrence_workspace(*desc);
+  *bytes = ttt::recurrence_workspace(*desc, entry);
   return ok();
 }
 
@@ -652,7 +652,7 @@ int ttt_recurrence_fwd(const ttt_rec_desc* desc, const void* x, const void* gate
   if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"h0", h0}, {"seq_starts", seq_starts}, {"o", o},
                                     {"h_final", h_final}, {"saved", saved}, {"ws", ws}}))
     return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
-  const size_t need = ttt::recurrence_workspace(*desc);
+  const size_t need = ttt::recurrence_workspace(*desc, TTT_ENTRY_FWD);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
   if (desc->B == 0 || (n == 0 && !h_final)) return ok();
@@ -678,7 +678,7 @@ int ttt_recurrence_bwd(const ttt_rec_desc* desc, const void* x, const void* gate
                                     {"d_o", d_o}, {"d_hfinal", d_hfinal}, {"dx", dx}, {"dgate", dgate}, {"dh0", dh0},
                                     {"ws", ws}}))
     return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
-  const size_t need = ttt::recurrence_workspace(*desc);
+  const size_t need = ttt::recurrence_workspace(*desc, TTT_ENTRY_BWD);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
   if (desc->B == 0 || (n == 0 && !dh0)) return ok();

@@ -9,9 +9,11 @@
 // runs compose: that is what splits the token axis.
 //
 // All sequences lie behind one another on one token axis (a dense [B,T,D] is the
-// packed case with a start every T tokens).  A tile is kTile tokens x 64 V
-// channels; a wave holds kLW tokens of it in registers, V channels a lane, and
-// the waves' maps meet in LDS.
+// packed case with a start every T tokens).  A tile is kWaves LW tokens x 64
+// V channels; a wave holds LW tokens of it in registers, V channels a lane, and the
+// waves' maps meet in LDS.  The backward keeps its inputs packed as they were loaded
+// and forms a_t again in each of its three walks: that costs arithmetic, of which
+// there is room, and saves registers, of which there is none.
 //
 // Tiles meet through memory, in one pass over the data: a tile publishes its map
 // as soon as it has it, then reads the maps of the tiles before it (after it, in
@@ -45,8 +47,8 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
-constexpr int kLW = 16;                // tokens a wave holds
-constexpr int kTile = kWaves * kLW;  // tokens of a tile
+constexpr int kFwdLW = 16, kBwdLW = 16;  // tokens a wave holds
+constexpr int kRun = kWaves * kBwdLW;    // tokens between two states in the saved context
 constexpr int kGroup = 32;           // tiles of a group
 constexpr int kCounterStride = 32;   // ints between two channel blocks' counters: a cache line each
 constexpr int kPolls = 1 << 20;      // of a wave, together; a look takes about a microsecond
@@ -61,7 +63,7 @@ struct RecArgs {
   const float* h0;
   void* o;
   float* h_final;
-  float* ckpt;  // [nt][Dp]: the state that enters each tile
+  float* ckpt;  // [runs][Dp]: the state that enters each run of kRun tokens
   uint64_t* maps;    // [nt][Dp]: each tile's map, all ones until it is there
   uint64_t* groups;  // [ng][Dp]: each whole group's
   int* counters;     // [ncb]: tiles taken
@@ -96,26 +98,65 @@ template <> struct Io<bf16_t, 2> {
   static __device__ __forceinline__ Raw put(const float (&f)[2]) { return pack_bf16x2(f[0], f[1]); }
 };
 
-// The element at channel c of row t: the row's address is the same for the
-// whole wave, the lane adds a 32-bit offset.
+// A value that is the same in every lane, kept as such.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Up to LW rows of a tensor from row t on, as a buffer resource over just them: a
+// load past them reads zero and a store past them does nothing, so neither the
+// last tile's rows nor the last block's lanes need a branch.
+// A range is at most 2^30 bytes: kNowhere, as a lane's offset, stays behind it for
+// every row, and so does kNoRow in place of a row's, added to either kind of lane.
+constexpr uint32_t kNowhere = 0x40000000u, kNoRow = 0x80000000u;
+template <typename Raw, int LW> struct Rows {
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t stride;  // bytes from row to row, at most 2^30 / LW
+  __device__ __forceinline__ Rows(const void* base, int64_t ld, int D, int elem, int t, int n) {
+    const int rows = min(max(n - t, 0), LW);
+    const uint32_t bytes = rows > 0 ? static_cast<uint32_t>(rows - 1) * static_cast<uint32_t>(ld * elem) + D * elem : 0;
+    const char* p = uniform(static_cast<const char*>(base) + (rows > 0 ? t * ld * elem : 0));
+    rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, uniform(static_cast<int>(bytes)), 0x00020000);
+    stride = uniform(static_cast<int>(ld * elem));
+  }
+  __device__ __forceinline__ Raw load(int j, uint32_t off) const {
+    if constexpr (sizeof(Raw) == 2) return __builtin_amdgcn_raw_buffer_load_b16(rs, static_cast<int>(off + j * stride), 0, 0);
+    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(off + j * stride), 0, 0));
+  }
+  __device__ __forceinline__ void store(int j, uint32_t off, bool ok, Raw v) const {  // ok: the same for the wave
+    const int at = static_cast<int>(off + (ok ? j * stride : kNoRow));
+    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(v, rs, at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rs, at, 0, 0);
+  }
+};
+
 template <typename Raw> __device__ __forceinline__ Raw load_at(const void* base, int64_t row_bytes, uint32_t off) {
   return *reinterpret_cast<const Raw*>(static_cast<const char*>(base) + row_bytes + off);
-}
-// kLW rows from row t on; rows past the last of n read the last.
-template <typename Raw> __device__ __forceinline__ void load_rows(const void* base, int64_t row_bytes, int t, int n, uint32_t off,
-                                                                  Raw (&r)[kLW]) {
-  if (t + kLW <= n) {
-    const char* p = static_cast<const char*>(base) + t * row_bytes;
-#pragma unroll
-    for (int j = 0; j < kLW; ++j, p += row_bytes) r[j] = load_at<Raw>(p, 0, off);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) r[j] = load_at<Raw>(base, min(t + j, n - 1) * row_bytes, off);
-  }
 }
 template <typename Raw> __device__ __forceinline__ void store_at(void* base, int64_t row_bytes, uint32_t off, Raw v) {
   *reinterpret_cast<Raw*>(static_cast<char*>(base) + row_bytes + off) = v;
 }
+
+// The same value, of which the compiler knows nothing: what was formed from it
+// before is formed again, not kept in registers.
+template <typename Raw> __device__ __forceinline__ Raw afresh(Raw r) {
+  if constexpr (sizeof(Raw) == 2) {
+    uint32_t q = r;
+    asm volatile("" : "+v"(q));
+    r = static_cast<Raw>(q);
+  } else {
+    asm volatile("" : "+v"(r));
+  }
+  return r;
+}
+
+// Keeps the compiler from forming the coefficients of many tokens ahead, which
+// would hold them all in registers; the other waves hide the latency instead.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // a of a gate value.
 template <int GATE> __device__ __forceinline__ float gate_a(float z) {
@@ -140,18 +181,21 @@ template <int GATE> __device__ __forceinline__ float gate_rest(float z, float a)
 // sequence.  first: where the sequence of the tile's first token starts; last:
 // where that of its last token ends.  Every value is clamped to the tile or to
 // 0 .. n - 1, whatever `starts` holds.
-struct Meta {
+template <int LW> struct Meta {
+  static constexpr int kTile = kWaves * LW;
   int start[kTile], end[kTile];
   int lo, hi, first, last;
 };
 // The same for one wave's tokens: bits of those that belong to a sequence, start
-// one, end one; and the tile's first and last, or first = the tile's first token
-// and last = its last where the tile has no token of a sequence.
+// one, end one.  inside: the whole tile lies inside one sequence, without its start
+// or its end.  first, last: as in Meta, or the tile's own first and last token
+// where it has none of a sequence.
 struct Bits {
+  bool inside;
   uint32_t ok, start, end;
   int first, last;
 };
-constexpr uint32_t kAll = static_cast<uint32_t>((uint64_t{1} << kLW) - 1);
+template <int LW> constexpr uint32_t kAll = static_cast<uint32_t>((uint64_t{1} << LW) - 1);
 
 // The largest j in 0 .. count - 1 with p[j] <= t, or -1 (p sorted); 64 probes a
 // step, the result uniform over the wave.
@@ -170,14 +214,16 @@ __device__ __forceinline__ int last_not_above(const int32_t* p, int count, int t
   }
 }
 
-__device__ __forceinline__ Bits tile_meta(const RecArgs& a, int t0, Meta& m) {
+template <int LW> __device__ __forceinline__ Bits tile_meta(const RecArgs& a, int t0, Meta<LW>& m) {
+  constexpr int kTile = Meta<LW>::kTile;
   const int tid = threadIdx.x;
   const int tl = t0 + kTile - 1;
+  bool one = false;  // the first and the last token are of the same sequence
   if (!a.starts) {
     if (tl < a.n) {
       const int from = t0 - t0 % a.T;
       // inside one sequence, and neither its start nor its end
-      if (from < t0 && from + a.T - 1 > tl) return Bits{kAll, 0, 0, from, from + a.T - 1};
+      if (from < t0 && from + a.T - 1 > tl) return Bits{true, kAll<LW>, 0, 0, from, from + a.T - 1};
     }
     if (tid < kTile) {
       const int t = t0 + tid;
@@ -208,6 +254,7 @@ __device__ __forceinline__ Bits tile_meta(const RecArgs& a, int t0, Meta& m) {
       if (q > t0 && q - 1 <= tl) m.end[q - 1 - t0] = j;
     }
     const int sl = last_not_above(a.starts, a.B + 1, tl);
+    one = uniform(sl) == uniform(s0);
     if (tid == 0) {
       m.lo = max(t0, a.starts[0]);
       m.hi = min(min(t0 + kTile, a.n), a.starts[a.B]);
@@ -216,15 +263,17 @@ __device__ __forceinline__ Bits tile_meta(const RecArgs& a, int t0, Meta& m) {
     }
   }
   __syncthreads();
-  const int lane = tid & 63, at = (tid >> 6) * kLW + lane % kLW, t = t0 + at;
-  const bool ok = lane < kLW && t >= m.lo && t < m.hi;
-  const bool some = m.lo < m.hi;
-  return Bits{static_cast<uint32_t>(__ballot(ok)), static_cast<uint32_t>(__ballot(ok && m.start[at] >= 0)),
-              static_cast<uint32_t>(__ballot(ok && m.end[at] >= 0)), some ? m.first : t0, some ? m.last : tl};
+  const int lo = uniform(m.lo), hi = uniform(m.hi), first = uniform(m.first), last = uniform(m.last);
+  if (one && lo <= t0 && hi > tl && first < t0 && last > tl) return Bits{true, kAll<LW>, 0, 0, first, last};
+  const int lane = tid & 63, at = (tid >> 6) * LW + lane % LW, t = t0 + at;
+  const bool ok = lane < LW && t >= lo && t < hi;
+  return Bits{false, static_cast<uint32_t>(__ballot(ok)), static_cast<uint32_t>(__ballot(ok && m.start[at] >= 0)),
+              static_cast<uint32_t>(__ballot(ok && m.end[at] >= 0)), lo < hi ? first : t0, lo < hi ? last : tl};
 }
 
 // Sequences without a token: the state passes through (dst = src, or zero).
 // Tile i of the grid takes its share of the sequences, a wave one at a time.
+template <int V>
 __device__ __forceinline__ void pass_empty(const RecArgs& a, int i, int c, bool in, const float* src, float* dst) {
   if (!dst) return;
   if (!a.starts && a.T > 0) return;
@@ -233,7 +282,10 @@ __device__ __forceinline__ void pass_empty(const RecArgs& a, int i, int c, bool 
   for (int s = static_cast<int>(static_cast<int64_t>(a.B) * i / a.nt) + wave; s < s1; s += kWaves) {
     if (a.starts && a.starts[s + 1] > a.starts[s]) continue;
     const int64_t at = static_cast<int64_t>(s) * a.D + c;
-    if (in) dst[at] = src ? src[at] : 0.0f;
+    if (in) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) dst[at + v] = src ? src[at + v] : 0.0f;
+    }
   }
 }
 
@@ -401,11 +453,11 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ maps
 }
 
 // LINKED: there is more than one tile.
-template <typename E, int V, int GATE, int IN, bool LINKED>
+template <typename E, int V, int GATE, int IN, int LW, bool LINKED>
 __global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(RecArgs a) {
   using IO = Io<E, V>;
   using Raw = typename IO::Raw;
-  __shared__ Meta m;
+  __shared__ Meta<LW> m;
   __shared__ __attribute__((aligned(16))) float part[kWaves][64][2 * V];
   __shared__ __attribute__((aligned(16))) float look[kWaves][64][2 * V];
   const int lane = threadIdx.x & 63;
@@ -414,139 +466,123 @@ __global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(RecArgs a) {
   const int i = LINKED ? take_tile(a, cb, 1) : 0;
   const int c = (cb * 64 + lane) * V;
   const bool in = c < a.D;
-  const uint32_t cl = in ? c : 0;  // lanes past the last channel read the first and store nothing
-  const uint32_t off = cl * sizeof(E);
-  const int t0 = i * kTile, tw = t0 + wave * kLW;
-  const int64_t rx = a.ldx * static_cast<int64_t>(sizeof(E)), rg = a.ldg * static_cast<int64_t>(sizeof(E));
-  const int64_t ro = static_cast<int64_t>(a.D) * sizeof(E);
+  const uint32_t cl = in ? c : 0;
+  const uint32_t off = in ? c * sizeof(E) : kNowhere;
+  const int t0 = i * kWaves * LW, tw = t0 + wave * LW;
 
-  Raw xr[kLW], gr[kLW];
-  if (a.n > 0) {
-    load_rows<Raw>(a.x, rx, tw, a.n, off, xr);
-    load_rows<Raw>(a.g, rg, tw, a.n, off, gr);
-  } else {
+  Raw xr[LW], gr[LW];
+  const Rows<Raw, LW> xs(a.x, a.ldx, a.D, sizeof(E), tw, a.n), gs(a.g, a.ldg, a.D, sizeof(E), tw, a.n);
 #pragma unroll
-    for (int j = 0; j < kLW; ++j) xr[j] = gr[j] = Raw(0);
-  }
-  const Bits bits = tile_meta(a, t0, m);
-  const uint32_t okm = bits.ok, sm = bits.start, em = bits.end;
-  if (okm != kAll) {
-    // a token of no sequence: a = 1 and u = 0 leave what passes over it as it is
-#pragma unroll
-    for (int j = 0; j < kLW; ++j)
-      if (!(okm >> j & 1)) xr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
-  }
+  for (int j = 0; j < LW; ++j) gr[j] = gs.load(j, off), xr[j] = xs.load(j, off);
+  const Bits bits = tile_meta<LW>(a, t0, m);
+  const uint32_t okm = uniform(bits.ok), sm = uniform(bits.start), em = uniform(bits.end);
 
-  float av[kLW][V], uv[kLW][V];
-  float A[V], h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kLW; ++j) {
-    float x[V], z[V];
-    IO::get(xr[j], x);
-    IO::get(gr[j], z);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      av[j][v] = gate_a<GATE>(z[v]);
-      uv[j][v] = IN == TTT_REC_PLAIN ? x[v] : gate_rest<GATE>(z[v], av[j][v]) * x[v];
-    }
-  }
-  auto initial = [&](int j, float (&f)[V]) {  // h0 of the sequence that starts at the wave's token j
-    const int s = __builtin_amdgcn_readfirstlane(m.start[wave * kLW + j]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-  };
-  if (sm == 0) {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j)
+  // EDGE: the tile holds a start, an end or a token of no sequence.
+  auto body = [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
+    auto coefficients = [&](int j, float (&f)[V], float (&u)[V]) {
+      Raw g = afresh(gr[j]), xx = afresh(xr[j]);
+      // a token of no sequence: a = 1 and u = 0 leave what passes over it as it is
+      if (EDGE && !(okm >> j & 1)) xx = Raw(0), g = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+      float x[V], z[V];
+      IO::get(xx, x);
+      IO::get(g, z);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[v] = av[j][v] * h[v] + uv[j][v];
-        A[v] *= av[j][v];
+        f[v] = gate_a<GATE>(z[v]);
+        u[v] = IN == TTT_REC_PLAIN ? x[v] : gate_rest<GATE>(z[v], f[v]) * x[v];
       }
-  } else {
+    };
+    float A[V], h[V];
+    auto initial = [&](int j) {  // h0 of the sequence that starts at the wave's token j
+      const int s = uniform(m.start[wave * LW + j]);
 #pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      if (sm >> j & 1) initial(j, h);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = av[j][v] * h[v] + uv[j][v];
-        A[v] *= av[j][v];
-      }
-    }
-    // a start: what enters no longer counts.  The sign of A carries it to the readers of `part`.
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = -1.0f;
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
-  __syncthreads();
+      for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+    };
 
-  // fold the maps of waves 0 .. upto - 1 onto h; A: the product, dropped at a start
-  auto fold_waves = [&](int upto, float (&hh)[V], float (&AA)[V]) {
-    for (int w = 0; w < upto; ++w) {
+    // the map of the wave's tokens
+    float fs[LW][V], us[LW][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < LW; ++j) {
+      in_order();
+      if (EDGE && (sm >> j & 1)) initial(j);
+      coefficients(j, fs[j], us[j]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
-        const bool reset = pa < 0.0f;
-        hh[v] = reset ? pb : pa * hh[v] + pb;
-        AA[v] = reset ? 0.0f : pa * AA[v];
+        h[v] = fs[j][v] * h[v] + us[j][v];
+        A[v] *= fs[j][v];
       }
     }
-  };
-  if constexpr (LINKED) {
-    if (wave == 0) {
+    if (EDGE && sm) {
+      // a start: what enters no longer counts.  The sign of A carries it to the readers of `part`.
 #pragma unroll
-      for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
-      fold_waves(kWaves, h, A);
+      for (int v = 0; v < V; ++v) A[v] = -1.0f;
     }
-    publish_tile<V>(a, i, 1, c, look, A, h);
-    fold_way<V>(a, Way(i, bits.first / kTile, 1), c, look, h);
-  } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.0f;
-  }
-  if (a.ckpt && wave == 0) {
+    for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
+    __syncthreads();
+
+    // fold the maps of waves 0 .. upto - 1 onto h; A: the product, dropped at a start
+    auto fold_waves = [&](int upto) {
+      for (int w = 0; w < upto; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v] = h[v];
-  }
-  fold_waves(wave, h, A);
-  if (okm == kAll && (sm | em) == 0) {
-    char* p = static_cast<char*>(a.o) + tw * ro;
+        for (int v = 0; v < V; ++v) {
+          const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+          const bool reset = EDGE && pa < 0.0f;
+          h[v] = reset ? pb : pa * h[v] + pb;
+          A[v] = reset ? 0.0f : pa * A[v];
+        }
+      }
+    };
+    if constexpr (LINKED) {
+      if (wave == 0) {
 #pragma unroll
-    for (int j = 0; j < kLW; ++j, p += ro) {
+        for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+        fold_waves(kWaves);
+      }
+      publish_tile<V>(a, i, 1, c, look, A, h);
+      fold_way<V>(a, Way(i, uniform(bits.first) / (kWaves * LW), 1), c, look, h);
+    } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
-      if (in) store_at<Raw>(p, 0, off, IO::put(h));
+      for (int v = 0; v < V; ++v) h[v] = 0.0f;
     }
-  } else {
+    fold_waves(wave);
+    if (a.ckpt && (wave * LW) % kRun == 0 && tw < a.n) {
 #pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      if (sm >> j & 1) initial(j, h);
+      for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(tw / kRun) * a.Dp + c + v] = h[v];
+    }
+    const Rows<Raw, LW> os(a.o, a.D, a.D, sizeof(E), tw, a.n);
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = av[j][v] * h[v] + uv[j][v];
-      if (in && (okm >> j & 1)) store_at<Raw>(a.o, (tw + j) * ro, off, IO::put(h));
-      if (in && a.h_final && (em >> j & 1)) {
-        const int s = __builtin_amdgcn_readfirstlane(m.end[wave * kLW + j]);
+    for (int j = 0; j < LW; ++j) {
+      in_order();
+      if (EDGE && (sm >> j & 1)) initial(j);
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = fs[j][v] * h[v] + us[j][v];
+      os.store(j, off, !EDGE || (okm >> j & 1), IO::put(h));
+      if (EDGE && in && a.h_final && (em >> j & 1)) {
+        const int s = uniform(m.end[wave * LW + j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a.h_final[static_cast<int64_t>(s) * a.D + c + v] = h[v];
       }
     }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.h0, a.h_final);
+  };
+  if (uniform(bits.inside)) body(std::false_type{});
+  else body(std::true_type{});
+  pass_empty<V>(a, i, c, in, a.h0, a.h_final);
 }
 
 // The backward: the same tiles, e running from the end.  The tile's states are
 // formed again from the state that entered it (ckpt) and the waves' forward maps.
-template <typename E, int V, int GATE, int IN, bool LINKED>
-__global__ __launch_bounds__(kThreads, 2) void rec_bwd_kernel(RecArgs a) {
+template <typename E, int V, int GATE, int IN, int LW, bool LINKED>
+__global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(RecArgs a) {
+  static_assert(kWaves * LW == kRun, "a tile starts where the forward saved a state");
   using IO = Io<E, V>;
   using Raw = typename IO::Raw;
-  __shared__ Meta m;
-  __shared__ __attribute__((aligned(16))) float part[kWaves][64][2 * V];   // forward maps
-  __shared__ __attribute__((aligned(16))) float rpart[kWaves][64][2 * V];  // maps of e, from the end
+  __shared__ Meta<LW> m;
+  __shared__ __attribute__((aligned(16))) float part[kWaves][64][2 * V];   // the waves' maps of h
+  __shared__ __attribute__((aligned(16))) float rpart[kWaves][64][2 * V];  // and of e, from the end
   __shared__ __attribute__((aligned(16))) float look[kWaves][64][2 * V];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -555,211 +591,169 @@ __global__ __launch_bounds__(kThreads, 2) void rec_bwd_kernel(RecArgs a) {
   const int c = (cb * 64 + lane) * V;
   const bool in = c < a.D;
   const uint32_t cl = in ? c : 0;
-  const uint32_t off = cl * sizeof(E);
-  const int t0 = i * kTile, tw = t0 + wave * kLW;
-  const int64_t rx = a.ldx * static_cast<int64_t>(sizeof(E)), rg = a.ldg * static_cast<int64_t>(sizeof(E));
-  const int64_t ro = static_cast<int64_t>(a.D) * sizeof(E);
+  const uint32_t off = in ? c * sizeof(E) : kNowhere;
+  const int t0 = i * kWaves * LW, tw = t0 + wave * LW;
 
-  Raw xr[kLW], gr[kLW], dr[kLW];
-  if (a.n > 0) {
-    load_rows<Raw>(a.g, rg, tw, a.n, off, gr);
-    load_rows<Raw>(a.d_o, ro, tw, a.n, off, dr);
-    load_rows<Raw>(a.x, rx, tw, a.n, off, xr);
-  } else {
+  Raw xr[LW], gr[LW], dr[LW];
+  const Rows<Raw, LW> xs(a.x, a.ldx, a.D, sizeof(E), tw, a.n), gs(a.g, a.ldg, a.D, sizeof(E), tw, a.n);
+  const Rows<Raw, LW> ds(a.d_o, a.D, a.D, sizeof(E), tw, a.n);
 #pragma unroll
-    for (int j = 0; j < kLW; ++j) xr[j] = gr[j] = dr[j] = Raw(0);
-  }
-  const Bits bits = tile_meta(a, t0, m);
-  const uint32_t okm = bits.ok, sm = bits.start, em = bits.end;
-  if (okm != kAll) {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j)
-      if (!(okm >> j & 1)) xr[j] = dr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
-  }
+  for (int j = 0; j < LW; ++j) gr[j] = gs.load(j, off), xr[j] = xs.load(j, off), dr[j] = ds.load(j, off);
+  const Bits bits = tile_meta<LW>(a, t0, m);
+  const uint32_t okm = uniform(bits.ok), sm = uniform(bits.start), em = uniform(bits.end);
 
-  float av[kLW][V];
+  auto body = [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
+    float h[V], e[V], P[V];
+    auto coefficients = [&](int j, float (&f)[V], float (&rest)[V]) {
+      Raw g = afresh(gr[j]);
+      if (EDGE && !(okm >> j & 1)) g = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+      float z[V];
+      IO::get(g, z);
 #pragma unroll
-  for (int j = 0; j < kLW; ++j) {
-    float z[V];
-    IO::get(gr[j], z);
+      for (int v = 0; v < V; ++v) {
+        f[v] = gate_a<GATE>(z[v]);
+        rest[v] = gate_rest<GATE>(z[v], f[v]);
+      }
+    };
+    auto value = [&](const Raw (&r)[LW], int j, float (&f)[V]) {
+      Raw q = afresh(r[j]);
+      if (EDGE && !(okm >> j & 1)) q = Raw(0);
+      IO::get(q, f);
+    };
+    auto initial = [&](int j) {
+      const int s = uniform(m.start[wave * LW + j]);
 #pragma unroll
-    for (int v = 0; v < V; ++v) av[j][v] = gate_a<GATE>(z[v]);
-  }
-  // u_t, and 1 - a_t where the input is scaled by it
-  auto input = [&](int j, float (&u)[V], float (&rest)[V], float (&x)[V]) {
-    float z[V];
-    IO::get(xr[j], x);
-    IO::get(gr[j], z);
+      for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+    };
+    auto final_grad = [&](int j, float (&f)[V]) {
+      const int s = uniform(m.end[wave * LW + j]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = a.d_hfinal ? a.d_hfinal[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+    };
+
+    // Both maps of the wave's tokens in one walk: with P_j = a_0 ... a_j, h <- a h + u
+    // as in the forward, and e in front of the tokens is sum_j P_j do_j + P_last e
+    // behind them.  An end cuts that sum: behind its token only d_hfinal adds.
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.0f, h[v] = e[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < LW; ++j) {
+      in_order();
+      if (EDGE && (sm >> j & 1)) initial(j);
+      float f[V], rest[V], x[V], d[V];
+      coefficients(j, f, rest);
+      value(xr, j, x);
+      value(dr, j, d);
+      if (EDGE && (em >> j & 1)) {
+        float q[V];
+        final_grad(j, q);
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] += q[v];
+      }
+      const bool open = !EDGE || (em & ((1u << j) - 1)) == 0;  // no end before this token
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = f[v] * h[v] + (IN == TTT_REC_PLAIN ? x[v] : rest[v] * x[v]);
+        P[v] *= f[v];
+        if (open) e[v] += P[v] * d[v];
+      }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      rest[v] = IN == TTT_REC_CONVEX || GATE == TTT_GATE_SIGMOID ? gate_rest<GATE>(z[v], av[j][v]) : 0.0f;
-      u[v] = IN == TTT_REC_PLAIN ? x[v] : rest[v] * x[v];
+      part[wave][lane][2 * v] = EDGE && sm ? -1.0f : P[v];
+      part[wave][lane][2 * v + 1] = h[v];
+      rpart[wave][lane][2 * v] = EDGE && em ? -1.0f : P[v];
+      rpart[wave][lane][2 * v + 1] = e[v];
     }
-  };
-  auto initial = [&](int j, float (&f)[V]) {
-    const int s = __builtin_amdgcn_readfirstlane(m.start[wave * kLW + j]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-  };
-  auto final_grad = [&](int j, float (&f)[V]) {
-    const int s = __builtin_amdgcn_readfirstlane(m.end[wave * kLW + j]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = a.d_hfinal ? a.d_hfinal[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-  };
+    __syncthreads();
 
-  // e's map over the wave's tokens, from the end
-  float A[V], e[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, e[v] = 0.0f;
-  auto back = [&](int j) {
-    float d[V];
-    IO::get(dr[j], d);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      e[v] = av[j][v] * (d[v] + e[v]);
-      A[v] *= av[j][v];
-    }
-  };
-  if (em == 0) {
-#pragma unroll
-    for (int j = kLW - 1; j >= 0; --j) back(j);
-  } else {
-#pragma unroll
-    for (int j = kLW - 1; j >= 0; --j) {
-      if (em >> j & 1) final_grad(j, e);
-      back(j);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = -1.0f;
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) rpart[wave][lane][2 * v] = A[v], rpart[wave][lane][2 * v + 1] = e[v];
-
-  // the state's map over them
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
-  auto state = [&](int j) {
-    float u[V], rest[V], x[V];
-    input(j, u, rest, x);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = av[j][v] * h[v] + u[v];
-      A[v] *= av[j][v];
-    }
-  };
-  if (sm == 0) {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) state(j);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      if (sm >> j & 1) initial(j, h);
-      state(j);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = -1.0f;
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
-  __syncthreads();
-
-  if constexpr (LINKED) {
-    if (wave == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) A[v] = 1.0f, e[v] = 0.0f;
-#pragma unroll
-      for (int w = kWaves - 1; w >= 0; --w)
+    // fold the maps of e of waves kWaves - 1 .. from onto e; P: the product
+    auto fold_back = [&](int from) {
+      for (int w = kWaves - 1; w >= from; --w) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
-          e[v] = pa < 0.0f ? pb : pa * e[v] + pb;
-          A[v] = pa < 0.0f ? 0.0f : pa * A[v];
+          const bool reset = EDGE && pa < 0.0f;
+          e[v] = reset ? pb : pa * e[v] + pb;
+          P[v] = reset ? 0.0f : pa * P[v];
         }
+      }
+    };
+    if constexpr (LINKED) {
+      if (wave == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) P[v] = 1.0f, e[v] = 0.0f;
+        fold_back(0);
+      }
+      publish_tile<V>(a, i, -1, c, look, P, e);
     }
-    publish_tile<V>(a, i, -1, c, look, A, e);
-  }
-  // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
-  float wv[kLW][V];
+    // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
+    float wv[LW][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
-  for (int w = 0; w < wave; ++w) {
+    for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
+    for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
-      h[v] = pa < 0.0f ? pb : pa * h[v] + pb;
+      for (int v = 0; v < V; ++v) {
+        const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+        h[v] = EDGE && pa < 0.0f ? pb : pa * h[v] + pb;
+      }
     }
-  }
-  auto slope = [&](int j) {
-    float u[V], rest[V], x[V];
-    input(j, u, rest, x);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float da = GATE == TTT_GATE_SIGMOID ? av[j][v] * rest[v] : av[j][v];
-      wv[j][v] = da * (IN == TTT_REC_PLAIN ? h[v] : h[v] - x[v]);
-      h[v] = av[j][v] * h[v] + u[v];
+    for (int j = 0; j < LW; ++j) {
+      in_order();
+      if (EDGE && (sm >> j & 1)) initial(j);
+      float f[V], rest[V], x[V];
+      coefficients(j, f, rest);
+      value(xr, j, x);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float da = GATE == TTT_GATE_SIGMOID ? f[v] * rest[v] : f[v];
+        wv[j][v] = da * (IN == TTT_REC_PLAIN ? h[v] : h[v] - x[v]);
+        h[v] = f[v] * h[v] + (IN == TTT_REC_PLAIN ? x[v] : rest[v] * x[v]);
+        wv[j][v] = afresh(wv[j][v]);  // formed here, not where it is used
+      }
     }
-  };
-  if (sm == 0) {
+    if constexpr (LINKED) {
+      fold_way<V>(a, Way(i, uniform(bits.last) / (kWaves * LW), -1), c, look, e);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kLW; ++j) slope(j);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kLW; ++j) {
-      if (sm >> j & 1) initial(j, h);
-      slope(j);
+      for (int v = 0; v < V; ++v) e[v] = 0.0f;
     }
-  }
-  if constexpr (LINKED) {
-    fold_way<V>(a, Way(i, bits.last / kTile, -1), c, look, e);
-  } else {
+    fold_back(wave + 1);
+    const Rows<Raw, LW> dxs(a.dx, a.ldx, a.D, sizeof(E), tw, a.n), dgs(a.dg, a.ldg, a.D, sizeof(E), tw, a.n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = 0.0f;
-  }
-  for (int w = kWaves - 1; w > wave; --w) {
+    for (int j = LW - 1; j >= 0; --j) {
+      in_order();
+      if (EDGE && (em >> j & 1)) final_grad(j, e);
+      float f[V], rest[V], d[V], ox[V], og[V];
+      coefficients(j, f, rest);
+      value(dr, j, d);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
-      e[v] = pa < 0.0f ? pb : pa * e[v] + pb;
-    }
-  }
-  char* px = static_cast<char*>(a.dx) + (tw + kLW - 1) * rx;
-  char* pg = static_cast<char*>(a.dg) + (tw + kLW - 1) * rg;
-  auto gradients = [&](int j, bool store) {
-    float d[V], ox[V], og[V], u[V], rest[V], x[V];
-    IO::get(dr[j], d);
-    if constexpr (IN == TTT_REC_CONVEX) input(j, u, rest, x);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float dh = d[v] + e[v];
-      ox[v] = IN == TTT_REC_PLAIN ? dh : dh * rest[v];
-      og[v] = dh * wv[j][v];
-      e[v] = av[j][v] * dh;
-    }
-    if (store) {
-      store_at<Raw>(px, 0, off, IO::put(ox));
-      store_at<Raw>(pg, 0, off, IO::put(og));
-    }
-    px -= rx;
-    pg -= rg;
-  };
-  if (okm == kAll && (sm | em) == 0) {
-#pragma unroll
-    for (int j = kLW - 1; j >= 0; --j) gradients(j, in);
-  } else {
-#pragma unroll
-    for (int j = kLW - 1; j >= 0; --j) {
-      if (em >> j & 1) final_grad(j, e);
-      gradients(j, in && (okm >> j & 1));
-      if (in && a.dh0 && (sm >> j & 1)) {
-        const int s = __builtin_amdgcn_readfirstlane(m.start[wave * kLW + j]);
+      for (int v = 0; v < V; ++v) {
+        const float dh = d[v] + e[v];
+        ox[v] = IN == TTT_REC_PLAIN ? dh : dh * rest[v];
+        og[v] = dh * wv[j][v];
+        e[v] = f[v] * dh;
+      }
+      dxs.store(j, off, !EDGE || (okm >> j & 1), IO::put(ox));
+      dgs.store(j, off, !EDGE || (okm >> j & 1), IO::put(og));
+      if (EDGE && in && a.dh0 && (sm >> j & 1)) {
+        const int s = uniform(m.start[wave * LW + j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a.dh0[static_cast<int64_t>(s) * a.D + c + v] = e[v];
       }
     }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) pass_empty(a, i, c + v, in, a.d_hfinal, a.dh0);
+  };
+  if (uniform(bits.inside)) body(std::false_type{});
+  else body(std::true_type{});
+  pass_empty<V>(a, i, c, in, a.d_hfinal, a.dh0);
+}
+
+// A problem without tokens: every sequence's state passes through.
+__global__ __launch_bounds__(kThreads) void rec_empty_kernel(RecArgs a, const float* src, float* dst) {
+  const int c = static_cast<int>(blockIdx.x) * 64 + (threadIdx.x & 63);
+  pass_empty<1>(a, 0, c, c < a.D, src, dst);
 }
 
 // One token for each row: h[slot] <- a h[slot] + u, o = h[slot].  Rows that name
@@ -857,20 +851,22 @@ template <typename F> hipError_t dispatch(const ttt_rec_desc& d, int V, F&& f) {
 }
 
 int64_t tokens(const ttt_rec_desc& d) { return d.packed ? d.T : static_cast<int64_t>(d.B) * d.T; }
-int64_t tiles(const ttt_rec_desc& d) {
-  const int64_t nt = (tokens(d) + kTile - 1) / kTile;
+// Tiles of `tile` tokens; a problem without tokens has one, for its states.
+int64_t tiles(const ttt_rec_desc& d, int tile) {
+  const int64_t nt = (tokens(d) + tile - 1) / tile;
   return nt > 0 ? nt : 1;
 }
+constexpr int kFwdTile = kWaves * kFwdLW, kBwdTile = kWaves * kBwdLW;
 // Room for either channel block width, 64 and 128.
 int64_t padded_channels(const ttt_rec_desc& d) { return (static_cast<int64_t>(d.D) + 127) / 128 * 128; }
 
-RecArgs make_args(const ttt_rec_desc& d, int V) {
+RecArgs make_args(const ttt_rec_desc& d, int V, int tile) {
   RecArgs a{};
   a.B = d.B;
   a.T = d.T;
   a.n = static_cast<int>(tokens(d));
   a.D = d.D;
-  a.nt = static_cast<int>(tiles(d));
+  a.nt = static_cast<int>(tiles(d, tile));
   a.ncb = (d.D + 64 * V - 1) / (64 * V);
   a.Dp = static_cast<int>(padded_channels(d));
   a.ldx = d.ldx ? d.ldx : d.D;
@@ -880,26 +876,39 @@ RecArgs make_args(const ttt_rec_desc& d, int V) {
 
 }  // namespace
 
-bool recurrence_grid_fits(const ttt_rec_desc& d) { return tiles(d) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31); }
+bool recurrence_grid_fits(const ttt_rec_desc& d) {
+  const int64_t least = kFwdTile < kBwdTile ? kFwdTile : kBwdTile;
+  return tiles(d, least) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31);
+}
+
+namespace {
 
 // The maps of the tiles and of the whole groups, then the counters.
-size_t map_words(const ttt_rec_desc& d) {
-  return static_cast<size_t>(tiles(d) + tiles(d) / kGroup) * padded_channels(d);
+size_t map_words(const ttt_rec_desc& d, int tile) {
+  return static_cast<size_t>(tiles(d, tile) + tiles(d, tile) / kGroup) * padded_channels(d);
 }
 size_t counter_ints(const ttt_rec_desc& d) { return static_cast<size_t>((d.D + 63) / 64) * kCounterStride; }
 
-size_t recurrence_workspace(const ttt_rec_desc& d) {
-  if (tiles(d) == 1) return 0;
-  return align256(map_words(d) * sizeof(uint64_t)) + align256(counter_ints(d) * sizeof(int));
+}  // namespace
+
+size_t recurrence_workspace(const ttt_rec_desc& d, int entry) {
+  const int tile = entry == TTT_ENTRY_FWD ? kFwdTile : kBwdTile;
+  if (tiles(d, tile) == 1) return 0;
+  return align256(map_words(d, tile) * sizeof(uint64_t)) + align256(counter_ints(d) * sizeof(int));
 }
+
+size_t recurrence_saved(const ttt_rec_desc& d) {
+  return align256(static_cast<size_t>(tiles(d, kRun)) * padded_channels(d) * sizeof(float));
+}
+
 namespace {
 
 // Lays out the workspace and clears it (a kernel, so that a graph can hold it).
-hipError_t link_tiles(const ttt_rec_desc& d, RecArgs& a, void* ws, hipStream_t s) {
+hipError_t link_tiles(const ttt_rec_desc& d, int tile, RecArgs& a, void* ws, hipStream_t s) {
   a.maps = static_cast<uint64_t*>(ws);
   a.groups = a.maps + static_cast<size_t>(a.nt) * a.Dp;
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + align256(map_words(d) * sizeof(uint64_t)));
-  const int64_t n = static_cast<int64_t>(map_words(d) / 2);  // Dp is even
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + align256(map_words(d, tile) * sizeof(uint64_t)));
+  const int64_t n = static_cast<int64_t>(map_words(d, tile) / 2);  // Dp is even
   const int nc = static_cast<int>(counter_ints(d));
   const int64_t work = n > nc ? n : nc;
   KernelScope scope(TTT_KERNEL_REC_CLEAR, s);
@@ -909,26 +918,26 @@ hipError_t link_tiles(const ttt_rec_desc& d, RecArgs& a, void* ws, hipStream_t s
 
 }  // namespace
 
-size_t recurrence_saved(const ttt_rec_desc& d) {
-  return align256(static_cast<size_t>(tiles(d)) * padded_channels(d) * sizeof(float));
-}
-
 hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const void* gate, const float* h0, const int32_t* starts,
                                  void* o, float* h_final, void* saved, void* ws, hipStream_t s) {
   const int V = lane_channels(d.dtype, d.D, d.ldx, d.ldg);
-  RecArgs a = make_args(d, V);
+  RecArgs a = make_args(d, V, kFwdTile);
   a.x = x; a.g = gate; a.h0 = h0; a.starts = d.packed ? starts : nullptr;
   a.o = o; a.h_final = h_final; a.ckpt = static_cast<float*>(saved);
+  if (a.n == 0) {
+    rec_empty_kernel<<<(d.D + 63) / 64, kThreads, 0, s>>>(a, h0, h_final);
+    return hipGetLastError();
+  }
   if (a.nt > 1) {
-    const hipError_t e = link_tiles(d, a, ws, s);
+    const hipError_t e = link_tiles(d, kFwdTile, a, ws, s);
     if (e != hipSuccess) return e;
   }
   return dispatch(d, V, [&](auto e, auto v, auto gk, auto in) {
     using E = decltype(e);
     const dim3 grid(static_cast<uint32_t>(a.nt) * a.ncb);
     KernelScope scope(TTT_KERNEL_REC_FWD, s);
-    if (a.nt > 1) rec_fwd_kernel<E, v(), gk(), in(), true><<<grid, kThreads, 0, s>>>(a);
-    else rec_fwd_kernel<E, v(), gk(), in(), false><<<grid, kThreads, 0, s>>>(a);
+    if (a.nt > 1) rec_fwd_kernel<E, v(), gk(), in(), kFwdLW, true><<<grid, kThreads, 0, s>>>(a);
+    else rec_fwd_kernel<E, v(), gk(), in(), kFwdLW, false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -937,20 +946,24 @@ hipError_t recurrence_bwd_launch(const ttt_rec_desc& d, const void* x, const voi
                                  const void* saved, const void* d_o, const float* d_hfinal, void* dx, void* dgate, float* dh0,
                                  void* ws, hipStream_t s) {
   const int V = lane_channels(d.dtype, d.D, d.ldx, d.ldg);
-  RecArgs a = make_args(d, V);
+  RecArgs a = make_args(d, V, kBwdTile);
   a.x = x; a.g = gate; a.h0 = h0; a.starts = d.packed ? starts : nullptr;
   a.ckpt = const_cast<float*>(static_cast<const float*>(saved));
   a.d_o = d_o; a.d_hfinal = d_hfinal; a.dx = dx; a.dg = dgate; a.dh0 = dh0;
+  if (a.n == 0) {
+    rec_empty_kernel<<<(d.D + 63) / 64, kThreads, 0, s>>>(a, d_hfinal, dh0);
+    return hipGetLastError();
+  }
   if (a.nt > 1) {
-    const hipError_t e = link_tiles(d, a, ws, s);
+    const hipError_t e = link_tiles(d, kBwdTile, a, ws, s);
     if (e != hipSuccess) return e;
   }
   return dispatch(d, V, [&](auto e, auto v, auto gk, auto in) {
     using E = decltype(e);
     const dim3 grid(static_cast<uint32_t>(a.nt) * a.ncb);
     KernelScope scope(TTT_KERNEL_REC_BWD, s);
-    if (a.nt > 1) rec_bwd_kernel<E, v(), gk(), in(), true><<<grid, kThreads, 0, s>>>(a);
-    else rec_bwd_kernel<E, v(), gk(), in(), false><<<grid, kThreads, 0, s>>>(a);
+    if (a.nt > 1) rec_bwd_kernel<E, v(), gk(), in(), kBwdLW, true><<<grid, kThreads, 0, s>>>(a);
+    else rec_bwd_kernel<E, v(), gk(), in(), kBwdLW, false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }

@@ -8,6 +8,7 @@ raises at load time: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from enum import IntEnum
 
@@ -431,65 +432,86 @@ def inplace_ttt_bwd_guarded(B, T, d_model, d_ff, C, eta, clip_tau, doc_starts, z
                                          _p(dw_init), _p(ws), int(ws_bytes), _stream(stream)))
 
 
-_TORCH_DTYPE = {DType.F32: "torch.float32", DType.BF16: "torch.bfloat16"}
+_torch_types = None
+_raw_stream = None
 
 
-class _Call:
-    """Checks the torch tensors of one call against its desc and collects their device.
+def _types():
+    """torch's types by DType, then int32 and uint8; torch is imported with the first tensor call."""
+    global _torch_types, _raw_stream
+    if _torch_types is None:
+        import torch
+        # the current stream's handle without the Stream object around it, where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _torch_types = (torch.float32, torch.bfloat16, torch.int32, torch.uint8)
+    return _torch_types
+
+
+def _io_type(desc):
+    """The torch type of a desc's tensors (None for an invalid dtype, which the library rejects)."""
+    return _types()[desc.dtype] if desc.dtype in (0, 1) else None
+
+
+def _device(x):
+    """The device index of a call's first tensor (-1 on the host), None for a raw pointer."""
+    return x.get_device() if hasattr(x, "get_device") else None
+
+
+def _arg(name, x, dev, dtype, rows, cols, ld=0):
+    """The pointer of one tensor of a call: ``rows`` rows of ``cols`` elements, ``ld`` elements apart (0: dense).
 
     A tensor on the host, on another device than the call's first, of another
     type or with fewer elements than the kernels touch would fault the GPU; it
     raises ValueError here.  Integers are device pointers and are taken as they are."""
+    if x is None or type(x) is int:
+        return x
+    try:
+        if x.dtype is dtype and x.get_device() == dev and dev >= 0 and (not ld or ld == cols) and x.is_contiguous() \
+                and x.numel() >= rows * cols:
+            return x.data_ptr()
+    except AttributeError:
+        raise TypeError(f"cannot pass {type(x)!r} as a device pointer") from None
+    if x.get_device() < 0:
+        raise ValueError(f"{name} must be on the GPU, not on {x.device}")
+    if dev is not None and x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, the tensors before it on cuda:{dev}")
+    if dtype is not None and x.dtype is not dtype:
+        raise ValueError(f"{name} must be {str(dtype)[6:]}, not {str(x.dtype)[6:]}")
+    if ld and ld != cols:
+        st = x.stride()
+        if x.dim() < 2 or st[-1] != 1 or x.shape[-1] != cols or (x.shape[-2] > 1 and st[-2] != ld) or \
+                any(x.shape[i] > 1 and st[i] != ld * math.prod(x.shape[i + 1:-1]) for i in range(x.dim() - 2)):
+            raise ValueError(f"{name} must have rows of {cols} elements, {ld} apart (got shape {tuple(x.shape)}, "
+                             f"strides {st})")
+    elif not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if x.numel() < rows * cols:
+        raise ValueError(f"{name} has {x.numel()} elements, {rows * cols} are needed")
+    return x.data_ptr()
 
-    def __init__(self):
-        self.device = None
 
-    def __call__(self, name, x, dtype, rows, cols, ld=0):
-        """``rows`` rows of ``cols`` elements, ``ld`` elements apart (0: dense); returns the pointer."""
-        if x is None or isinstance(x, int):
-            return x
-        if not hasattr(x, "data_ptr"):
-            raise TypeError(f"cannot pass {type(x)!r} as a device pointer")
-        if x.device != self.device:
-            if self.device is not None:
-                raise ValueError(f"{name} is on {x.device}, the tensors before it on {self.device}")
-            if x.device.type != "cuda":
-                raise ValueError(f"{name} must be on the GPU, not on {x.device}")
-            self.device = x.device
-        if str(x.dtype) != dtype:
-            raise ValueError(f"{name} must be {dtype[6:]}, not {str(x.dtype)[6:]}")
-        if ld and ld != cols:
-            st = x.stride()
-            if x.dim() < 2 or st[-1] != 1 or x.shape[-1] != cols or st[-2] != ld or \
-                    any(st[i] != st[i + 1] * x.shape[i + 1] for i in range(x.dim() - 2)):
-                raise ValueError(f"{name} must have rows of {cols} elements, {ld} apart (got shape {tuple(x.shape)}, "
-                                 f"strides {st})")
-        elif not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if x.numel() < rows * cols:
-            raise ValueError(f"{name} has {x.numel()} elements, {rows * cols} are needed")
-        return x.data_ptr()
+def _ws(ws, ws_bytes, dev):
+    """(pointer, bytes) of a workspace."""
+    if hasattr(ws, "data_ptr"):
+        size = ws.numel() * ws.element_size()
+        return _arg("ws", ws, dev, ws.dtype, 0, 0), size if ws_bytes is None else min(size, int(ws_bytes))
+    return ws, int(ws_bytes or 0)
 
-    def run(self, f, *args, ws=None, ws_bytes=None, stream=None):
-        """Call ``f`` with the device of the tensors current, on ``stream`` (None: that device's current stream)."""
-        if ws_bytes is not None or ws is not None:
-            if hasattr(ws, "data_ptr"):
-                size = ws.numel() * ws.element_size()
-                ws_bytes = size if ws_bytes is None else min(size, int(ws_bytes))
-                ws = self("ws", ws, str(ws.dtype), 0, 0)
-            args = (*args, ws, ws_bytes or 0)
-        elif f.argtypes[-2] is ctypes.c_size_t:
-            args = (*args, None, 0)
-        if self.device is None:
-            _check(f(*args, _stream(stream)))
-            return
-        import torch
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
-                self.device = None
-                _check(f(*args, _stream(stream)))
-            return
-        _check(f(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+
+def _call(f, dev, stream, *args):
+    """Call ``f`` with device ``dev`` current, on ``stream`` (None: that device's current stream)."""
+    if dev is None:
+        _check(f(*args, _stream(stream)))
+        return
+    import torch
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(f(*args, _raw_stream(dev) if stream is None else _stream(stream)))
+        return
+    status = f(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status != 0:
+        raise TTTError(status, ttt_last_error())
 
 
 def ttt_recurrence_workspace_size(desc: TTTRecDesc, entry: int) -> int:
@@ -504,42 +526,42 @@ def ttt_recurrence_saved_size(desc: TTTRecDesc) -> int:
     return n.value
 
 
-def _rec_tokens(desc):
-    return desc.T if desc.packed else desc.B * desc.T
-
-
 def ttt_recurrence_fwd(desc, x, gate, h0, seq_starts, o, h_final, saved, ws, ws_bytes=None, stream=None):
     """``seq_starts``: int32 device tensor of B + 1 positions for a packed desc, else None."""
-    L, c = lib(), _Call()
-    dt, n, D = _TORCH_DTYPE.get(desc.dtype), _rec_tokens(desc), desc.D
-    c.run(L.ttt_recurrence_fwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
-          c("h0", h0, "torch.float32", desc.B, D), c("seq_starts", seq_starts, "torch.int32", 1, desc.B + 1),
-          c("o", o, dt, n, D), c("h_final", h_final, "torch.float32", desc.B, D),
-          c("saved", saved, "torch.uint8", 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
-          ws=ws, ws_bytes=ws_bytes, stream=stream)
+    f32, _, i32, u8 = _types()
+    dt, dev, B, D = _io_type(desc), _device(x), desc.B, desc.D
+    n = desc.T if desc.packed else B * desc.T
+    _call(lib().ttt_recurrence_fwd, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
+          _arg("gate", gate, dev, dt, n, D, desc.ldg), _arg("h0", h0, dev, f32, B, D),
+          _arg("seq_starts", seq_starts, dev, i32, 1, B + 1), _arg("o", o, dev, dt, n, D),
+          _arg("h_final", h_final, dev, f32, B, D),
+          _arg("saved", saved, dev, u8, 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
+          *_ws(ws, ws_bytes, dev))
 
 
 def ttt_recurrence_bwd(desc, x, gate, h0, seq_starts, saved, d_o, d_hfinal, dx, dgate, dh0, ws, ws_bytes=None,
                        stream=None):
-    L, c = lib(), _Call()
-    dt, n, D = _TORCH_DTYPE.get(desc.dtype), _rec_tokens(desc), desc.D
-    c.run(L.ttt_recurrence_bwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
-          c("h0", h0, "torch.float32", desc.B, D), c("seq_starts", seq_starts, "torch.int32", 1, desc.B + 1),
-          c("saved", saved, "torch.uint8", 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
-          c("d_o", d_o, dt, n, D), c("d_hfinal", d_hfinal, "torch.float32", desc.B, D),
-          c("dx", dx, dt, n, D, desc.ldx), c("dgate", dgate, dt, n, D, desc.ldg),
-          c("dh0", dh0, "torch.float32", desc.B, D), ws=ws, ws_bytes=ws_bytes, stream=stream)
+    f32, _, i32, u8 = _types()
+    dt, dev, B, D = _io_type(desc), _device(x), desc.B, desc.D
+    n = desc.T if desc.packed else B * desc.T
+    _call(lib().ttt_recurrence_bwd, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
+          _arg("gate", gate, dev, dt, n, D, desc.ldg), _arg("h0", h0, dev, f32, B, D),
+          _arg("seq_starts", seq_starts, dev, i32, 1, B + 1),
+          _arg("saved", saved, dev, u8, 1, 0 if saved is None else ttt_recurrence_saved_size(desc)),
+          _arg("d_o", d_o, dev, dt, n, D), _arg("d_hfinal", d_hfinal, dev, f32, B, D),
+          _arg("dx", dx, dev, dt, n, D, desc.ldx), _arg("dgate", dgate, dev, dt, n, D, desc.ldg),
+          _arg("dh0", dh0, dev, f32, B, D), *_ws(ws, ws_bytes, dev))
 
 
 def ttt_recurrence_step(desc, x, gate, slots, h, o, n_states=None, stream=None):
     """``h``: [n_states, D] float32, updated in place; ``n_states`` is only needed where h is a raw pointer."""
-    L, c = lib(), _Call()
-    dt, n, D = _TORCH_DTYPE.get(desc.dtype), desc.B, desc.D
+    f32, _, i32, _ = _types()
+    dt, dev, n, D = _io_type(desc), _device(x), desc.B, desc.D
     if n_states is None:
         n_states = h.numel() // D if hasattr(h, "numel") and D > 0 else 0
-    c.run(L.ttt_recurrence_step, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("gate", gate, dt, n, D, desc.ldg),
-          c("slots", slots, "torch.int32", 1, n), n_states, c("h", h, "torch.float32", n_states, D), c("o", o, dt, n, D),
-          stream=stream)
+    _call(lib().ttt_recurrence_step, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
+          _arg("gate", gate, dev, dt, n, D, desc.ldg), _arg("slots", slots, dev, i32, 1, n), n_states,
+          _arg("h", h, dev, f32, n_states, D), _arg("o", o, dev, dt, n, D))
 
 
 def ttt_layernorm_workspace_size(desc: TTTLnDesc) -> int:
@@ -549,20 +571,21 @@ def ttt_layernorm_workspace_size(desc: TTTLnDesc) -> int:
 
 
 def ttt_layernorm_fwd(desc, x, res, w, b, y, r, mean, rstd, stream=None):
-    L, c = lib(), _Call()
-    dt, n, D, G, f32 = _TORCH_DTYPE.get(desc.dtype), desc.rows, desc.D, desc.groups, "torch.float32"
-    c.run(L.ttt_layernorm_fwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("res", res, dt, n, D),
-          c("w", w, f32, G, D), c("b", b, f32, G, D), c("y", y, dt, n, D), c("r", r, dt, n, D),
-          c("mean", mean, f32, n, 1), c("rstd", rstd, f32, n, 1), stream=stream)
+    f32 = _types()[0]
+    dt, dev, n, D, G = _io_type(desc), _device(x), desc.rows, desc.D, desc.groups
+    _call(lib().ttt_layernorm_fwd, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
+          _arg("res", res, dev, dt, n, D), _arg("w", w, dev, f32, G, D), _arg("b", b, dev, f32, G, D),
+          _arg("y", y, dev, dt, n, D), _arg("r", r, dev, dt, n, D), _arg("mean", mean, dev, f32, n, 1),
+          _arg("rstd", rstd, dev, f32, n, 1))
 
 
 def ttt_layernorm_bwd(desc, x, w, mean, rstd, dy, dr, dx, dw, db, ws, ws_bytes=None, stream=None):
-    L, c = lib(), _Call()
-    dt, n, D, G, f32 = _TORCH_DTYPE.get(desc.dtype), desc.rows, desc.D, desc.groups, "torch.float32"
-    c.run(L.ttt_layernorm_bwd, ctypes.byref(desc), c("x", x, dt, n, D, desc.ldx), c("w", w, f32, G, D),
-          c("mean", mean, f32, n, 1), c("rstd", rstd, f32, n, 1), c("dy", dy, dt, n, D), c("dr", dr, dt, n, D),
-          c("dx", dx, dt, n, D, desc.ldx), c("dw", dw, f32, G, D), c("db", db, f32, G, D), ws=ws, ws_bytes=ws_bytes,
-          stream=stream)
+    f32 = _types()[0]
+    dt, dev, n, D, G = _io_type(desc), _device(x), desc.rows, desc.D, desc.groups
+    _call(lib().ttt_layernorm_bwd, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
+          _arg("w", w, dev, f32, G, D), _arg("mean", mean, dev, f32, n, 1), _arg("rstd", rstd, dev, f32, n, 1),
+          _arg("dy", dy, dev, dt, n, D), _arg("dr", dr, dev, dt, n, D), _arg("dx", dx, dev, dt, n, D, desc.ldx),
+          _arg("dw", dw, dev, f32, G, D), _arg("db", db, dev, f32, G, D), *_ws(ws, ws_bytes, dev))
 
 
 def ttt_timing_enable(on: bool) -> None:

@@ -7,16 +7,16 @@
 //
 // Both passes are bound by memory: a row is read once into registers, a thread
 // holding NIT pieces of VEC elements (16 bytes where the rows allow it).  Narrow
-// rows take a part of a wave each, wide rows the whole workgroup, whose size is
-// the row's number of pieces.  A workgroup walks over rows of one group, so the
-// weights stay in registers, and takes UR rows at a time: their loads are in
-// flight together and they share the barriers of a cross-wave sum.  The variance
-// is the mean of (r - mu)^2 in a second sum over the registers, exact also where
-// the mean is far larger than the deviation.
+// rows take a part of a wave each, wide rows as many waves as they have pieces
+// for.  A workgroup holds several rows side by side (slots), walks over rows of one
+// group, so that the weights stay in registers, and takes UR rows a slot at a time:
+// they share the barriers of a cross-wave sum, and the loads of the next UR are in
+// flight meanwhile.  The variance is the mean of (r - mu)^2 in a second sum over the
+// registers, exact also where the mean is far larger than the deviation.
 //
-// dw and db: a thread owns its columns, sums them over the workgroup's rows in
-// fp32 and writes one partial row; ln_reduce_kernel adds the partial rows in a
-// fixed order.
+// dw and db: a thread owns its columns and sums them over its rows in fp32, the
+// slots meet in LDS, and the workgroup writes one partial row; ln_reduce_kernel adds
+// the partial rows in a fixed order.
 
 #include <cstdint>
 #include <type_traits>
@@ -33,6 +33,9 @@ struct LnArgs {
   int rows, D, G, period;
   int per_group;  // rows of a group
   int slices;     // workgroups of a group
+  int wpr;        // waves of a row (wide rows)
+  uint32_t magic; // k / period = (k magic >> 32) >> shift for 0 <= k < 2^31, period > 1
+  int shift;
   int64_t ldx;
   float eps;
   const void* x;  // backward: the rows that were normalised
@@ -85,23 +88,42 @@ template <> struct Piece<float, 1> {
 // The k-th row of group g.
 __device__ __forceinline__ int64_t row_of(const LnArgs& a, int g, int k) {
   if (a.G == 1) return k;
-  const int q = k / a.period;
-  return (static_cast<int64_t>(q) * a.G + g) * a.period + (k - q * a.period);
+  const int q = a.period == 1 ? k : static_cast<int>(__umulhi(static_cast<uint32_t>(k), a.magic) >> a.shift);
+  return (q * a.G + g) * a.period + (k - q * a.period);  // below rows, so below 2^31
 }
 
-// The sum of N values over the TPR lanes of a row (TPR <= 64), or over the
-// workgroup (TPR == 0, through `lds`, which alternates between two halves so that
-// one barrier a call is enough).  Every thread gets the sum; the order is fixed.
+// v plus the value of the lane that CTRL names in the same 16 lanes.
+template <int CTRL> __device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over each aligned group of LANES lanes, in every lane of it.
+template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
+  v = add_dpp<0xB1>(v);                             // lanes 0 1 | 2 3
+  v = add_dpp<0x4E>(v);                             // 0 .. 3
+  v = add_dpp<0x141>(v);                            // 0 .. 7, mirrored
+  if constexpr (LANES >= 16) v = add_dpp<0x140>(v); // 0 .. 15, mirrored
+  if constexpr (LANES >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (LANES >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// The sum of N values over the TPR lanes of a row (TPR <= 64), or over the `waves`
+// waves of a row (TPR == 0, through `lds`, which alternates between two halves so
+// that one barrier a call is enough).  Every thread gets the sum; the order is fixed.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* lds, int& half) {
-  constexpr int kLanes = TPR ? TPR : 64;
+__device__ __forceinline__ void row_sum(float (&v)[N], int waves, float* lds, int& half) {
 #pragma unroll
-  for (int s = 1; s < kLanes; s <<= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], s);
+  for (int k = 0; k < N; ++k) v[k] = lanes_sum<TPR ? TPR : 64>(v[k]);
   if constexpr (TPR == 0) {
-    const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
     if (waves > 1) {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), first = wave / waves * waves;
       float* p = lds + half * N * kMaxWaves;
       half ^= 1;
       if ((threadIdx.x & 63) == 0) {
@@ -109,79 +131,128 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* lds, int& half) {
         for (int k = 0; k < N; ++k) p[k * kMaxWaves + wave] = v[k];
       }
       __syncthreads();
+      // at most 16 waves: 16 lanes read one value each and add them up
+      const int w = threadIdx.x & 15;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        float s = 0.0f;
-        for (int w = 0; w < waves; ++w) s += p[k * kMaxWaves + w];
-        v[k] = s;
-      }
+      for (int k = 0; k < N; ++k) v[k] = lanes_sum<16>(w < waves ? p[k * kMaxWaves + first + w] : 0.0f);
     }
   }
 }
 
-template <typename E, int VEC, int TPR, int NIT, int UR>
-__global__ __launch_bounds__(TPR ? 256 : 1024) void ln_fwd_kernel(LnArgs a) {
+// The same value, of which the compiler knows nothing: what was formed from it
+// before is formed again, not kept in registers.
+template <typename Raw> __device__ __forceinline__ Raw afresh(Raw r) {
+  if constexpr (sizeof(Raw) == 2) {
+    uint32_t q = r;
+    asm volatile("" : "+v"(q));
+    return static_cast<Raw>(q);
+  } else {
+    asm volatile("" : "+v"(r));
+    return r;
+  }
+}
+
+// Where a thread stands: its slot, its place in the row and the row's pieces.
+template <int VEC, int TPR, int NIT> struct Place {
+  int tpr, slots, slot, tr;
+  int col[NIT];   // first column of each piece, 0 where it has none
+  bool has[NIT];
+  __device__ __forceinline__ explicit Place(const LnArgs& a) {
+    tpr = TPR ? TPR : a.wpr * 64;
+    slots = static_cast<int>(blockDim.x) / tpr;
+    slot = threadIdx.x / tpr;
+    tr = threadIdx.x - slot * tpr;
+#pragma unroll
+    for (int i = 0; i < NIT; ++i) {
+      const int c = (i * tpr + tr) * VEC;
+      has[i] = c < a.D;
+      col[i] = has[i] ? c : 0;
+    }
+  }
+};
+
+// UR rows of a slot as they lie in memory, NT tensors of them.
+template <typename E, int VEC, int TPR, int NIT, int UR, int NT> struct Batch {
+  using Raw = typename Piece<E, VEC>::Raw;
+  Raw r[NT][UR][NIT];
+  int64_t row[UR];
+  bool ok[UR];
+  __device__ __forceinline__ void rows(const LnArgs& a, const Place<VEC, TPR, NIT>& at, int g, int64_t k0) {
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+      const int64_t k = k0 + u * at.slots + at.slot;
+      ok[u] = k < a.per_group;
+      row[u] = row_of(a, g, static_cast<int>(ok[u] ? k : 0));
+    }
+  }
+  __device__ __forceinline__ void load(int n, const void* base, int64_t ld, const Place<VEC, TPR, NIT>& at) {
+#pragma unroll
+    for (int u = 0; u < UR; ++u)
+#pragma unroll
+      for (int i = 0; i < NIT; ++i) r[n][u][i] = *reinterpret_cast<const Raw*>(static_cast<const E*>(base) + row[u] * ld + at.col[i]);
+  }
+};
+
+// A workgroup's size at most.
+constexpr int max_threads(int tpr, int ur) { return tpr ? 256 : ur > 1 ? 512 : 1024; }
+
+template <typename E, int VEC, int TPR, int NIT, int UR, bool RES>
+__global__ __launch_bounds__(max_threads(TPR, UR)) void ln_fwd_kernel(LnArgs a) {
   using P = Piece<E, VEC>;
   using Raw = typename P::Raw;
   __shared__ float lds[2 * UR * kMaxWaves];
   int half = 0;
-  const int tpr = TPR ? TPR : blockDim.x;
-  const int slots = TPR ? 256 / tpr : 1;  // rows side by side
-  const int slot = TPR ? threadIdx.x / tpr : 0, tr = TPR ? threadIdx.x % tpr : threadIdx.x;
+  const Place<VEC, TPR, NIT> at(a);
   const int g = blockIdx.x % a.G, slice = blockIdx.x / a.G;
-  const E* X = static_cast<const E*>(a.x);
-  const E* R = static_cast<const E*>(a.res);
   float w[NIT][VEC], b[NIT][VEC];
-  bool has[NIT];
 #pragma unroll
-  for (int i = 0; i < NIT; ++i) {
-    const int c = (i * tpr + tr) * VEC;
-    has[i] = c < a.D;
+  for (int i = 0; i < NIT; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      w[i][e] = has[i] && a.w ? a.w[static_cast<int64_t>(g) * a.D + c + e] : 1.0f;
-      b[i][e] = has[i] && a.b ? a.b[static_cast<int64_t>(g) * a.D + c + e] : 0.0f;
+      w[i][e] = a.w ? a.w[static_cast<int64_t>(g) * a.D + at.col[i] + e] : 1.0f;
+      b[i][e] = a.b ? a.b[static_cast<int64_t>(g) * a.D + at.col[i] + e] : 0.0f;
     }
-  }
   const float inv = 1.0f / static_cast<float>(a.D);
-  for (int64_t k0 = static_cast<int64_t>(slice) * slots * UR; k0 < a.per_group; k0 += static_cast<int64_t>(a.slices) * slots * UR) {
+  const int64_t step = static_cast<int64_t>(a.slices) * at.slots * UR;
+  int64_t k0 = static_cast<int64_t>(slice) * at.slots * UR;
+  Batch<E, VEC, TPR, NIT, UR, RES ? 2 : 1> next;
+  auto fetch = [&](int64_t k) {
+    next.rows(a, at, g, k);
+    next.load(0, a.x, a.ldx, at);
+    if constexpr (RES) next.load(1, a.res, a.D, at);
+  };
+  // the next rows' loads are in flight while these are worked on, where the registers allow it
+  constexpr bool AHEAD = NIT * VEC <= 8;
+  if (AHEAD) fetch(k0);
+  for (; k0 < a.per_group; k0 += step) {
+    if (!AHEAD) fetch(k0);
     float f[UR][NIT][VEC], sum[UR];
     int64_t row[UR];
     bool ok[UR];
-    Raw xr[UR][NIT], rr[UR][NIT];
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
-      const int64_t k = k0 + u * slots + slot;
-      ok[u] = k < a.per_group;
-      row[u] = row_of(a, g, static_cast<int>(ok[u] ? k : 0));
-#pragma unroll
-      for (int i = 0; i < NIT; ++i) {
-        const int c = has[i] ? (i * tpr + tr) * VEC : 0;
-        xr[u][i] = *reinterpret_cast<const Raw*>(X + row[u] * a.ldx + c);
-        if (R) rr[u][i] = *reinterpret_cast<const Raw*>(R + row[u] * a.D + c);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < UR; ++u) {
+      row[u] = next.row[u];
+      ok[u] = next.ok[u];
       sum[u] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
-        P::get(xr[u][i], f[u][i]);
-        if (R) {
+        P::get(next.r[0][u][i], f[u][i]);
+        if constexpr (RES) {
           float q[VEC];
-          P::get(rr[u][i], q);
+          P::get(next.r[1][u][i], q);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[u][i][e] += q[e];
           // the stream is normalised as it is kept, so that the backward sees the same rows
           const Raw kept = P::put(f[u][i]);
           P::get(kept, f[u][i]);
-          if (ok[u] && has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.r) + row[u] * a.D + (i * tpr + tr) * VEC) = kept;
+          if (ok[u] && at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.r) + row[u] * a.D + at.col[i]) = kept;
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[u] += has[i] ? f[u][i][e] : 0.0f;
+        for (int e = 0; e < VEC; ++e) sum[u] += at.has[i] ? f[u][i][e] : 0.0f;
       }
     }
-    row_sum<TPR, UR>(sum, lds, half);
+    if (AHEAD && k0 + step < a.per_group) fetch(k0 + step);
+    row_sum<TPR, UR>(sum, a.wpr, lds, half);
     float mu[UR], var[UR];
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
@@ -192,15 +263,15 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void ln_fwd_kernel(LnArgs a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           f[u][i][e] -= mu[u];
-          var[u] += has[i] ? f[u][i][e] * f[u][i][e] : 0.0f;
+          var[u] += at.has[i] ? f[u][i][e] * f[u][i][e] : 0.0f;
         }
     }
-    row_sum<TPR, UR>(var, lds, half);
+    row_sum<TPR, UR>(var, a.wpr, lds, half);
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
       const float s = 1.0f / sqrtf(var[u] * inv + a.eps);
       if (!ok[u]) continue;
-      if (tr == 0) {
+      if (at.tr == 0) {
         if (a.mean) a.mean[row[u]] = mu[u];
         if (a.rstd) a.rstd[row[u]] = s;
       }
@@ -209,129 +280,121 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void ln_fwd_kernel(LnArgs a) {
         float y[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) y[e] = f[u][i][e] * s * w[i][e] + b[i][e];
-        if (has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.y) + row[u] * a.D + (i * tpr + tr) * VEC) = P::put(y);
+        if (at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.y) + row[u] * a.D + at.col[i]) = P::put(y);
       }
     }
   }
 }
 
-template <typename E, int VEC, int TPR, int NIT, int UR>
-__global__ __launch_bounds__(TPR ? 256 : 1024) void ln_bwd_kernel(LnArgs a) {
+template <typename E, int VEC, int TPR, int NIT, int UR, bool RES>
+__global__ __launch_bounds__(max_threads(TPR, UR)) void ln_bwd_kernel(LnArgs a) {
   using P = Piece<E, VEC>;
   using Raw = typename P::Raw;
+  constexpr int kThreads = max_threads(TPR, UR);
   __shared__ float lds[4 * UR * kMaxWaves];
-  __shared__ float cols[TPR ? 256 * VEC : 1];
+  __shared__ float cols[kThreads * VEC];
   int half = 0;
-  const int tpr = TPR ? TPR : blockDim.x;
-  const int slots = TPR ? 256 / tpr : 1;
-  const int slot = TPR ? threadIdx.x / tpr : 0, tr = TPR ? threadIdx.x % tpr : threadIdx.x;
+  const Place<VEC, TPR, NIT> at(a);
   const int g = blockIdx.x % a.G, slice = blockIdx.x / a.G;
-  const E* X = static_cast<const E*>(a.x);
-  const E* DY = static_cast<const E*>(a.dy);
-  const E* DR = static_cast<const E*>(a.dr);
   float w[NIT][VEC], dw[NIT][VEC], db[NIT][VEC];
-  bool has[NIT];
 #pragma unroll
-  for (int i = 0; i < NIT; ++i) {
-    const int c = (i * tpr + tr) * VEC;
-    has[i] = c < a.D;
+  for (int i = 0; i < NIT; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      w[i][e] = has[i] && a.w ? a.w[static_cast<int64_t>(g) * a.D + c + e] : 1.0f;
+      // a piece that the row does not have counts for nothing: t = w dy = 0
+      w[i][e] = !at.has[i] ? 0.0f : a.w ? a.w[static_cast<int64_t>(g) * a.D + at.col[i] + e] : 1.0f;
       dw[i][e] = db[i][e] = 0.0f;
     }
-  }
   const float inv = 1.0f / static_cast<float>(a.D);
-  for (int64_t k0 = static_cast<int64_t>(slice) * slots * UR; k0 < a.per_group; k0 += static_cast<int64_t>(a.slices) * slots * UR) {
-    float n[UR][NIT][VEC], t[UR][NIT][VEC], sum[2 * UR], s[UR];
-    int64_t row[UR];
-    bool ok[UR];
-    Raw xr[UR][NIT], yr[UR][NIT], rr[UR][NIT];
+  const int64_t step = static_cast<int64_t>(a.slices) * at.slots * UR;
+  int64_t k0 = static_cast<int64_t>(slice) * at.slots * UR;
+  Batch<E, VEC, TPR, NIT, UR, RES ? 3 : 2> next;
+  float mu_next[UR], s_next[UR];
+  auto fetch = [&](int64_t k) {
+    next.rows(a, at, g, k);
+    next.load(0, a.x, a.ldx, at);
+    next.load(1, a.dy, a.D, at);
+    if constexpr (RES) next.load(2, a.dr, a.D, at);
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
-      const int64_t k = k0 + u * slots + slot;
-      ok[u] = k < a.per_group;
-      row[u] = row_of(a, g, static_cast<int>(ok[u] ? k : 0));
-#pragma unroll
-      for (int i = 0; i < NIT; ++i) {
-        const int c = has[i] ? (i * tpr + tr) * VEC : 0;
-        xr[u][i] = *reinterpret_cast<const Raw*>(X + row[u] * a.ldx + c);
-        yr[u][i] = *reinterpret_cast<const Raw*>(DY + row[u] * a.D + c);
-        if (DR) rr[u][i] = *reinterpret_cast<const Raw*>(DR + row[u] * a.D + c);
-      }
+      mu_next[u] = a.mean[next.row[u]];
+      s_next[u] = a.rstd[next.row[u]];
     }
+  };
+  constexpr bool AHEAD = NIT * VEC <= 8;
+  if (AHEAD && k0 < a.per_group) fetch(k0);
+  for (; k0 < a.per_group; k0 += step) {
+    if (!AHEAD) fetch(k0);
+    const Batch<E, VEC, TPR, NIT, UR, RES ? 3 : 2> cur = next;
+    float sum[2 * UR], mu[UR], s[UR];
+#pragma unroll
+    for (int u = 0; u < UR; ++u) mu[u] = mu_next[u], s[u] = s_next[u];
+    if (AHEAD && k0 + step < a.per_group) fetch(k0 + step);
+    // n and t = w dy of a piece; formed from the packed rows in both walks
+    auto values = [&](int u, int i, float (&n)[VEC], float (&dy)[VEC]) {
+      P::get(afresh(cur.r[0][u][i]), n);
+      P::get(afresh(cur.r[1][u][i]), dy);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) n[e] = (n[e] - mu[u]) * s[u];
+    };
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
-      const float mu = a.mean[row[u]];
-      s[u] = a.rstd[row[u]];
       sum[2 * u] = sum[2 * u + 1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
-        P::get(xr[u][i], n[u][i]);
-        P::get(yr[u][i], t[u][i]);
+        float n[VEC], dy[VEC];
+        values(u, i, n, dy);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float dy = t[u][i][e];
-          n[u][i][e] = (n[u][i][e] - mu) * s[u];
-          if (ok[u]) {
-            dw[i][e] += dy * n[u][i][e];
-            db[i][e] += dy;
-          }
-          t[u][i][e] = w[i][e] * dy;
-          sum[2 * u] += has[i] ? t[u][i][e] : 0.0f;
-          sum[2 * u + 1] += has[i] ? t[u][i][e] * n[u][i][e] : 0.0f;
+          dw[i][e] += cur.ok[u] ? dy[e] * n[e] : 0.0f;
+          db[i][e] += cur.ok[u] ? dy[e] : 0.0f;
+          const float t = w[i][e] * dy[e];
+          sum[2 * u] += at.has[i] ? t : 0.0f;
+          sum[2 * u + 1] += at.has[i] ? t * n[e] : 0.0f;
         }
       }
     }
-    row_sum<TPR, 2 * UR>(sum, lds, half);
+    row_sum<TPR, 2 * UR>(sum, a.wpr, lds, half);
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
-      if (!ok[u]) continue;
+      if (!cur.ok[u]) continue;
       const float m1 = sum[2 * u] * inv, m2 = sum[2 * u + 1] * inv;
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
-        float d[VEC], q[VEC];
-        if (DR) P::get(rr[u][i], q);
+        float n[VEC], d[VEC], q[VEC];
+        values(u, i, n, d);
+        if constexpr (RES) P::get(cur.r[2][u][i], q);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          d[e] = s[u] * (t[u][i][e] - m1 - n[u][i][e] * m2);
-          if (DR) d[e] += q[e];
+          d[e] = s[u] * (w[i][e] * d[e] - m1 - n[e] * m2);
+          if constexpr (RES) d[e] += q[e];
         }
-        if (has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.dx) + row[u] * a.ldx + (i * tpr + tr) * VEC) = P::put(d);
+        if (at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.dx) + cur.row[u] * a.ldx + at.col[i]) = P::put(d);
       }
     }
   }
   if (!a.part) return;
+  // the slots' sums meet in LDS, the first slot's threads add them up
   float* out = a.part + (static_cast<int64_t>(slice) * a.G + g) * 2 * a.D;
-  if constexpr (TPR) {
-    // the rows side by side: their sums meet in LDS, the first row's threads add them up
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < 2; ++which) {
 #pragma unroll
-      for (int i = 0; i < NIT; ++i) {
+    for (int i = 0; i < NIT; ++i) {
+      if (at.slots > 1) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) cols[threadIdx.x * VEC + e] = which ? db[i][e] : dw[i][e];
+        for (int e = 0; e < VEC; ++e) cols[e * kThreads + threadIdx.x] = which ? db[i][e] : dw[i][e];
         __syncthreads();
-        if (slot == 0 && has[i]) {
+      }
+      if (at.slot == 0 && at.has[i]) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float v = 0.0f;
-            for (int q = 0; q < slots; ++q) v += cols[(q * tpr + tr) * VEC + e];
-            out[which * a.D + (i * tpr + tr) * VEC + e] = v;
-          }
+        for (int e = 0; e < VEC; ++e) {
+          float v = which ? db[i][e] : dw[i][e];
+          for (int q = 1; q < at.slots; ++q) v += cols[e * kThreads + q * at.tpr + at.tr];
+          out[which * a.D + at.col[i] + e] = v;
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NIT; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (has[i]) {
-          out[(i * tpr + tr) * VEC + e] = dw[i][e];
-          out[a.D + (i * tpr + tr) * VEC + e] = db[i][e];
-        }
   }
 }
 
@@ -361,14 +424,14 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
       }
       sum[0] += f;
     }
-    row_sum<0, 1>(sum, lds, half);
+    row_sum<0, 1>(sum, kMaxWaves, lds, half);
     const float mu = sum[0] * inv;
     const E* src = q ? r : x;  // each thread reads the columns that it wrote
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) {
       const float f = Elem<E>::ld(src, c) - mu;
       var[0] += f * f;
     }
-    row_sum<0, 1>(var, lds, half);
+    row_sum<0, 1>(var, kMaxWaves, lds, half);
     const float s = 1.0f / sqrtf(var[0] * inv + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mu;
@@ -406,7 +469,7 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
       sum[0] += t;
       sum[1] += t * n;
     }
-    row_sum<0, 2>(sum, lds, half);
+    row_sum<0, 2>(sum, kMaxWaves, lds, half);
     const float m1 = sum[0] * inv, m2 = sum[1] * inv;
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) {
       const float n = (Elem<E>::ld(x, c) - mu) * s, t = Elem<E>::ld(dy, c) * (w ? w[c] : 1.0f);
@@ -415,25 +478,27 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
   }
 }
 
-// dw[g][c], db[g][c] = the sum of their `slices` partial rows: 64 columns a
-// workgroup, its waves each add a part of the rows.
-constexpr int kReduceWaves = 16;
+// dw[g][c], db[g][c] = the sum of their `slices` partial rows: 32 columns a
+// workgroup, 32 threads a column, each adds every 32nd partial row.
+constexpr int kReduceCols = 32, kReduceThreads = 1024, kReduceRows = kReduceThreads / kReduceCols;
 
-__global__ __launch_bounds__(kReduceWaves * 64) void ln_reduce_kernel(const float* __restrict__ part, int slices, int G, int D,
-                                                                      float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sums[kReduceWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const float* __restrict__ part, int slices, int G, int D,
+                                                                   float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sums[kReduceRows][kReduceCols];
+  const int lane = threadIdx.x % kReduceCols, row = threadIdx.x / kReduceCols;
   const int64_t cols = static_cast<int64_t>(G) * 2 * D;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceCols + lane;
   float v = 0.0f;
-  if (c < cols)
-    for (int s = wave; s < slices; s += kReduceWaves) v += part[s * cols + c];
-  sums[wave][lane] = v;
+  if (c < cols) {
+#pragma unroll 8
+    for (int s = row; s < slices; s += kReduceRows) v += part[s * cols + c];
+  }
+  sums[row][lane] = v;
   __syncthreads();
-  if (wave != 0 || c >= cols) return;
+  if (row != 0 || c >= cols) return;
   v = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kReduceWaves; ++w) v += sums[w][lane];
+  for (int w = 0; w < kReduceRows; ++w) v += sums[w][lane];
   const int64_t g = c / (2 * D), q = c - g * 2 * D;
   float* to = q < D ? dw : db;
   if (to) to[g * D + (q < D ? q : q - D)] = v;
@@ -444,11 +509,14 @@ __global__ __launch_bounds__(kReduceWaves * 64) void ln_reduce_kernel(const floa
 // How a row is laid over threads.
 struct Plan {
   int vec;      // elements of a piece
-  int tpr;      // lanes of a row (8 .. 64), or 0: the workgroup
+  int tpr;      // lanes of a row (8 .. 64), or 0: whole waves
   int nit;      // pieces of a thread; 0: the long kernels
-  int threads;  // of a workgroup
+  int wpr;      // waves of a row where tpr is 0
   int slots;    // rows side by side
+  int threads;  // of a workgroup
 };
+
+constexpr int kWideThreads = 512;  // of a workgroup of wide rows, where one row does not take more
 
 Plan make_plan(const ttt_ln_desc& d) {
   const int wide = d.dtype == TTT_BF16 ? 8 : 4;
@@ -463,40 +531,60 @@ Plan make_plan(const ttt_ln_desc& d) {
     p.slots = 256 / p.tpr;
     return p;
   }
-  p.slots = 1;
-  p.nit = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : pieces <= 4096 ? 4 : 0;
-  p.threads = p.nit ? ((pieces + p.nit - 1) / p.nit + 63) / 64 * 64 : kLongThreads;
+  if (p.vec == 1) p.nit = pieces <= 128 ? 1 : pieces <= 4096 ? 4 : 0;
+  else p.nit = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 0;
+  if (!p.nit) {
+    p.slots = 1;
+    p.threads = kLongThreads;
+    return p;
+  }
+  p.wpr = ((pieces + p.nit - 1) / p.nit + 63) / 64;
+  p.slots = p.wpr * 64 >= kWideThreads ? 1 : kWideThreads / (p.wpr * 64);
+  p.threads = p.slots * p.wpr * 64;
   return p;
 }
 
 // Workgroups of each group: enough for every CU to hold several, and no more than
 // there are rows for (`unroll` of them a step).
-int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int per_cu) {
-  const int per_group = static_cast<int>(d.rows / d.groups);
-  const int64_t steps = (static_cast<int64_t>(per_group) + p.slots * unroll - 1) / (p.slots * unroll);
-  const int64_t want = (256 * per_cu + d.groups - 1) / d.groups;
+int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int threads_per_cu) {
+  const int64_t per_group = d.rows / d.groups;
+  const int64_t steps = (per_group + p.slots * unroll - 1) / (p.slots * unroll);
+  const int64_t want = (static_cast<int64_t>(256) * threads_per_cu / p.threads + d.groups - 1) / d.groups;
   const int64_t n = steps < want ? steps : want;
   return static_cast<int>(n > 0 ? n : 1);
 }
 
-constexpr int kFwdPerCu = 8, kBwdPerCu = 2;
-// Rows a workgroup takes at once; few rows go to as many workgroups as there are.
-int unroll_of(const ttt_ln_desc& d, const Plan& p) {
-  if (p.nit > 1) return 1;
-  return d.rows >= 4096 * p.slots ? 4 : 1;
+// Threads a CU.  The backward's workgroups each write a partial row of dw and db, and
+// 16384 x 2048 bf16 took 53 us with 512, 58 with 1024 and 67 with 2048.
+constexpr int kFwdPerCu = 2048, kBwdPerCu = 512;
+
+// Rows a slot takes at once, where there are enough for every workgroup; few rows go
+// to as many workgroups as there are.  Narrow rows have no barrier to share but short
+// loads: forward of 262144 x 128 bf16 42 us with one, 38 with two, 34.5 with four;
+// the backward (registers for two tensors more) 43, 42 and 59.
+int fwd_unroll(const ttt_ln_desc& d, const Plan& p) {
+  if (p.nit != 1 || p.threads > kWideThreads || d.rows < 4096 * p.slots) return 1;
+  return p.tpr ? 4 : 2;
+}
+int bwd_unroll(const ttt_ln_desc& d, const Plan& p) {
+  return p.nit != 1 || p.threads > kWideThreads || d.rows < 4096 * p.slots ? 1 : 2;
 }
 
 int bwd_slices(const ttt_ln_desc& d) {
   const Plan p = make_plan(d);
-  return slices_of(d, p, p.nit ? unroll_of(d, p) : 1, kBwdPerCu);
+  return slices_of(d, p, bwd_unroll(d, p), kBwdPerCu);
 }
 
-template <typename F> hipError_t dispatch(const ttt_ln_desc& d, const Plan& p, int unroll, F&& f) {
+// Calls f with the element type and the plan as compile-time values.
+template <bool FWD, typename F> hipError_t dispatch(const ttt_ln_desc& d, const Plan& p, int unroll, bool res, F&& f) {
+  auto with_res = [&](auto e, auto vec, auto tpr, auto nit, auto ur) {
+    return res ? f(e, vec, tpr, nit, ur, std::true_type{}) : f(e, vec, tpr, nit, ur, std::false_type{});
+  };
   auto with_rows = [&](auto e, auto vec, auto tpr, auto nit) {
     if constexpr (nit() == 1) {
-      if (unroll == 4) return f(e, vec, tpr, nit, std::integral_constant<int, 4>{});
+      if (unroll > 1) return with_res(e, vec, tpr, nit, std::integral_constant<int, FWD && tpr() != 0 ? 4 : 2>{});
     }
-    return f(e, vec, tpr, nit, std::integral_constant<int, 1>{});
+    return with_res(e, vec, tpr, nit, std::integral_constant<int, 1>{});
   };
   auto with_plan = [&](auto e, auto vec) {
     std::integral_constant<int, 1> one;
@@ -507,9 +595,8 @@ template <typename F> hipError_t dispatch(const ttt_ln_desc& d, const Plan& p, i
       case 64: return with_rows(e, vec, std::integral_constant<int, 64>{}, one);
     }
     std::integral_constant<int, 0> group;
-    if (p.nit == 1) return with_rows(e, vec, group, one);
-    if (p.nit == 2) return with_rows(e, vec, group, std::integral_constant<int, 2>{});
-    return with_rows(e, vec, group, std::integral_constant<int, 4>{});
+    if (p.nit > 1) return with_rows(e, vec, group, std::integral_constant<int, vec() == 1 ? 4 : 2>{});
+    return with_rows(e, vec, group, one);
   };
   auto one = std::integral_constant<int, 1>{};
   if (d.dtype == TTT_BF16) return p.vec == 8 ? with_plan(bf16_t{}, std::integral_constant<int, 8>{}) : with_plan(bf16_t{}, one);
@@ -523,6 +610,12 @@ LnArgs make_args(const ttt_ln_desc& d) {
   a.G = d.groups;
   a.period = d.period;
   a.per_group = a.rows / a.G;
+  // With 2^(s-1) < period <= 2^s, magic = ceil(2^(31+s) / period) is below 2^32 and off
+  // by less than 2^s / 2^(31+s) of a quotient's step for every k < 2^31: the floor is exact.
+  int s = 1;
+  while ((int64_t{1} << s) < a.period) ++s;
+  a.shift = s - 1;
+  a.magic = static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + a.period - 1) / a.period);
   a.ldx = d.ldx ? d.ldx : d.D;
   a.eps = d.eps;
   return a;
@@ -539,8 +632,9 @@ hipError_t layernorm_fwd_launch(const ttt_ln_desc& d, const void* x, const void*
   const Plan p = make_plan(d);
   LnArgs a = make_args(d);
   a.x = x; a.res = res; a.w = w; a.b = b; a.y = y; a.r = r; a.mean = mean; a.rstd = rstd;
-  const int unroll = p.nit ? unroll_of(d, p) : 1;
+  const int unroll = fwd_unroll(d, p);
   a.slices = slices_of(d, p, unroll, kFwdPerCu);
+  a.wpr = p.wpr;
   const dim3 grid(static_cast<uint32_t>(a.slices) * a.G);
   KernelScope scope(TTT_KERNEL_LN_FWD, s);
   if (!p.nit) {
@@ -548,8 +642,8 @@ hipError_t layernorm_fwd_launch(const ttt_ln_desc& d, const void* x, const void*
     else ln_fwd_long_kernel<float><<<grid, kLongThreads, 0, s>>>(a);
     return hipGetLastError();
   }
-  return dispatch(d, p, unroll, [&](auto e, auto vec, auto tpr, auto nit, auto ur) {
-    ln_fwd_kernel<decltype(e), vec(), tpr(), nit(), ur()><<<grid, p.threads, 0, s>>>(a);
+  return dispatch<true>(d, p, unroll, res != nullptr, [&](auto e, auto vec, auto tpr, auto nit, auto ur, auto with) {
+    ln_fwd_kernel<decltype(e), vec(), tpr(), nit(), ur(), with()><<<grid, p.threads, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -561,8 +655,9 @@ hipError_t layernorm_bwd_launch(const ttt_ln_desc& d, const void* x, const float
   a.x = x; a.w = w; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
   a.dy = dy; a.dr = dr; a.dx = dx;
   a.part = dw || db ? static_cast<float*>(ws) : nullptr;
-  const int unroll = p.nit ? unroll_of(d, p) : 1;
+  const int unroll = bwd_unroll(d, p);
   a.slices = bwd_slices(d);
+  a.wpr = p.wpr;
   const dim3 grid(static_cast<uint32_t>(a.slices) * a.G);
   hipError_t st;
   {
@@ -572,8 +667,8 @@ hipError_t layernorm_bwd_launch(const ttt_ln_desc& d, const void* x, const float
       else ln_bwd_long_kernel<float><<<grid, kLongThreads, 0, s>>>(a);
       st = hipGetLastError();
     } else {
-      st = dispatch(d, p, unroll, [&](auto e, auto vec, auto tpr, auto nit, auto ur) {
-        ln_bwd_kernel<decltype(e), vec(), tpr(), nit(), ur()><<<grid, p.threads, 0, s>>>(a);
+      st = dispatch<false>(d, p, unroll, dr != nullptr, [&](auto e, auto vec, auto tpr, auto nit, auto ur, auto with) {
+        ln_bwd_kernel<decltype(e), vec(), tpr(), nit(), ur(), with()><<<grid, p.threads, 0, s>>>(a);
         return hipGetLastError();
       });
     }
@@ -581,7 +676,7 @@ hipError_t layernorm_bwd_launch(const ttt_ln_desc& d, const void* x, const float
   if (st != hipSuccess || !a.part) return st;
   const int64_t cols = static_cast<int64_t>(d.groups) * 2 * d.D;
   KernelScope scope(TTT_KERNEL_LN_REDUCE, s);
-  ln_reduce_kernel<<<static_cast<uint32_t>((cols + 63) / 64), kReduceWaves * 64, 0, s>>>(a.part, a.slices, a.G, a.D, dw, db);
+  ln_reduce_kernel<<<static_cast<uint32_t>((cols + kReduceCols - 1) / kReduceCols), kReduceThreads, 0, s>>>(a.part, a.slices, a.G, a.D, dw, db);
   return hipGetLastError();
 }
 

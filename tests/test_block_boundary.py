@@ -173,6 +173,9 @@ def test_binding_refuses_tensors_that_would_fault():
         def __init__(self, t, device="cuda:0"):
             self.t, self.device = t, torch.device(device)
 
+        def get_device(self):
+            return self.device.index
+
         def __getattr__(self, name):
             return getattr(self.t, name)
 

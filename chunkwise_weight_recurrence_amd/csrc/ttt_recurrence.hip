@@ -47,8 +47,8 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
-constexpr int kFwdLW = 16, kBwdLW = 16;  // tokens a wave holds
-constexpr int kRun = kWaves * kBwdLW;    // tokens between two states in the saved context
+constexpr int kBwdLW = 16;           // tokens a wave holds in the backward
+constexpr int kRun = kWaves * kBwdLW;  // tokens between two states in the saved context
 constexpr int kGroup = 32;           // tiles of a group
 constexpr int kCounterStride = 32;   // ints between two channel blocks' counters: a cache line each
 constexpr int kPolls = 1 << 20;      // of a wave, together; a look takes about a microsecond
@@ -152,6 +152,13 @@ template <typename Raw> __device__ __forceinline__ Raw afresh(Raw r) {
     asm volatile("" : "+v"(r));
   }
   return r;
+}
+
+// Bit j of a mask that is the same for the wave, tested where it is asked: the
+// compiler would keep the results of all tests in scalar registers otherwise.
+__device__ __forceinline__ bool bit(uint32_t mask, int j) {
+  asm volatile("" : "+s"(mask));
+  return mask >> j & 1;
 }
 
 // Keeps the compiler from forming the coefficients of many tokens ahead, which
@@ -454,7 +461,7 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ maps
 
 // LINKED: there is more than one tile.
 template <typename E, int V, int GATE, int IN, int LW, bool LINKED>
-__global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(RecArgs a) {
+__global__ __launch_bounds__(kThreads, LW == 32 ? 2 : 4) void rec_fwd_kernel(RecArgs a) {
   using IO = Io<E, V>;
   using Raw = typename IO::Raw;
   __shared__ Meta<LW> m;
@@ -476,100 +483,110 @@ __global__ __launch_bounds__(kThreads, 4) void rec_fwd_kernel(RecArgs a) {
   for (int j = 0; j < LW; ++j) gr[j] = gs.load(j, off), xr[j] = xs.load(j, off);
   const Bits bits = tile_meta<LW>(a, t0, m);
   const uint32_t okm = uniform(bits.ok), sm = uniform(bits.start), em = uniform(bits.end);
+  if (okm != kAll<LW>) {
+    // a token of no sequence: a = 1 and u = 0 leave what passes over it as it is
+#pragma unroll
+    for (int j = 0; j < LW; ++j)
+      if (!(okm >> j & 1)) xr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+  }
+  float f[LW][V], u[LW][V];
+#pragma unroll
+  for (int j = 0; j < LW; ++j) {
+    float x[V], z[V];
+    IO::get(xr[j], x);
+    IO::get(gr[j], z);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f[j][v] = gate_a<GATE>(z[v]);
+      u[j][v] = IN == TTT_REC_PLAIN ? x[v] : gate_rest<GATE>(z[v], f[j][v]) * x[v];
+    }
+  }
+  float A[V], h[V];
+  auto initial = [&](int j) {  // h0 of the sequence that starts at the wave's token j
+    const int s = uniform(m.start[wave * LW + j]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+  };
 
-  // EDGE: the tile holds a start, an end or a token of no sequence.
-  auto body = [&](auto edge) {
-    constexpr bool EDGE = decltype(edge)::value;
-    auto coefficients = [&](int j, float (&f)[V], float (&u)[V]) {
-      Raw g = afresh(gr[j]), xx = afresh(xr[j]);
-      // a token of no sequence: a = 1 and u = 0 leave what passes over it as it is
-      if (EDGE && !(okm >> j & 1)) xx = Raw(0), g = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
-      float x[V], z[V];
-      IO::get(xx, x);
-      IO::get(g, z);
+  // The map of the wave's tokens.  Both walks have a form without tests for the waves
+  // that lie inside one sequence; only the short walks are there twice, since a kernel
+  // with two whole bodies took 10% longer in either.
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+  if (sm == 0) {
+#pragma unroll
+    for (int j = 0; j < LW; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f[v] = gate_a<GATE>(z[v]);
-        u[v] = IN == TTT_REC_PLAIN ? x[v] : gate_rest<GATE>(z[v], f[v]) * x[v];
+        h[v] = f[j][v] * h[v] + u[j][v];
+        A[v] *= f[j][v];
       }
-    };
-    float A[V], h[V];
-    auto initial = [&](int j) {  // h0 of the sequence that starts at the wave's token j
-      const int s = uniform(m.start[wave * LW + j]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-    };
-
-    // the map of the wave's tokens
-    float fs[LW][V], us[LW][V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+  } else {
+    // what enters counts no longer behind a start: the sign of A says so to the readers of `part`
 #pragma unroll
     for (int j = 0; j < LW; ++j) {
-      in_order();
-      if (EDGE && (sm >> j & 1)) initial(j);
-      coefficients(j, fs[j], us[j]);
+      if (sm >> j & 1) initial(j);
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = f[j][v] * h[v] + u[j][v];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = -1.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
+  __syncthreads();
+
+  // fold the maps of waves 0 .. upto - 1 onto h; A: the product, dropped at a start
+  auto fold_waves = [&](int upto) {
+    for (int w = 0; w < upto; ++w) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[v] = fs[j][v] * h[v] + us[j][v];
-        A[v] *= fs[j][v];
+        const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+        const bool reset = pa < 0.0f;
+        h[v] = reset ? pb : pa * h[v] + pb;
+        A[v] = reset ? 0.0f : pa * A[v];
       }
     }
-    if (EDGE && sm) {
-      // a start: what enters no longer counts.  The sign of A carries it to the readers of `part`.
+  };
+  if constexpr (LINKED) {
+    if (wave == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) A[v] = -1.0f;
+      for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
+      fold_waves(kWaves);
     }
+    publish_tile<V>(a, i, 1, c, look, A, h);
+    fold_way<V>(a, Way(i, uniform(bits.first) / (kWaves * LW), 1), c, look, h);
+  } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) part[wave][lane][2 * v] = A[v], part[wave][lane][2 * v + 1] = h[v];
-    __syncthreads();
-
-    // fold the maps of waves 0 .. upto - 1 onto h; A: the product, dropped at a start
-    auto fold_waves = [&](int upto) {
-      for (int w = 0; w < upto; ++w) {
+    for (int v = 0; v < V; ++v) h[v] = 0.0f;
+  }
+  fold_waves(wave);
+  if (a.ckpt && (wave * LW) % kRun == 0 && tw < a.n) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
-          const bool reset = EDGE && pa < 0.0f;
-          h[v] = reset ? pb : pa * h[v] + pb;
-          A[v] = reset ? 0.0f : pa * A[v];
-        }
-      }
-    };
-    if constexpr (LINKED) {
-      if (wave == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.0f, h[v] = 0.0f;
-        fold_waves(kWaves);
-      }
-      publish_tile<V>(a, i, 1, c, look, A, h);
-      fold_way<V>(a, Way(i, uniform(bits.first) / (kWaves * LW), 1), c, look, h);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = 0.0f;
-    }
-    fold_waves(wave);
-    if (a.ckpt && (wave * LW) % kRun == 0 && tw < a.n) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(tw / kRun) * a.Dp + c + v] = h[v];
-    }
-    const Rows<Raw, LW> os(a.o, a.D, a.D, sizeof(E), tw, a.n);
+    for (int v = 0; v < V; ++v) a.ckpt[static_cast<int64_t>(tw / kRun) * a.Dp + c + v] = h[v];
+  }
+  const Rows<Raw, LW> os(a.o, a.D, a.D, sizeof(E), tw, a.n);
+  if (okm == kAll<LW> && (sm | em) == 0) {
 #pragma unroll
     for (int j = 0; j < LW; ++j) {
-      in_order();
-      if (EDGE && (sm >> j & 1)) initial(j);
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = fs[j][v] * h[v] + us[j][v];
-      os.store(j, off, !EDGE || (okm >> j & 1), IO::put(h));
-      if (EDGE && in && a.h_final && (em >> j & 1)) {
+      for (int v = 0; v < V; ++v) h[v] = f[j][v] * h[v] + u[j][v];
+      os.store(j, off, true, IO::put(h));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < LW; ++j) {
+      if (sm >> j & 1) initial(j);
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = f[j][v] * h[v] + u[j][v];
+      os.store(j, off, okm >> j & 1, IO::put(h));
+      if (in && a.h_final && (em >> j & 1)) {
         const int s = uniform(m.end[wave * LW + j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a.h_final[static_cast<int64_t>(s) * a.D + c + v] = h[v];
       }
     }
-  };
-  if (uniform(bits.inside)) body(std::false_type{});
-  else body(std::true_type{});
+  }
   pass_empty<V>(a, i, c, in, a.h0, a.h_final);
 }
 
@@ -601,111 +618,113 @@ __global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(RecArgs a) {
   for (int j = 0; j < LW; ++j) gr[j] = gs.load(j, off), xr[j] = xs.load(j, off), dr[j] = ds.load(j, off);
   const Bits bits = tile_meta<LW>(a, t0, m);
   const uint32_t okm = uniform(bits.ok), sm = uniform(bits.start), em = uniform(bits.end);
+  if (okm != kAll<LW>) {
+#pragma unroll
+    for (int j = 0; j < LW; ++j)
+      if (!(okm >> j & 1)) xr[j] = dr[j] = Raw(0), gr[j] = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
+  }
+  const bool inner = okm == kAll<LW> && (sm | em) == 0;  // the wave lies inside one sequence
+  float h[V], e[V], P[V];
+  auto coefficients = [&](int j, float (&f)[V], float (&rest)[V]) {
+    float z[V];
+    IO::get(afresh(gr[j]), z);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f[v] = gate_a<GATE>(z[v]);
+      rest[v] = gate_rest<GATE>(z[v], f[v]);
+    }
+  };
+  auto initial = [&](int j) {
+    const int s = uniform(m.start[wave * LW + j]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+  };
+  auto final_grad = [&](int j, float (&q)[V]) {
+    const int s = uniform(m.end[wave * LW + j]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) q[v] = a.d_hfinal ? a.d_hfinal[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
+  };
 
-  auto body = [&](auto edge) {
+  // Both maps of the wave's tokens in one walk: with P_j = a_0 ... a_j, h <- a h + u
+  // as in the forward, and e in front of the tokens is sum_j P_j do_j + P_last e
+  // behind them.  The first end cuts that sum: behind its token only d_hfinal adds.
+  float cut[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) P[v] = 1.0f, h[v] = e[v] = cut[v] = 0.0f;
+  auto both_maps = [&](auto edge) {
     constexpr bool EDGE = decltype(edge)::value;
-    float h[V], e[V], P[V];
-    auto coefficients = [&](int j, float (&f)[V], float (&rest)[V]) {
-      Raw g = afresh(gr[j]);
-      if (EDGE && !(okm >> j & 1)) g = GATE == TTT_GATE_SIGMOID ? IO::kInf : Raw(0);
-      float z[V];
-      IO::get(g, z);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        f[v] = gate_a<GATE>(z[v]);
-        rest[v] = gate_rest<GATE>(z[v], f[v]);
-      }
-    };
-    auto value = [&](const Raw (&r)[LW], int j, float (&f)[V]) {
-      Raw q = afresh(r[j]);
-      if (EDGE && !(okm >> j & 1)) q = Raw(0);
-      IO::get(q, f);
-    };
-    auto initial = [&](int j) {
-      const int s = uniform(m.start[wave * LW + j]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = a.h0 ? a.h0[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-    };
-    auto final_grad = [&](int j, float (&f)[V]) {
-      const int s = uniform(m.end[wave * LW + j]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = a.d_hfinal ? a.d_hfinal[static_cast<int64_t>(s) * a.D + cl + v] : 0.0f;
-    };
-
-    // Both maps of the wave's tokens in one walk: with P_j = a_0 ... a_j, h <- a h + u
-    // as in the forward, and e in front of the tokens is sum_j P_j do_j + P_last e
-    // behind them.  An end cuts that sum: behind its token only d_hfinal adds.
-#pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, h[v] = e[v] = 0.0f;
 #pragma unroll
     for (int j = 0; j < LW; ++j) {
       in_order();
-      if (EDGE && (sm >> j & 1)) initial(j);
+      if (EDGE && bit(sm, j)) initial(j);
       float f[V], rest[V], x[V], d[V];
       coefficients(j, f, rest);
-      value(xr, j, x);
-      value(dr, j, d);
-      if (EDGE && (em >> j & 1)) {
-        float q[V];
-        final_grad(j, q);
-#pragma unroll
-        for (int v = 0; v < V; ++v) d[v] += q[v];
-      }
-      const bool open = !EDGE || (em & ((1u << j) - 1)) == 0;  // no end before this token
+      IO::get(afresh(xr[j]), x);
+      IO::get(afresh(dr[j]), d);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         h[v] = f[v] * h[v] + (IN == TTT_REC_PLAIN ? x[v] : rest[v] * x[v]);
         P[v] *= f[v];
-        if (open) e[v] += P[v] * d[v];
+        e[v] += P[v] * d[v];
+      }
+      if (EDGE && bit(em, j) && (em & ((1u << j) - 1)) == 0) {
+        final_grad(j, cut);
+#pragma unroll
+        for (int v = 0; v < V; ++v) cut[v] = e[v] + P[v] * cut[v];
       }
     }
+  };
+  if (inner) both_maps(std::false_type{});
+  else both_maps(std::true_type{});
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      part[wave][lane][2 * v] = EDGE && sm ? -1.0f : P[v];
-      part[wave][lane][2 * v + 1] = h[v];
-      rpart[wave][lane][2 * v] = EDGE && em ? -1.0f : P[v];
-      rpart[wave][lane][2 * v + 1] = e[v];
-    }
-    __syncthreads();
+  for (int v = 0; v < V; ++v) {
+    part[wave][lane][2 * v] = sm ? -1.0f : P[v];
+    part[wave][lane][2 * v + 1] = h[v];
+    rpart[wave][lane][2 * v] = em ? -1.0f : P[v];
+    rpart[wave][lane][2 * v + 1] = em ? cut[v] : e[v];
+  }
+  __syncthreads();
 
-    // fold the maps of e of waves kWaves - 1 .. from onto e; P: the product
-    auto fold_back = [&](int from) {
-      for (int w = kWaves - 1; w >= from; --w) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
-          const bool reset = EDGE && pa < 0.0f;
-          e[v] = reset ? pb : pa * e[v] + pb;
-          P[v] = reset ? 0.0f : pa * P[v];
-        }
-      }
-    };
-    if constexpr (LINKED) {
-      if (wave == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) P[v] = 1.0f, e[v] = 0.0f;
-        fold_back(0);
-      }
-      publish_tile<V>(a, i, -1, c, look, P, e);
-    }
-    // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
-    float wv[LW][V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
-    for (int w = 0; w < wave; ++w) {
+  // fold the maps of e of waves kWaves - 1 .. from onto e; P: the product
+  auto fold_back = [&](int from) {
+    for (int w = kWaves - 1; w >= from; --w) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
-        h[v] = EDGE && pa < 0.0f ? pb : pa * h[v] + pb;
+        const float pa = rpart[w][lane][2 * v], pb = rpart[w][lane][2 * v + 1];
+        const bool reset = pa < 0.0f;
+        e[v] = reset ? pb : pa * e[v] + pb;
+        P[v] = reset ? 0.0f : pa * P[v];
       }
     }
+  };
+  if constexpr (LINKED) {
+    if (wave == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) P[v] = 1.0f, e[v] = 0.0f;
+      fold_back(0);
+    }
+    publish_tile<V>(a, i, -1, c, look, P, e);
+  }
+  // h_{t-1} of every token, kept as w_t = a'_t (h_{t-1} - (0 or x_t))
+  float wv[LW][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = a.ckpt[static_cast<int64_t>(i) * a.Dp + c + v];
+  for (int w = 0; w < wave; ++w) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float pa = part[w][lane][2 * v], pb = part[w][lane][2 * v + 1];
+      h[v] = pa < 0.0f ? pb : pa * h[v] + pb;
+    }
+  }
+  auto slopes = [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
     for (int j = 0; j < LW; ++j) {
       in_order();
-      if (EDGE && (sm >> j & 1)) initial(j);
+      if (EDGE && bit(sm, j)) initial(j);
       float f[V], rest[V], x[V];
       coefficients(j, f, rest);
-      value(xr, j, x);
+      IO::get(afresh(xr[j]), x);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float da = GATE == TTT_GATE_SIGMOID ? f[v] * rest[v] : f[v];
@@ -714,21 +733,26 @@ __global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(RecArgs a) {
         wv[j][v] = afresh(wv[j][v]);  // formed here, not where it is used
       }
     }
-    if constexpr (LINKED) {
-      fold_way<V>(a, Way(i, uniform(bits.last) / (kWaves * LW), -1), c, look, e);
-    } else {
+  };
+  if (inner) slopes(std::false_type{});
+  else slopes(std::true_type{});
+  if constexpr (LINKED) {
+    fold_way<V>(a, Way(i, uniform(bits.last) / (kWaves * LW), -1), c, look, e);
+  } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) e[v] = 0.0f;
-    }
-    fold_back(wave + 1);
-    const Rows<Raw, LW> dxs(a.dx, a.ldx, a.D, sizeof(E), tw, a.n), dgs(a.dg, a.ldg, a.D, sizeof(E), tw, a.n);
+    for (int v = 0; v < V; ++v) e[v] = 0.0f;
+  }
+  fold_back(wave + 1);
+  const Rows<Raw, LW> dxs(a.dx, a.ldx, a.D, sizeof(E), tw, a.n), dgs(a.dg, a.ldg, a.D, sizeof(E), tw, a.n);
+  auto gradients = [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
     for (int j = LW - 1; j >= 0; --j) {
       in_order();
-      if (EDGE && (em >> j & 1)) final_grad(j, e);
+      if (EDGE && bit(em, j)) final_grad(j, e);
       float f[V], rest[V], d[V], ox[V], og[V];
       coefficients(j, f, rest);
-      value(dr, j, d);
+      IO::get(afresh(dr[j]), d);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float dh = d[v] + e[v];
@@ -736,17 +760,17 @@ __global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(RecArgs a) {
         og[v] = dh * wv[j][v];
         e[v] = f[v] * dh;
       }
-      dxs.store(j, off, !EDGE || (okm >> j & 1), IO::put(ox));
-      dgs.store(j, off, !EDGE || (okm >> j & 1), IO::put(og));
-      if (EDGE && in && a.dh0 && (sm >> j & 1)) {
+      dxs.store(j, off, !EDGE || bit(okm, j), IO::put(ox));
+      dgs.store(j, off, !EDGE || bit(okm, j), IO::put(og));
+      if (EDGE && bit(sm, j) && a.dh0 && in) {
         const int s = uniform(m.start[wave * LW + j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a.dh0[static_cast<int64_t>(s) * a.D + c + v] = e[v];
       }
     }
   };
-  if (uniform(bits.inside)) body(std::false_type{});
-  else body(std::true_type{});
+  if (inner) gradients(std::false_type{});
+  else gradients(std::true_type{});
   pass_empty<V>(a, i, c, in, a.d_hfinal, a.dh0);
 }
 
@@ -856,7 +880,15 @@ int64_t tiles(const ttt_rec_desc& d, int tile) {
   const int64_t nt = (tokens(d) + tile - 1) / tile;
   return nt > 0 ? nt : 1;
 }
-constexpr int kFwdTile = kWaves * kFwdLW, kBwdTile = kWaves * kBwdLW;
+constexpr int kBwdTile = kWaves * kBwdLW;
+// The forward's tile: 256 tokens where that leaves eight tiles a CU, else 128.  A larger
+// tile reads fewer of the others' maps: 131072 x 2048 bf16 (32 tiles of 256 a CU) takes
+// 375 us with 256 and 402 with 128; 4 x 4096 x 2048 (4 a CU) 72 and 62.
+int fwd_tile(const ttt_rec_desc& d) {
+  const int64_t blocks = (static_cast<int64_t>(d.D) + 127) / 128;
+  const int64_t nt = tiles(d, kWaves * 32);
+  return nt > 1 && nt * blocks >= 8 * 256 ? kWaves * 32 : kWaves * 16;
+}
 // Room for either channel block width, 64 and 128.
 int64_t padded_channels(const ttt_rec_desc& d) { return (static_cast<int64_t>(d.D) + 127) / 128 * 128; }
 
@@ -877,8 +909,7 @@ RecArgs make_args(const ttt_rec_desc& d, int V, int tile) {
 }  // namespace
 
 bool recurrence_grid_fits(const ttt_rec_desc& d) {
-  const int64_t least = kFwdTile < kBwdTile ? kFwdTile : kBwdTile;
-  return tiles(d, least) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31);
+  return tiles(d, kBwdTile) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31);
 }
 
 namespace {
@@ -892,7 +923,7 @@ size_t counter_ints(const ttt_rec_desc& d) { return static_cast<size_t>((d.D + 6
 }  // namespace
 
 size_t recurrence_workspace(const ttt_rec_desc& d, int entry) {
-  const int tile = entry == TTT_ENTRY_FWD ? kFwdTile : kBwdTile;
+  const int tile = entry == TTT_ENTRY_FWD ? fwd_tile(d) : kBwdTile;
   if (tiles(d, tile) == 1) return 0;
   return align256(map_words(d, tile) * sizeof(uint64_t)) + align256(counter_ints(d) * sizeof(int));
 }
@@ -921,7 +952,8 @@ hipError_t link_tiles(const ttt_rec_desc& d, int tile, RecArgs& a, void* ws, hip
 hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const void* gate, const float* h0, const int32_t* starts,
                                  void* o, float* h_final, void* saved, void* ws, hipStream_t s) {
   const int V = lane_channels(d.dtype, d.D, d.ldx, d.ldg);
-  RecArgs a = make_args(d, V, kFwdTile);
+  const int tile = fwd_tile(d);
+  RecArgs a = make_args(d, V, tile);
   a.x = x; a.g = gate; a.h0 = h0; a.starts = d.packed ? starts : nullptr;
   a.o = o; a.h_final = h_final; a.ckpt = static_cast<float*>(saved);
   if (a.n == 0) {
@@ -929,15 +961,16 @@ hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const voi
     return hipGetLastError();
   }
   if (a.nt > 1) {
-    const hipError_t e = link_tiles(d, kFwdTile, a, ws, s);
+    const hipError_t e = link_tiles(d, tile, a, ws, s);
     if (e != hipSuccess) return e;
   }
   return dispatch(d, V, [&](auto e, auto v, auto gk, auto in) {
     using E = decltype(e);
     const dim3 grid(static_cast<uint32_t>(a.nt) * a.ncb);
     KernelScope scope(TTT_KERNEL_REC_FWD, s);
-    if (a.nt > 1) rec_fwd_kernel<E, v(), gk(), in(), kFwdLW, true><<<grid, kThreads, 0, s>>>(a);
-    else rec_fwd_kernel<E, v(), gk(), in(), kFwdLW, false><<<grid, kThreads, 0, s>>>(a);
+    if (tile == kWaves * 32) rec_fwd_kernel<E, v(), gk(), in(), 32, true><<<grid, kThreads, 0, s>>>(a);
+    else if (a.nt > 1) rec_fwd_kernel<E, v(), gk(), in(), 16, true><<<grid, kThreads, 0, s>>>(a);
+    else rec_fwd_kernel<E, v(), gk(), in(), 16, false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }

@@ -228,6 +228,28 @@ def test_long_sequences_and_resuming():
     assert worst(g["dh0"], want["dh0"], want["e_dh0"], "f32") <= 1
 
 
+@pytest.mark.parametrize("dtype,n,D,gate,kind", [("bf16", 4300, 16384, "sigmoid", "convex"), ("bf16", 4200, 16385, "log", "convex"),
+                                                 ("f32", 9000, 8000, "sigmoid", "plain")])
+def test_large_problems(dtype, n, D, gate, kind):
+    """Enough tiles for the forward's larger ones, and for more than a group of them; checked on some channels."""
+    lens = [n - 2911, 0, 1, 255, 256, 257, 2142]
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    assert starts[-1] == n
+    for st in (starts, [0, n]):
+        inp = _make(50, n, len(st) - 1, D, dtype, gate, z_mean=5.0)
+        out = _train(inp, gate, kind, dtype, starts=st)
+        at = np.unique(np.concatenate([[0, 1, 126, 127, 128, D - 130, D - 2, D - 1], np.random.default_rng(0).integers(0, D, 30)]))
+        some = {k: v[:, at] for k, v in inp.items()}
+        _check(some, {k: v[:, at] for k, v in out.items()}, st, gate, kind, dtype)
+
+
+def test_one_tile_of_very_many_channels():
+    inp = _make(51, 200, 2, 270_000, "bf16", "sigmoid")
+    out = _train(inp, "sigmoid", "convex", "bf16", starts=[0, 70, 200])
+    at = np.array([0, 1, 135_000, 269_998, 269_999])
+    _check({k: v[:, at] for k, v in inp.items()}, {k: v[:, at] for k, v in out.items()}, [0, 70, 200], "sigmoid", "convex", "bf16")
+
+
 def test_offsets_past_32_bits():
     """The last of two sequences lies behind the first 2^31 elements."""
     import torch

@@ -6,9 +6,15 @@
 //   dx = s (t - mean(t) - n mean(t n)) (+ dr);  dw_g = sum dy n;  db_g = sum dy.
 //
 // Both passes are bound by memory: a row is read once into registers, a thread
-// holding NIT pieces of VEC elements (16 bytes where the rows allow it).  Narrow
+// holding NIT pieces of VEC elements (16 bytes; rows need not be aligned to them,
+// and a last piece that would pass the row's end moves back into it, over elements
+// that the piece before has too and that count once: both directions of 60000 x 999
+// bf16 166 us, element by element 200, and of 1800000 x 33 220 and 600 us).  Narrow
 // rows take a part of a wave each, wide rows as many waves as they have pieces
-// for.  A workgroup holds several rows side by side (slots), walks over rows of one
+// for.  Measured, where a copy reaches 4.7 to 4.8 TB/s: forward of
+// 32768 x 2560 bf16 with a residual (671 MB) 139 us, both directions of 16384 x 2048
+// bf16 with one (537 MB) 108 us, of 262144 x 128 in 16 groups (340 MB) 77 us.
+// A workgroup holds several rows side by side (slots), walks over rows of one
 // group, so that the weights stay in registers, and takes UR rows a slot at a time:
 // they share the barriers of a cross-wave sum, and the loads of the next UR are in
 // flight meanwhile.  The variance is the mean of (r - mu)^2 in a second sum over the
@@ -18,6 +24,7 @@
 // slots meet in LDS, and the workgroup writes one partial row; ln_reduce_kernel adds
 // the partial rows in a fixed order.
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -55,6 +62,7 @@ struct LnArgs {
 template <typename E, int VEC> struct Piece;
 template <> struct Piece<bf16_t, 8> {
   typedef uint32_t Raw __attribute__((ext_vector_type(4)));
+  typedef Raw Stored __attribute__((aligned(2)));  // as it lies in memory
   static __device__ __forceinline__ void get(const Raw& r, float (&f)[8]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -68,6 +76,7 @@ template <> struct Piece<bf16_t, 8> {
 };
 template <> struct Piece<float, 4> {
   typedef float Raw __attribute__((ext_vector_type(4)));
+  typedef Raw Stored __attribute__((aligned(4)));
   static __device__ __forceinline__ void get(const Raw& r, float (&f)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = r[k];
@@ -76,11 +85,13 @@ template <> struct Piece<float, 4> {
 };
 template <> struct Piece<bf16_t, 1> {
   using Raw = uint16_t;
+  using Stored = uint16_t;
   static __device__ __forceinline__ void get(const Raw& r, float (&f)[1]) { f[0] = bf16_to_f32(r); }
   static __device__ __forceinline__ Raw put(const float (&f)[1]) { return f32_to_bf16(f[0]); }
 };
 template <> struct Piece<float, 1> {
   using Raw = float;
+  using Stored = float;
   static __device__ __forceinline__ void get(const Raw& r, float (&f)[1]) { f[0] = r; }
   static __device__ __forceinline__ Raw put(const float (&f)[1]) { return f[0]; }
 };
@@ -157,6 +168,7 @@ template <int VEC, int TPR, int NIT> struct Place {
   int tpr, slots, slot, tr;
   int col[NIT];   // first column of each piece, 0 where it has none
   bool has[NIT];
+  int twice[NIT];  // elements at the piece's front that the piece before has too
   __device__ __forceinline__ explicit Place(const LnArgs& a) {
     tpr = TPR ? TPR : a.wpr * 64;
     slots = static_cast<int>(blockDim.x) / tpr;
@@ -165,10 +177,14 @@ template <int VEC, int TPR, int NIT> struct Place {
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
       const int c = (i * tpr + tr) * VEC;
-      has[i] = c < a.D;
-      col[i] = has[i] ? c : 0;
+      has[i] = i < NIT - 1 || c < a.D;  // a thread's pieces but the last are whole
+      col[i] = has[i] ? min(c, a.D - VEC) : 0;
+      twice[i] = i == NIT - 1 && has[i] ? c - col[i] : 0;
     }
   }
+  // v where this thread is the one that counts the element, else 0, also where v is
+  // no number
+  __device__ __forceinline__ float once(int i, int e, float v) const { return i < NIT - 1 || (has[i] && e >= twice[i]) ? v : 0.0f; }
 };
 
 // UR rows of a slot as they lie in memory, NT tensors of them.
@@ -189,7 +205,7 @@ template <typename E, int VEC, int TPR, int NIT, int UR, int NT> struct Batch {
 #pragma unroll
     for (int u = 0; u < UR; ++u)
 #pragma unroll
-      for (int i = 0; i < NIT; ++i) r[n][u][i] = *reinterpret_cast<const Raw*>(static_cast<const E*>(base) + row[u] * ld + at.col[i]);
+      for (int i = 0; i < NIT; ++i) r[n][u][i] = *reinterpret_cast<const typename Piece<E, VEC>::Stored*>(static_cast<const E*>(base) + row[u] * ld + at.col[i]);
   }
 };
 
@@ -243,16 +259,24 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_fwd_kernel(LnArgs a) 
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[u][i][e] += q[e];
           // the stream is normalised as it is kept, so that the backward sees the same rows
-          const Raw kept = P::put(f[u][i]);
-          P::get(kept, f[u][i]);
-          if (ok[u] && at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.r) + row[u] * a.D + at.col[i]) = kept;
+          P::get(P::put(f[u][i]), f[u][i]);
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[u] += at.has[i] ? f[u][i][e] : 0.0f;
+        for (int e = 0; e < VEC; ++e) sum[u] += at.once(i, e, f[u][i][e]);
       }
     }
     if (AHEAD && k0 + step < a.per_group) fetch(k0 + step);
     row_sum<TPR, UR>(sum, a.wpr, lds, half);
+    // Kept only now that every thread of the row has read it: r may be res, and pieces
+    // overlap.  The rounding is exact, f was rounded before.
+    if constexpr (RES) {
+#pragma unroll
+      for (int u = 0; u < UR; ++u)
+#pragma unroll
+        for (int i = 0; i < NIT; ++i)
+          if (ok[u] && at.has[i])
+            *reinterpret_cast<typename P::Stored*>(static_cast<E*>(a.r) + row[u] * a.D + at.col[i]) = P::put(f[u][i]);
+    }
     float mu[UR], var[UR];
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
@@ -263,7 +287,7 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_fwd_kernel(LnArgs a) 
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           f[u][i][e] -= mu[u];
-          var[u] += at.has[i] ? f[u][i][e] * f[u][i][e] : 0.0f;
+          var[u] += at.once(i, e, f[u][i][e] * f[u][i][e]);
         }
     }
     row_sum<TPR, UR>(var, a.wpr, lds, half);
@@ -280,7 +304,7 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_fwd_kernel(LnArgs a) 
         float y[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) y[e] = f[u][i][e] * s * w[i][e] + b[i][e];
-        if (at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.y) + row[u] * a.D + at.col[i]) = P::put(y);
+        if (at.has[i]) *reinterpret_cast<typename P::Stored*>(static_cast<E*>(a.y) + row[u] * a.D + at.col[i]) = P::put(y);
       }
     }
   }
@@ -292,19 +316,34 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_bwd_kernel(LnArgs a) 
   using Raw = typename P::Raw;
   constexpr int kThreads = max_threads(TPR, UR);
   __shared__ float lds[4 * UR * kMaxWaves];
-  __shared__ float cols[kThreads * VEC];
+  __shared__ float cols[NIT == 1 ? kThreads * VEC : 1];  // rows of more pieces are alone in a workgroup
   int half = 0;
   const Place<VEC, TPR, NIT> at(a);
   const int g = blockIdx.x % a.G, slice = blockIdx.x / a.G;
-  float w[NIT][VEC], dw[NIT][VEC], db[NIT][VEC];
+  // The widest rows leave no registers for the weights, which are read again for each
+  // row (from L2), nor, with 24 columns of a thread, for its sums of dw: those lie in LDS.
+  constexpr bool KEEP = NIT == 1, FAR = NIT * VEC >= 20;
+  __shared__ float4 far[FAR ? NIT * VEC / 4 * kThreads : 1];
+  const float* wg = a.w ? a.w + static_cast<int64_t>(g) * a.D : nullptr;
+  float w[KEEP ? NIT : 1][VEC], dw[FAR ? 1 : NIT][VEC], db[NIT][VEC];
 #pragma unroll
   for (int i = 0; i < NIT; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      // a piece that the row does not have counts for nothing: t = w dy = 0
-      w[i][e] = !at.has[i] ? 0.0f : a.w ? a.w[static_cast<int64_t>(g) * a.D + at.col[i] + e] : 1.0f;
-      dw[i][e] = db[i][e] = 0.0f;
+      if constexpr (KEEP) w[i][e] = wg ? wg[at.col[i] + e] : 1.0f;
+      if constexpr (!FAR) dw[i][e] = 0.0f;
+      db[i][e] = 0.0f;
     }
+  if constexpr (FAR) {
+#pragma unroll
+    for (int q = 0; q < NIT * VEC / 4; ++q) far[q * kThreads + threadIdx.x] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  auto weights = [&](int i, float (&v)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if constexpr (KEEP) v[e] = w[i][e];
+      else v[e] = wg ? wg[at.col[i] + e] : 1.0f;
+  };
   const float inv = 1.0f / static_cast<float>(a.D);
   const int64_t step = static_cast<int64_t>(a.slices) * at.slots * UR;
   int64_t k0 = static_cast<int64_t>(slice) * at.slots * UR;
@@ -342,15 +381,29 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_bwd_kernel(LnArgs a) 
       sum[2 * u] = sum[2 * u + 1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
-        float n[VEC], dy[VEC];
+        if constexpr (!KEEP) __builtin_amdgcn_sched_barrier(0);  // one piece's weights at a time
+        float n[VEC], dy[VEC], wi[VEC];
         values(u, i, n, dy);
+        weights(i, wi);
+        if constexpr (FAR) {  // one row at a time, which is there
+#pragma unroll
+          for (int q = 0; q < VEC / 4; ++q) {
+            float4& to = far[(i * (VEC / 4) + q) * kThreads + threadIdx.x];
+            float4 v = to;
+            v.x += dy[4 * q] * n[4 * q];
+            v.y += dy[4 * q + 1] * n[4 * q + 1];
+            v.z += dy[4 * q + 2] * n[4 * q + 2];
+            v.w += dy[4 * q + 3] * n[4 * q + 3];
+            to = v;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          dw[i][e] += cur.ok[u] ? dy[e] * n[e] : 0.0f;
+          if constexpr (!FAR) dw[i][e] += cur.ok[u] ? dy[e] * n[e] : 0.0f;
           db[i][e] += cur.ok[u] ? dy[e] : 0.0f;
-          const float t = w[i][e] * dy[e];
-          sum[2 * u] += at.has[i] ? t : 0.0f;
-          sum[2 * u + 1] += at.has[i] ? t * n[e] : 0.0f;
+          const float t = wi[e] * dy[e];
+          sum[2 * u] += at.once(i, e, t);
+          sum[2 * u + 1] += at.once(i, e, t * n[e]);
         }
       }
     }
@@ -361,15 +414,24 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_bwd_kernel(LnArgs a) 
       const float m1 = sum[2 * u] * inv, m2 = sum[2 * u + 1] * inv;
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
-        float n[VEC], d[VEC], q[VEC];
+        if constexpr (!KEEP) __builtin_amdgcn_sched_barrier(0);
+        float n[VEC], d[VEC], q[VEC], wi[VEC];
         values(u, i, n, d);
+        weights(i, wi);
         if constexpr (RES) P::get(cur.r[2][u][i], q);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          d[e] = s[u] * (w[i][e] * d[e] - m1 - n[e] * m2);
+          d[e] = s[u] * (wi[e] * d[e] - m1 - n[e] * m2);
           if constexpr (RES) d[e] += q[e];
         }
-        if (at.has[i]) *reinterpret_cast<Raw*>(static_cast<E*>(a.dx) + cur.row[u] * a.ldx + at.col[i]) = P::put(d);
+        E* to = static_cast<E*>(a.dx) + cur.row[u] * a.ldx + at.col[i];
+        if (at.twice[i] == 0) {
+          if (at.has[i]) *reinterpret_cast<typename P::Stored*>(to) = P::put(d);
+        } else {  // one piece of a row: the elements of its own
+#pragma unroll
+          for (int e = 1; e < VEC; ++e)
+            if (e >= at.twice[i]) Elem<E>::st(to, e, d[e]);
+        }
       }
     }
   }
@@ -380,25 +442,33 @@ __global__ __launch_bounds__(max_threads(TPR, UR)) void ln_bwd_kernel(LnArgs a) 
   for (int which = 0; which < 2; ++which) {
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
-      if (at.slots > 1) {
-        __syncthreads();
+      if constexpr (NIT == 1) {
+        if (at.slots > 1) {
+          __syncthreads();
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) cols[e * kThreads + threadIdx.x] = which ? db[i][e] : dw[i][e];
-        __syncthreads();
+          for (int e = 0; e < VEC; ++e) cols[e * kThreads + threadIdx.x] = which ? db[i][e] : dw[i][e];
+          __syncthreads();
+        }
       }
       if (at.slot == 0 && at.has[i]) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float v = which ? db[i][e] : dw[i][e];
-          for (int q = 1; q < at.slots; ++q) v += cols[e * kThreads + q * at.tpr + at.tr];
-          out[which * a.D + at.col[i] + e] = v;
+          float v;
+          if constexpr (FAR) v = which ? db[i][e] : reinterpret_cast<const float*>(&far[(i * (VEC / 4) + e / 4) * kThreads + threadIdx.x])[e % 4];
+          else v = which ? db[i][e] : dw[i][e];
+          if constexpr (NIT == 1)
+            for (int q = 1; q < at.slots; ++q) v += cols[e * kThreads + q * at.tpr + at.tr];
+          if (e >= at.twice[i]) out[which * a.D + at.col[i] + e] = v;
         }
       }
     }
   }
 }
 
-// Rows that no workgroup holds in registers: every sum walks over the row again.
+// Rows that no workgroup holds in registers (see make_plan): every sum walks over the
+// row again, which L2 still has by then.  Bound by those walks: 1500 x 32768 bf16 take
+// 134 us forward (196 MB, 1.5 TB/s) and 379 backward, where dw and db are read and
+// written for every row.
 constexpr int kLongThreads = 1024;
 
 template <typename E>
@@ -520,9 +590,8 @@ constexpr int kWideThreads = 512;  // of a workgroup of wide rows, where one row
 
 Plan make_plan(const ttt_ln_desc& d) {
   const int wide = d.dtype == TTT_BF16 ? 8 : 4;
-  const int64_t ldx = d.ldx ? d.ldx : d.D;
   Plan p{};
-  p.vec = d.D % wide == 0 && ldx % wide == 0 ? wide : 1;
+  p.vec = d.D >= wide ? wide : 1;
   const int pieces = (d.D + p.vec - 1) / p.vec;
   if (pieces <= 64) {
     p.tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
@@ -531,8 +600,11 @@ Plan make_plan(const ttt_ln_desc& d) {
     p.slots = 256 / p.tpr;
     return p;
   }
-  if (p.vec == 1) p.nit = pieces <= 128 ? 1 : pieces <= 4096 ? 4 : 0;
-  else p.nit = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 0;
+  // Pieces of a thread.  More than three of 8 elements (five of 4), held twice in the
+  // backward and with their sums, do not fit in a thread's 128 registers; below that they
+  // are the faster way, also where the compiler keeps some in scratch: both directions of
+  // 3000 x 19992 bf16 242 us, by the long kernels 875.
+  p.nit = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : pieces <= 3072 ? 3 : pieces <= 5120 && d.dtype == TTT_F32 ? 5 : 0;
   if (!p.nit) {
     p.slots = 1;
     p.threads = kLongThreads;
@@ -544,12 +616,13 @@ Plan make_plan(const ttt_ln_desc& d) {
   return p;
 }
 
-// Workgroups of each group: enough for every CU to hold several, and no more than
-// there are rows for (`unroll` of them a step).
+// Workgroups of each group: enough for every CU to hold several, one at least (backward
+// of 7000 x 8192 bf16 with 1024 threads: 128 workgroups 114 us, 256 76), and no more
+// than there are rows for (`unroll` of them a step).
 int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int threads_per_cu) {
   const int64_t per_group = d.rows / d.groups;
   const int64_t steps = (per_group + p.slots * unroll - 1) / (p.slots * unroll);
-  const int64_t want = (static_cast<int64_t>(256) * threads_per_cu / p.threads + d.groups - 1) / d.groups;
+  const int64_t want = (static_cast<int64_t>(256) * std::max(threads_per_cu / p.threads, 1) + d.groups - 1) / d.groups;
   const int64_t n = steps < want ? steps : want;
   return static_cast<int>(n > 0 ? n : 1);
 }
@@ -588,6 +661,7 @@ template <bool FWD, typename F> hipError_t dispatch(const ttt_ln_desc& d, const 
   };
   auto with_plan = [&](auto e, auto vec) {
     std::integral_constant<int, 1> one;
+    if constexpr (vec() == 1) return with_rows(e, vec, std::integral_constant<int, 8>{}, one);  // D below 8
     switch (p.tpr) {
       case 8: return with_rows(e, vec, std::integral_constant<int, 8>{}, one);
       case 16: return with_rows(e, vec, std::integral_constant<int, 16>{}, one);
@@ -595,7 +669,11 @@ template <bool FWD, typename F> hipError_t dispatch(const ttt_ln_desc& d, const 
       case 64: return with_rows(e, vec, std::integral_constant<int, 64>{}, one);
     }
     std::integral_constant<int, 0> group;
-    if (p.nit > 1) return with_rows(e, vec, group, std::integral_constant<int, vec() == 1 ? 4 : 2>{});
+    if constexpr (std::is_same_v<decltype(e), float>) {
+      if (p.nit == 5) return with_rows(e, vec, group, std::integral_constant<int, 5>{});
+    }
+    if (p.nit == 3) return with_rows(e, vec, group, std::integral_constant<int, 3>{});
+    if (p.nit == 2) return with_rows(e, vec, group, std::integral_constant<int, 2>{});
     return with_rows(e, vec, group, one);
   };
   auto one = std::integral_constant<int, 1>{};

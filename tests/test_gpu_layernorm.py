@@ -185,6 +185,42 @@ def test_strided_rows_and_residual_in_place():
         assert torch.equal(same.y, apart.y) and torch.equal(stream, apart.r)
 
 
+@pytest.mark.parametrize("D,dtype", [(9, "bf16"), (5, "f32"), (515, "bf16"), (1027, "bf16"), (8191, "bf16"), (8193, "bf16"),
+                                     (16385, "bf16"), (24575, "bf16"), (24577, "bf16"), (4099, "f32"), (8194, "f32"),
+                                     (12291, "f32"), (20479, "f32"), (20481, "f32")])
+def test_rows_that_end_inside_a_piece(D, dtype):
+    """The last piece of a row reaches back over its neighbour: each element counts once and
+    is kept, with rows beyond the first of a workgroup and the residual stream in place."""
+    import torch
+    rows = 300 if D > 64 else 9001
+    out = _run(rows, D, dtype, residual=True, seed=10)
+    rng = np.random.default_rng(10)
+    x, res = rounded(rng, (rows, D), dtype, mean=0.5, std=2.0).cuda(), rounded(rng, (rows, D), dtype).cuda()
+    w, b = rounded(rng, (1, D), "f32", mean=1.0, std=0.3).cuda(), rounded(rng, (1, D), "f32").cuda()
+    kept, y = (x.float() + res.float()).to(x.dtype), torch.empty_like(x)
+    B.ttt_layernorm_fwd(B.make_ln_desc(rows, D, dtype=dtype, eps=EPS), x, res, w, b, y, res, None, None)
+    assert torch.equal(y, out["y"]) and torch.equal(res, kept)
+
+
+@pytest.mark.parametrize("D", [33, 1001, 20001])
+def test_infinity_in_the_last_columns(D):
+    """An infinity where two pieces overlap: the mean is infinite, not NaN, and other rows are untouched."""
+    import torch
+    rng = np.random.default_rng(11)
+    x = rounded(rng, (5, D), "bf16")
+    desc = B.make_ln_desc(5, D)
+    means = []
+    for bad in (None, 0, D - 1, D - 2, D - 7):
+        v = x.clone()
+        if bad is not None:
+            v[2, bad] = float("inf")
+        mean, y = torch.empty(5, device="cuda"), torch.empty_like(v, device="cuda")
+        B.ttt_layernorm_fwd(desc, v.cuda(), None, None, None, y, None, mean, None)
+        means.append(mean.cpu())
+    for m in means[1:]:
+        assert m[2] == float("inf") and torch.equal(m[[0, 1, 3, 4]], means[0][[0, 1, 3, 4]])
+
+
 def test_repeats_to_the_bit():
     import torch
     a = _run(9000, 128, "bf16", groups=4, period=750, seed=7)

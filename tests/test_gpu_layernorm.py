@@ -252,6 +252,29 @@ def test_offsets_past_32_bits():
     assert worst(dw, g["dw"], g["e_dw"], "f32") <= 1 and worst(db, g["db"], g["e_db"], "f32") <= 1
 
 
+def test_a_weight_of_many_groups():
+    """More columns of dw and db than one launch of the reduction has workgroups for: two rows a group."""
+    import torch
+    G, D = 1 << 20, 72
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    x, dy = (torch.randn(2 * G, D, device="cuda", dtype=torch.bfloat16, generator=gen) for _ in range(2))
+    w = torch.randn(G, D, device="cuda", generator=gen)
+    desc = B.make_ln_desc(2 * G, D, groups=G, eps=EPS)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = (torch.empty(2 * G, device="cuda") for _ in range(2))
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    ws = torch.empty(B.ttt_layernorm_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    B.ttt_layernorm_fwd(desc, x, None, w, None, y, None, mean, rstd)
+    B.ttt_layernorm_bwd(desc, x, w, mean, rstd, dy, None, dx, dw, db, ws)
+    for g0 in (0, 5, 466_000, 466_033, 932_060, G - 4):   # 2^25 columns are 233 016.9 groups' dw and db
+        rows = torch.cat([torch.arange(g0, g0 + 4), torch.arange(G + g0, G + g0 + 4)])
+        part = rows.cuda()
+        want = ln.backward(f64(x[part]), f64(w[g0:g0 + 4]), EPS, f64(dy[part]), None, 4, 1)
+        assert worst(dw[g0:g0 + 4], want["dw"], want["e_dw"], "f32") <= 1
+        assert worst(db[g0:g0 + 4], want["db"], want["e_db"], "f32") <= 1
+        assert worst(dx[part], want["dx"], want["e_dx"], "bf16") <= 1
+
+
 def test_graph_replays():
     import torch
     from chunkwise_weight_recurrence_amd.layer import LayerNormBuffers

@@ -696,8 +696,8 @@ int ttt_recurrence_step(const ttt_rec_desc* desc, const void* x, const void* gat
   if (n_states < 0) return fail(TTT_ERR_INVALID_ARG, "n_states must be >= 0 (got %d)", n_states);
   if (!slots && n_states < desc->B)
     return fail(TTT_ERR_INVALID_ARG, "without slots n_states must be >= B (got %d, %d)", n_states, desc->B);
-  if (static_cast<double>(n_states) * desc->D > 4.0e12)
-    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d states of %d channels)", n_states, desc->D);
+  if (static_cast<double>(n_states) * desc->D > 4.0e12 || !ttt::recurrence_step_grid_fits(*desc))
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d rows, %d states of %d channels)", desc->B, n_states, desc->D);
   if (desc->B == 0) return ok();
   if (!x || !gate || !h || !o) return fail(TTT_ERR_INVALID_ARG, "x, gate, h and o are required");
   if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"slots", slots}, {"h", h}, {"o", o}}))

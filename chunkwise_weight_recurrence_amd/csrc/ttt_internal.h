@@ -160,6 +160,7 @@ hipError_t mlp_bwd_launch(const ttt_mlp_desc& d, const void* q, const void* k, c
 
 // ---- gated linear recurrence (ttt_recurrence.hip) ----
 bool recurrence_grid_fits(const ttt_rec_desc& d);
+bool recurrence_step_grid_fits(const ttt_rec_desc& d);
 size_t recurrence_workspace(const ttt_rec_desc& d, int entry);
 size_t recurrence_saved(const ttt_rec_desc& d);
 hipError_t recurrence_fwd_launch(const ttt_rec_desc& d, const void* x, const void* gate, const float* h0,

@@ -266,7 +266,7 @@ template <int LW> __device__ __forceinline__ Bits tile_meta(const RecArgs& a, in
       m.lo = max(t0, a.starts[0]);
       m.hi = min(min(t0 + kTile, a.n), a.starts[a.B]);
       m.first = min(max(a.starts[s0], 0), t0);
-      m.last = sl < 0 || sl >= a.B ? tl : min(max(a.starts[sl + 1] - 1, tl), max(a.n - 1, tl));
+      m.last = sl < 0 || sl >= a.B ? tl : min(max(a.starts[sl + 1], tl + 1) - 1, max(a.n - 1, tl));
     }
   }
   __syncthreads();
@@ -908,8 +908,14 @@ RecArgs make_args(const ttt_rec_desc& d, int V, int tile) {
 
 }  // namespace
 
+constexpr int64_t kMaxLaunch = int64_t{1} << 32;  // a launch has fewer threads
+
+bool recurrence_step_grid_fits(const ttt_rec_desc& d) {
+  return d.B * ((static_cast<int64_t>(d.D) + kStepThreads - 1) / kStepThreads) * kStepThreads < kMaxLaunch;
+}
+
 bool recurrence_grid_fits(const ttt_rec_desc& d) {
-  return tiles(d, kBwdTile) * ((static_cast<int64_t>(d.D) + 63) / 64) < (int64_t{1} << 31);
+  return tiles(d, kBwdTile) * ((static_cast<int64_t>(d.D) + 63) / 64) * kThreads < kMaxLaunch;
 }
 
 namespace {

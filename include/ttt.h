@@ -461,14 +461,17 @@ typedef enum { TTT_REC_PLAIN = 0, TTT_REC_CONVEX = 1 } ttt_rec_input;
 
 typedef struct {
   int32_t B;      /* sequences (rows of one token each for ttt_recurrence_step) */
-  int32_t T;      /* tokens of each sequence; packed: token rows of the buffers */
-  int32_t D;      /* channels, >= 1; per-head channels [B,H,T,d] are B*H sequences of d */
+  int32_t T;      /* tokens of each sequence; packed: token rows of the buffers; in
+                     all below 2^31 - 4096, and tokens / 128 times D / 64, each
+                     rounded up, below 2^23                                     */
+  int32_t D;      /* channels, 1 .. 2^23; per-head channels [B,H,T,d] are B*H sequences of d */
   int32_t packed; /* 0: x is [B,T,D]; 1: x is [T,D], the sequences one behind the other */
   int32_t dtype;  /* ttt_dtype of x, gate, o and their gradients                */
   int32_t gate;   /* ttt_rec_gate                                               */
   int32_t input;  /* ttt_rec_input                                              */
   int32_t reserved; /* 0                                                        */
-  int64_t ldx;    /* elements from one token's x (and dx) to the next; 0 means D */
+  int64_t ldx;    /* elements from one token's x (and dx) to the next, up to 2^23;
+                     0 means D                                                  */
   int64_t ldg;    /* the same for gate (and dgate)                              */
 } ttt_rec_desc;
 
@@ -484,7 +487,8 @@ TTT_API int ttt_recurrence_workspace_size(const ttt_rec_desc* desc, int entry, s
 TTT_API int ttt_recurrence_saved_size(const ttt_rec_desc* desc, size_t* bytes);
 
 /*
- * ttt_recurrence_fwd -- the recurrence over whole sequences.
+ * ttt_recurrence_fwd -- the recurrence over whole sequences.  Outputs overlap neither
+ * inputs nor each other (so in all of these entry points, where nothing else is said).
  *   x, gate    [B,T,D] or [T,D] dtype, rows ldx / ldg apart
  *   h0         [B,D] f32 or NULL (zero)
  *   seq_starts DEVICE array [B+1] int32, ascending (packed only, else NULL):
@@ -544,7 +548,7 @@ typedef struct {
   int64_t rows;   /* 0 .. 2^31 - 1; a multiple of groups * period when groups > 1 */
   int64_t ldx;    /* elements from one row of x (and dx) to the next; 0 means D   */
   int32_t D;      /* 1 .. 2^24                                                    */
-  int32_t groups; /* >= 1                                                         */
+  int32_t groups; /* 1 .. 2^20, groups * D up to 10^9                             */
   int32_t period; /* >= 1                                                         */
   int32_t dtype;  /* ttt_dtype of x, res, y, r and their gradients                */
   float eps;      /* added to the variance, >= 0                                  */
@@ -556,7 +560,8 @@ typedef struct {
  *   y = (r - mean(r)) / sqrt(var(r) + eps) * w_g + b_g    (var over D, biased)
  *   x       [rows,D] dtype, rows ldx apart
  *   res     [rows,D] dtype or NULL;  r [rows,D] dtype (written; required with res,
- *           else NULL).  r may be res: the residual stream is then updated in place
+ *           else NULL).  r may be res: the residual stream is then updated in place.
+ *           No other output overlaps an input or another output
  *   w, b    [groups,D] f32, each may be NULL (1 and 0)
  *   y       [rows,D] dtype (written)
  *   mean, rstd  [rows] f32 or NULL (written: mean(r) and 1 / sqrt(var(r) + eps))

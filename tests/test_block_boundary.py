@@ -60,6 +60,8 @@ def test_enums_match_header():
     (dict(ldx=63), -1, "ldx, ldg"), (dict(ldg=1), -1, "ldx, ldg"), (dict(ldx=-64), -1, "ldx, ldg"),
     (dict(B=1 << 16, T=1 << 15), -2, "too large"), (dict(D=(1 << 24) + 1), -2, "too large"),
     (dict(ldx=1 << 40), -2, "too large"), (dict(B=1, T=2_000_000_000, D=1 << 20), -2, "too large"),
+    # a launch has fewer than 2^32 threads
+    (dict(B=1, T=(1 << 30) - 127, D=64), -2, "too large"), (dict(B=1 << 20, T=1, D=(1 << 16) + 64), -2, "too large"),
 ])
 def test_recurrence_desc(L, kw, code, msg):
     d = _rec(**kw)
@@ -110,6 +112,7 @@ def test_step_refusals():
     assert _step(_rec(T=1, packed=True)) == -1
     assert _step(d, n_states=2) == -1 and "n_states" in ttt.ttt_last_error()   # three rows without slots
     assert _step(d, n_states=-1) == -1
+    assert _step(_rec(B=1 << 24, T=1), n_states=1 << 24) == -2 and "too large" in ttt.ttt_last_error()
     for name in ("x", "gate", "h", "o"):
         assert _step(d, **{name: None}) == -1 and "required" in ttt.ttt_last_error()
     assert _step(d, h=FAKE + 8) == -1 and "h must be 16-byte aligned" in ttt.ttt_last_error()

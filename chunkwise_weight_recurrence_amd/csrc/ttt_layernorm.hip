@@ -610,7 +610,8 @@ Plan make_plan(const ttt_ln_desc& d) {
   // backward and with their sums, do not fit in a thread's 128 registers; below that they
   // are the faster way, also where the compiler keeps some in scratch: both directions of
   // 3000 x 19992 bf16 242 us, by the long kernels 875.
-  p.nit = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : pieces <= 3072 ? 3 : pieces <= 5120 && d.dtype == TTT_F32 ? 5 : 0;
+  constexpr int kAll = kLongThreads;  // a piece each
+  p.nit = pieces <= kAll ? 1 : pieces <= 2 * kAll ? 2 : pieces <= 3 * kAll ? 3 : pieces <= 5 * kAll && d.dtype == TTT_F32 ? 5 : 0;
   if (!p.nit) {
     p.slots = 1;
     p.threads = kLongThreads;

@@ -316,3 +316,32 @@ def test_graph_replays():
             both(probs[1 - k])
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(outs(probs[1 - k]), eager[1 - k])), (r, k)
+
+
+def test_two_streams_at_once():
+    """Each with its own workspace; the default stream of the call is the current one."""
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import LayerNormBuffers
+    rng = np.random.default_rng(13)
+    probs = []
+    for rows, D in ((3000, 1000), (20000, 96)):
+        x, dy = (rounded(rng, (rows, D), "bf16").cuda() for _ in range(2))
+        probs.append((LayerNormBuffers(x, rounded(rng, (1, D), "f32").cuda(), with_bwd=True), dy))
+    want = []
+    for p, dy in probs:
+        p.forward()
+        p.backward(dy)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (p.y, p.dx, p.dw, p.db)])
+        for t in (p.y, p.dx, p.dw, p.db):
+            t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in probs]
+    for _ in range(5):
+        for (p, dy), s in zip(probs, streams):
+            with torch.cuda.stream(s):
+                p.forward()
+                p.backward(dy)
+    torch.cuda.synchronize()
+    for (p, _), w in zip(probs, want):
+        assert all(torch.equal(a, b) for a, b in zip((p.y, p.dx, p.dw, p.db), w))

@@ -344,6 +344,33 @@ def test_steps_continue_a_prompt():
     assert worst(torch.cat(outs, 1).reshape(-1, D), want, eo, "bf16") <= 1 and worst(h, hf, ef, "f32") <= 1
 
 
+def test_a_captured_step_reads_its_slots_at_each_replay():
+    """A decode loop: one graph, with other rows, gates and slots for every token, against eager steps."""
+    import torch
+    rows, pool, D = 6, 9, 200
+    inp = _make(16, 5 * rows, pool, D, "bf16", "sigmoid")
+    desc = B.make_rec_desc(rows, 1, D)
+    x, z = (inp[k].view(5, rows, D).cuda() for k in ("x", "z"))
+    slots = torch.tensor([[0, 1, 2, 3, 4, 5], [5, 4, -1, 2, 1, 0], [8, 8, 8, 7, 0, 9], [-1] * 6, [6, 0, 6, 0, 6, 0]],
+                         dtype=torch.int32).cuda()
+    xs, zs, ss = torch.empty_like(x[0]), torch.empty_like(z[0]), torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    h, o = inp["h0"].cuda(), torch.zeros(rows, D, dtype=torch.bfloat16, device="cuda")
+    he, oe = h.clone(), o.clone()
+    B.ttt_recurrence_step(desc, xs, zs, ss, h, o)   # the library is loaded before the capture
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.ttt_recurrence_step(desc, xs, zs, ss, h, o)
+    for t in range(5):
+        xs.copy_(x[t])
+        zs.copy_(z[t])
+        ss.copy_(slots[t])
+        g.replay()
+        row = slots[t].clone()   # its own allocation: a pointer is 16-byte aligned
+        B.ttt_recurrence_step(desc, x[t].clone(), z[t].clone(), row, he, oe)
+        torch.cuda.synchronize()
+        assert torch.equal(h, he) and torch.equal(o, oe), t
+
+
 def test_two_graphs_share_a_workspace_and_replay():
     """Captured forwards and backwards of two problems over one workspace, replayed in turn
     with eager calls of both between them: every replay gives the eager results."""

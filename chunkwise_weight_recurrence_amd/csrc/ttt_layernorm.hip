@@ -12,8 +12,8 @@
 // bf16 166 us, element by element 200, and of 1800000 x 33 220 and 600 us).  Narrow
 // rows take a part of a wave each, wide rows as many waves as they have pieces
 // for.  Measured, where a copy reaches 4.7 to 4.8 TB/s: forward of
-// 32768 x 2560 bf16 with a residual (671 MB) 139 us, both directions of 16384 x 2048
-// bf16 with one (537 MB) 108 us, of 262144 x 128 in 16 groups (340 MB) 77 us.
+// 32768 x 2560 bf16 with a residual (671 MB) 136 us, both directions of 16384 x 2048
+// bf16 with one (537 MB) 103 us, of 262144 x 128 in 16 groups (340 MB) 75 us.
 // A workgroup holds several rows side by side (slots), walks over rows of one
 // group, so that the weights stay in registers, and takes UR rows a slot at a time:
 // they share the barriers of a cross-wave sum, and the loads of the next UR are in
@@ -623,20 +623,33 @@ Plan make_plan(const ttt_ln_desc& d) {
   return p;
 }
 
-// Workgroups of each group: enough for every CU to hold several, one at least (backward
-// of 7000 x 8192 bf16 with 1024 threads: 128 workgroups 114 us, 256 76), and no more
-// than there are rows for (`unroll` of them a step).
-int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int threads_per_cu) {
+// Workgroups a CU, each of which walks over its share of the rows.  The forward has
+// about 1024 lanes a CU that hold a piece: idle lanes do not count, since it is the
+// loads in flight that matter.  32768 x 2560 bf16 with a residual takes 124 us (2048
+// threads 135), 4000 x 1024 14 (20), 50000 x 640 42.0 (42.5; 1024 threads 44),
+// 7000 x 6000 48.8 (rounded down to one 55.5).  Narrow rows take
+// 1024 threads, idle lanes or not: 262144 x 128 34.7 us (2048 threads 36.8), 500000 x 100
+// 42.5 (2048 45.3, 1024 lanes with a piece 47).  Rows that no workgroup holds: 1500 x 32768
+// 135 us with two of 1024 threads, 205 with one.
+int fwd_per_cu(const ttt_ln_desc& d, const Plan& p) {
+  if (p.tpr) return 1024 / p.threads;
+  if (!p.nit) return 2;
+  const int per = p.vec * p.nit, lanes = p.slots * ((d.D + per - 1) / per);
+  return (1024 + lanes - 1) / lanes;
+}
+// The backward's workgroups each write a partial row of dw and db: 512 threads, one
+// workgroup at least.  16384 x 2048 bf16 took 53 us with 512, 58 with 1024 and 67 with
+// 2048; 7000 x 8192 76 with one of 1024 threads on every CU, 114 on every other.
+int bwd_per_cu(const Plan& p) { return std::max(512 / p.threads, 1); }
+
+// Workgroups of each group, no more than there are rows for (`unroll` of them a step).
+int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int per_cu) {
   const int64_t per_group = d.rows / d.groups;
   const int64_t steps = (per_group + p.slots * unroll - 1) / (p.slots * unroll);
-  const int64_t want = (static_cast<int64_t>(256) * std::max(threads_per_cu / p.threads, 1) + d.groups - 1) / d.groups;
+  const int64_t want = (static_cast<int64_t>(256) * per_cu + d.groups - 1) / d.groups;
   const int64_t n = steps < want ? steps : want;
   return static_cast<int>(n > 0 ? n : 1);
 }
-
-// Threads a CU.  The backward's workgroups each write a partial row of dw and db, and
-// 16384 x 2048 bf16 took 53 us with 512, 58 with 1024 and 67 with 2048.
-constexpr int kFwdPerCu = 2048, kBwdPerCu = 512;
 
 // Rows a slot takes at once, where there are enough for every workgroup; few rows go
 // to as many workgroups as there are.  Narrow rows have no barrier to share but short
@@ -652,7 +665,7 @@ int bwd_unroll(const ttt_ln_desc& d, const Plan& p) {
 
 int bwd_slices(const ttt_ln_desc& d) {
   const Plan p = make_plan(d);
-  return slices_of(d, p, bwd_unroll(d, p), kBwdPerCu);
+  return slices_of(d, p, bwd_unroll(d, p), bwd_per_cu(p));
 }
 
 // Calls f with the element type and the plan as compile-time values.
@@ -718,7 +731,7 @@ hipError_t layernorm_fwd_launch(const ttt_ln_desc& d, const void* x, const void*
   LnArgs a = make_args(d);
   a.x = x; a.res = res; a.w = w; a.b = b; a.y = y; a.r = r; a.mean = mean; a.rstd = rstd;
   const int unroll = fwd_unroll(d, p);
-  a.slices = slices_of(d, p, unroll, kFwdPerCu);
+  a.slices = slices_of(d, p, unroll, fwd_per_cu(d, p));
   a.wpr = p.wpr;
   const dim3 grid(static_cast<uint32_t>(a.slices) * a.G);
   KernelScope scope(TTT_KERNEL_LN_FWD, s);

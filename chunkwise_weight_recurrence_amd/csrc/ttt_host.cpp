@@ -585,6 +585,9 @@ int check_rec_desc(const ttt_rec_desc* d) {
   // Token indices are 32-bit, rounded up to whole tiles; a wave's 32 rows lie within 2^30 bytes.
   if (n > (int64_t{1} << 31) - 4096 || d->D > (1 << 23) || !ttt::recurrence_grid_fits(*d))
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens of %d channels)", static_cast<long long>(n), d->D);
+  // Sequences are counted in 32 bits too, a workgroup's stride past the last one included; they may all be empty.
+  if (d->B > INT32_MAX - 4095 || static_cast<double>(d->B) * d->D > 4.0e12)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d sequences of %d channels)", d->B, d->D);
   const int64_t ld = d->ldx > d->ldg ? d->ldx : d->ldg;
   if (ld > (1 << 23) || static_cast<double>(n) * static_cast<double>(ld > d->D ? ld : d->D) > 4.0e12)
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (rows %lld elements apart)", static_cast<long long>(ld));

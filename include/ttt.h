@@ -460,7 +460,8 @@ typedef enum { TTT_GATE_SIGMOID = 0, TTT_GATE_LOG = 1 } ttt_rec_gate;
 typedef enum { TTT_REC_PLAIN = 0, TTT_REC_CONVEX = 1 } ttt_rec_input;
 
 typedef struct {
-  int32_t B;      /* sequences (rows of one token each for ttt_recurrence_step) */
+  int32_t B;      /* sequences (rows of one token each for ttt_recurrence_step), up
+                     to 2^31 - 4096, B * D up to 4e12                           */
   int32_t T;      /* tokens of each sequence; packed: token rows of the buffers; in
                      all below 2^31 - 4096, and tokens / 128 times D / 64, each
                      rounded up, below 2^23                                     */

@@ -71,6 +71,20 @@ def test_recurrence_desc(L, kw, code, msg):
         assert st == code and msg in ttt.ttt_last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=(1 << 31) - 1, packed=True), dict(B=(1 << 31) - 4095, packed=True, D=1), dict(B=(1 << 31) - 4095, T=0, D=1),
+    dict(B=1 << 30, T=0, D=1 << 13), dict(B=1 << 30, D=1 << 13, packed=True),
+])
+def test_recurrence_sequence_count(L, kw):
+    """Sequences without a token are no tokens, but they are indexed in 32 bits as those are."""
+    d, n = _rec(**kw), ctypes.c_size_t(0)
+    p = dict(seq_starts=FAKE) if d.packed else {}
+    for st in (_fwd(d, **p), _bwd(d, **p), L.ttt_recurrence_workspace_size(ctypes.byref(d), 0, ctypes.byref(n)),
+               L.ttt_recurrence_saved_size(ctypes.byref(d), ctypes.byref(n))):
+        assert st == -2 and "too large" in ttt.ttt_last_error()
+    assert _fwd(_rec(B=(1 << 31) - 4096, T=0, D=1)) == 0   # without h_final there is nothing to launch
+
+
 def test_recurrence_pointers_and_workspace(L):
     d, p = _rec(), _rec(packed=True)
     assert _fwd(None) == -1 and "desc is NULL" in ttt.ttt_last_error()

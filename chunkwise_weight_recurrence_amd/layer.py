@@ -231,8 +231,12 @@ class RecurrenceBuffers:
 
     def __init__(self, x, gate, kind="sigmoid", input="convex", h0=None, seq_starts=None, with_bwd=False):
         torch = _torch()
-        D = x.shape[-1]
         packed = seq_starts is not None
+        if x.dim() < (2 if packed else 3) or math.prod(x.shape[:1 if packed else 2]) * x.shape[-1] != x.numel():
+            raise ValueError(f"x must be {'[T,D]' if packed else '[B,T,D]'} (got shape {tuple(x.shape)})")
+        if gate.shape[-1:] != x.shape[-1:] or gate.numel() != x.numel():
+            raise ValueError(f"gate must have x's shape {tuple(x.shape)} (got {tuple(gate.shape)})")
+        D = x.shape[-1]
         Bn, T = (seq_starts.numel() - 1, x.shape[0]) if packed else x.shape[:2]
         self.x, self.gate, self.h0, self.seq_starts = x, gate, h0, seq_starts
         self.desc = B.make_rec_desc(Bn, T, D, dtype="bf16" if x.dtype == torch.bfloat16 else "f32", gate=kind,
@@ -269,6 +273,8 @@ class LayerNormBuffers:
 
     def __init__(self, x, w=None, b=None, res=None, groups=1, period=1, eps=1e-5, with_bwd=False):
         torch = _torch()
+        if res is not None and (res.shape[-1:] != x.shape[-1:] or res.numel() != x.numel()):
+            raise ValueError(f"res must have x's shape {tuple(x.shape)} (got {tuple(res.shape)})")
         D = x.shape[-1]
         rows = x.numel() // D
         f32, d = torch.float32, x.device

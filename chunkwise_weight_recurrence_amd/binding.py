@@ -272,15 +272,24 @@ def make_mlp_desc(B, H, T, dk, dh, dv, C, dtype="bf16", loss="mse", act="gelu", 
                       enum(Decay, decay), float(lr_bias))
 
 
+def _fit32(**sizes):
+    """Raises where ctypes would keep the low 32 bits of a size in silence."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit in 32 bits (got {v})")
+
+
 def make_rec_desc(B, T, D, dtype="bf16", gate="sigmoid", input="convex", packed=False, ldx=0, ldg=0):
     """Build a TTTRecDesc from names ("bf16"/"f32", "sigmoid"/"log", "plain"/"convex")."""
     def enum(cls, x):
         return int(cls[x.upper()]) if isinstance(x, str) else int(x)
+    _fit32(B=B, T=T, D=D)
     return TTTRecDesc(B, T, D, int(packed), enum(DType, dtype), enum(Gate, gate), enum(RecInput, input), 0, ldx, ldg)
 
 
 def make_ln_desc(rows, D, dtype="bf16", groups=1, period=1, eps=1e-5, ldx=0):
     """Build a TTTLnDesc; ``dtype`` by name ("bf16"/"f32")."""
+    _fit32(D=D, groups=groups, period=period)
     return TTTLnDesc(rows, ldx, D, groups, period, int(DType[dtype.upper()]) if isinstance(dtype, str) else int(dtype),
                      float(eps), 0)
 
@@ -559,6 +568,8 @@ def ttt_recurrence_step(desc, x, gate, slots, h, o, n_states=None, stream=None):
     dt, dev, n, D = _io_type(desc), _device(x), desc.B, desc.D
     if n_states is None:
         n_states = h.numel() // D if hasattr(h, "numel") and D > 0 else 0
+    if not -2 ** 31 <= n_states < 2 ** 31:
+        _fit32(n_states=n_states)
     _call(lib().ttt_recurrence_step, dev, stream, ctypes.byref(desc), _arg("x", x, dev, dt, n, D, desc.ldx),
           _arg("gate", gate, dev, dt, n, D, desc.ldg), _arg("slots", slots, dev, i32, 1, n), n_states,
           _arg("h", h, dev, f32, n_states, D), _arg("o", o, dev, dt, n, D))

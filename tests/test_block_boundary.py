@@ -213,3 +213,19 @@ def test_binding_refuses_tensors_that_would_fault():
     with pytest.raises(ValueError, match="w has 64 elements, 128 are needed"):
         y = torch.zeros(12, 64, dtype=torch.bfloat16)
         ttt.ttt_layernorm_fwd(_ln(groups=2), f(y), None, f(torch.zeros(64)), None, f(y), None, None, None)
+
+
+def test_sizes_past_32_bits_are_refused_not_cut():
+    """A field of a descriptor would keep the low 32 bits: 2^32 + 128 tokens were 128."""
+    big = (1 << 32) + 128
+    for name in ("B", "T", "D"):
+        with pytest.raises(ValueError, match=f"{name} must fit in 32 bits"):
+            _rec(**{name: big})
+    for name in ("D", "groups", "period"):
+        with pytest.raises(ValueError, match=f"{name} must fit in 32 bits"):
+            _ln(**{name: big})
+    with pytest.raises(ValueError, match="T must fit in 32 bits"):
+        _rec(T=-(1 << 32))
+    assert _ln(rows=big).rows == big
+    with pytest.raises(ValueError, match="n_states must fit in 32 bits"):
+        ttt.ttt_recurrence_step(_rec(T=1), FAKE, FAKE, None, FAKE, FAKE, n_states=(1 << 32) + 3)

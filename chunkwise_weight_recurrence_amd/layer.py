@@ -222,6 +222,15 @@ class InplaceBuffers:
                               self.w, self.o, self.ws, self.ws_bytes, stream=stream)
 
 
+def _row_distance(x):
+    """Elements from one row of ``x`` ([..., D]) to the next: the stride of its innermost leading axis of more than one."""
+    if x.numel() > 0:
+        for i in range(x.dim() - 2, -1, -1):
+            if x.shape[i] > 1:
+                return x.stride(i)
+    return x.shape[-1]
+
+
 class RecurrenceBuffers:
     """Outputs and workspace of the gated linear recurrence over x and gate ([B,T,D], or packed [T,D]).
 
@@ -240,8 +249,7 @@ class RecurrenceBuffers:
         Bn, T = (seq_starts.numel() - 1, x.shape[0]) if packed else x.shape[:2]
         self.x, self.gate, self.h0, self.seq_starts = x, gate, h0, seq_starts
         self.desc = B.make_rec_desc(Bn, T, D, dtype="bf16" if x.dtype == torch.bfloat16 else "f32", gate=kind,
-                                    input=input, packed=packed, ldx=x.stride(-2) if x.shape[-2] > 1 else D,
-                                    ldg=gate.stride(-2) if gate.shape[-2] > 1 else D)
+                                    input=input, packed=packed, ldx=_row_distance(x), ldg=_row_distance(gate))
         d = x.device
         self.o = torch.empty(x.shape, dtype=x.dtype, device=d)
         self.h_final = torch.empty((Bn, D), dtype=torch.float32, device=d)
@@ -280,8 +288,7 @@ class LayerNormBuffers:
         f32, d = torch.float32, x.device
         self.x, self.w, self.b, self.res = x, w, b, res
         dtype = "bf16" if x.dtype == torch.bfloat16 else "f32"
-        ld = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else D
-        self.desc = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=eps, ldx=ld)
+        self.desc = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=eps, ldx=_row_distance(x))
         # the backward reads the rows that were normalised: the dense r where there is a residual
         self.desc_bwd = self.desc if res is None else B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period,
                                                                      eps=eps)

@@ -30,3 +30,16 @@ def test_layer_norm_takes_a_residual_of_its_own_shape_only():
         LayerNormBuffers(_zeros(2, 5, 8), res=_zeros(2, 6, 8))
     for shape in ((2, 5, 8), (10, 8)):
         assert LayerNormBuffers(_zeros(2, 5, 8), res=_zeros(*shape)).desc.rows == 10
+
+
+def test_the_row_distance_of_any_strided_view():
+    wide = _zeros(3, 6, 40)
+    for rows, ld in ((wide[..., :16], 40), (wide[:, :1, :16], 240), (wide[:, 5:, 8:24], 240), (wide[1:2, :, :16], 40),
+                     (wide[1:2, 3:4, :16], 16), (wide[:, ::2, :16], 80), (wide[:, :0, :16], 16), (_zeros(3, 1, 16), 16)):
+        buf = RecurrenceBuffers(rows, rows, with_bwd=True)
+        assert (buf.desc.ldx, buf.desc.ldg) == (ld, ld) and buf.dx.stride() == rows.stride() == buf.dgate.stride()
+        norm = LayerNormBuffers(rows, with_bwd=True)
+        assert norm.desc.ldx == ld and norm.dx.stride() == rows.stride()
+    d = RecurrenceBuffers(wide[:, :1, :16], _zeros(3, 1, 16)).desc   # one of them strided
+    assert (d.ldx, d.ldg) == (240, 16)
+    assert LayerNormBuffers(_zeros(16)).desc.ldx == 16 and LayerNormBuffers(wide[0, :, :16]).desc.ldx == 40

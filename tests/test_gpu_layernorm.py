@@ -345,3 +345,25 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (p, _), w in zip(probs, want):
         assert all(torch.equal(a, b) for a, b in zip((p.y, p.dx, p.dw, p.db), w))
+
+
+def test_single_strided_tokens():
+    """[B,1,D] views of a wider tensor: the rows' distance is that of the batch axis."""
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import LayerNormBuffers
+    rng = np.random.default_rng(14)
+    for Bn, T, D, room in ((7, 4, 64, 200), (3, 2, 33, 47)):
+        wide = torch.full((Bn, T, room), float("nan"), dtype=torch.bfloat16, device="cuda")
+        x = wide[:, :1, :D]
+        x.copy_(rounded(rng, (Bn, 1, D), "bf16"))
+        w, dy = rounded(rng, (1, D), "f32").cuda(), rounded(rng, (Bn, 1, D), "bf16").cuda()
+        buf = LayerNormBuffers(x, w, with_bwd=True)
+        dwide = torch.full_like(wide, 7.0)
+        buf.dx = dwide[:, :1, :D]
+        buf.forward()
+        buf.backward(dy)
+        f = ln.forward(f64(x).reshape(Bn, D), f64(w), None, EPS)
+        g = ln.backward(f64(x).reshape(Bn, D), f64(w), EPS, f64(dy).reshape(Bn, D))
+        assert worst(buf.y.reshape(Bn, D), f["y"], f["e_y"], "bf16") <= 1
+        assert worst(buf.dx.reshape(Bn, D), g["dx"], g["e_dx"], "bf16") <= 1 and worst(buf.dw, g["dw"], g["e_dw"], "f32") <= 1
+        assert (dwide[:, 1:] == 7.0).all() and (dwide[..., D:] == 7.0).all()

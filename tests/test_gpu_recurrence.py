@@ -443,3 +443,23 @@ def test_unsorted_starts_stay_inside_the_buffers():
     for starts in ([0, 900, 100, 1000], [1000, 500, 0, 200], [-50, 2000, -7, 5000], [2 ** 31 - 1, -2 ** 31, 0, 3]):
         inp = _make(40, n, 3, D, "bf16", "sigmoid")
         _train(inp, "sigmoid", "convex", "bf16", starts=starts)
+
+
+def test_single_strided_tokens():
+    """[B,1,D] views of a projection: the rows' distance is that of the batch axis."""
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import RecurrenceBuffers
+    Bn, T, D = 5, 3, 48
+    inp = _make(60, Bn, Bn, D, "bf16", "sigmoid")
+    both = torch.full((Bn, T, 2 * D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x, z = both[:, :1, :D], both[:, :1, D:]
+    x.copy_(inp["x"].view(Bn, 1, D))
+    z.copy_(inp["z"].view(Bn, 1, D))
+    buf = RecurrenceBuffers(x, z, h0=inp["h0"].cuda(), with_bwd=True)
+    dboth = torch.full_like(both, 7.0)
+    buf.dx, buf.dgate = dboth[:, :1, :D], dboth[:, :1, D:]
+    buf.forward()
+    buf.backward(inp["d_o"].view(Bn, 1, D).cuda(), inp["d_hf"].cuda())
+    out = dict(o=buf.o.view(Bn, D), h_final=buf.h_final, dh0=buf.dh0, dx=buf.dx.reshape(Bn, D), dgate=buf.dgate.reshape(Bn, D))
+    _check(inp, out, rec.dense_starts(Bn, 1), "sigmoid", "convex", "bf16")
+    assert (dboth[:, 1:] == 7.0).all()

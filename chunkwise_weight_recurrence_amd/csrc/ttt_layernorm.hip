@@ -681,20 +681,23 @@ template <bool FWD, typename F> hipError_t dispatch(const ttt_ln_desc& d, const 
   };
   auto with_plan = [&](auto e, auto vec) {
     std::integral_constant<int, 1> one;
-    if constexpr (vec() == 1) return with_rows(e, vec, std::integral_constant<int, 8>{}, one);  // D below 8
-    switch (p.tpr) {
-      case 8: return with_rows(e, vec, std::integral_constant<int, 8>{}, one);
-      case 16: return with_rows(e, vec, std::integral_constant<int, 16>{}, one);
-      case 32: return with_rows(e, vec, std::integral_constant<int, 32>{}, one);
-      case 64: return with_rows(e, vec, std::integral_constant<int, 64>{}, one);
+    if constexpr (vec() == 1) {  // fewer columns than a piece has
+      return with_rows(e, vec, std::integral_constant<int, 8>{}, one);
+    } else {
+      switch (p.tpr) {
+        case 8: return with_rows(e, vec, std::integral_constant<int, 8>{}, one);
+        case 16: return with_rows(e, vec, std::integral_constant<int, 16>{}, one);
+        case 32: return with_rows(e, vec, std::integral_constant<int, 32>{}, one);
+        case 64: return with_rows(e, vec, std::integral_constant<int, 64>{}, one);
+      }
+      std::integral_constant<int, 0> group;
+      if constexpr (std::is_same_v<decltype(e), float>) {
+        if (p.nit == 5) return with_rows(e, vec, group, std::integral_constant<int, 5>{});
+      }
+      if (p.nit == 3) return with_rows(e, vec, group, std::integral_constant<int, 3>{});
+      if (p.nit == 2) return with_rows(e, vec, group, std::integral_constant<int, 2>{});
+      return with_rows(e, vec, group, one);
     }
-    std::integral_constant<int, 0> group;
-    if constexpr (std::is_same_v<decltype(e), float>) {
-      if (p.nit == 5) return with_rows(e, vec, group, std::integral_constant<int, 5>{});
-    }
-    if (p.nit == 3) return with_rows(e, vec, group, std::integral_constant<int, 3>{});
-    if (p.nit == 2) return with_rows(e, vec, group, std::integral_constant<int, 2>{});
-    return with_rows(e, vec, group, one);
   };
   auto one = std::integral_constant<int, 1>{};
   if (d.dtype == TTT_BF16) return p.vec == 8 ? with_plan(bf16_t{}, std::integral_constant<int, 8>{}) : with_plan(bf16_t{}, one);

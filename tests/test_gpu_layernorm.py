@@ -49,7 +49,7 @@ def _run(rows, D, dtype, groups=1, period=1, residual=False, affine=True, seed=0
     return out
 
 
-# narrow rows (a part of a wave), a whole wave, several waves, two and four pieces a thread
+# narrow rows (a part of a wave), a whole wave, several waves; one piece a thread in each
 WIDTHS = [1, 2, 7, 8, 16, 24, 63, 64, 65, 128, 130, 256, 500, 512, 513, 520, 1000, 1001, 1024, 2048, 2560, 4000]
 
 
@@ -66,6 +66,7 @@ def test_wide_rows(D, dtype):
     _run(5, D, dtype, residual=D % 2 == 0)
 
 
+# One row of a slot at a time: several at a time need 4096 rows a slot (test_rows_of_a_slot_together).
 @pytest.mark.parametrize("rows,D,dtype", [(20000, 24, "bf16"), (9001, 128, "bf16"), (5003, 520, "f32"), (8200, 33, "f32")])
 def test_many_rows(rows, D, dtype):
     """Several steps of a workgroup, four rows at a time, a ragged last one."""
@@ -367,3 +368,63 @@ def test_single_strided_tokens():
         assert worst(buf.y.reshape(Bn, D), f["y"], f["e_y"], "bf16") <= 1
         assert worst(buf.dx.reshape(Bn, D), g["dx"], g["e_dx"], "bf16") <= 1 and worst(buf.dw, g["dw"], g["e_dw"], "f32") <= 1
         assert (dwide[:, 1:] == 7.0).all() and (dwide[..., D:] == 7.0).all()
+
+
+# From 4096 rows a slot on (slots: 256 threads over the lanes of a narrow row, 512 over a wide one's), a slot takes
+# several rows at a time: narrow forwards four, others two.  Each case here has more steps than workgroups, so that
+# rows loaded ahead are used, and its last step is ragged.
+TOGETHER = [("bf16", 150001, 24, 1, 1, 0, True), ("bf16", 70007, 128, 1, 1, 0, False), ("bf16", 40007, 200, 1, 1, 0, True),
+            ("bf16", 20003, 300, 1, 1, 0, True), ("bf16", 150001, 5, 1, 1, 0, True), ("f32", 70001, 63, 1, 1, 0, True),
+            ("bf16", 17003, 520, 1, 1, 0, True), ("bf16", 8301, 2048, 1, 1, 0, True), ("bf16", 4501, 2560, 1, 1, 0, True),
+            ("f32", 17003, 261, 1, 1, 0, False), ("f32", 4501, 2000, 1, 1, 0, True),
+            # a weight for each group, rows apart (their residual stream in place)
+            ("bf16", 3 * 11 * 4001, 24, 3, 11, 40, True), ("bf16", 4 * 100 * 43, 520, 4, 100, 528, True),
+            ("bf16", 3 * 7 * 3301, 128, 3, 7, 144, False), ("bf16", 4 * 43 * 101, 523, 4, 101, 531, False)]
+
+
+@pytest.mark.parametrize("dtype,rows,D,groups,period,ldx,residual", TOGETHER)
+def test_rows_of_a_slot_together(dtype, rows, D, groups, period, ldx, residual):
+    """Every row against the oracle.  dy is whole numbers, so db's sums are exact in fp32 whatever their order, and one
+    row too many or too few shows; dw's are off by at most the additions that a product passes through."""
+    import torch
+    rng = np.random.default_rng(15)
+    ld = ldx or D
+    wide = torch.full((rows, ld), float("nan"), dtype=torch_dtype(dtype), device="cuda")
+    x = wide[:, :D]
+    x.copy_(rounded(rng, (rows, D), dtype, mean=0.5, std=2.0))
+    res = rounded(rng, (rows, D), dtype).cuda() if residual else None
+    kept = (x.float() + res.float()).to(x.dtype) if residual else x
+    w, b = rounded(rng, (groups, D), "f32", mean=1.0, std=0.3).cuda(), rounded(rng, (groups, D), "f32").cuda()
+    dy = torch.from_numpy(rng.integers(-3, 4, (rows, D)).astype(np.float32)).to(x.dtype).cuda()
+    dr = rounded(rng, (rows, D), dtype).cuda() if residual else None
+    nan = float("nan")
+    y = torch.full((rows, D), nan, dtype=x.dtype, device="cuda")
+    mean, rstd = (torch.full((rows,), nan, device="cuda") for _ in range(2))
+    dw, db = (torch.full((groups, D), nan, device="cuda") for _ in range(2))
+    desc = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=EPS, ldx=ldx)
+    back = B.make_ln_desc(rows, D, dtype=dtype, groups=groups, period=period, eps=EPS) if residual else desc
+    dwide = torch.full((rows, D if residual else ld), 7.0, dtype=x.dtype, device="cuda")
+    dx = dwide[:, :D]
+    ws = torch.full((B.ttt_layernorm_workspace_size(back),), 255, dtype=torch.uint8, device="cuda")
+    B.ttt_layernorm_fwd(desc, x, res, w, b, y, res, mean, rstd)
+    B.ttt_layernorm_bwd(back, res if residual else x, w, mean, rstd, dy, dr, dx, dw, db, ws)
+    torch.cuda.synchronize()
+    if residual:
+        assert torch.equal(res, kept)
+    assert (dwide[:, D:] == 7.0).all()
+    r = f64(kept)
+    f = ln.forward(r, f64(w), f64(b), EPS, groups, period)
+    g = ln.backward(r, f64(w), EPS, f64(dy), f64(dr) if residual else None, groups, period)
+    errs = dict(y=worst(y, f["y"], f["e_y"], dtype), mean=worst(mean, f["mean"], f["e_mean"], "f32"),
+                rstd=worst(rstd, f["rstd"], f["e_rstd"], "f32"), dx=worst(dx, g["dx"], g["e_dx"], dtype))
+    # A thread adds at most 18 rows here (as many as its slot has of the workgroup's), the workgroup 32 slots, the
+    # reduction 512 / 32 partial rows a thread and then 32 threads' sums; the product itself is rounded once.
+    ops = 18 + 32 + 16 + 32 + 1
+    at = ln.groups_of(rows, groups, period)
+    size, off = (np.zeros((groups, D)) for _ in range(2))
+    for k in range(groups):
+        size[k] = np.abs(f64(dy)[at == k] * f["n"][at == k]).sum(0)
+        off[k] = (np.abs(f64(dy)[at == k]) * f["e_n"][at == k]).sum(0)
+    errs["dw"] = worst(dw, g["dw"], off + ops * ln.U * size, "f32")
+    assert all(e <= 1.0 for e in errs.values()), errs
+    assert np.array_equal(f64(db), g["db"])

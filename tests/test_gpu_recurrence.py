@@ -8,7 +8,7 @@ import pytest
 
 from chunkwise_weight_recurrence_amd import binding as B
 from oracle import recurrence_oracle as rec
-from tests.block_utils import f64, rounded, torch_dtype, worst
+from tests.block_utils import HALF, f64, rounded, torch_dtype, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -463,3 +463,58 @@ def test_single_strided_tokens():
     out = dict(o=buf.o.view(Bn, D), h_final=buf.h_final, dh0=buf.dh0, dx=buf.dx.reshape(Bn, D), dgate=buf.dgate.reshape(Bn, D))
     _check(inp, out, rec.dense_starts(Bn, 1), "sigmoid", "convex", "bf16")
     assert (dboth[:, 1:] == 7.0).all()
+
+
+def _exact_inputs(n, S, D, dtype, seed, halvings=8):
+    """Inputs whose every state, gradient and map is exact in fp32 in whatever order it is formed: whole numbers as x
+    and d_o, gates that keep everything (a = 1) but for a few tokens a channel where a is a half.  Made on the GPU."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def whole(*shape, dt=torch_dtype(dtype)):
+        return torch.randint(-2, 3, shape, generator=gen, device="cuda").to(dt)
+
+    z = torch.full((n, D), float("inf"), dtype=torch_dtype(dtype), device="cuda")
+    z.scatter_(0, torch.randint(0, n, (halvings, D), generator=gen, device="cuda"), 0.0)
+    return dict(x=whole(n, D), z=z, h0=whole(S, D, dt=torch.float32), d_o=whole(n, D), d_hf=whole(S, D, dt=torch.float32))
+
+
+# Sequences over more than three groups of 32 tiles, so that maps of whole groups are read: a dense one, two of them, and
+# packed ones whose long sequence begins and ends inside a group.  The last two have enough tiles for the forward's larger.
+@pytest.mark.parametrize("dtype,D,starts", [
+    ("bf16", 200, [0, 13000]), ("bf16", 201, [0, 13000]), ("f32", 130, [0, 13000]), ("f32", 67, [0, 13000, 26000]),
+    ("bf16", 66, [0, 700, 25111, 25111, 26000]), ("bf16", 35, [300, 1000, 1001, 25000]),
+    ("bf16", 2600, [0, 26000]), ("bf16", 2601, [0, 700, 25711, 26000]),
+])
+def test_a_long_way_back_is_exact(dtype, D, starts):
+    """A map left out, read twice or in another place shows in every later token: nothing here is rounded but outputs."""
+    import torch
+    n, S = starts[-1], len(starts) - 1
+    inp = _exact_inputs(n, S, D, dtype, seed=70)
+    T = n // S
+    runs = [dict(starts=starts)] + ([dict(B_=S, T=T)] if starts == list(range(0, n + 1, T)) else [])
+    at = np.unique(np.linspace(0, D - 1, 40).astype(int))
+    x, z, d_o, h0, dhf = (f64(inp[k][:, at]) for k in ("x", "z", "d_o", "h0", "d_hf"))
+    o, hf, _, _ = rec.forward(x, z, starts, "sigmoid", "plain", h0)
+    g = rec.backward(x, z, starts, "sigmoid", "plain", d_o, h0, dhf)
+    assert max(np.abs(v).max() for v in (o, hf, g["dx"], g["dh0"])) < 2 ** 15   # 2^-8 .. 2^15: 23 bits
+    for run in runs:
+        out = {k: v[:, at] for k, v in _train(inp, "sigmoid", "plain", dtype, **run).items()}
+        first = starts[0]
+        for k, want, t in (("o", o, dtype), ("h_final", hf, "f32"), ("dx", g["dx"], dtype), ("dh0", g["dh0"], "f32")):
+            want = torch.from_numpy(want).to(torch.float32).to(torch_dtype(t))
+            got = out[k].cpu()
+            if k in ("o", "dx"):
+                want, got = want[first:], got[first:]
+            assert torch.equal(got, want), (k, int((got != want).any(1).nonzero()[0]))
+        # dgate is a quarter of dh h where the gate is a half, and zero elsewhere: a product, rounded
+        assert worst(out["dgate"][first:], g["dgate"][first:], 2 * HALF["f32"] * np.abs(g["dgate"][first:]), dtype) <= 1
+
+
+@pytest.mark.parametrize("D", [34, 33])
+@pytest.mark.parametrize("gate,kind", KINDS)
+def test_long_bf16_sequences(D, gate, kind):
+    """More than three groups of tiles with ordinary gates, two channels a lane and one."""
+    starts = [0, 300, 12900, 13000]
+    inp = _make(71, 13000, 3, D, "bf16", gate, z_mean=5.0)
+    _check(inp, _train(inp, gate, kind, "bf16", starts=starts), starts, gate, kind, "bf16")

@@ -518,3 +518,28 @@ def test_long_bf16_sequences(D, gate, kind):
     starts = [0, 300, 12900, 13000]
     inp = _make(71, 13000, 3, D, "bf16", gate, z_mean=5.0)
     _check(inp, _train(inp, gate, kind, "bf16", starts=starts), starts, gate, kind, "bf16")
+
+
+def test_unsorted_starts_write_nothing_around_the_buffers():
+    """Each output, the saved context and the workspace lies inside a larger buffer, whose rest stays as it was."""
+    import torch
+    n, D, S = 1000, 40, 3
+    inp = {k: v.cuda() for k, v in _make(40, n, S, D, "bf16", "sigmoid").items()}
+    desc = B.make_rec_desc(S, n, D, packed=True)
+    sizes = dict(saved=B.ttt_recurrence_saved_size(desc), ws=max(B.ttt_recurrence_workspace_size(desc, e) for e in (0, 1)),
+                 o=n * D * 2, dx=n * D * 2, dgate=n * D * 2, h_final=S * D * 4, dh0=S * D * 4)
+    room = 1 << 16   # bytes on either side
+    for starts in ([0, 900, 100, 1000], [1000, 500, 0, 200], [-50, 2000, -7, 5000], [2 ** 31 - 1, -2 ** 31, 0, 3], [0, 400, 1000, 700]):
+        whole = {k: torch.full((size + 2 * room,), 0xA5, dtype=torch.uint8, device="cuda") for k, size in sizes.items()}
+        part = {k: whole[k][room:room + size] for k, size in sizes.items()}
+        for k in ("o", "dx", "dgate"):
+            part[k] = part[k].view(torch.bfloat16).view(n, D)
+        for k in ("h_final", "dh0"):
+            part[k] = part[k].view(torch.float32).view(S, D)
+        st = torch.tensor(starts, dtype=torch.int32).cuda()
+        B.ttt_recurrence_fwd(desc, inp["x"], inp["z"], inp["h0"], st, part["o"], part["h_final"], part["saved"], part["ws"])
+        B.ttt_recurrence_bwd(desc, inp["x"], inp["z"], inp["h0"], st, part["saved"], inp["d_o"], inp["d_hf"], part["dx"],
+                             part["dgate"], part["dh0"], part["ws"])
+        torch.cuda.synchronize()
+        for k, size in sizes.items():
+            assert (whole[k][:room] == 0xA5).all() and (whole[k][room + size:] == 0xA5).all(), (k, starts)

@@ -13,7 +13,7 @@
 // rows take a part of a wave each, wide rows as many waves as they have pieces
 // for.  Measured, where a copy reaches 4.7 to 4.8 TB/s: forward of
 // 32768 x 2560 bf16 with a residual (671 MB) 136 us, both directions of 16384 x 2048
-// bf16 with one (537 MB) 103 us, of 262144 x 128 in 16 groups (340 MB) 75 us.
+// bf16 with one (537 MB) 103 us, of 262144 x 128 in 16 groups (340 MB) 76 us.
 // A workgroup holds several rows side by side (slots), walks over rows of one
 // group, so that the weights stay in registers, and takes UR rows a slot at a time:
 // they share the barriers of a cross-wave sum, and the loads of the next UR are in
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
 
 // dw[g][c], db[g][c] = the sum of their `slices` partial rows: 32 columns a
 // workgroup, 32 threads a column, each adds every 32nd partial row.  Bound by latency:
-// 6 us for the 4 to 8 MB of a training step.
+// 5 us for the 4 MB of a training step.
 constexpr int kReduceCols = 32, kReduceThreads = 1024, kReduceRows = kReduceThreads / kReduceCols;
 constexpr int kReduceGrid = 1 << 20;  // workgroups at most: a launch has fewer than 2^32 threads
 
@@ -625,12 +625,13 @@ Plan make_plan(const ttt_ln_desc& d) {
 
 // Workgroups a CU, each of which walks over its share of the rows.  The forward has
 // about 1024 lanes a CU that hold a piece: idle lanes do not count, since it is the
-// loads in flight that matter.  32768 x 2560 bf16 with a residual takes 124 us (2048
-// threads 135), 4000 x 1024 14 (20), 50000 x 640 42.0 (42.5; 1024 threads 44),
-// 7000 x 6000 48.8 (rounded down to one 55.5).  Narrow rows take
-// 1024 threads, idle lanes or not: 262144 x 128 34.7 us (2048 threads 36.8), 500000 x 100
-// 42.5 (2048 45.3, 1024 lanes with a piece 47).  Rows that no workgroup holds: 1500 x 32768
-// 135 us with two of 1024 threads, 205 with one.
+// loads in flight that matter.  32768 x 2560 bf16 with a residual takes 136 us (2048
+// threads 146), 4000 x 1024 12.7 (18.1), 50000 x 640 39.2 (1024 threads 41.1),
+// 7000 x 6000 47.6 (rounded down to one 57.5).  Narrow rows take
+// 1024 threads, idle lanes or not: 262144 x 128 29.9 us (2048 threads 31.6), 500000 x 100
+// 42.2 (2048 42.7, 1024 lanes with a piece 46.3).  Rows that no workgroup holds: 1500 x 32768
+// 135 us with two of 1024 threads, 199 with one.  (These and the figures below: mean device
+// time of a launch, other inputs from launch to launch.)
 int fwd_per_cu(const ttt_ln_desc& d, const Plan& p) {
   if (p.tpr) return 1024 / p.threads;
   if (!p.nit) return 2;
@@ -638,8 +639,9 @@ int fwd_per_cu(const ttt_ln_desc& d, const Plan& p) {
   return (1024 + lanes - 1) / lanes;
 }
 // The backward's workgroups each write a partial row of dw and db: 512 threads, one
-// workgroup at least.  16384 x 2048 bf16 took 53 us with 512, 58 with 1024 and 67 with
-// 2048; 7000 x 8192 76 with one of 1024 threads on every CU, 114 on every other.
+// workgroup at least.  16384 x 2048 bf16 takes 50 us with 512, 56 with 1024 and 68 with
+// 2048, 262144 x 128 41, 47 and 49; 7000 x 8192 81 with one of 1024 threads on every CU,
+// 122 on every other.
 int bwd_per_cu(const Plan& p) { return std::max(512 / p.threads, 1); }
 
 // Workgroups of each group, no more than there are rows for (`unroll` of them a step).
@@ -652,9 +654,11 @@ int slices_of(const ttt_ln_desc& d, const Plan& p, int unroll, int per_cu) {
 }
 
 // Rows a slot takes at once, where there are enough for every workgroup; few rows go
-// to as many workgroups as there are.  Narrow rows have no barrier to share but short
-// loads: forward of 262144 x 128 bf16 42 us with one, 38 with two, 34.5 with four;
-// the backward (registers for two tensors more) 43, 42 and 59.
+// to as many workgroups as there are.  Wide rows share barriers: forward of 50000 x 640
+// bf16 45.6 us with one and 39.2 with two, 16384 x 2048 with a residual 53.6 and 51.0, its
+// backward 48.5 and 50.4.  Narrow rows have no barrier to share but short loads: forward of
+// 262144 x 128 34.0 us with one, 33.1 with two, 29.9 with four; the backward (registers for
+// two tensors more) 45.8, 40.7 and 43.1.
 int fwd_unroll(const ttt_ln_desc& d, const Plan& p) {
   if (p.nit != 1 || p.threads > kWideThreads || d.rows < 4096 * p.slots) return 1;
   return p.tpr ? 4 : 2;

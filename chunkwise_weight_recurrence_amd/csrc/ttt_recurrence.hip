@@ -461,11 +461,16 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(uint4* __restrict__ maps
 }
 
 // The forward.  Reads x and z and writes o once, in one pass.  Bound by memory on long
-// problems: 131072 x 2048 bf16 376 us, 4.3 TB/s (a copy 4.8; the same kernel without
-// any exchange 310 us), of which the exchange of maps, 31 KB read for a tile of 96 KB,
-// is the rest.  With few tiles it is bound by latency, a tile's loads, its map and one
-// look back behind one another: 4 x 4096 x 2048 bf16 62 us, 3.2 TB/s; 19 sequences of
-// 9001 x 1001 f32 (4-byte loads, 2.2 rounds of workgroups) 42 us, 2.5 TB/s.
+// problems: 131072 x 2048 bf16 380 to 390 us, 4.1 to 4.2 TB/s (a copy 4.8).  The same
+// kernel without any exchange of maps takes 326: a tile of 192 KB reads 53 KB of them on
+// average, from L2 (what comes from beyond it is 1.01 times x and z).  Two bf16 channels
+// and 32 tokens a wave take 165 registers, so a CU has one workgroup, whose loads, walks,
+// map, look back and stores follow one another: 37 packed prompts, 30011 x 2560 (2360
+// tiles, 9.2 rounds), 134 us, 3.4 TB/s, and 110 without the exchange.  16 tokens a wave
+// (110 registers, two workgroups) are bound by the same latencies: 4 x 4096 x 2048 bf16
+// 61 us, 3.3 TB/s, 45 without the exchange.  f32 has room for four workgroups: 19
+// sequences of 9001 x 1001 (1.1 rounds) 41 us, 2.6 TB/s; their rows of 4004 bytes share
+// cache lines between channel blocks, and 1.5 times x and z come from beyond the L2.
 // LINKED: there is more than one tile.
 template <typename E, int V, int GATE, int IN, int LW, bool LINKED>
 __global__ __launch_bounds__(kThreads, LW == 32 ? 2 : 4) void rec_fwd_kernel(RecArgs a) {
@@ -600,7 +605,8 @@ __global__ __launch_bounds__(kThreads, LW == 32 ? 2 : 4) void rec_fwd_kernel(Rec
 // The backward: the same tiles, e running from the end.  The tile's states are
 // formed again from the state that entered it (ckpt) and the waves' forward maps, so
 // h is neither kept nor read.  Bound by memory and by the three walks' arithmetic
-// (a_t formed in each): 4 x 4096 x 2048 bf16 85 us for 336 MB, 3.9 TB/s.
+// (a_t formed in each): 4 x 4096 x 2048 bf16 85 us for 336 MB, 3.9 TB/s; 9001 x 1001 f32
+// (91 registers, two workgroups a CU, 2.2 rounds) 56 us for 180 MB, 3.2 TB/s.
 template <typename E, int V, int GATE, int IN, int LW, bool LINKED>
 __global__ __launch_bounds__(kThreads, 4) void rec_bwd_kernel(RecArgs a) {
   static_assert(kWaves * LW == kRun, "a tile starts where the forward saved a state");
@@ -790,8 +796,7 @@ __global__ __launch_bounds__(kThreads) void rec_empty_kernel(RecArgs a, const fl
 }
 
 // One token for each row, a workgroup kStepThreads V channels of it: 256 rows of 4096
-// bf16 (25 MB) 5.2 us, with its states in the Infinity Cache; eight rows of
-// 2048 3.3 us, which is latency.
+// bf16 (15 MB, 3 us at a copy's rate) 5.5 us; eight rows of 2048 3.2 us, which is latency.
 // h[slot] <- a h[slot] + u, o = h[slot].  Rows that name
 // one slot are consecutive tokens of it, in row order: the first of them does
 // them all, so that the result does not depend on which workgroup comes first.
@@ -895,7 +900,8 @@ int64_t tiles(const ttt_rec_desc& d, int tile) {
 constexpr int kBwdTile = kWaves * kBwdLW;
 // The forward's tile: 256 tokens where that leaves eight tiles a CU, else 128.  A larger
 // tile reads fewer of the others' maps: 131072 x 2048 bf16 (32 tiles of 256 a CU) takes
-// 375 us with 256 and 402 with 128; 4 x 4096 x 2048 (4 a CU) 72 and 62.
+// 380 to 390 us with 256 and 420 with 128, 30011 x 2560 packed (9) 128 and 130; below, 4 x
+// 4096 x 2048 (4) takes 61 with either, 9001 x 1001 f32 (1) 44 and 41.
 int fwd_tile(const ttt_rec_desc& d) {
   const int64_t blocks = (static_cast<int64_t>(d.D) + 127) / 128;
   const int64_t nt = tiles(d, kWaves * 32);

@@ -454,7 +454,9 @@ TTT_API size_t ttt_noalloc_scratch_bytes(void);
  *   a_t = Sigmoid(gate_t) (SIGMOID) or exp(gate_t) (LOG, as log_decay: <= 0);
  *   h_t = a_t h_{t-1} + x_t (PLAIN)   or   a_t h_{t-1} + (1 - a_t) x_t (CONVEX);
  *   o_t = h_t rounded to dtype.
- * A sequence's state is kept in float32 throughout.
+ * A sequence's state is kept in float32 throughout.  An infinite x, state or
+ * gradient may go on as NaN in its own sequence, since the factors of many tokens
+ * are multiplied before they meet it and may be 0 by then.
  */
 typedef enum { TTT_GATE_SIGMOID = 0, TTT_GATE_LOG = 1 } ttt_rec_gate;
 typedef enum { TTT_REC_PLAIN = 0, TTT_REC_CONVEX = 1 } ttt_rec_input;
@@ -463,7 +465,7 @@ typedef struct {
   int32_t B;      /* sequences (rows of one token each for ttt_recurrence_step), up
                      to 2^31 - 4096, B * D up to 4e12                           */
   int32_t T;      /* tokens of each sequence; packed: token rows of the buffers; in
-                     all below 2^31 - 4096, and tokens / 128 times D / 64, each
+                     all up to 2^31 - 4096, and tokens / 128 times D / 64, each
                      rounded up, below 2^23                                     */
   int32_t D;      /* channels, 1 .. 2^23; per-head channels [B,H,T,d] are B*H sequences of d */
   int32_t packed; /* 0: x is [B,T,D]; 1: x is [T,D], the sequences one behind the other */

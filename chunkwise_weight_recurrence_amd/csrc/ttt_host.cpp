@@ -701,6 +701,8 @@ int ttt_recurrence_step(const ttt_rec_desc* desc, const void* x, const void* gat
     return fail(TTT_ERR_INVALID_ARG, "without slots n_states must be >= B (got %d, %d)", n_states, desc->B);
   if (static_cast<double>(n_states) * desc->D > 4.0e12 || !ttt::recurrence_step_grid_fits(*desc))
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d rows, %d states of %d channels)", desc->B, n_states, desc->D);
+  // Each row looks for its slot among all others: 2^24 rows would hold the GPU for minutes.
+  if (slots && desc->B > 1 << 20) return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d rows with slots)", desc->B);
   if (desc->B == 0) return ok();
   if (!x || !gate || !h || !o) return fail(TTT_ERR_INVALID_ARG, "x, gate, h and o are required");
   if (const char* bad = misaligned({{"x", x}, {"gate", gate}, {"slots", slots}, {"h", h}, {"o", o}}))

@@ -799,7 +799,9 @@ __global__ __launch_bounds__(kThreads) void rec_empty_kernel(RecArgs a, const fl
 // bf16 (15 MB, 3 us at a copy's rate) 5.5 us; eight rows of 2048 3.2 us, which is latency.
 // h[slot] <- a h[slot] + u, o = h[slot].  Rows that name
 // one slot are consecutive tokens of it, in row order: the first of them does
-// them all, so that the result does not depend on which workgroup comes first.
+// them all, so that the result does not depend on which workgroup comes first.  The
+// search for them is B slots a workgroup: 4096 rows of 2048 bf16 58 us (without slots
+// 20), 32768 rows 2.5 ms (0.16).
 constexpr int kStepThreads = 256;
 
 struct StepArgs {

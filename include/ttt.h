@@ -533,7 +533,9 @@ TTT_API int ttt_recurrence_bwd(const ttt_rec_desc* desc, const void* x, const vo
  *            or NULL (row b has state b; then n_states >= B).  A row whose slot
  *            is not in 0 .. n_states - 1 is padding: its o and every state are
  *            left as they were.  Rows with the same slot are consecutive tokens of
- *            it, in row order.
+ *            it, in row order.  Each row looks for its slot among all others, so B
+ *            is up to 2^20 here, and from some thousand rows on the time grows with
+ *            its square
  *   h        [n_states,D] f32, read and updated in place
  * No workspace.
  */

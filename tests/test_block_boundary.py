@@ -132,6 +132,14 @@ def test_step_refusals():
     assert _step(d, h=FAKE + 8) == -1 and "h must be 16-byte aligned" in ttt.ttt_last_error()
 
 
+def test_step_with_slots_is_bounded():
+    """Each row looks for its slot among all others: millions of rows would hold the GPU for minutes."""
+    n = (1 << 20) + 1
+    assert _step(_rec(B=n, T=1), slots=FAKE) == -2 and "too large" in ttt.ttt_last_error()
+    assert _step(_rec(B=n - 1, T=1), slots=FAKE, x=None) == -1 and "required" in ttt.ttt_last_error()
+    assert _step(_rec(B=n, T=1), n_states=n, x=None) == -1 and "required" in ttt.ttt_last_error()   # without slots
+
+
 def _ln(**kw):
     base = dict(rows=12, D=64)
     base.update(kw)

@@ -23,7 +23,9 @@ EXPORTS = ("ttt_workspace_size", "ttt_saved_size", "ttt_chunk_fwd", "ttt_chunk_b
            "ttt_last_error", "ttt_version", "ttt_timing_enable", "ttt_timing_read", "ttt_chunk_bwd_noalloc",
            "ttt_noalloc_scratch_bytes", "ttt_recurrence_workspace_size", "ttt_recurrence_saved_size",
            "ttt_recurrence_fwd", "ttt_recurrence_bwd", "ttt_recurrence_step", "ttt_layernorm_fwd",
-           "ttt_layernorm_workspace_size", "ttt_layernorm_bwd")
+           "ttt_layernorm_workspace_size", "ttt_layernorm_bwd", "ttt_delta_workspace_size", "ttt_delta_saved_size",
+           "ttt_delta_fwd", "ttt_delta_bwd", "ttt_delta_step", "ttt_qknorm_fwd", "ttt_qknorm_workspace_size",
+           "ttt_qknorm_bwd")
 
 
 class Status(IntEnum):
@@ -69,6 +71,17 @@ class RecInput(IntEnum):
     CONVEX = 1
 
 
+class HeadNorm(IntEnum):
+    NONE = 0
+    RMS = 1
+    L2 = 2
+
+
+class RopePairs(IntEnum):
+    HALF = 0
+    INTERLEAVED = 1
+
+
 class Kernel(IntEnum):
     """Mirror of ``ttt_kernel`` (per-kernel timing ids)."""
     FWD = 0
@@ -104,6 +117,15 @@ class Kernel(IntEnum):
     LN_BWD = 30
     LN_REDUCE = 31
     REC_CLEAR = 32
+    DELTA_PLAN = 33
+    DELTA_PREP = 34
+    DELTA_FWD = 35
+    DELTA_BWD = 36
+    DELTA_GRAD = 37
+    DELTA_STEP = 38
+    QK_FWD = 39
+    QK_BWD = 40
+    QK_REDUCE = 41
 
 
 ENTRY_FWD = 0
@@ -138,6 +160,23 @@ class TTTLnDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("D", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("period", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class TTTDeltaDesc(ctypes.Structure):
+    """Mirror of ``ttt_delta_desc``."""
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("packed", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("scale", ctypes.c_float), ("lr_max", ctypes.c_float),
+                ("lr_bias", ctypes.c_float), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("ldg", ctypes.c_int64), ("ldb", ctypes.c_int64)]
+
+
+class TTTQkNormDesc(ctypes.Structure):
+    """Mirror of ``ttt_qknorm_desc``."""
+    _fields_ = [("tokens", ctypes.c_int64), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("pairing", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("period", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rot_scale", ctypes.c_float)]
 
 
 class TTTError(RuntimeError):
@@ -210,7 +249,16 @@ def lib():
     L.ttt_layernorm_fwd.argtypes = [nptr] + [vp] * 9
     L.ttt_layernorm_workspace_size.argtypes = [nptr, ctypes.POINTER(sz)]
     L.ttt_layernorm_bwd.argtypes = [nptr] + [vp] * 10 + [sz, vp]
-    for name in EXPORTS[-8:]:
+    eptr, qptr = ctypes.POINTER(TTTDeltaDesc), ctypes.POINTER(TTTQkNormDesc)
+    L.ttt_delta_workspace_size.argtypes = [eptr, i32, ctypes.POINTER(sz)]
+    L.ttt_delta_saved_size.argtypes = [eptr, ctypes.POINTER(sz)]
+    L.ttt_delta_fwd.argtypes = [eptr] + [vp] * 11 + [sz, vp]
+    L.ttt_delta_bwd.argtypes = [eptr] + [vp] * 16 + [sz, vp]
+    L.ttt_delta_step.argtypes = [eptr] + [vp] * 6 + [i32] + [vp] * 4
+    L.ttt_qknorm_fwd.argtypes = [qptr] + [vp] * 9
+    L.ttt_qknorm_workspace_size.argtypes = [qptr, ctypes.POINTER(sz)]
+    L.ttt_qknorm_bwd.argtypes = [qptr] + [vp] * 13 + [sz, vp]
+    for name in EXPORTS[-16:]:
         getattr(L, name).restype = i32
     L.ttt_last_error.argtypes = []
     L.ttt_last_error.restype = ctypes.c_char_p
@@ -292,6 +340,31 @@ def make_ln_desc(rows, D, dtype="bf16", groups=1, period=1, eps=1e-5, ldx=0):
     _fit32(D=D, groups=groups, period=period)
     return TTTLnDesc(rows, ldx, D, groups, period, int(DType[dtype.upper()]) if isinstance(dtype, str) else int(dtype),
                      float(eps), 0)
+
+
+def make_delta_desc(B, T, H, dk, dv, Hk=None, dtype="bf16", gate="sigmoid", packed=False, scale=None, lr_max=1.0,
+                    lr_bias=0.0, ldq=0, ldk=0, ldv=0, ldg=0, ldb=0):
+    """Build a TTTDeltaDesc from names ("bf16"/"f32", "sigmoid"/"log"); ``Hk`` None: H, ``scale`` None: dk ** -0.5."""
+    def enum(cls, x):
+        return int(cls[x.upper()]) if isinstance(x, str) else int(x)
+    Hk = H if Hk is None else Hk
+    _fit32(B=B, T=T, H=H, Hk=Hk, dk=dk, dv=dv)
+    if scale is None:
+        scale = dk ** -0.5 if dk > 0 else 1.0
+    return TTTDeltaDesc(B, T, H, Hk, dk, dv, int(packed), enum(DType, dtype), enum(Gate, gate), float(scale), float(lr_max),
+                        float(lr_bias), ldq, ldk, ldv, ldg, ldb)
+
+
+def make_qknorm_desc(tokens, Hq, Hk, d, rot=None, pairing="half", norm="rms", dtype="bf16", period=0, eps=1e-6,
+                     rot_scale=1.0, ldq=0, ldk=0):
+    """Build a TTTQkNormDesc from names ("half"/"interleaved", "none"/"rms"/"l2", "bf16"/"f32"); ``rot`` None: all of
+    an even d."""
+    def enum(cls, x):
+        return int(cls[x.upper()]) if isinstance(x, str) else int(x)
+    rot = d // 2 * 2 if rot is None else rot
+    _fit32(Hq=Hq, Hk=Hk, d=d, rot=rot, period=period)
+    return TTTQkNormDesc(tokens, ldq, ldk, Hq, Hk, d, rot, enum(RopePairs, pairing), enum(HeadNorm, norm), period,
+                         enum(DType, dtype), float(eps), float(rot_scale))
 
 
 def ttt_last_error() -> str:
@@ -597,6 +670,109 @@ def ttt_layernorm_bwd(desc, x, w, mean, rstd, dy, dr, dx, dw, db, ws, ws_bytes=N
           _arg("w", w, dev, f32, G, D), _arg("mean", mean, dev, f32, n, 1), _arg("rstd", rstd, dev, f32, n, 1),
           _arg("dy", dy, dev, dt, n, D), _arg("dr", dr, dev, dt, n, D), _arg("dx", dx, dev, dt, n, D, desc.ldx),
           _arg("dw", dw, dev, f32, G, D), _arg("db", db, dev, f32, G, D), *_ws(ws, ws_bytes, dev))
+
+
+def _tokens(name, x, dev, dtype, n, H, d, ld):
+    """The pointer of ``n`` tokens of ``H`` heads of ``d`` elements, tokens ``ld`` elements apart (0: dense) and the heads
+    of one side by side: [..,H,d] or [..,H * d].  The checks are _arg's."""
+    if x is None or type(x) is int:
+        return x
+    if ld and ld != H * d and hasattr(x, "stride") and x.dim() >= 2 and x.shape[-1] == d and x.shape[-2] == H:
+        if H > 1 and x.stride(-2) != d or d > 1 and x.stride(-1) != 1:
+            raise ValueError(f"{name} must have {H} heads of {d} elements side by side (got shape {tuple(x.shape)}, "
+                             f"strides {x.stride()})")
+        x = x.flatten(-2) if x.numel() else x.reshape(*x.shape[:-2], H * d)
+        if x.dim() == 1:
+            x = x[None]
+    return _arg(name, x, dev, dtype, n, H * d, ld)
+
+
+def _delta_inputs(desc, n, dev, q, k, v, gate, beta, d=""):
+    """The pointers of q, k, v, gate and beta, or with d = "d" of their gradients."""
+    dt, H, Hk = _io_type(desc), desc.H, desc.Hk
+    return (_tokens(d + "q", q, dev, dt, n, Hk, desc.dk, desc.ldq), _tokens(d + "k", k, dev, dt, n, Hk, desc.dk, desc.ldk),
+            _tokens(d + "v", v, dev, dt, n, H, desc.dv, desc.ldv), _tokens(d + "gate", gate, dev, dt, n, H, 1, desc.ldg),
+            _tokens(d + "beta", beta, dev, dt, n, H, 1, desc.ldb))
+
+
+def ttt_delta_workspace_size(desc: TTTDeltaDesc, entry: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_delta_workspace_size(ctypes.byref(desc), int(entry), ctypes.byref(n)))
+    return n.value
+
+
+def ttt_delta_saved_size(desc: TTTDeltaDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_delta_saved_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def ttt_delta_fwd(desc, q, k, v, gate, beta, s0, seq_starts, o, s_final, saved, ws, ws_bytes=None, stream=None):
+    """``gate`` None: no decay.  ``seq_starts``: int32 device tensor of B + 1 positions for a packed desc, else None."""
+    f32, _, i32, u8 = _types()
+    dt, dev, B = _io_type(desc), _device(q), desc.B
+    n, state = desc.T if desc.packed else B * desc.T, desc.H * desc.dk * desc.dv
+    _call(lib().ttt_delta_fwd, dev, stream, ctypes.byref(desc), *_delta_inputs(desc, n, dev, q, k, v, gate, beta),
+          _arg("s0", s0, dev, f32, B, state), _arg("seq_starts", seq_starts, dev, i32, 1, B + 1),
+          _arg("o", o, dev, dt, n, desc.H * desc.dv), _arg("s_final", s_final, dev, f32, B, state),
+          _arg("saved", saved, dev, u8, 1, 0 if saved is None else ttt_delta_saved_size(desc)), *_ws(ws, ws_bytes, dev))
+
+
+def ttt_delta_bwd(desc, q, k, v, gate, beta, seq_starts, saved, d_o, d_sfinal, dq, dk, dv, dgate, dbeta, ds0, ws,
+                  ws_bytes=None, stream=None):
+    f32, _, i32, u8 = _types()
+    dt, dev, B = _io_type(desc), _device(q), desc.B
+    n, state = desc.T if desc.packed else B * desc.T, desc.H * desc.dk * desc.dv
+    _call(lib().ttt_delta_bwd, dev, stream, ctypes.byref(desc), *_delta_inputs(desc, n, dev, q, k, v, gate, beta),
+          _arg("seq_starts", seq_starts, dev, i32, 1, B + 1),
+          _arg("saved", saved, dev, u8, 1, 0 if saved is None else ttt_delta_saved_size(desc)),
+          _arg("d_o", d_o, dev, dt, n, desc.H * desc.dv), _arg("d_sfinal", d_sfinal, dev, f32, B, state),
+          *_delta_inputs(desc, n, dev, dq, dk, dv, dgate, dbeta, "d"), _arg("ds0", ds0, dev, f32, B, state),
+          *_ws(ws, ws_bytes, dev))
+
+
+def ttt_delta_step(desc, q, k, v, gate, beta, slots, s, s_new, o, n_states=None, stream=None):
+    """``s``, ``s_new``: [n_states,H,dk,dv] float32, the same tensor for an update in place; ``n_states`` is only needed
+    where s is a raw pointer."""
+    f32, _, i32, _ = _types()
+    dt, dev, n, state = _io_type(desc), _device(q), desc.B, desc.H * desc.dk * desc.dv
+    if n_states is None:
+        n_states = s.numel() // state if hasattr(s, "numel") and state > 0 else 0
+    if not -2 ** 31 <= n_states < 2 ** 31:
+        _fit32(n_states=n_states)
+    _call(lib().ttt_delta_step, dev, stream, ctypes.byref(desc), *_delta_inputs(desc, n, dev, q, k, v, gate, beta),
+          _arg("slots", slots, dev, i32, 1, n), n_states, _arg("s", s, dev, f32, n_states, state),
+          _arg("s_new", s_new, dev, f32, n_states, state), _arg("o", o, dev, dt, n, desc.H * desc.dv))
+
+
+def ttt_qknorm_workspace_size(desc: TTTQkNormDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ttt_qknorm_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def _qk_inputs(desc, dev, q, k, wq, wk, positions, inv_freq):
+    f32, _, i32, _ = _types()
+    dt, n, d = _io_type(desc), desc.tokens, desc.d
+    return (_tokens("q", q, dev, dt, n, desc.Hq, d, desc.ldq), _tokens("k", k, dev, dt, n, desc.Hk, d, desc.ldk),
+            _arg("wq", wq, dev, f32, 1, d), _arg("wk", wk, dev, f32, 1, d), _arg("positions", positions, dev, i32, 1, n),
+            _arg("inv_freq", inv_freq, dev, f32, 1, desc.rot // 2))
+
+
+def ttt_qknorm_fwd(desc, q, k, wq, wk, positions, inv_freq, yq, yk, stream=None):
+    """``positions``: int32 device tensor [tokens], or None; ``inv_freq``: float32 device tensor [rot / 2]."""
+    dt, dev, n, d = _io_type(desc), _device(q), desc.tokens, desc.d
+    _call(lib().ttt_qknorm_fwd, dev, stream, ctypes.byref(desc), *_qk_inputs(desc, dev, q, k, wq, wk, positions, inv_freq),
+          _arg("yq", yq, dev, dt, n, desc.Hq * d), _arg("yk", yk, dev, dt, n, desc.Hk * d))
+
+
+def ttt_qknorm_bwd(desc, q, k, wq, wk, positions, inv_freq, dyq, dyk, dq, dk, dwq, dwk, ws, ws_bytes=None, stream=None):
+    f32 = _types()[0]
+    dt, dev, n, d = _io_type(desc), _device(q), desc.tokens, desc.d
+    _call(lib().ttt_qknorm_bwd, dev, stream, ctypes.byref(desc), *_qk_inputs(desc, dev, q, k, wq, wk, positions, inv_freq),
+          _arg("dyq", dyq, dev, dt, n, desc.Hq * d), _arg("dyk", dyk, dev, dt, n, desc.Hk * d),
+          _tokens("dq", dq, dev, dt, n, desc.Hq, d, desc.ldq), _tokens("dk", dk, dev, dt, n, desc.Hk, d, desc.ldk),
+          _arg("dwq", dwq, dev, f32, 1, d), _arg("dwk", dwk, dev, f32, 1, d), *_ws(ws, ws_bytes, dev))
 
 
 def ttt_timing_enable(on: bool) -> None:

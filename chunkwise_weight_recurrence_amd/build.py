@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libttt.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["ttt_host.cpp", "ttt_timing.cpp", "ttt_generic.hip", "ttt_mfma_fwd.hip", "ttt_mfma_bwd.hip", "ttt_decay_prep.hip", "ttt_linear.hip", "inplace.hip", "ttt_mlp.hip", "ttt_mlp_bwd.hip", "ttt_norm.hip", "ttt_noalloc.hip",
-           "ttt_recurrence.hip", "ttt_layernorm.hip"]
+           "ttt_recurrence.hip", "ttt_layernorm.hip", "ttt_delta.hip", "ttt_delta_bwd.hip", "ttt_qknorm.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++20", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",

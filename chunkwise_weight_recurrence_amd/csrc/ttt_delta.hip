@@ -1,0 +1,658 @@
+// Gated delta rule: chunk table, chunk preparation, forward sweep and single-token step (see
+// ttt_delta_common.h for the mathematics).
+
+#include "ttt_delta_common.h"
+
+namespace ttt {
+namespace delta {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// The chunk table of packed sequences: entries of seq_starts are held to 0 .. n and to ascend,
+// so whatever they are, the chunks fit the table and the tokens the buffers.
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, int B, int n, int C, int slots, int* edge, int* base,
+                                                            int4* table) {
+  __shared__ int part[kPlanThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // running maximum of the starts
+  int carry = 0;
+  for (int i0 = 0; i0 <= B; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int m = i <= B ? min(max(starts[i], 0), n) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(m, d, 64);
+      if (lane >= d) m = max(m, o);
+    }
+    if (lane == 63) part[wave] = m;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int j = 0; j < kPlanThreads / 64; ++j) {
+      if (j < wave) before = max(before, part[j]);
+      all = max(all, part[j]);
+    }
+    if (i <= B) edge[i] = max(m, before);
+    carry = all;
+    __syncthreads();
+  }
+  // sums of the chunk counts
+  carry = 0;
+  for (int i0 = 0; i0 <= B; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int c = i < B ? (edge[i + 1] - edge[i] + C - 1) / C : 0;
+    const int own = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(c, d, 64);
+      if (lane >= d) c += o;
+    }
+    if (lane == 63) part[wave] = c;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int j = 0; j < kPlanThreads / 64; ++j) {
+      if (j < wave) before += part[j];
+      all += part[j];
+    }
+    if (i <= B) base[i] = before + c - own;
+    carry = all;
+    __syncthreads();
+  }
+  const int total = carry;
+  for (int c = threadIdx.x; c < slots; c += kPlanThreads) {
+    int4 w = {0, -1, 0, 0};
+    if (c < total) {
+      int lo = 0, hi = B;  // the last sequence whose base is <= c
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= c) lo = mid;
+        else hi = mid;
+      }
+      const int first = edge[lo] + (c - base[lo]) * C;
+      w = {first, min(C, edge[lo + 1] - first), lo, 0};
+    }
+    table[c] = w;
+  }
+}
+
+// ---- T and P of every chunk ----
+
+constexpr int kPrepThreads = 256;
+
+// 16 x 16 blocks of a [C][C + 4] fp32 matrix as operands of v_mfma_f32_16x16x4_f32.
+template <int LD> __device__ __forceinline__ f32x4_t block_row(const float* m, int bi, int bj) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  return *reinterpret_cast<const f32x4_t*>(m + (16 * bi + i) * LD + 16 * bj + 4 * g);
+}
+template <int LD> __device__ __forceinline__ f32x4_t block_col(const float* m, int bi, int bj) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  f32x4_t f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) f[r] = m[(16 * bi + 4 * g + r) * LD + 16 * bj + i];
+  return f;
+}
+
+// A [C][C] fp32 matrix in operand order; TRANS: its transpose.  TERMS: 2 writes hi and lo for bf16.
+template <typename E, int LD, bool TRANS, int TERMS>
+__device__ __forceinline__ void tri_store(const float* m, char* dst) {
+  using T = Tri<E>;
+  constexpr int kThreads = kPrepThreads;
+  for (int idx = threadIdx.x; idx < T::kFrags * 64; idx += kThreads) {
+    const int place = idx >> 6, lane = idx & 63, i = lane & 15, g = lane >> 4;
+    const int p = place < 2 ? 0 : 1, kp = (place - p * (p + 1)) >> 1, mt = 2 * p + (place & 1);
+    f32x4_t x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int row = 16 * mt + i, col = 32 * kp + 16 * h + 4 * g + j;
+        if (TRANS) {  // the mirrored pair of the transpose
+          row = 16 * (2 * (T::NP - 1 - p) + (mt & 1)) + i;
+          col = 32 * (T::NP - 1 - kp) + 16 * h + 4 * g + j;
+        }
+        x[h][j] = TRANS ? m[col * LD + row] : m[row * LD + col];
+      }
+    if constexpr (std::is_same_v<E, float>) {
+      *reinterpret_cast<f32x8*>(dst + place * T::kFragBytes + lane * 32) = f32x8{x[0], x[1]};
+    } else {
+      const Split<bf16_t> s(x[0], x[1]);
+      *reinterpret_cast<bf16x8_t*>(dst + place * T::kFragBytes + lane * 16) = s.hi;
+      if (TERMS == 2) *reinterpret_cast<bf16x8_t*>(dst + T::kHalfBytes + place * T::kFragBytes + lane * 16) = s.lo;
+    }
+  }
+}
+
+// T = (1 + A)^-1 by blocks of 16: the diagonal ones by forward substitution, a column a lane, then
+// T_ij = -T_ii sum_{j<=l<i} A_il T_lj one diagonal after the other, all in fp32.
+template <int C, int LD> __device__ __forceinline__ void invert(const float* A, float* T) {
+  constexpr int NB = C / 16;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  if (wave < NB && lane < 16) {
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+      for (int l = 0; l < r; ++l) s -= A[(16 * wave + r) * LD + 16 * wave + l] * x[l];
+      x[r] = s;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) T[(16 * wave + r) * LD + 16 * wave + lane] = x[r];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int d = 1; d < NB; ++d) {
+    if (wave < NB - d) {
+      const int bj = wave, bi = wave + d;
+      f32x4_t s = zero4();
+#pragma unroll
+      for (int l = 0; l < d; ++l) s = mfma16(block_row<LD>(A, bi, bj + l), block_col<LD>(T, bj + l, bj), s);
+      f32x4_t x = zero4();
+      x = mfma16(block_row<LD>(T, bi, bi), s, x);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) T[(16 * bi + 4 * g + r) * LD + 16 * bj + i] = -x[r];
+    }
+    __syncthreads();
+  }
+}
+
+// A chunk and head a workgroup: its gates' sums, K K^T and Q K^T (row tile w by wave w), the inverse.
+// BWD writes the transposes, the scores in two terms.
+template <typename E, int DKP, bool BWD>
+__global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
+  constexpr int C = Chunk<E>::C, LD = C + 4;
+  using Lds = Tile<E, DKP>;
+  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) float A[C * LD];
+  __shared__ __attribute__((aligned(16))) float T[C * LD];
+  __shared__ __attribute__((aligned(16))) float P[C * LD];
+  __shared__ double G[C];
+  __shared__ float eta[C];
+  const int chunk = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const Where w = locate<C>(a, chunk);
+  if (w.len < 0) return;
+  const int hk = h / (a.H / a.Hk);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const bool wq = a.wide_q, wk = a.wide_k;
+  const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+  if (wave == 0) {
+    double Gt;
+    float et, rs, z;
+    gate_lane<E, C>(a, w, h, lane, Gt, et, rs, z);
+    const double last = __shfl(Gt, C - 1, 64);
+    if (lane < C) {
+      G[lane] = Gt;
+      eta[lane] = et;
+      float* vec = a.vec + item * 3 * C + lane;
+      vec[0] = exp2_(static_cast<float>(Gt));
+      vec[C] = exp2_(static_cast<float>(last - Gt));
+      vec[2 * C] = et;
+    }
+  }
+  stage<E, C, DKP, kPrepThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
+  stage<E, C, DKP, kPrepThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+  for (int x = threadIdx.x; x < C * LD; x += kPrepThreads) T[x] = 0.0f;
+  __syncthreads();
+  for (int mt = wave; mt < C / 16; mt += kPrepThreads / 64) {
+    f32x4_t kk[C / 16], qk[C / 16];
+#pragma unroll
+    for (int nt = 0; nt < C / 16; ++nt) kk[nt] = qk[nt] = zero4();
+#pragma unroll
+    for (int kp = 0; kp < DKP / 32; ++kp) {
+      const auto ka = row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), qa = row_frag<DKP>(Q, 16 * mt + i, 32 * kp + 8 * g);
+#pragma unroll
+      for (int nt = 0; nt < C / 16; ++nt) {
+        if (nt <= mt) {
+          const auto b = row_frag<DKP>(K, 16 * nt + i, 32 * kp + 8 * g);
+          kk[nt] = mma(ka, b, kk[nt]);
+          qk[nt] = mma(qa, b, qk[nt]);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < C / 16; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * mt + 4 * g + r, col = 16 * nt + i;
+        const float d = row >= col ? exp2_(static_cast<float>(G[row] - G[col])) : 0.0f;
+        A[row * LD + col] = row > col ? eta[row] * d * kk[nt][r] : 0.0f;
+        P[row * LD + col] = row >= col ? a.scale * d * qk[nt][r] : 0.0f;
+      }
+  }
+  __syncthreads();
+  invert<C, LD>(A, T);
+  tri_store<E, LD, BWD, 2>(T, a.t + item * Tri<E>::kBytes);
+  tri_store<E, LD, BWD, BWD ? 2 : 1>(P, a.p + item * Tri<E>::kBytes);
+}
+
+// ---- forward sweep ----
+
+// A wave holds 16 columns of a head's state in its result registers and walks the chunks; the WAVES of a
+// workgroup share the chunk's keys and queries in LDS.  The state and what is added to it are products
+// of two-term operands: its error does not grow with the length.
+template <typename E, int DKP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16;
+  using Lds = Tile<E, DKP>;
+  using TR = Tri<E>;
+  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) float vec[3 * C];
+  const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
+  const int h = chain % a.H, seq = chain / a.H, hk = h / (a.H / a.Hk);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
+  const bool in = col < a.dv, live = col < a.dvp;
+  const bool wq = a.wide_q, wk = a.wide_k;
+  const int first = a.packed ? a.base[seq] : seq * a.chunks_per_seq;
+  const int end = a.packed ? a.base[seq + 1] : first + a.chunks_per_seq;
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  f32x4_t S[ND];
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = state_row(t, g) + r;
+      S[t][r] = a.s0 && in && row < a.dk ? a.s0[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
+    }
+  for (int chunk = first; chunk < end; ++chunk) {
+    const Where w = locate<C>(a, chunk);
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    __syncthreads();
+    stage<E, C, DKP, WAVES * 64>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
+    stage<E, C, DKP, WAVES * 64>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+    for (int x = threadIdx.x; x < 3 * C; x += WAVES * 64) vec[x] = a.vec[item * 3 * C + x];
+    __syncthreads();
+    if (a.before && live) {
+      E* dst = static_cast<E*>(a.before) + item * DKP * a.dvp + col;
+#pragma unroll
+      for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Elem<E>::st(dst, static_cast<int64_t>(state_row(t, g) + r) * a.dvp, S[t][r]);
+    }
+    // K S and Q S
+    f32x4_t ks[NT], o[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) ks[mt] = o[mt] = zero4();
+#pragma unroll
+    for (int kp = 0; kp < DKP / 32; ++kp) {
+      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) {
+        ks[mt] = mma(row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), s, ks[mt]);
+        o[mt] = mma(row_frag<DKP>(Q, 16 * mt + i, 32 * kp + 8 * g), s, o[mt]);
+      }
+    }
+    // eta (V - e^G K S)
+    const E* v = static_cast<const E*>(a.v) + w.token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(vec + 16 * mt + 4 * g);
+      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(vec + 2 * C + 16 * mt + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * g + r;
+        const float x = in && t < w.len ? Elem<E>::ld(v, t * a.ldv) : 0.0f;
+        ks[mt][r] = et[r] * (x - gm[r] * ks[mt][r]);
+        o[mt][r] *= a.scale * gm[r];
+      }
+    }
+    // U = T (that), then O += P U
+    f32x4_t u[NT];
+    const char* tp = a.t + item * TR::kBytes;
+    const char* pp = a.p + item * TR::kBytes;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) u[mt] = zero4();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri_load2<E>(tp, TR::at(mt, kp)), rhs, u[mt]);
+    }
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> us(u[2 * kp], u[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(tri_load<E>(pp, TR::at(mt, kp)), us, o[mt]);
+    }
+    // S = e^{G_C} S + K^T (e^{G_C - G} U)
+    const float decay = vec[C - 1];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      f32x4_t x[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[j] = u[2 * kp + j] * *reinterpret_cast<const f32x4_t*>(vec + C + 16 * (2 * kp + j) + 4 * g);
+      const Split<E> us(x[0], x[1]);
+#pragma unroll
+      for (int t = 0; t < ND; ++t) S[t] = mma(state_col<DKP>(K, 32 * kp, t), us, S[t]);
+    }
+    E* op = static_cast<E*>(a.o) + (w.token * a.H + h) * a.dv + col;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * g + r;
+        if (in && t < w.len) Elem<E>::st(op, static_cast<int64_t>(t) * a.H * a.dv, o[mt][r]);
+        if (a.u && live) Elem<E>::st(static_cast<E*>(a.u) + item * C * a.dvp + col, static_cast<int64_t>(t) * a.dvp, u[mt][r]);
+      }
+  }
+  if (a.s_final && in) {
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_row(t, g) + r;
+        if (row < a.dk) a.s_final[state + static_cast<int64_t>(row) * a.dv + col] = S[t][r];
+      }
+  }
+}
+
+// ---- one token ----
+
+constexpr int kStepThreads = 256;
+
+// A workgroup has kStepCols columns of one head's state of one row, a thread a run of the dk rows of one
+// column; the two products over dk meet in LDS.  Rows that name one slot are consecutive tokens of it, in
+// row order: the first of them does them all.
+constexpr int kStepCols = 32, kStepRuns = kStepThreads / kStepCols;
+
+struct StepArgs {
+  int B, H, Hk, dk, dv, gate_kind, n_states, ncb;
+  float scale, lr_max, lr_bias;
+  int64_t ldq, ldk, ldv, ldg, ldb;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* gate;
+  const void* beta;
+  const int32_t* slots;
+  const float* s;
+  float* s_new;
+  void* o;
+};
+
+template <typename E, int NR>  // NR: rows of the state a thread holds
+__global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a) {
+  __shared__ float part[2][kStepRuns][kStepCols];
+  __shared__ float ks[kStepRuns * NR], qs[kStepRuns * NR];
+  __shared__ uint64_t same[kStepThreads / 64];
+  const int cb = blockIdx.x % a.ncb, h = blockIdx.x / a.ncb % a.H, b = blockIdx.x / a.ncb / a.H;
+  const int hk = h / (a.H / a.Hk);
+  const int c = threadIdx.x % kStepCols, run = threadIdx.x / kStepCols, col = cb * kStepCols + c;
+  int slot = b;
+  if (a.slots) {
+    slot = __builtin_amdgcn_readfirstlane(a.slots[b]);
+    int before = 0;
+    for (int j = threadIdx.x; j < b; j += kStepThreads) before |= a.slots[j] == slot;
+    if (__syncthreads_or(before)) return;
+  }
+  if (slot < 0 || slot >= a.n_states) return;
+  const int64_t at = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv + col;
+  float S[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = r * kStepRuns + run;
+    S[r] = row < a.dk && col < a.dv ? a.s[at + static_cast<int64_t>(row) * a.dv] : 0.0f;
+  }
+  auto token = [&](int row) {
+    const int64_t rr = row;
+    for (int x = threadIdx.x; x < kStepRuns * NR; x += kStepThreads) {
+      ks[x] = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.k), rr * a.ldk + hk * a.dk + x) : 0.0f;
+      qs[x] = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.q), rr * a.ldq + hk * a.dk + x) : 0.0f;
+    }
+    const float vt = col < a.dv ? Elem<E>::ld(static_cast<const E*>(a.v), rr * a.ldv + static_cast<int64_t>(h) * a.dv + col) : 0.0f;
+    const float decay = a.gate ? exp2_(log2_decay(Elem<E>::ld(static_cast<const E*>(a.gate), rr * a.ldg + h), a.gate_kind)) : 1.0f;
+    const float eta = a.lr_max / (1.0f + __expf(-(Elem<E>::ld(static_cast<const E*>(a.beta), rr * a.ldb + h) + a.lr_bias)));
+    __syncthreads();
+    float e = 0.0f, kq = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float kr = ks[r * kStepRuns + run], qr = qs[r * kStepRuns + run];
+      S[r] *= decay;
+      e += kr * S[r];
+      o += qr * S[r];
+    }
+    part[0][run][c] = e;
+    part[1][run][c] = o;
+    __syncthreads();
+    e = vt;
+    o = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kStepRuns; ++j) {
+      e -= part[0][j][c];
+      o += part[1][j][c];
+    }
+    const float u = eta * e;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) S[r] += ks[r * kStepRuns + run] * u;
+    // o = S^T q = (the decayed state)^T q + (k.q) u
+    for (int x = 0; x < a.dk; ++x) kq += ks[x] * qs[x];
+    if (run == 0 && col < a.dv) Elem<E>::st(static_cast<E*>(a.o), (rr * a.H + h) * a.dv + col, a.scale * (o + kq * u));
+    __syncthreads();
+  };
+  token(b);
+  if (a.slots) {
+    for (int j0 = b + 1; j0 < a.B; j0 += kStepThreads) {
+      const int j = j0 + threadIdx.x;
+      const uint64_t hit = __ballot(j < a.B && a.slots[j] == slot);
+      if ((threadIdx.x & 63) == 0) same[threadIdx.x >> 6] = hit;
+      __syncthreads();
+      for (int w = 0; w < kStepThreads / 64; ++w)
+        for (uint64_t left = same[w]; left; left &= left - 1) token(j0 + w * 64 + __builtin_ctzll(left));
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = r * kStepRuns + run;
+    if (row < a.dk && col < a.dv) a.s_new[at + static_cast<int64_t>(row) * a.dv] = S[r];
+  }
+}
+
+template <typename F> hipError_t by_width(int dk, F&& f) {
+  if (dk <= 64) return f(std::integral_constant<int, 64>{});
+  if (dk <= 128) return f(std::integral_constant<int, 128>{});
+  return f(std::integral_constant<int, 256>{});
+}
+
+}  // namespace
+
+template <typename E, int DKP, bool BWD> hipError_t launch_prep(const Args& a, hipStream_t s) {
+  KernelScope scope(TTT_KERNEL_DELTA_PREP, s);
+  prep_kernel<E, DKP, BWD><<<static_cast<uint32_t>(a.chunks) * a.H, kPrepThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+template hipError_t launch_prep<bf16_t, 64, true>(const Args&, hipStream_t);
+template hipError_t launch_prep<bf16_t, 128, true>(const Args&, hipStream_t);
+template hipError_t launch_prep<bf16_t, 256, true>(const Args&, hipStream_t);
+template hipError_t launch_prep<float, 64, true>(const Args&, hipStream_t);
+template hipError_t launch_prep<float, 128, true>(const Args&, hipStream_t);
+template hipError_t launch_prep<float, 256, true>(const Args&, hipStream_t);
+
+}  // namespace delta
+
+namespace {
+
+using delta::Args;
+
+int chunk_tokens(int dtype) { return dtype == TTT_F32 ? delta::Chunk<float>::C : delta::Chunk<bf16_t>::C; }
+int64_t all_tokens(const ttt_delta_desc& d) { return d.packed ? d.T : static_cast<int64_t>(d.B) * d.T; }
+size_t elem_bytes(const ttt_delta_desc& d) { return d.dtype == TTT_F32 ? 4 : 2; }
+int padded_dk(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+size_t tri_bytes(const ttt_delta_desc& d) { return d.dtype == TTT_F32 ? delta::Tri<float>::kBytes : delta::Tri<bf16_t>::kBytes; }
+
+}  // namespace
+
+// Chunk slots: what the sequences take, or for packed ones the most that any lengths take.
+int64_t delta_chunks(const ttt_delta_desc& d) {
+  const int C = chunk_tokens(d.dtype);
+  if (!d.packed) return d.B * ((static_cast<int64_t>(d.T) + C - 1) / C);
+  const int64_t n = d.T;
+  return n == 0 ? 0 : n / C + (d.B < n ? d.B : n);
+}
+
+namespace {
+
+struct Layout {
+  size_t edge, base, table, vec, t, p, y, after, bytes;
+};
+Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
+  const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, C = chunk_tokens(d.dtype), e = elem_bytes(d);
+  const size_t dvp = (d.dv + 31) / 32 * 32;
+  Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += align256(bytes);
+    return was;
+  };
+  if (d.packed && items > 0) {
+    l.edge = take(sizeof(int) * (static_cast<size_t>(d.B) + 1));
+    l.base = take(sizeof(int) * (static_cast<size_t>(d.B) + 1));
+    l.table = take(sizeof(int4) * static_cast<size_t>(delta_chunks(d)));
+  }
+  l.vec = take(items * 3 * C * sizeof(float));
+  l.t = take(items * tri_bytes(d));
+  l.p = take(items * tri_bytes(d));
+  if (bwd) {
+    l.y = take(items * C * dvp * e);
+    l.after = take(items * padded_dk(d.dk) * dvp * e);
+  }
+  l.bytes = at;
+  return l;
+}
+
+Args make_args(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate, const void* beta, const void* d_o) {
+  Args a{};
+  a.B = d.B; a.T = d.T; a.H = d.H; a.Hk = d.Hk; a.dk = d.dk; a.dv = d.dv;
+  a.dvp = (d.dv + 31) / 32 * 32;
+  a.packed = d.packed; a.gate_kind = d.gate;
+  a.scale = d.scale; a.lr_max = d.lr_max; a.lr_bias = d.lr_bias;
+  a.n = all_tokens(d);
+  a.ldq = d.ldq ? d.ldq : static_cast<int64_t>(d.Hk) * d.dk;
+  a.ldk = d.ldk ? d.ldk : static_cast<int64_t>(d.Hk) * d.dk;
+  a.ldv = d.ldv ? d.ldv : static_cast<int64_t>(d.H) * d.dv;
+  a.ldg = d.ldg ? d.ldg : d.H;
+  a.ldb = d.ldb ? d.ldb : d.H;
+  const int V = 16 / static_cast<int>(elem_bytes(d));
+  auto wide = [&](const void* p, int width, int64_t ld) {
+    return width % V == 0 && ld % V == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  };
+  a.q = q; a.k = k; a.v = v; a.gate = gate; a.beta = beta; a.d_o = d_o;
+  a.wide_q = wide(q, d.dk, a.ldq);
+  a.wide_k = wide(k, d.dk, a.ldk);
+  a.wide_do = wide(d_o, d.dv, 0);
+  a.chunks = static_cast<int>(delta_chunks(d));
+  a.chunks_per_seq = d.packed ? 0 : (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype);
+  return a;
+}
+
+void place(Args& a, const ttt_delta_desc& d, const Layout& l, void* ws, const void* saved) {
+  char* w = static_cast<char*>(ws);
+  a.vec = reinterpret_cast<float*>(w + l.vec);
+  a.t = w + l.t;
+  a.p = w + l.p;
+  a.base = reinterpret_cast<const int*>(w + l.base);
+  a.table = reinterpret_cast<const int4*>(w + l.table);
+  if (saved) {
+    const size_t items = static_cast<size_t>(a.chunks) * a.H;
+    a.u = const_cast<char*>(static_cast<const char*>(saved));
+    a.before = static_cast<char*>(a.u) + align256(items * chunk_tokens(d.dtype) * a.dvp * elem_bytes(d));
+  }
+}
+
+hipError_t plan(const ttt_delta_desc& d, const Layout& l, const int32_t* starts, void* ws, hipStream_t s) {
+  char* w = static_cast<char*>(ws);
+  KernelScope scope(TTT_KERNEL_DELTA_PLAN, s);
+  delta::plan_kernel<<<1, delta::kPlanThreads, 0, s>>>(starts, d.B, d.T, chunk_tokens(d.dtype), static_cast<int>(delta_chunks(d)),
+                                                       reinterpret_cast<int*>(w + l.edge), reinterpret_cast<int*>(w + l.base),
+                                                       reinterpret_cast<int4*>(w + l.table));
+  return hipGetLastError();
+}
+
+// Without tokens every state passes through.
+__global__ void delta_pass_kernel(int64_t n, const float* src, float* dst) {
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) dst[i] = src ? src[i] : 0.0f;
+}
+hipError_t pass_states(const ttt_delta_desc& d, const float* src, float* dst, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(d.B) * d.H * d.dk * d.dv;
+  if (!dst || n == 0) return hipSuccess;
+  const int64_t blocks = (n + 255) / 256;
+  delta_pass_kernel<<<static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(n, src, dst);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t delta_workspace(const ttt_delta_desc& d, int entry) {
+  return delta_chunks(d) == 0 ? 0 : ws_layout(d, entry == TTT_ENTRY_BWD).bytes;
+}
+size_t delta_saved(const ttt_delta_desc& d) {
+  const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, e = elem_bytes(d), dvp = (d.dv + 31) / 32 * 32;
+  return align256(items * chunk_tokens(d.dtype) * dvp * e) + align256(items * padded_dk(d.dk) * dvp * e);
+}
+
+hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate, const void* beta,
+                            const float* s0, const int32_t* starts, void* o, float* s_final, void* saved, void* ws, hipStream_t s) {
+  Args a = make_args(d, q, k, v, gate, beta, nullptr);
+  if (a.n == 0) return pass_states(d, s0, s_final, s);
+  a.s0 = s0; a.o = o; a.s_final = s_final;
+  const Layout l = ws_layout(d, false);
+  place(a, d, l, ws, saved);
+  if (d.packed) {
+    const hipError_t e = plan(d, l, starts, ws, s);
+    if (e != hipSuccess) return e;
+  }
+  auto run = [&](auto elem, auto width) {
+    using E = decltype(elem);
+    constexpr int DKP = width();
+    hipError_t e = delta::launch_prep<E, DKP, false>(a, s);
+    if (e != hipSuccess) return e;
+    constexpr int W = 4;
+    const int groups = (a.dvp / 16 + W - 1) / W;
+    KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
+    delta::fwd_kernel<E, DKP, W><<<static_cast<uint32_t>(d.B) * d.H * groups, W * 64, 0, s>>>(a, groups);
+    return hipGetLastError();
+  };
+  return delta::by_width(d.dk, [&](auto width) { return d.dtype == TTT_F32 ? run(float{}, width) : run(bf16_t{}, width); });
+}
+
+hipError_t delta_bwd_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate, const void* beta,
+                            const int32_t* starts, const void* saved, const void* d_o, const float* d_sfinal, void* dq, void* dk,
+                            void* dv, void* dgate, void* dbeta, float* ds0, void* ws, hipStream_t s) {
+  Args a = make_args(d, q, k, v, gate, beta, d_o);
+  if (a.n == 0) return pass_states(d, d_sfinal, ds0, s);
+  a.d_sfinal = d_sfinal;
+  a.dq = dq; a.dk_out = dk; a.dv_out = dv; a.dgate = dgate; a.dbeta = dbeta; a.ds0 = ds0;
+  const Layout l = ws_layout(d, true);
+  place(a, d, l, ws, saved);
+  a.y = static_cast<char*>(ws) + l.y;
+  a.after = static_cast<char*>(ws) + l.after;
+  if (d.packed) {
+    const hipError_t e = plan(d, l, starts, ws, s);
+    if (e != hipSuccess) return e;
+  }
+  return delta::by_width(d.dk, [&](auto width) {
+    return d.dtype == TTT_F32 ? delta::launch_bwd<float, width()>(a, s) : delta::launch_bwd<bf16_t, width()>(a, s);
+  });
+}
+
+hipError_t delta_step_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate, const void* beta,
+                             const int32_t* slots, int n_states, const float* st, float* s_new, void* o, hipStream_t s) {
+  const Args b = make_args(d, q, k, v, gate, beta, nullptr);
+  delta::StepArgs a{d.B, d.H, d.Hk, d.dk, d.dv, d.gate, n_states, (d.dv + delta::kStepCols - 1) / delta::kStepCols,
+                    d.scale, d.lr_max, d.lr_bias, b.ldq, b.ldk, b.ldv, b.ldg, b.ldb, q, k, v, gate, beta, slots, st, s_new, o};
+  const uint32_t grid = static_cast<uint32_t>(d.B) * d.H * a.ncb;
+  KernelScope scope(TTT_KERNEL_DELTA_STEP, s);
+  return delta::by_width(d.dk, [&](auto width) {
+    constexpr int NR = width() / delta::kStepRuns;
+    if (d.dtype == TTT_F32) delta::step_kernel<float, NR><<<grid, delta::kStepThreads, 0, s>>>(a);
+    else delta::step_kernel<bf16_t, NR><<<grid, delta::kStepThreads, 0, s>>>(a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace ttt

@@ -1,0 +1,421 @@
+// Gated delta rule, backward (ttt_delta_common.h has the forward's formulas).  With dO and the gradient dS'
+// of the state that leaves a chunk, R_ij = e^{G_i - G_j} and P, T as in the forward:
+//   dU = P^T dO + e^{G_C - G} K dS';   Y = T^T dU;   dV = eta Y;
+//   dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y).
+// That much is walked through, in the forward's way with everything transposed.  The rest
+// is free of it, a chunk a workgroup: with X = scale R o (dO U^T) and M_ij = -eta_i R_ij Y_i.U_j (j < i),
+//   dQ = scale e^G dO S^T + X K;
+//   dK = [-e^G eta Y S^T + M K] + e^{G_C - G} U dS'^T + X^T Q + M^T K;
+//   deta_i = Y_i.e_i, so dbeta_i = (1 - sigmoid) Y_i.U_i.
+// Each G_i stands in R, e^G and e^{G_C - G}; what it gathers are row sums that are there already:
+//   dG_i = q_i.dq_i - k_i.dk_i + 2 k_i.[...]_i,  and dG_C also e^{G_C} <dS', S> + sum_i e^{G_C - G_i} k_i.(dS' u_i);
+// log a_t has the sum of dG_i over i >= t.  Terms that cancel in that sum come from the same rounded X, M, U
+// and dS', so they cancel to fp32.
+
+#include "ttt_delta_common.h"
+
+namespace ttt {
+namespace delta {
+namespace {
+
+template <typename E, int DKP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16;
+  using Lds = Tile<E, DKP>;
+  using TR = Tri<E>;
+  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) float vec[3 * C];
+  const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
+  const int h = chain % a.H, seq = chain / a.H, hk = h / (a.H / a.Hk);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
+  const bool in = col < a.dv, live = col < a.dvp;
+  const bool wq = a.wide_q, wk = a.wide_k;
+  const int first = a.packed ? a.base[seq] : seq * a.chunks_per_seq;
+  const int end = a.packed ? a.base[seq + 1] : first + a.chunks_per_seq;
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  f32x4_t S[ND];  // dS
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = state_row(t, g) + r;
+      S[t][r] = a.d_sfinal && in && row < a.dk ? a.d_sfinal[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
+    }
+  for (int chunk = end - 1; chunk >= first; --chunk) {
+    const Where w = locate<C>(a, chunk);
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    __syncthreads();
+    stage<E, C, DKP, WAVES * 64>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
+    stage<E, C, DKP, WAVES * 64>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+    for (int x = threadIdx.x; x < 3 * C; x += WAVES * 64) vec[x] = a.vec[item * 3 * C + x];
+    __syncthreads();
+    if (live) {
+      E* dst = static_cast<E*>(a.after) + item * DKP * a.dvp + col;
+#pragma unroll
+      for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Elem<E>::st(dst, static_cast<int64_t>(state_row(t, g) + r) * a.dvp, S[t][r]);
+    }
+    // e^{G_C - G} K dS', then + P^T dO
+    f32x4_t du[NT], go[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) du[mt] = zero4();
+#pragma unroll
+    for (int kp = 0; kp < DKP / 32; ++kp) {
+      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) du[mt] = mma(row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), s, du[mt]);
+    }
+    const E* dop = static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv + col;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      du[mt] *= *reinterpret_cast<const f32x4_t*>(vec + C + 16 * mt + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * g + r;
+        go[mt][r] = in && t < w.len ? Elem<E>::ld(dop, static_cast<int64_t>(t) * a.H * a.dv) : 0.0f;
+      }
+    }
+    const char* tp = a.t + item * TR::kBytes;
+    const char* pp = a.p + item * TR::kBytes;
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> s(go[2 * kp], go[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(tri_load2<E>(pp, TR::at_t(mt, kp)), s, du[mt]);
+    }
+    // Y = T^T dU
+    f32x4_t y[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) y[mt] = zero4();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> s(du[2 * kp], du[2 * kp + 1]);
+#pragma unroll
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri_load2<E>(tp, TR::at_t(mt, kp)), s, y[mt]);
+    }
+    const float decay = vec[C - 1];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
+    f32x4_t ey[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(vec + 16 * mt + 4 * g);
+      ey[mt] = y[mt] * *reinterpret_cast<const f32x4_t*>(vec + 2 * C + 16 * mt + 4 * g);
+      go[mt] *= gm * a.scale;
+      du[mt] = -(gm * ey[mt]);
+    }
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> s(go[2 * kp], go[2 * kp + 1]), n(du[2 * kp], du[2 * kp + 1]);
+#pragma unroll
+      for (int t = 0; t < ND; ++t) {
+        S[t] = mma(state_col<DKP>(Q, 32 * kp, t), s, S[t]);
+        S[t] = mma(state_col<DKP>(K, 32 * kp, t), n, S[t]);
+      }
+    }
+    E* vp = static_cast<E*>(a.dv_out) + w.token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * g + r;
+        if (in && t < w.len) Elem<E>::st(vp, t * a.ldv, ey[mt][r]);
+        if (live) Elem<E>::st(static_cast<E*>(a.y) + item * C * a.dvp + col, static_cast<int64_t>(t) * a.dvp, y[mt][r]);
+      }
+  }
+  if (a.ds0 && in) {
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_row(t, g) + r;
+        if (row < a.dk) a.ds0[state + static_cast<int64_t>(row) * a.dv + col] = S[t][r];
+      }
+  }
+}
+
+// ---- what does not depend on the walk ----
+
+constexpr int kGradThreads = 256, kSlab = 128;  // columns of dO, U and Y in LDS at a time
+
+template <typename E> __device__ __forceinline__ float dot8(typename Frag<E>::Raw a, typename Frag<E>::Raw b) {
+  float s = 0.0f;
+  if constexpr (std::is_same_v<E, float>) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += a.a[j] * b.a[j] + a.b[j] * b.b[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += from_bf(a[j]) * from_bf(b[j]);
+  }
+  return s;
+}
+
+// Four rows r0 .. r0 + 3 of column col0 + i, as a result tile has them.
+template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const bf16_t* lds, int r0, int col0) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  const int i = threadIdx.x & 15;
+  const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r0 + (i >> 2), col0 + 4 * (i & 3))));
+  f32x4_t f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = bf16_to_f32(static_cast<uint16_t>(x[j]));
+  return f;
+}
+template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const float* lds, int r0, int col0) {
+  f32x4_t f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = lds[Tile<float, NCOL>::at(r0 + j, col0 + (threadIdx.x & 15))];
+  return f;
+}
+
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+
+// A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
+// dK summed in registers.  For the triangular products wave w has row tile w, for the others a quarter
+// of the key channels.
+template <typename E, int DKP, bool SHARED>
+__global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = DKP / 64;
+  using Lds = Tile<E, DKP>;
+  using Slab = Tile<E, kSlab>;
+  using Sq = Tile<E, C>;
+  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
+  __shared__ __attribute__((aligned(16))) E dO[C * Slab::kRow];
+  __shared__ __attribute__((aligned(16))) E U[C * Slab::kRow];
+  __shared__ __attribute__((aligned(16))) E Y[C * Slab::kRow];
+  __shared__ __attribute__((aligned(16))) E X[C * Sq::kRow];
+  __shared__ __attribute__((aligned(16))) E M[C * Sq::kRow];
+  __shared__ double G[C];
+  __shared__ __attribute__((aligned(16))) float vec[3][C];  // e^G, e^{G_C - G}, eta
+  __shared__ float sums[4][4][C], energy[4], yu[C];
+  const int chunk = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.H / a.Hk;
+  const Where w = locate<C>(a, chunk);
+  if (w.len < 0) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const bool wq = a.wide_q, wk = a.wide_k, wo = a.wide_do;
+  stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
+  stage<E, C, DKP, kGradThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+  f32x4_t dq_sum[SHARED ? NT : 1][NJ], dk_sum[SHARED ? NT : 1][NJ];
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) dq_sum[mt][j] = dk_sum[mt][j] = zero4();
+  }
+  auto store = [&](const f32x4_t& dq, const f32x4_t& dk, int mt, int j) {
+    const int col = wave * (DKP / 4) + 16 * j + i;
+    if (col >= a.dk) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * mt + 4 * g + r;
+      if (t < w.len) {
+        Elem<E>::st(static_cast<E*>(a.dq) + w.token * a.ldq + hk * a.dk + col, t * a.ldq, dq[r]);
+        Elem<E>::st(static_cast<E*>(a.dk_out) + w.token * a.ldk + hk * a.dk + col, t * a.ldk, dk[r]);
+      }
+    }
+  };
+  for (int hs = 0; hs < (SHARED ? share : 1); ++hs) {
+    const int h = hk * share + hs;
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    float sig = 0.0f, z = 0.0f;  // of lane t's token, in wave 0
+    __syncthreads();
+    if (wave == 0) {
+      double Gt;
+      float eta;
+      gate_lane<E, C>(a, w, h, lane, Gt, eta, sig, z);
+      const double last = __shfl(Gt, C - 1, 64);
+      if (lane < C) {
+        G[lane] = Gt;
+        vec[0][lane] = exp2_(static_cast<float>(Gt));
+        vec[1][lane] = exp2_(static_cast<float>(last - Gt));
+        vec[2][lane] = eta;
+      }
+    }
+    f32x4_t xs[NT], ms[NT], dq[NT][NJ], dkr[NT][NJ], dks[NT][NJ];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      xs[mt] = ms[mt] = zero4();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) dq[mt][j] = dkr[mt][j] = dks[mt][j] = zero4();
+    }
+    float en = 0.0f;
+    for (int c0 = 0; c0 < a.dvp; c0 += kSlab) {
+      const int width = min(kSlab, a.dvp - c0);
+      if (c0 > 0) __syncthreads();
+      stage<E, C, kSlab, kGradThreads>(dO, static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv + c0, static_cast<int64_t>(a.H) * a.dv,
+                                       w.len, min(width, a.dv - c0), wo, width);
+      stage<E, C, kSlab, kGradThreads>(U, static_cast<const E*>(a.u) + item * C * a.dvp + c0, a.dvp, C, width, true, width);
+      stage<E, C, kSlab, kGradThreads>(Y, static_cast<const E*>(a.y) + item * C * a.dvp + c0, a.dvp, C, width, true, width);
+      __syncthreads();
+      if (wave < NT) {
+        for (int kp = 0; kp < width / 32; ++kp) {
+          const auto ox = row_frag<kSlab>(dO, 16 * wave + i, 32 * kp + 8 * g), yx = row_frag<kSlab>(Y, 16 * wave + i, 32 * kp + 8 * g);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt <= wave) {
+              const auto ux = row_frag<kSlab>(U, 16 * nt + i, 32 * kp + 8 * g);
+              xs[nt] = mma(ox, ux, xs[nt]);
+              ms[nt] = mma(yx, ux, ms[nt]);
+            }
+          }
+        }
+      }
+      for (int kp = 0; kp < width / 32; ++kp) {
+        typename Frag<E>::Raw sb[NJ], sa[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int64_t at = (item * DKP + wave * (DKP / 4) + 16 * j + i) * a.dvp + c0 + 32 * kp + 8 * g;
+          sb[j] = *reinterpret_cast<const typename Frag<E>::Raw*>(static_cast<const E*>(a.before) + at);
+          sa[j] = *reinterpret_cast<const typename Frag<E>::Raw*>(static_cast<const E*>(a.after) + at);
+          en += dot8<E>(sb[j], sa[j]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          const auto ox = row_frag<kSlab>(dO, 16 * mt + i, 32 * kp + 8 * g), yx = row_frag<kSlab>(Y, 16 * mt + i, 32 * kp + 8 * g);
+          const auto ux = row_frag<kSlab>(U, 16 * mt + i, 32 * kp + 8 * g);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            dq[mt][j] = mma(ox, sb[j], dq[mt][j]);
+            dkr[mt][j] = mma(yx, sb[j], dkr[mt][j]);
+            dks[mt][j] = mma(ux, sa[j], dks[mt][j]);
+          }
+        }
+      }
+    }
+    if (wave < NT) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * wave + 4 * g + r, col = 16 * nt + i;
+          const float d = row >= col ? exp2_(static_cast<float>(G[row] - G[col])) : 0.0f;
+          Elem<E>::st(X, Sq::at(row, col), row >= col ? a.scale * d * xs[nt][r] : 0.0f);
+          Elem<E>::st(M, Sq::at(row, col), row > col ? -vec[2][row] * d * ms[nt][r] : 0.0f);
+          if (row == col) yu[row] = ms[nt][r];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
+      const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
+      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
+      f32x4_t d1 = zero4(), d2 = zero4(), d3 = zero4(), d4 = zero4();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int c0 = wave * (DKP / 4) + 16 * j;
+        dq[mt][j] *= gm * a.scale;
+        dkr[mt][j] *= -(gm * et);
+        dks[mt][j] *= rest;
+#pragma unroll
+        for (int p = 0; p <= mt / 2; ++p) {
+          const auto kc = plain_col<DKP>(K, 32 * p, c0);
+          dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc, dq[mt][j]);
+          dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc, dkr[mt][j]);
+        }
+        const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0);
+        d1 += qv * dq[mt][j];
+        d3 += kv * dkr[mt][j];
+        d4 += kv * dks[mt][j];
+        f32x4_t dk = dkr[mt][j] + dks[mt][j];
+#pragma unroll
+        for (int p = mt / 2; p < NP; ++p) {
+          dk = mma(plain_col<C>(X, 32 * p, 16 * mt), plain_col<DKP>(Q, 32 * p, c0), dk);
+          dk = mma(plain_col<C>(M, 32 * p, 16 * mt), plain_col<DKP>(K, 32 * p, c0), dk);
+        }
+        d2 += kv * dk;
+        if constexpr (SHARED) {
+          dq_sum[mt][j] += dq[mt][j];
+          dk_sum[mt][j] += dk;
+        } else {
+          store(dq[mt][j], dk, mt, j);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float s1 = sum16(d1[r]), s2 = sum16(d2[r]), s3 = sum16(d3[r]), s4 = sum16(d4[r]);
+        if (i == 0) {
+          const int t = 16 * mt + 4 * g + r;
+          sums[wave][0][t] = s1;
+          sums[wave][1][t] = s2;
+          sums[wave][2][t] = s3;
+          sums[wave][3][t] = s4;
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) en += __shfl_xor(en, d, 64);
+    if (lane == 0) energy[wave] = en;
+    __syncthreads();
+    if (wave == 0) {
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, all = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        all += energy[v];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] += lane < C ? sums[v][s][lane] : 0.0f;
+      }
+      float dG = x[0] - x[1] + 2.0f * x[2], H = x[3];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) H += __shfl_xor(H, d, 64);
+#pragma unroll
+      for (int d = 1; d < C; d <<= 1) {
+        const float o = __shfl_down(dG, d, 64);
+        if (lane + d < C) dG += o;
+      }
+      if (lane < w.len) {
+        const int64_t row = w.token + lane;
+        Elem<E>::st(static_cast<E*>(a.dbeta), row * a.ldb + h, sig * yu[lane]);
+        if (a.dgate) {
+          float d = dG + vec[0][C - 1] * all + H;
+          if (a.gate_kind == TTT_GATE_SIGMOID) d *= 1.0f / (1.0f + __expf(z));
+          if (log2_decay(z, a.gate_kind) <= -150.0f) d = 0.0f;  // the decay itself is zero there
+          Elem<E>::st(static_cast<E*>(a.dgate), row * a.ldg + h, d);
+        }
+      }
+    }
+  }
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) store(dq_sum[mt][j], dk_sum[mt][j], mt, j);
+  }
+}
+
+}  // namespace
+
+template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t s) {
+  hipError_t e = launch_prep<E, DKP, true>(a, s);
+  if (e != hipSuccess) return e;
+  {
+    constexpr int W = 4;
+    const int groups = (a.dvp / 16 + W - 1) / W;
+    KernelScope scope(TTT_KERNEL_DELTA_BWD, s);
+    bwd_kernel<E, DKP, W><<<static_cast<uint32_t>(a.B) * a.H * groups, W * 64, 0, s>>>(a, groups);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  KernelScope scope(TTT_KERNEL_DELTA_GRAD, s);
+  const uint32_t grid = static_cast<uint32_t>(a.chunks) * a.Hk;
+  if (a.H == a.Hk) grad_kernel<E, DKP, false><<<grid, kGradThreads, 0, s>>>(a);
+  else grad_kernel<E, DKP, true><<<grid, kGradThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+template hipError_t launch_bwd<bf16_t, 64>(const Args&, hipStream_t);
+template hipError_t launch_bwd<bf16_t, 128>(const Args&, hipStream_t);
+template hipError_t launch_bwd<bf16_t, 256>(const Args&, hipStream_t);
+template hipError_t launch_bwd<float, 64>(const Args&, hipStream_t);
+template hipError_t launch_bwd<float, 128>(const Args&, hipStream_t);
+template hipError_t launch_bwd<float, 256>(const Args&, hipStream_t);
+
+}  // namespace delta
+}  // namespace ttt

@@ -1,0 +1,296 @@
+// Gated delta rule on gfx950: what its kernels share.
+//
+// Per head, with a_t = sigmoid(gate_t) or exp(gate_t) and eta_t = lr_max sigmoid(beta_t + b):
+//   e_t = v_t - a_t S_{t-1}^T k_t;  S_t = a_t S_{t-1} + eta_t k_t e_t^T;  o_t = scale S_t^T q_t.
+// A chunk of C tokens that starts from the state S, with G_i = sum_{j<=i} log a_j and
+// R_ij = e^{G_i - G_j}, has its updates u_i = eta_i e_i from one triangular system:
+//   (1 + A) U = eta (V - e^G K S),  A_ij = eta_i R_ij k_i.k_j  (j < i);
+//   O = scale (e^G Q S + (R o Q K^T) U);   S' = e^{G_C} S + K^T (e^{G_C - G} U).
+// T = (1 + A)^-1 and the scores P = scale R o Q K^T do not depend on the state: one kernel
+// forms them for every chunk at once, and only the products with S are walked through.
+// Columns of S do not meet, so a wave walks 16 of them with no other wave's help.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mfma_util.h"
+#include "ttt_device.h"
+#include "ttt_internal.h"
+
+namespace ttt {
+namespace delta {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+struct Args {
+  int B, T, H, Hk, dk, dv, dvp;  // dvp: dv rounded up to 32, the width of U, Y and the kept states
+  int packed, gate_kind;
+  int wide_q, wide_k, wide_do;   // whether every row of a head starts on 16 bytes
+  float scale, lr_max, lr_bias;
+  int64_t n;                     // tokens
+  int64_t ldq, ldk, ldv, ldg, ldb;
+  int chunks, chunks_per_seq;    // chunk slots; of a sequence (dense)
+  const int* base;               // packed: [B + 1] the sequences' first chunks
+  const int4* table;             // packed: [chunks] first token, tokens, sequence
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* gate;
+  const void* beta;
+  const float* s0;
+  void* o;
+  float* s_final;
+  float* vec;                    // [chunks][H][3][C]: e^G, e^{G_C - G}, eta
+  char* t;                       // [chunks][H] T, or its transpose, in operand order
+  char* p;                       // the same of the scores
+  void* u;                       // [chunks][H][C][dvp]
+  void* before;                  // [chunks][H][dkp][dvp]: the state that enters the chunk
+  void* y;                       // as u: T^T dU
+  void* after;                   // as before: the gradient of the state that leaves it
+  const void* d_o;
+  const float* d_sfinal;
+  void* dq;
+  void* dk_out;
+  void* dv_out;
+  void* dgate;
+  void* dbeta;
+  float* ds0;
+};
+
+// Tokens of a chunk.  64 bf16 rows of 128 are 16 KB; fp32 rows are twice that, and the
+// 256-channel backward keeps four such tiles in LDS.
+template <typename E> struct Chunk;
+template <> struct Chunk<bf16_t> { static constexpr int C = 64; };
+template <> struct Chunk<float> { static constexpr int C = 32; };
+
+struct Where {
+  int64_t token;  // first
+  int len, seq;
+};
+
+// A chunk's tokens; len < 0: the slot is empty.
+template <int C> __device__ __forceinline__ Where locate(const Args& a, int chunk) {
+  if (a.packed) {
+    const int4 w = a.table[chunk];
+    return {__builtin_amdgcn_readfirstlane(w.x), __builtin_amdgcn_readfirstlane(w.y), __builtin_amdgcn_readfirstlane(w.z)};
+  }
+  const int seq = chunk / a.chunks_per_seq, c = chunk % a.chunks_per_seq;
+  return {static_cast<int64_t>(seq) * a.T + c * C, min(C, a.T - c * C), seq};
+}
+
+// ---- tiles in LDS ----
+
+// A [rows][NCOL] tile: bf16 with swizzled 16-byte granules, fp32 with rows 16 bytes longer.
+template <typename E, int NCOL> struct Tile;
+template <int NCOL> struct Tile<bf16_t, NCOL> {
+  static constexpr int kRow = NCOL;
+  static __device__ __forceinline__ int at(int row, int col) { return swz<NCOL>(row, col); }
+};
+template <int NCOL> struct Tile<float, NCOL> {
+  static constexpr int kRow = NCOL + 4;
+  static __device__ __forceinline__ int at(int row, int col) { return row * kRow + col; }
+};
+
+// Rows 0 .. len - 1 and columns 0 .. nc - 1 of a row-major matrix into a tile of ROWS x NCOL; the
+// rest becomes zero.  wide: every row starts on 16 bytes and nc is a whole number of pieces.
+template <typename E, int ROWS, int NCOL, int THREADS>
+__device__ __forceinline__ void stage(E* lds, const E* src, int64_t ld, int len, int nc, bool wide, int width = NCOL) {
+  constexpr int V = 16 / sizeof(E);
+  if (wide) {
+    const int pieces = width / V;
+    for (int i = threadIdx.x; i < ROWS * pieces; i += THREADS) {
+      const int row = i / pieces, col = (i % pieces) * V;
+      uint4 x = {0, 0, 0, 0};
+      if (row < len && col < nc) x = *reinterpret_cast<const uint4*>(src + row * ld + col);
+      *reinterpret_cast<uint4*>(lds + Tile<E, NCOL>::at(row, col)) = x;
+    }
+  } else {
+    for (int i = threadIdx.x; i < ROWS * width; i += THREADS) {
+      const int row = i / width, col = i % width;
+      lds[Tile<E, NCOL>::at(row, col)] = row < len && col < nc ? src[row * ld + col] : E{};
+    }
+  }
+}
+
+// ---- matrix-core operands ----
+//
+// v_mfma_f32_16x16x32_bf16 and, for fp32, eight v_mfma_f32_16x16x4_f32: lane (i, g) = (l % 16,
+// l / 16) of an A operand holds eight k of row i, of a B operand eight k of column i; which
+// eight is free as long as A and B agree.  A result lane holds rows 4 g + r of column i, so two
+// result tiles, one above the other, are a B operand whose k are {4 g + 0..3, 16 + 4 g + 0..3}.
+// fp32 values that a bf16 product needs whole go in as two terms, x = hi + lo (2^-17 of x is lost).
+
+template <typename E> struct Frag;
+template <> struct Frag<bf16_t> { using Raw = bf16x8_t; };
+struct f32x8 { f32x4_t a, b; };
+template <> struct Frag<float> { using Raw = f32x8; };
+
+template <typename E> struct Split;  // eight fp32 values as an operand
+template <> struct Split<bf16_t> {
+  bf16x8_t hi, lo;
+  __device__ __forceinline__ Split() {}
+  __device__ __forceinline__ Split(f32x4_t x, f32x4_t y) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = j < 4 ? x[j & 3] : y[j & 3];
+      hi[j] = to_bf(f);
+      lo[j] = to_bf(f - from_bf(hi[j]));
+    }
+  }
+};
+template <> struct Split<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ Split() {}
+  __device__ __forceinline__ Split(f32x4_t x, f32x4_t y) : a(x), b(y) {}
+};
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(f32x4_t a, f32x4_t b, f32x4_t c) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x4_t mma(f32x8 a, f32x8 b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
+__device__ __forceinline__ f32x4_t mma(bf16x8_t a, bf16x8_t b, f32x4_t c) { return mfma16(a, b, c); }
+// a is exact in its type; b in two terms
+__device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Split<bf16_t>& b, f32x4_t c) { return mfma16(a, b.hi, mfma16(a, b.lo, c)); }
+__device__ __forceinline__ f32x4_t mma(f32x8 a, const Split<float>& b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
+// both in two terms
+__device__ __forceinline__ f32x4_t mma(const Split<bf16_t>& a, const Split<bf16_t>& b, f32x4_t c) {
+  return mfma16(a.hi, b.hi, mfma16(a.hi, b.lo, mfma16(a.lo, b.hi, c)));
+}
+__device__ __forceinline__ f32x4_t mma(const Split<float>& a, const Split<float>& b, f32x4_t c) {
+  return mfma16(a.b, b.b, mfma16(a.a, b.a, c));
+}
+__device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+// Eight consecutive columns of a row of a tile.
+template <int NCOL> __device__ __forceinline__ bf16x8_t row_frag(const bf16_t* lds, int row, int col) {
+  return *reinterpret_cast<const bf16x8_t*>(lds + Tile<bf16_t, NCOL>::at(row, col));
+}
+template <int NCOL> __device__ __forceinline__ f32x8 row_frag(const float* lds, int row, int col) {
+  const float* p = lds + Tile<float, NCOL>::at(row, col);
+  return {*reinterpret_cast<const f32x4_t*>(p), *reinterpret_cast<const f32x4_t*>(p + 4)};
+}
+// Rows r0 .. r0 + 3 and r1 .. r1 + 3 of a column.  Lane i's column is col4(i / 4) + i % 4, where
+// col4 is what the lane i' with i' % 4 = i / 4 gave as `piece`: ds_read_b64_tr_b16 hands lane
+// 4 a + b of each 16 lanes element b of the 8-byte pieces that lanes a, a + 4, a + 8, a + 12 name.
+template <int NCOL>
+__device__ __forceinline__ bf16x8_t col_frag(const bf16_t* lds, int r0, int r1, int piece, int /*col*/) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  const int i4 = (threadIdx.x & 15) >> 2;
+  const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r0 + i4, piece)));
+  const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r1 + i4, piece)));
+  typedef short v8s __attribute__((ext_vector_type(8)));
+  const v8s z = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8_t, z);
+}
+template <int NCOL>
+__device__ __forceinline__ f32x8 col_frag(const float* lds, int r0, int r1, int /*piece*/, int col) {
+  f32x8 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f.a[j] = lds[Tile<float, NCOL>::at(r0 + j, col)];
+    f.b[j] = lds[Tile<float, NCOL>::at(r1 + j, col)];
+  }
+  return f;
+}
+
+// The states' tiles: row 4 g + r of tile t is channel 32 (t / 2) + 8 g + 4 (t % 2) + r, so a pair of
+// tiles as a B operand has eight consecutive channels a lane.
+__device__ __forceinline__ int state_row(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
+// Column operand of tile t's rows over the tokens of a pair of token tiles (row 0 = token `tok`).
+template <int NCOL, typename E>
+__device__ __forceinline__ typename Frag<E>::Raw state_col(const E* lds, int tok, int t) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  return col_frag<NCOL>(lds, tok + 4 * g, tok + 16 + 4 * g, state_row(t, i & 3), state_row(t, i >> 2) + (i & 3));
+}
+// Column operand of columns col0 + i over rows row0 + 8 g + 0..7.
+template <int NCOL, typename E>
+__device__ __forceinline__ typename Frag<E>::Raw plain_col(const E* lds, int row0, int col0) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  return col_frag<NCOL>(lds, row0 + 8 * g, row0 + 8 * g + 4, col0 + 4 * (i & 3), col0 + i);
+}
+
+// ---- T and P in operand order ----
+//
+// An A operand of row tile mt over the pair kp of token tiles: lane (i, g) row 16 mt + i, columns
+// 32 kp + {4 g + 0..3, 16 + 4 g + 0..3}.  Only those that can hold a value are there: kp <= mt / 2 of a
+// lower triangle, kp >= mt / 2 of a transpose.  Each is 64 lanes of 16 bytes (hi, then lo) or 32 (fp32).
+template <typename E> struct Tri {
+  static constexpr int C = Chunk<E>::C, NP = C / 32, kFrags = NP * (NP + 1);
+  static constexpr int kFragBytes = 64 * 8 * sizeof(E);
+  static constexpr int kHalfBytes = kFrags * kFragBytes;                    // one term
+  static constexpr int kBytes = (sizeof(E) == 2 ? 2 : 1) * kHalfBytes;      // both
+  // The place of (mt, kp), kp <= mt / 2; a transpose's (mt, kp) goes where the mirrored pair's is.
+  static __device__ __forceinline__ int at(int mt, int kp) {
+    const int p = mt >> 1;
+    return p * (p + 1) + kp * 2 + (mt & 1);
+  }
+  static __device__ __forceinline__ int at_t(int mt, int kp) { return at(2 * (NP - 1 - (mt >> 1)) + (mt & 1), NP - 1 - kp); }
+};
+template <typename E> __device__ __forceinline__ typename Frag<E>::Raw tri_load(const char* base, int place) {
+  using R = typename Frag<E>::Raw;
+  return *reinterpret_cast<const R*>(base + place * Tri<E>::kFragBytes + (threadIdx.x & 63) * sizeof(R));
+}
+template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* base, int place) {
+  Split<E> s;
+  if constexpr (std::is_same_v<E, float>) {
+    const f32x8 f = tri_load<float>(base, place);
+    s.a = f.a;
+    s.b = f.b;
+  } else {
+    s.hi = tri_load<bf16_t>(base, place);
+    s.lo = tri_load<bf16_t>(base + Tri<bf16_t>::kHalfBytes, place);
+  }
+  return s;
+}
+
+// ---- gates ----
+
+// Log2 of the decay.  Below 2^-150 it is zero in fp32, and stays finite in the sums; a NaN stays one.
+__device__ __forceinline__ float log2_decay(float z, int kind) {
+  const float l = kind == TTT_GATE_LOG ? z : fminf(z, 0.0f) - log1pf(__expf(-fabsf(z)));
+  const float l2 = z != z ? z : l * 1.4426950408889634f;
+  return l2 < -150.0f ? -150.0f : l2;
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// One lane a token: the sum of log2 a up to it (in 64 bits: differences of far sums are exact enough for
+// fp32), and eta; tokens that are not there keep the sum and have eta = 0.
+template <typename E, int C>
+__device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, int t, double& G, float& eta, float& rest_sig, float& z) {
+  z = 0.0f;
+  eta = rest_sig = 0.0f;
+  double l = 0.0;
+  if (t < w.len) {
+    const int64_t row = w.token + t;
+    if (a.gate) {
+      z = Elem<E>::ld(static_cast<const E*>(a.gate), row * a.ldg + h);
+      l = log2_decay(z, a.gate_kind);
+    }
+    const float b = Elem<E>::ld(static_cast<const E*>(a.beta), row * a.ldb + h) + a.lr_bias;
+    eta = a.lr_max / (1.0f + __expf(-b));
+    rest_sig = 1.0f / (1.0f + __expf(b));
+  }
+#pragma unroll
+  for (int d = 1; d < C; d <<= 1) {
+    const double o = __shfl_up(l, d, 64);
+    if ((threadIdx.x & 63) >= d) l += o;
+  }
+  G = l;
+}
+
+// The chunks' T and P into the workspace (ttt_delta.hip; BWD: the transposes), and the backward's three
+// kernels (ttt_delta_bwd.hip).
+template <typename E, int DKP, bool BWD> hipError_t launch_prep(const Args& a, hipStream_t s);
+template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t s);
+
+}  // namespace delta
+}  // namespace ttt

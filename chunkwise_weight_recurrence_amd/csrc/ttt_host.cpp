@@ -761,3 +761,228 @@ int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const float* w, co
 }
 
 }  // extern "C"
+
+namespace {
+
+int check_delta_desc(const ttt_delta_desc* d) {
+  if (!d) return fail(TTT_ERR_INVALID_ARG, "desc is NULL");
+  if (d->B < 0 || d->T < 0) return fail(TTT_ERR_INVALID_ARG, "B, T must be >= 0 (got %d, %d)", d->B, d->T);
+  if (d->H < 1 || d->Hk < 1 || d->H % d->Hk != 0)
+    return fail(TTT_ERR_INVALID_ARG, "H, Hk must be >= 1 and Hk a divisor of H (got %d, %d)", d->H, d->Hk);
+  if (d->dk < 1 || d->dv < 1) return fail(TTT_ERR_INVALID_ARG, "dk, dv must be >= 1 (got %d, %d)", d->dk, d->dv);
+  if (d->packed != 0 && d->packed != 1) return fail(TTT_ERR_INVALID_ARG, "packed must be 0 or 1 (got %d)", d->packed);
+  if (d->dtype != TTT_F32 && d->dtype != TTT_BF16) return fail(TTT_ERR_INVALID_ARG, "invalid dtype %d", d->dtype);
+  if (d->gate != TTT_GATE_SIGMOID && d->gate != TTT_GATE_LOG) return fail(TTT_ERR_INVALID_ARG, "invalid gate %d", d->gate);
+  if (!std::isfinite(d->scale) || !std::isfinite(d->lr_max) || !std::isfinite(d->lr_bias))
+    return fail(TTT_ERR_INVALID_ARG, "scale, lr_max and lr_bias must be finite");
+  if (d->dk > kMaxDim || d->dv > kMaxDim)
+    return fail(TTT_ERR_UNSUPPORTED, "need dk, dv <= %d (got %d, %d)", kMaxDim, d->dk, d->dv);
+  const int64_t wk = static_cast<int64_t>(d->Hk) * d->dk, wv = static_cast<int64_t>(d->H) * d->dv;
+  if ((d->ldq != 0 && d->ldq < wk) || (d->ldk != 0 && d->ldk < wk) || (d->ldv != 0 && d->ldv < wv) ||
+      (d->ldg != 0 && d->ldg < d->H) || (d->ldb != 0 && d->ldb < d->H))
+    return fail(TTT_ERR_INVALID_ARG, "ldq, ldk, ldv, ldg, ldb must be 0 or at least a token's elements");
+  constexpr int64_t kMaxLd = 1 << 23;
+  const int64_t n = d->packed ? d->T : static_cast<int64_t>(d->B) * d->T;
+  // Tokens are counted in 32 bits, rounded up to whole chunks; a launch has fewer than 2^32 threads.
+  if (wk > kMaxLd || wv > kMaxLd || d->ldq > kMaxLd || d->ldk > kMaxLd || d->ldv > kMaxLd || d->ldg > kMaxLd || d->ldb > kMaxLd ||
+      n > INT32_MAX - 4095 || d->B > INT32_MAX - 4095 || static_cast<double>(d->B) * wv * d->dk > 4.0e12 ||
+      static_cast<double>(ttt::delta_chunks(*d)) * d->H >= 1 << 24 || static_cast<double>(d->B) * d->H * ((d->dv + 15) / 16) >= 1 << 24)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens, %d sequences of %d heads)", static_cast<long long>(n), d->B, d->H);
+  return TTT_OK;
+}
+
+// The first tensor whose pointer is no multiple of an element, or nullptr.
+const char* off_element(int dtype, std::initializer_list<std::pair<const char*, const void*>> ptrs) {
+  for (const auto& p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p.second) & (dtype == TTT_F32 ? 3u : 1u)) return p.first;
+  return nullptr;
+}
+
+int check_qknorm_desc(const ttt_qknorm_desc* d) {
+  if (!d) return fail(TTT_ERR_INVALID_ARG, "desc is NULL");
+  if (d->tokens < 0) return fail(TTT_ERR_INVALID_ARG, "tokens must be >= 0 (got %lld)", static_cast<long long>(d->tokens));
+  if (d->Hq < 1 || d->Hk < 0) return fail(TTT_ERR_INVALID_ARG, "need Hq >= 1, Hk >= 0 (got %d, %d)", d->Hq, d->Hk);
+  if (d->d < 1) return fail(TTT_ERR_INVALID_ARG, "d must be >= 1 (got %d)", d->d);
+  if (d->rot < 0 || d->rot > d->d || d->rot % 2 != 0)
+    return fail(TTT_ERR_INVALID_ARG, "rot must be even, 0 .. d (got %d of %d)", d->rot, d->d);
+  if (d->pairing != TTT_ROPE_HALF && d->pairing != TTT_ROPE_INTERLEAVED)
+    return fail(TTT_ERR_INVALID_ARG, "invalid pairing %d", d->pairing);
+  if (d->norm < TTT_HEADNORM_NONE || d->norm > TTT_HEADNORM_L2) return fail(TTT_ERR_INVALID_ARG, "invalid norm %d", d->norm);
+  if (d->period < 0) return fail(TTT_ERR_INVALID_ARG, "period must be >= 0 (got %d)", d->period);
+  if (d->dtype != TTT_F32 && d->dtype != TTT_BF16) return fail(TTT_ERR_INVALID_ARG, "invalid dtype %d", d->dtype);
+  if (!std::isfinite(d->eps) || d->eps < 0.0f) return fail(TTT_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!std::isfinite(d->rot_scale)) return fail(TTT_ERR_INVALID_ARG, "rot_scale must be finite");
+  const int64_t wq = static_cast<int64_t>(d->Hq) * d->d, wk = static_cast<int64_t>(d->Hk) * d->d;
+  if ((d->ldq != 0 && d->ldq < wq) || (d->ldk != 0 && d->ldk < wk))
+    return fail(TTT_ERR_INVALID_ARG, "ldq, ldk must be 0 or at least a token's elements (got %lld, %lld)",
+                static_cast<long long>(d->ldq), static_cast<long long>(d->ldk));
+  constexpr int64_t kMaxLd = 1 << 23;
+  if (d->d > 512 || wq > kMaxLd || wk > kMaxLd || d->ldq > kMaxLd || d->ldk > kMaxLd || d->tokens > INT32_MAX - 4095)
+    return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens of %d and %d heads of %d)", static_cast<long long>(d->tokens),
+                d->Hq, d->Hk, d->d);
+  return TTT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ttt_delta_workspace_size(const ttt_delta_desc* desc, int entry, size_t* bytes) {
+  const int st = check_delta_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  if (entry != TTT_ENTRY_FWD && entry != TTT_ENTRY_BWD)
+    return fail(TTT_ERR_INVALID_ARG, "invalid entry %d (0 = forward, 1 = backward)", entry);
+  *bytes = ttt::delta_workspace(*desc, entry);
+  return ok();
+}
+
+int ttt_delta_saved_size(const ttt_delta_desc* desc, size_t* bytes) {
+  const int st = check_delta_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ttt::delta_saved(*desc);
+  return ok();
+}
+
+int ttt_delta_fwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                  const void* beta, const float* s0, const int32_t* seq_starts, void* o, float* s_final, void* saved,
+                  void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_delta_desc(desc);
+  if (st != TTT_OK) return st;
+  const int64_t n = desc->packed ? desc->T : static_cast<int64_t>(desc->B) * desc->T;
+  if (n > 0 && desc->B > 0 && (!q || !k || !v || !beta || !o)) return fail(TTT_ERR_INVALID_ARG, "q, k, v, beta and o are required");
+  if (desc->packed ? !seq_starts && desc->B > 0 : seq_starts != nullptr)
+    return fail(TTT_ERR_INVALID_ARG, "seq_starts is required with packed sequences, and NULL without");
+  if (overlap(s0, s_final, sizeof(float) * desc->B * static_cast<size_t>(desc->H) * desc->dk * desc->dv))
+    return fail(TTT_ERR_INVALID_ARG, "s_final must not overlap s0");
+  if (const char* bad = off_element(desc->dtype, {{"q", q}, {"k", k}, {"v", v}, {"gate", gate}, {"beta", beta}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be aligned to its elements", bad);
+  if (const char* bad = misaligned({{"s0", s0}, {"seq_starts", seq_starts}, {"o", o}, {"s_final", s_final}, {"saved", saved},
+                                    {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const size_t need = ttt::delta_workspace(*desc, TTT_ENTRY_FWD);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  if (desc->B == 0 || (n == 0 && !s_final)) return ok();
+  const hipError_t e = ttt::delta_fwd_launch(*desc, q, k, v, gate, beta, s0, seq_starts, o, s_final, saved, ws,
+                                             static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_delta_fwd launch");
+  return ok();
+}
+
+int ttt_delta_bwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                  const void* beta, const int32_t* seq_starts, const void* saved, const void* d_o, const float* d_sfinal,
+                  void* dq, void* dk, void* dv, void* dgate, void* dbeta, float* ds0, void* ws, size_t ws_bytes,
+                  void* stream) {
+  const int st = check_delta_desc(desc);
+  if (st != TTT_OK) return st;
+  const int64_t n = desc->packed ? desc->T : static_cast<int64_t>(desc->B) * desc->T;
+  if (n > 0 && desc->B > 0 && (!q || !k || !v || !beta || !saved || !d_o || !dq || !dk || !dv || !dbeta))
+    return fail(TTT_ERR_INVALID_ARG, "q, k, v, beta, saved, d_o, dq, dk, dv and dbeta are required");
+  if (n > 0 && desc->B > 0 && !gate != !dgate) return fail(TTT_ERR_INVALID_ARG, "gate and dgate go together");
+  if (desc->packed ? !seq_starts && desc->B > 0 : seq_starts != nullptr)
+    return fail(TTT_ERR_INVALID_ARG, "seq_starts is required with packed sequences, and NULL without");
+  if (overlap(d_sfinal, ds0, sizeof(float) * desc->B * static_cast<size_t>(desc->H) * desc->dk * desc->dv))
+    return fail(TTT_ERR_INVALID_ARG, "ds0 must not overlap d_sfinal");
+  if (const char* bad = off_element(desc->dtype, {{"q", q}, {"k", k}, {"v", v}, {"gate", gate}, {"beta", beta}, {"dq", dq},
+                                                  {"dk", dk}, {"dv", dv}, {"dgate", dgate}, {"dbeta", dbeta}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be aligned to its elements", bad);
+  if (const char* bad = misaligned({{"seq_starts", seq_starts}, {"saved", saved}, {"d_o", d_o}, {"d_sfinal", d_sfinal},
+                                    {"ds0", ds0}, {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const size_t need = ttt::delta_workspace(*desc, TTT_ENTRY_BWD);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  if (desc->B == 0 || (n == 0 && !ds0)) return ok();
+  const hipError_t e = ttt::delta_bwd_launch(*desc, q, k, v, gate, beta, seq_starts, saved, d_o, d_sfinal, dq, dk, dv, dgate,
+                                             dbeta, ds0, ws, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_delta_bwd launch");
+  return ok();
+}
+
+int ttt_delta_step(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                   const void* beta, const int32_t* slots, int n_states, const float* s, float* s_new, void* o,
+                   void* stream) {
+  const int st = check_delta_desc(desc);
+  if (st != TTT_OK) return st;
+  if (desc->T != 1 || desc->packed) return fail(TTT_ERR_INVALID_ARG, "a step has T = 1 and packed = 0");
+  if (n_states < 0) return fail(TTT_ERR_INVALID_ARG, "n_states must be >= 0 (got %d)", n_states);
+  if (!slots && n_states < desc->B)
+    return fail(TTT_ERR_INVALID_ARG, "without slots n_states must be >= B (got %d, %d)", n_states, desc->B);
+  const double state = static_cast<double>(desc->H) * desc->dk * desc->dv;
+  if (n_states * state > 4.0e12) return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d states)", n_states);
+  // Each row looks for its slot among all others: 2^24 rows would hold the GPU for minutes.
+  if (slots && desc->B > 1 << 20) return fail(TTT_ERR_UNSUPPORTED, "problem too large (%d rows with slots)", desc->B);
+  if (desc->B == 0) return ok();
+  if (!q || !k || !v || !beta || !s || !s_new || !o)
+    return fail(TTT_ERR_INVALID_ARG, "q, k, v, beta, s, s_new and o are required");
+  if (s != s_new && overlap(s, s_new, sizeof(float) * static_cast<size_t>(n_states * state)))
+    return fail(TTT_ERR_INVALID_ARG, "s_new must be s or not overlap it");
+  if (const char* bad = off_element(desc->dtype, {{"q", q}, {"k", k}, {"v", v}, {"gate", gate}, {"beta", beta}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be aligned to its elements", bad);
+  if (const char* bad = misaligned({{"slots", slots}, {"s", s}, {"s_new", s_new}, {"o", o}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const hipError_t e = ttt::delta_step_launch(*desc, q, k, v, gate, beta, slots, n_states, s, s_new, o,
+                                              static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_delta_step launch");
+  return ok();
+}
+
+int ttt_qknorm_fwd(const ttt_qknorm_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const int32_t* positions, const float* inv_freq, void* yq, void* yk, void* stream) {
+  const int st = check_qknorm_desc(desc);
+  if (st != TTT_OK) return st;
+  if (desc->tokens == 0) return ok();
+  if (!q || !yq || (desc->Hk > 0 && (!k || !yk))) return fail(TTT_ERR_INVALID_ARG, "q, yq, and with Hk > 0 k and yk are required");
+  if (desc->rot > 0 && !inv_freq) return fail(TTT_ERR_INVALID_ARG, "inv_freq is required with rot > 0");
+  const bool strided_q = desc->ldq != 0 && desc->ldq != static_cast<int64_t>(desc->Hq) * desc->d;
+  const bool strided_k = desc->ldk != 0 && desc->ldk != static_cast<int64_t>(desc->Hk) * desc->d;
+  if ((yq == q && strided_q) || (desc->Hk > 0 && yk == k && strided_k))
+    return fail(TTT_ERR_INVALID_ARG, "yq may be q, and yk k, only where they are dense");
+  if (const char* bad = off_element(desc->dtype, {{"q", q}, {"k", k}, {"yq", yq}, {"yk", yk}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be aligned to its elements", bad);
+  if (const char* bad = misaligned({{"wq", wq}, {"wk", wk}, {"positions", positions}, {"inv_freq", inv_freq}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  const hipError_t e = ttt::qknorm_fwd_launch(*desc, q, k, wq, wk, positions, inv_freq, yq, yk, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_qknorm_fwd launch");
+  return ok();
+}
+
+int ttt_qknorm_workspace_size(const ttt_qknorm_desc* desc, size_t* bytes) {
+  const int st = check_qknorm_desc(desc);
+  if (st != TTT_OK) return st;
+  if (!bytes) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ttt::qknorm_workspace(*desc);
+  return ok();
+}
+
+int ttt_qknorm_bwd(const ttt_qknorm_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const int32_t* positions, const float* inv_freq, const void* dyq, const void* dyk, void* dq, void* dk,
+                   float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_qknorm_desc(desc);
+  if (st != TTT_OK) return st;
+  if (desc->tokens > 0) {
+    if (!q || !dyq || !dq || (desc->Hk > 0 && (!k || !dyk || !dk)))
+      return fail(TTT_ERR_INVALID_ARG, "q, dyq, dq, and with Hk > 0 k, dyk and dk are required");
+    if (desc->rot > 0 && !inv_freq) return fail(TTT_ERR_INVALID_ARG, "inv_freq is required with rot > 0");
+  }
+  if (const char* bad = off_element(desc->dtype, {{"q", q}, {"k", k}, {"dyq", dyq}, {"dyk", dyk}, {"dq", dq}, {"dk", dk}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be aligned to its elements", bad);
+  if (const char* bad = misaligned({{"wq", wq}, {"wk", wk}, {"positions", positions}, {"inv_freq", inv_freq}, {"dwq", dwq},
+                                    {"dwk", dwk}, {"ws", ws}}))
+    return fail(TTT_ERR_INVALID_ARG, "%s must be 16-byte aligned", bad);
+  if (dwq || dwk) {
+    const size_t need = ttt::qknorm_workspace(*desc);
+    if (!ws || ws_bytes < need)
+      return fail(TTT_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, ws_bytes, ws ? "" : " (NULL)");
+  } else if (desc->tokens == 0) {
+    return ok();
+  }
+  const hipError_t e = ttt::qknorm_bwd_launch(*desc, q, k, wq, wk, positions, inv_freq, dyq, dyk, dq, dk, dwq, dwk, ws,
+                                              static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "ttt_qknorm_bwd launch");
+  return ok();
+}
+
+}  // extern "C"

@@ -179,6 +179,29 @@ hipError_t layernorm_bwd_launch(const ttt_ln_desc& d, const void* x, const float
                                 const float* rstd, const void* dy, const void* dr, void* dx, float* dw, float* db,
                                 void* ws, hipStream_t s);
 
+// ---- gated delta rule (ttt_delta.hip, ttt_delta_bwd.hip) ----
+int64_t delta_chunks(const ttt_delta_desc& d);
+size_t delta_workspace(const ttt_delta_desc& d, int entry);
+size_t delta_saved(const ttt_delta_desc& d);
+hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate,
+                            const void* beta, const float* s0, const int32_t* starts, void* o, float* s_final,
+                            void* saved, void* ws, hipStream_t s);
+hipError_t delta_bwd_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate,
+                            const void* beta, const int32_t* starts, const void* saved, const void* d_o,
+                            const float* d_sfinal, void* dq, void* dk, void* dv, void* dgate, void* dbeta, float* ds0,
+                            void* ws, hipStream_t s);
+hipError_t delta_step_launch(const ttt_delta_desc& d, const void* q, const void* k, const void* v, const void* gate,
+                             const void* beta, const int32_t* slots, int n_states, const float* st, float* s_new,
+                             void* o, hipStream_t s);
+
+// ---- norm and rotation of queries and keys (ttt_qknorm.hip) ----
+size_t qknorm_workspace(const ttt_qknorm_desc& d);
+hipError_t qknorm_fwd_launch(const ttt_qknorm_desc& d, const void* q, const void* k, const float* wq, const float* wk,
+                             const int32_t* pos, const float* freq, void* yq, void* yk, hipStream_t s);
+hipError_t qknorm_bwd_launch(const ttt_qknorm_desc& d, const void* q, const void* k, const float* wq, const float* wk,
+                             const int32_t* pos, const float* freq, const void* dyq, const void* dyk, void* dq, void* dk,
+                             float* dwq, float* dwk, void* ws, hipStream_t s);
+
 // Brackets one kernel launch with HIP events on its stream while per-kernel
 // timing is on; does nothing otherwise.
 class KernelScope {

@@ -312,3 +312,99 @@ class LayerNormBuffers:
         """Fills dx (also the residual's gradient), dw and db."""
         B.ttt_layernorm_bwd(self.desc_bwd, self.x if self.r is None else self.r, self.w, self.mean, self.rstd, dy, dr,
                             self.dx, self.dw, self.db, self.ws, stream=stream)
+
+
+def _token_distance(x):
+    """Elements from one token of ``x`` ([..., H, d], the heads of a token side by side) to the next."""
+    H, d = x.shape[-2:]
+    if (H > 1 and x.stride(-2) != d) or (d > 1 and x.stride(-1) != 1):
+        raise ValueError(f"the heads of a token must lie side by side (got shape {tuple(x.shape)}, strides {x.stride()})")
+    if x.numel() > 0:
+        for i in range(x.dim() - 3, -1, -1):
+            if x.shape[i] > 1:
+                return x.stride(i)
+    return H * d
+
+
+class DeltaBuffers:
+    """Outputs and workspace of the gated delta rule over q, k [B,T,Hk,dk] and v [B,T,H,dv], or packed [T,Hk,dk], [T,H,dv].
+
+    Device tensors whose tokens may be strided (slices of one projection).
+    ``gate`` ([..,H], or None for no decay) and ``beta`` ([..,H]).  ``seq_starts``:
+    int32 device tensor of B + 1 positions for packed sequences.  ``s0``:
+    [B,H,dk,dv] float32 or None."""
+
+    def __init__(self, q, k, v, gate, beta, kind="sigmoid", s0=None, seq_starts=None, scale=None, lr_max=1.0, lr_bias=0.0,
+                 with_bwd=False):
+        torch = _torch()
+        packed = seq_starts is not None
+        lead = 1 if packed else 2
+        if q.dim() != lead + 2 or k.shape != q.shape or v.dim() != lead + 2 or v.shape[:lead] != q.shape[:lead]:
+            raise ValueError(f"q and k must be {'[T,Hk,dk]' if packed else '[B,T,Hk,dk]'} and v {'[T,H,dv]' if packed else '[B,T,H,dv]'} "
+                             f"(got shapes {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)})")
+        for name, x in (("gate", gate), ("beta", beta)):
+            if x is not None and x.shape != v.shape[:-1]:
+                raise ValueError(f"{name} must have shape {tuple(v.shape[:-1])} (got {tuple(x.shape)})")
+        Hk, dk = q.shape[-2:]
+        H, dv = v.shape[-2:]
+        Bn, T = (seq_starts.numel() - 1, q.shape[0]) if packed else q.shape[:2]
+        f32, d = torch.float32, q.device
+        self.q, self.k, self.v, self.gate, self.beta, self.s0, self.seq_starts = q, k, v, gate, beta, s0, seq_starts
+        self.desc = B.make_delta_desc(Bn, T, H, dk, dv, Hk=Hk, dtype="bf16" if q.dtype == torch.bfloat16 else "f32", gate=kind,
+                                      packed=packed, scale=scale, lr_max=lr_max, lr_bias=lr_bias, ldq=_token_distance(q),
+                                      ldk=_token_distance(k), ldv=_token_distance(v),
+                                      ldg=0 if gate is None else _row_distance(gate), ldb=_row_distance(beta))
+        self.o = torch.empty(v.shape, dtype=v.dtype, device=d)
+        self.s_final = torch.empty((Bn, H, dk, dv), dtype=f32, device=d)
+        size = B.ttt_delta_workspace_size(self.desc, B.ENTRY_FWD)
+        self.saved = None
+        if with_bwd:
+            size = max(size, B.ttt_delta_workspace_size(self.desc, B.ENTRY_BWD))
+            self.saved = torch.empty(B.ttt_delta_saved_size(self.desc), dtype=torch.uint8, device=d)
+            self.dq, self.dk, self.dv, self.dbeta = (torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=d)
+                                                     for x in (q, k, v, beta))
+            self.dgate = None if gate is None else torch.empty_strided(gate.shape, gate.stride(), dtype=gate.dtype, device=d)
+            self.ds0 = torch.empty((Bn, H, dk, dv), dtype=f32, device=d)
+        self.ws = torch.empty(max(size, 1), dtype=torch.uint8, device=d)
+
+    def forward(self, stream=None):
+        B.ttt_delta_fwd(self.desc, self.q, self.k, self.v, self.gate, self.beta, self.s0, self.seq_starts, self.o, self.s_final,
+                        self.saved, self.ws, stream=stream)
+
+    def backward(self, d_o, d_sfinal=None, stream=None):
+        """Fills dq, dk, dv, dgate and dbeta (with the strides of q, k, v, gate and beta) and ds0."""
+        B.ttt_delta_bwd(self.desc, self.q, self.k, self.v, self.gate, self.beta, self.seq_starts, self.saved, d_o, d_sfinal,
+                        self.dq, self.dk, self.dv, self.dgate, self.dbeta, self.ds0, self.ws, stream=stream)
+
+
+class QkNormBuffers:
+    """Outputs and workspace of the norm and rotation of q [..,Hq,d] and k [..,Hk,d] (tokens may be strided).
+
+    ``wq``, ``wk``: [d] float32 or None; ``positions``: int32 [tokens] or None (then token t is at t % period);
+    ``inv_freq``: float32 [rot / 2] or None for no rotation."""
+
+    def __init__(self, q, k, wq=None, wk=None, positions=None, inv_freq=None, norm="rms", pairing="half", period=0, eps=1e-6,
+                 rot_scale=1.0, with_bwd=False):
+        torch = _torch()
+        if q.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+            raise ValueError(f"q and k must be [..,Hq,d] and [..,Hk,d] (got shapes {tuple(q.shape)}, {tuple(k.shape)})")
+        f32, d = torch.float32, q.device
+        self.q, self.k, self.wq, self.wk, self.positions, self.inv_freq = q, k, wq, wk, positions, inv_freq
+        rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+        self.desc = B.make_qknorm_desc(math.prod(q.shape[:-2]), q.shape[-2], k.shape[-2], q.shape[-1], rot=rot, pairing=pairing,
+                                       norm=norm, dtype="bf16" if q.dtype == torch.bfloat16 else "f32", period=period, eps=eps,
+                                       rot_scale=rot_scale, ldq=_token_distance(q), ldk=_token_distance(k))
+        self.yq, self.yk = (torch.empty(x.shape, dtype=x.dtype, device=d) for x in (q, k))
+        if with_bwd:
+            self.dq, self.dk = (torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=d) for x in (q, k))
+            self.dwq, self.dwk = (None if w is None else torch.empty(q.shape[-1], dtype=f32, device=d) for w in (wq, wk))
+            self.ws = torch.empty(B.ttt_qknorm_workspace_size(self.desc), dtype=torch.uint8, device=d)
+
+    def forward(self, stream=None):
+        B.ttt_qknorm_fwd(self.desc, self.q, self.k, self.wq, self.wk, self.positions, self.inv_freq, self.yq, self.yk,
+                         stream=stream)
+
+    def backward(self, dyq, dyk, stream=None):
+        """Fills dq and dk (with the strides of q and k), dwq and dwk."""
+        B.ttt_qknorm_bwd(self.desc, self.q, self.k, self.wq, self.wk, self.positions, self.inv_freq, dyq, dyk, self.dq, self.dk,
+                         self.dwq, self.dwk, self.ws, stream=stream)

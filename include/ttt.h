@@ -28,7 +28,9 @@
  *     per-(batch, head) sequences are [B, H, T, d].  Every tensor other than
  *     beta, gamma, dbeta and dgamma, and the workspace and saved context, must
  *     start on a 16-byte boundary (rows are moved in 16-byte pieces); a
- *     misaligned pointer is rejected with TTT_ERR_INVALID_ARG.
+ *     misaligned pointer is rejected with TTT_ERR_INVALID_ARG.  (The gated delta
+ *     rule and the norm of queries and keys take slices of a projection: what they
+ *     say needs a boundary of its elements only.)
  *   - Results are deterministic: no floating-point atomics are used.
  */
 #ifndef TTT_H
@@ -593,6 +595,159 @@ TTT_API int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const floa
                               const float* rstd, const void* dy, const void* dr, void* dx, float* dw, float* db,
                               void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Gated delta rule: the fast-weight Linear with a gradient step a token (MSE loss,
+ * no act), and a decay before it.  Per sequence and value head, from S = s0:
+ *   a_t = Sigmoid(gate_t) (TTT_GATE_SIGMOID), exp(gate_t) (TTT_GATE_LOG, gate <= 0), or 1;
+ *   eta_t = lr_max Sigmoid(beta_t + lr_bias);
+ *   S <- a_t S;  e_t = v_t - S^T k_t;  S <- S + eta_t k_t e_t^T;  o_t = scale S^T q_t.
+ * Queries and keys may have fewer heads: value head h uses head h / (H / Hk).
+ * S is kept in float32.  In bf16 the products that make it take their operands in
+ * two bf16 terms (2^-17 of a value is lost), and those that only read it to form
+ * o or a gradient one.  A decay below 2^-150 counts as 2^-150, with no gradient.
+ * An infinity may go on as NaN in its own sequence; no value reaches another one.
+ */
+typedef struct {
+  int32_t B;      /* sequences (rows of one token each for ttt_delta_step)           */
+  int32_t T;      /* tokens of each; packed: token rows of the buffers               */
+  int32_t H;      /* value heads                                                     */
+  int32_t Hk;     /* query and key heads, a divisor of H                             */
+  int32_t dk, dv; /* 1 .. 256; S is dk x dv                                          */
+  int32_t packed; /* 0: q is [B,T,Hk,dk]; 1: q is [T,Hk,dk], the sequences one behind the other */
+  int32_t dtype;  /* ttt_dtype of q, k, v, gate, beta, o and their gradients         */
+  int32_t gate;   /* ttt_rec_gate                                                    */
+  float scale;    /* of o                                                            */
+  float lr_max;   /* eta's upper end: 1, or 2 as the fast-weight layer has it        */
+  float lr_bias;
+  int64_t ldq, ldk, ldv; /* elements from one token's q (k, v) to the next, the heads of a
+                     token side by side; 0 means dense; up to 2^23                   */
+  int64_t ldg, ldb; /* the same for gate and beta, [..,H]                            */
+} ttt_delta_desc;
+
+/*
+ * ttt_delta_workspace_size -- bytes of device workspace of ttt_delta_fwd
+ * (TTT_ENTRY_FWD) or ttt_delta_bwd (TTT_ENTRY_BWD).  ttt_delta_saved_size -- bytes of
+ * the saved context: the state at the start of each chunk of tokens (64 in bf16, 32 in
+ * fp32) and the updates eta e.  Both write *bytes (0 is possible) and return TTT_OK, or a
+ * negative status for an invalid desc.
+ */
+TTT_API int ttt_delta_workspace_size(const ttt_delta_desc* desc, int entry, size_t* bytes);
+TTT_API int ttt_delta_saved_size(const ttt_delta_desc* desc, size_t* bytes);
+
+/*
+ * ttt_delta_fwd -- the rule over whole sequences.  Outputs overlap neither inputs nor
+ * each other (here and in ttt_delta_bwd).
+ *   q, k       [B,T,Hk,dk] or [T,Hk,dk] dtype, tokens ldq / ldk apart
+ *   v          [B,T,H,dv] or [T,H,dv] dtype, tokens ldv apart
+ *   gate       [..,H] dtype, tokens ldg apart, or NULL (a = 1);  beta the same, ldb apart
+ *              (q, k, v, gate and beta start on a boundary of their elements, and so do
+ *              their gradients; the other tensors on 16 bytes)
+ *   s0         [B,H,dk,dv] f32 or NULL (zero)
+ *   seq_starts DEVICE array [B+1] int32, ascending (packed only, else NULL), as in
+ *              ttt_recurrence_fwd: sequences may be empty, rows of none are left as
+ *              they were.  The contents are not checked: entries are held to 0 .. T and
+ *              an entry below one before it counts as that one
+ *   o          [B,T,H,dv] or [T,H,dv] dtype, dense (written)
+ *   s_final    [B,H,dk,dv] f32 or NULL (written; s0 for an empty sequence)
+ *   saved      ttt_delta_saved_size bytes, or NULL (no backward)
+ *   ws, ws_bytes  at least ttt_delta_workspace_size bytes; calls that may run at the
+ *              same time need one each
+ * Calls may be captured into a graph.
+ */
+TTT_API int ttt_delta_fwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                          const void* beta, const float* s0, const int32_t* seq_starts, void* o, float* s_final,
+                          void* saved, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ttt_delta_bwd -- gradients of <d_o, O> + <d_sfinal, s_final>.
+ *   q, k, v, gate, beta, seq_starts  as passed to ttt_delta_fwd
+ *   saved      what ttt_delta_fwd wrote for the same desc and inputs (read, not checked)
+ *   d_o        as o;  d_sfinal [B,H,dk,dv] f32 or NULL (zero)
+ *   dq, dk, dv, dgate, dbeta  as q, k, v, gate and beta, with their distances (written;
+ *              shared heads' gradients are summed; dgate NULL where gate is)
+ *   ds0        [B,H,dk,dv] f32 or NULL (written)
+ */
+TTT_API int ttt_delta_bwd(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                          const void* beta, const int32_t* seq_starts, const void* saved, const void* d_o,
+                          const float* d_sfinal, void* dq, void* dk, void* dv, void* dgate, void* dbeta, float* ds0,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ttt_delta_step -- one token for each of B running sequences (T must be 1, packed 0),
+ * in float32 throughout.
+ *   q, k, v, gate, beta  as in ttt_delta_fwd with T = 1;  o [B,H,dv] dtype (written)
+ *   slots    DEVICE array [B] int32: the state of each row, or NULL (row b has state b;
+ *            then n_states >= B).  A row whose slot is not in 0 .. n_states - 1 is
+ *            padding: its o and every state are left as they were.  Rows with the same
+ *            slot are consecutive tokens of it, in row order.  B is up to 2^20
+ *   s        [n_states,H,dk,dv] f32: the states before
+ *   s_new    [n_states,H,dk,dv] f32: those of the rows' slots are written.  It may be s
+ *            (updated in place); else the two do not overlap, and s keeps the old states,
+ *            for a program that may take tokens back
+ * No workspace.
+ */
+TTT_API int ttt_delta_step(const ttt_delta_desc* desc, const void* q, const void* k, const void* v, const void* gate,
+                           const void* beta, const int32_t* slots, int n_states, const float* s, float* s_new, void* o,
+                           void* stream);
+
+/*
+ * Norm and position rotation of queries and keys, each head's row by itself, in one
+ * pass over both.  With x a row of d values:
+ *   h = x (NONE), x / sqrt(mean(x^2) + eps) (RMS) or x / sqrt(sum(x^2) + eps) (L2: unit
+ *   keys, as the delta rule wants them);  z = w (.) h;
+ *   y = z with its first rot columns turned, pair j by the angle pos * inv_freq_j:
+ *   (z_a, z_b) -> rot_scale (z_a cos - z_b sin, z_a sin + z_b cos).
+ * HALF: pair j is columns (j, j + rot / 2); INTERLEAVED: (2 j, 2 j + 1).  Contexts
+ * stretched by any rule come in as inv_freq and rot_scale.  Angles are formed in 64
+ * bits, so they are exact at any position.
+ */
+typedef enum { TTT_HEADNORM_NONE = 0, TTT_HEADNORM_RMS = 1, TTT_HEADNORM_L2 = 2 } ttt_headnorm;
+typedef enum { TTT_ROPE_HALF = 0, TTT_ROPE_INTERLEAVED = 1 } ttt_rope_pairs;
+
+typedef struct {
+  int64_t tokens; /* 0 .. 2^31 - 4096                                                */
+  int64_t ldq, ldk; /* elements from one token's q (k) to the next; 0 means dense; up to 2^23 */
+  int32_t Hq, Hk; /* heads of q (>= 1) and of k (>= 0)                               */
+  int32_t d;      /* 1 .. 512                                                        */
+  int32_t rot;    /* columns that are turned: even, 0 .. d                           */
+  int32_t pairing; /* ttt_rope_pairs                                                 */
+  int32_t norm;   /* ttt_headnorm                                                    */
+  int32_t period; /* without positions token t is at t % period (0: at t)            */
+  int32_t dtype;  /* ttt_dtype of q, k, y and their gradients                        */
+  float eps;      /* >= 0                                                            */
+  float rot_scale; /* of the turned columns                                          */
+} ttt_qknorm_desc;
+
+/*
+ * ttt_qknorm_fwd
+ *   q, k       [tokens,Hq,d], [tokens,Hk,d] dtype, tokens ldq / ldk apart (these, yq, yk and
+ *              all their gradients start on a boundary of their elements; 16 bytes are
+ *              faster);  k and yk are NULL when Hk = 0
+ *   wq, wk     [d] f32 or NULL (1)
+ *   positions  DEVICE array [tokens] int32, or NULL (see period)
+ *   inv_freq   [rot / 2] f32 (NULL when rot = 0)
+ *   yq, yk     [tokens,Hq,d], [tokens,Hk,d] dtype, dense (written).  yq may be q and yk k where
+ *              these are dense too; nothing else overlaps
+ */
+TTT_API int ttt_qknorm_fwd(const ttt_qknorm_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                           const int32_t* positions, const float* inv_freq, void* yq, void* yk, void* stream);
+
+/* Bytes of the workspace of ttt_qknorm_bwd: partial sums of dwq and dwk. */
+TTT_API int ttt_qknorm_workspace_size(const ttt_qknorm_desc* desc, size_t* bytes);
+
+/*
+ * ttt_qknorm_bwd -- gradients of <dyq, Yq> + <dyk, Yk>.
+ *   q, k, wq, wk, positions, inv_freq  as passed to ttt_qknorm_fwd (q and k as they were
+ *              before it)
+ *   dyq, dyk   as yq, yk
+ *   dq, dk     as q and k, tokens ldq / ldk apart (written).  No output overlaps an input
+ *   dwq, dwk   [d] f32, each may be NULL (written: sums over tokens and heads)
+ *   ws, ws_bytes  at least ttt_qknorm_workspace_size bytes; may be NULL where dwq and dwk are
+ */
+TTT_API int ttt_qknorm_bwd(const ttt_qknorm_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                           const int32_t* positions, const float* inv_freq, const void* dyq, const void* dyk, void* dq,
+                           void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream);
+
 /* Message for the last non-OK return on this thread ("" if none). */
 TTT_API const char* ttt_last_error(void);
 
@@ -648,7 +803,16 @@ typedef enum {
   TTT_KERNEL_LN_BWD = 30,        /* layer norm backward: dx and partial dw, db */
   TTT_KERNEL_LN_REDUCE = 31,     /* layer norm backward: sum of the partial dw, db */
   TTT_KERNEL_REC_CLEAR = 32,     /* gated linear recurrence: workspace cleared */
-  TTT_KERNEL_COUNT = 33
+  TTT_KERNEL_DELTA_PLAN = 33,    /* gated delta rule: chunk table of packed sequences */
+  TTT_KERNEL_DELTA_PREP = 34,    /* gated delta rule: inverses and scores of every chunk */
+  TTT_KERNEL_DELTA_FWD = 35,     /* gated delta rule forward: walk over the chunks */
+  TTT_KERNEL_DELTA_BWD = 36,     /* gated delta rule backward: walk over the chunks */
+  TTT_KERNEL_DELTA_GRAD = 37,    /* gated delta rule backward: gradients of every chunk */
+  TTT_KERNEL_DELTA_STEP = 38,    /* gated delta rule, one token a sequence */
+  TTT_KERNEL_QK_FWD = 39,        /* norm and rotation of queries and keys */
+  TTT_KERNEL_QK_BWD = 40,        /* its backward: dq, dk and partial dwq, dwk */
+  TTT_KERNEL_QK_REDUCE = 41,     /* its backward: sum of the partial dwq, dwk */
+  TTT_KERNEL_COUNT = 42
 } ttt_kernel;
 
 TTT_API int ttt_timing_enable(int on);

@@ -162,11 +162,14 @@ template <typename E, int DKP, bool BWD>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   constexpr int C = Chunk<E>::C, LD = C + 4;
   using Lds = Tile<E, DKP>;
-  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
+  // T and P take the place of the keys and queries
+  constexpr size_t kRowsBytes = 2 * C * Lds::kRow * sizeof(E), kSquares = 2 * C * LD * sizeof(float);
+  __shared__ __attribute__((aligned(16))) char pool[kRowsBytes > kSquares ? kRowsBytes : kSquares];
+  E* K = reinterpret_cast<E*>(pool);
+  E* Q = K + C * Lds::kRow;
+  float* T = reinterpret_cast<float*>(pool);
+  float* P = T + C * LD;
   __shared__ __attribute__((aligned(16))) float A[C * LD];
-  __shared__ __attribute__((aligned(16))) float T[C * LD];
-  __shared__ __attribute__((aligned(16))) float P[C * LD];
   __shared__ double G[C];
   __shared__ float eta[C];
   const int chunk = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -192,12 +195,21 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   }
   stage<E, C, DKP, kPrepThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
   stage<E, C, DKP, kPrepThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
-  for (int x = threadIdx.x; x < C * LD; x += kPrepThreads) T[x] = 0.0f;
   __syncthreads();
-  for (int mt = wave; mt < C / 16; mt += kPrepThreads / 64) {
-    f32x4_t kk[C / 16], qk[C / 16];
+  if (!a.dense && h % (a.H / a.Hk) == 0) {  // the walks' copy
+    E* dst = static_cast<E*>(a.kq) + (static_cast<int64_t>(chunk) * a.Hk + hk) * 2 * C * DKP;
+    constexpr int V = 16 / sizeof(E), kPieces = DKP / V;
+    for (int x = threadIdx.x; x < 2 * C * kPieces; x += kPrepThreads) {
+      const int row = x / kPieces, col = (x % kPieces) * V;
+      const E* src = row < C ? K + Lds::at(row, col) : Q + Lds::at(row - C, col);
+      *reinterpret_cast<uint4*>(dst + row * DKP + col) = *reinterpret_cast<const uint4*>(src);
+    }
+  }
+  const int mt = wave;  // row tile; C / 16 waves have one
+  f32x4_t kk[C / 16], qk[C / 16];
 #pragma unroll
-    for (int nt = 0; nt < C / 16; ++nt) kk[nt] = qk[nt] = zero4();
+  for (int nt = 0; nt < C / 16; ++nt) kk[nt] = qk[nt] = zero4();
+  if (mt < C / 16) {
 #pragma unroll
     for (int kp = 0; kp < DKP / 32; ++kp) {
       const auto ka = row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), qa = row_frag<DKP>(Q, 16 * mt + i, 32 * kp + 8 * g);
@@ -210,6 +222,10 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
         }
       }
     }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < C * LD; x += kPrepThreads) T[x] = 0.0f;
+  if (mt < C / 16) {
 #pragma unroll
     for (int nt = 0; nt < C / 16; ++nt)
 #pragma unroll
@@ -226,27 +242,23 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   tri_store<E, LD, BWD, BWD ? 2 : 1>(P, a.p + item * Tri<E>::kBytes);
 }
 
-// ---- forward sweep ----
+// ---- forward walk ----
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks; the WAVES of a
-// workgroup share the chunk's keys and queries in LDS.  The state and what is added to it are products
-// of two-term operands: its error does not grow with the length.
+// workgroup share what they read of a chunk in LDS, filled one chunk ahead.  The state and what is added to
+// it are products of two-term operands: its error does not grow with the length.
 template <typename E, int DKP, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16;
-  using Lds = Tile<E, DKP>;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, kBuf = kWalkBuffers<E, DKP, false>;
   using TR = Tri<E>;
-  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) float vec[3 * C];
+  using Raw = typename Frag<E>::Raw;
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false> tiles[kWalkBuffers<E, DKP, false>];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
-  const int h = chain % a.H, seq = chain / a.H, hk = h / (a.H / a.Hk);
+  const int h = chain % a.H, seq = chain / a.H;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
   const bool in = col < a.dv, live = col < a.dvp;
-  const bool wq = a.wide_q, wk = a.wide_k;
-  const int first = a.packed ? a.base[seq] : seq * a.chunks_per_seq;
-  const int end = a.packed ? a.base[seq + 1] : first + a.chunks_per_seq;
+  const Span span = span_of(a, seq);
   const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   f32x4_t S[ND];
 #pragma unroll
@@ -256,21 +268,23 @@ __global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
       const int row = state_row(t, g) + r;
       S[t][r] = a.s0 && in && row < a.dk ? a.s0[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
     }
-  for (int chunk = first; chunk < end; ++chunk) {
-    const Where w = locate<C>(a, chunk);
-    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
-    __syncthreads();
-    stage<E, C, DKP, WAVES * 64>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
-    stage<E, C, DKP, WAVES * 64>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
-    for (int x = threadIdx.x; x < 3 * C; x += WAVES * 64) vec[x] = a.vec[item * 3 * C + x];
-    __syncthreads();
-    if (a.before && live) {
-      E* dst = static_cast<E*>(a.before) + item * DKP * a.dvp + col;
-#pragma unroll
-      for (int t = 0; t < ND; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) Elem<E>::st(dst, static_cast<int64_t>(state_row(t, g) + r) * a.dvp, S[t][r]);
-    }
+  Stager<E, DKP, false, WAVES * 64> next;
+  Column<E, NT> v;
+  auto fetch_v = [&](int chunk) {
+    v.load(static_cast<const E*>(a.v) + span.token(chunk, C) * a.ldv + static_cast<int64_t>(h) * a.dv + col, a.ldv, span.len(chunk, C), in);
+  };
+  if (span.first < span.end) {
+    next.load(a, span.first, h, span.token0, span.len(span.first, C));
+    fetch_v(span.first);
+    next.store(tiles[0]);
+  }
+  __syncthreads();
+  for (int chunk = span.first; chunk < span.end; ++chunk) {
+    const WalkTile<E, DKP, false>& w = tiles[(chunk - span.first) & (kBuf - 1)];
+    const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
+    const int len = span.len(chunk, C);
+    const bool more = chunk + 1 < span.end;
+    if (more) next.load(a, chunk + 1, h, span.token(chunk + 1, C), span.len(chunk + 1, C));
     // K S and Q S
     f32x4_t ks[NT], o[NT];
 #pragma unroll
@@ -278,66 +292,64 @@ __global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
 #pragma unroll
     for (int kp = 0; kp < DKP / 32; ++kp) {
       const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+      if (a.before && live)
+        *reinterpret_cast<Raw*>(static_cast<E*>(a.before) + (item * a.dvp + col) * DKP + 32 * kp + 8 * g) = high(s);
 #pragma unroll
       for (int mt = 0; mt < NT; ++mt) {
-        ks[mt] = mma(row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), s, ks[mt]);
-        o[mt] = mma(row_frag<DKP>(Q, 16 * mt + i, 32 * kp + 8 * g), s, o[mt]);
+        ks[mt] = mma(row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g), s, ks[mt]);
+        o[mt] = mma(row_frag<DKP>(w.Q, 16 * mt + i, 32 * kp + 8 * g), s, o[mt]);
       }
     }
     // eta (V - e^G K S)
-    const E* v = static_cast<const E*>(a.v) + w.token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(vec + 16 * mt + 4 * g);
-      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(vec + 2 * C + 16 * mt + 4 * g);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * g + r;
-        const float x = in && t < w.len ? Elem<E>::ld(v, t * a.ldv) : 0.0f;
-        ks[mt][r] = et[r] * (x - gm[r] * ks[mt][r]);
-        o[mt][r] *= a.scale * gm[r];
-      }
+      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+      ks[mt] = et * (v.tile(mt) - gm * ks[mt]);
+      o[mt] *= a.scale * gm;
     }
+    if (more) fetch_v(chunk + 1);
     // U = T (that), then O += P U
     f32x4_t u[NT];
-    const char* tp = a.t + item * TR::kBytes;
-    const char* pp = a.p + item * TR::kBytes;
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) u[mt] = zero4();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       const Split<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
 #pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri_load2<E>(tp, TR::at(mt, kp)), rhs, u[mt]);
-    }
-#pragma unroll
-    for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> us(u[2 * kp], u[2 * kp + 1]);
-#pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(tri_load<E>(pp, TR::at(mt, kp)), us, o[mt]);
+      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri_load2<E>(w.T, TR::at(mt, kp)), rhs, u[mt]);
     }
     // S = e^{G_C} S + K^T (e^{G_C - G} U)
-    const float decay = vec[C - 1];
+    const float decay = w.vec[C - 1];
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       f32x4_t x[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[j] = u[2 * kp + j] * *reinterpret_cast<const f32x4_t*>(vec + C + 16 * (2 * kp + j) + 4 * g);
+      for (int j = 0; j < 2; ++j) x[j] = u[2 * kp + j] * *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * (2 * kp + j) + 4 * g);
       const Split<E> us(x[0], x[1]);
 #pragma unroll
-      for (int t = 0; t < ND; ++t) S[t] = mma(state_col<DKP>(K, 32 * kp, t), us, S[t]);
+      for (int t = 0; t < ND; ++t) S[t] = mma(state_col<DKP>(w.K, 32 * kp, t), us, S[t]);
     }
-    E* op = static_cast<E*>(a.o) + (w.token * a.H + h) * a.dv + col;
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> us(u[2 * kp], u[2 * kp + 1]);
+      if (a.u && live) *reinterpret_cast<Raw*>(static_cast<E*>(a.u) + (item * a.dvp + col) * C + 32 * kp + 8 * g) = high(us);
+#pragma unroll
+      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(tri_load<E>(w.P, TR::at(mt, kp)), us, o[mt]);
+    }
+    E* op = static_cast<E*>(a.o) + (token * a.H + h) * a.dv + col;
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * mt + 4 * g + r;
-        if (in && t < w.len) Elem<E>::st(op, static_cast<int64_t>(t) * a.H * a.dv, o[mt][r]);
-        if (a.u && live) Elem<E>::st(static_cast<E*>(a.u) + item * C * a.dvp + col, static_cast<int64_t>(t) * a.dvp, u[mt][r]);
+        if (in && t < len) Elem<E>::st(op, static_cast<int64_t>(t) * a.H * a.dv, o[mt][r]);
       }
+    if constexpr (kBuf == 1) __syncthreads();
+    if (more) next.store(tiles[(chunk + 1 - span.first) & (kBuf - 1)]);
+    __syncthreads();
   }
   if (a.s_final && in) {
 #pragma unroll
@@ -497,7 +509,7 @@ int64_t delta_chunks(const ttt_delta_desc& d) {
 namespace {
 
 struct Layout {
-  size_t edge, base, table, vec, t, p, y, after, bytes;
+  size_t edge, base, table, vec, t, p, kq, y, after, bytes;
 };
 Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, C = chunk_tokens(d.dtype), e = elem_bytes(d);
@@ -517,6 +529,7 @@ Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   l.vec = take(items * 3 * C * sizeof(float));
   l.t = take(items * tri_bytes(d));
   l.p = take(items * tri_bytes(d));
+  l.kq = take(static_cast<size_t>(delta_chunks(d)) * d.Hk * 2 * C * padded_dk(d.dk) * e);
   if (bwd) {
     l.y = take(items * C * dvp * e);
     l.after = take(items * padded_dk(d.dk) * dvp * e);
@@ -545,6 +558,7 @@ Args make_args(const ttt_delta_desc& d, const void* q, const void* k, const void
   a.wide_q = wide(q, d.dk, a.ldq);
   a.wide_k = wide(k, d.dk, a.ldk);
   a.wide_do = wide(d_o, d.dv, 0);
+  a.dense = a.wide_q && a.wide_k;
   a.chunks = static_cast<int>(delta_chunks(d));
   a.chunks_per_seq = d.packed ? 0 : (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype);
   return a;
@@ -555,6 +569,7 @@ void place(Args& a, const ttt_delta_desc& d, const Layout& l, void* ws, const vo
   a.vec = reinterpret_cast<float*>(w + l.vec);
   a.t = w + l.t;
   a.p = w + l.p;
+  a.kq = w + l.kq;
   a.base = reinterpret_cast<const int*>(w + l.base);
   a.table = reinterpret_cast<const int4*>(w + l.table);
   if (saved) {
@@ -611,11 +626,11 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     constexpr int DKP = width();
     hipError_t e = delta::launch_prep<E, DKP, false>(a, s);
     if (e != hipSuccess) return e;
-    constexpr int W = 4;
-    const int groups = (a.dvp / 16 + W - 1) / W;
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
-    delta::fwd_kernel<E, DKP, W><<<static_cast<uint32_t>(d.B) * d.H * groups, W * 64, 0, s>>>(a, groups);
-    return hipGetLastError();
+    return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
+      delta::fwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(d.B) * d.H * groups, waves() * 64, 0, s>>>(a, groups);
+      return hipGetLastError();
+    });
   };
   return delta::by_width(d.dk, [&](auto width) { return d.dtype == TTT_F32 ? run(float{}, width) : run(bf16_t{}, width); });
 }

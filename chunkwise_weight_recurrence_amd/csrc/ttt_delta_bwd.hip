@@ -20,20 +20,16 @@ namespace {
 
 template <typename E, int DKP, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16;
-  using Lds = Tile<E, DKP>;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, kBuf = kWalkBuffers<E, DKP, true>;
   using TR = Tri<E>;
-  __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) float vec[3 * C];
+  using Raw = typename Frag<E>::Raw;
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true> tiles[kWalkBuffers<E, DKP, true>];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
-  const int h = chain % a.H, seq = chain / a.H, hk = h / (a.H / a.Hk);
+  const int h = chain % a.H, seq = chain / a.H;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
   const bool in = col < a.dv, live = col < a.dvp;
-  const bool wq = a.wide_q, wk = a.wide_k;
-  const int first = a.packed ? a.base[seq] : seq * a.chunks_per_seq;
-  const int end = a.packed ? a.base[seq + 1] : first + a.chunks_per_seq;
+  const Span span = span_of(a, seq);
   const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   f32x4_t S[ND];  // dS
 #pragma unroll
@@ -43,48 +39,47 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
       const int row = state_row(t, g) + r;
       S[t][r] = a.d_sfinal && in && row < a.dk ? a.d_sfinal[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
     }
-  for (int chunk = end - 1; chunk >= first; --chunk) {
-    const Where w = locate<C>(a, chunk);
-    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
-    __syncthreads();
-    stage<E, C, DKP, WAVES * 64>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
-    stage<E, C, DKP, WAVES * 64>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
-    for (int x = threadIdx.x; x < 3 * C; x += WAVES * 64) vec[x] = a.vec[item * 3 * C + x];
-    __syncthreads();
-    if (live) {
-      E* dst = static_cast<E*>(a.after) + item * DKP * a.dvp + col;
-#pragma unroll
-      for (int t = 0; t < ND; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) Elem<E>::st(dst, static_cast<int64_t>(state_row(t, g) + r) * a.dvp, S[t][r]);
-    }
+  Stager<E, DKP, true, WAVES * 64> next;
+  Column<E, NT> d_o;
+  auto fetch_o = [&](int chunk) {
+    const int64_t ld = static_cast<int64_t>(a.H) * a.dv;
+    d_o.load(static_cast<const E*>(a.d_o) + span.token(chunk, C) * ld + static_cast<int64_t>(h) * a.dv + col, ld, span.len(chunk, C), in);
+  };
+  const int last = span.end - 1;
+  if (span.first < span.end) {
+    next.load(a, last, h, span.token(last, C), span.len(last, C));
+    fetch_o(last);
+    next.store(tiles[0]);
+  }
+  __syncthreads();
+  for (int chunk = last; chunk >= span.first; --chunk) {
+    const WalkTile<E, DKP, true>& w = tiles[(last - chunk) & (kBuf - 1)];
+    const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
+    const int len = span.len(chunk, C);
+    const bool more = chunk > span.first;
+    if (more) next.load(a, chunk - 1, h, span.token(chunk - 1, C), span.len(chunk - 1, C));
     // e^{G_C - G} K dS', then + P^T dO
     f32x4_t du[NT], go[NT];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) du[mt] = zero4();
+    for (int mt = 0; mt < NT; ++mt) {
+      du[mt] = zero4();
+      go[mt] = d_o.tile(mt);
+    }
+    if (more) fetch_o(chunk - 1);
 #pragma unroll
     for (int kp = 0; kp < DKP / 32; ++kp) {
       const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+      if (live) *reinterpret_cast<Raw*>(static_cast<E*>(a.after) + (item * a.dvp + col) * DKP + 32 * kp + 8 * g) = high(s);
 #pragma unroll
-      for (int mt = 0; mt < NT; ++mt) du[mt] = mma(row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), s, du[mt]);
+      for (int mt = 0; mt < NT; ++mt) du[mt] = mma(row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g), s, du[mt]);
     }
-    const E* dop = static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv + col;
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) {
-      du[mt] *= *reinterpret_cast<const f32x4_t*>(vec + C + 16 * mt + 4 * g);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * g + r;
-        go[mt][r] = in && t < w.len ? Elem<E>::ld(dop, static_cast<int64_t>(t) * a.H * a.dv) : 0.0f;
-      }
-    }
-    const char* tp = a.t + item * TR::kBytes;
-    const char* pp = a.p + item * TR::kBytes;
+    for (int mt = 0; mt < NT; ++mt) du[mt] *= *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> s(go[2 * kp], go[2 * kp + 1]);
+      const Raw s = high(Split<E>(go[2 * kp], go[2 * kp + 1]));  // dO is exact in its type
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(tri_load2<E>(pp, TR::at_t(mt, kp)), s, du[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(tri_load2<E>(w.P, TR::at_t(mt, kp)), s, du[mt]);
     }
     // Y = T^T dU
     f32x4_t y[NT];
@@ -94,16 +89,16 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
     for (int kp = 0; kp < NP; ++kp) {
       const Split<E> s(du[2 * kp], du[2 * kp + 1]);
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri_load2<E>(tp, TR::at_t(mt, kp)), s, y[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri_load2<E>(w.T, TR::at_t(mt, kp)), s, y[mt]);
     }
-    const float decay = vec[C - 1];
+    const float decay = w.vec[C - 1];
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
     f32x4_t ey[NT];
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(vec + 16 * mt + 4 * g);
-      ey[mt] = y[mt] * *reinterpret_cast<const f32x4_t*>(vec + 2 * C + 16 * mt + 4 * g);
+      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+      ey[mt] = y[mt] * *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
       go[mt] *= gm * a.scale;
       du[mt] = -(gm * ey[mt]);
     }
@@ -112,19 +107,23 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
       const Split<E> s(go[2 * kp], go[2 * kp + 1]), n(du[2 * kp], du[2 * kp + 1]);
 #pragma unroll
       for (int t = 0; t < ND; ++t) {
-        S[t] = mma(state_col<DKP>(Q, 32 * kp, t), s, S[t]);
-        S[t] = mma(state_col<DKP>(K, 32 * kp, t), n, S[t]);
+        S[t] = mma(state_col<DKP>(w.Q, 32 * kp, t), s, S[t]);
+        S[t] = mma(state_col<DKP>(w.K, 32 * kp, t), n, S[t]);
       }
+      if (live)
+        *reinterpret_cast<Raw*>(static_cast<E*>(a.y) + (item * a.dvp + col) * C + 32 * kp + 8 * g) = high(Split<E>(y[2 * kp], y[2 * kp + 1]));
     }
-    E* vp = static_cast<E*>(a.dv_out) + w.token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
+    E* vp = static_cast<E*>(a.dv_out) + token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * mt + 4 * g + r;
-        if (in && t < w.len) Elem<E>::st(vp, t * a.ldv, ey[mt][r]);
-        if (live) Elem<E>::st(static_cast<E*>(a.y) + item * C * a.dvp + col, static_cast<int64_t>(t) * a.dvp, y[mt][r]);
+        if (in && t < len) Elem<E>::st(vp, t * a.ldv, ey[mt][r]);
       }
+    if constexpr (kBuf == 1) __syncthreads();
+    if (more) next.store(tiles[(last - chunk + 1) & (kBuf - 1)]);
+    __syncthreads();
   }
   if (a.ds0 && in) {
 #pragma unroll
@@ -139,7 +138,7 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
 
 // ---- what does not depend on the walk ----
 
-constexpr int kGradThreads = 256, kSlab = 128;  // columns of dO, U and Y in LDS at a time
+constexpr int kGradThreads = 512, kSlab = 32;  // columns of the values in LDS at a time
 
 template <typename E> __device__ __forceinline__ float dot8(typename Frag<E>::Raw a, typename Frag<E>::Raw b) {
   float s = 0.0f;
@@ -178,29 +177,35 @@ __device__ __forceinline__ float sum16(float x) {
 }
 
 // A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
-// dK summed in registers.  For the triangular products wave w has row tile w, for the others a quarter
-// of the key channels.
+// dK summed in registers.  Of the triangular products a wave has a row tile of X or of M, of the others an
+// eighth of the key channels.  The value columns come 32 at a time.
 template <typename E, int DKP, bool SHARED>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = DKP / 64;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = (DKP + 127) / 128, NW = DKP / 16 / NJ;  // NW waves have channels
   using Lds = Tile<E, DKP>;
   using Slab = Tile<E, kSlab>;
   using Sq = Tile<E, C>;
   __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
   __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) E dO[C * Slab::kRow];
-  __shared__ __attribute__((aligned(16))) E U[C * Slab::kRow];
-  __shared__ __attribute__((aligned(16))) E Y[C * Slab::kRow];
+  __shared__ __attribute__((aligned(16))) E dO[C * Slab::kRow];     // [token][column]
+  __shared__ __attribute__((aligned(16))) E U[kSlab * Sq::kRow];    // [column][token]
+  __shared__ __attribute__((aligned(16))) E Y[kSlab * Sq::kRow];
+  __shared__ __attribute__((aligned(16))) E B[kSlab * Lds::kRow];   // [column][channel]: the state before
+  __shared__ __attribute__((aligned(16))) E A[kSlab * Lds::kRow];   // and the gradient of the one after
   __shared__ __attribute__((aligned(16))) E X[C * Sq::kRow];
   __shared__ __attribute__((aligned(16))) E M[C * Sq::kRow];
   __shared__ double G[C];
   __shared__ __attribute__((aligned(16))) float vec[3][C];  // e^G, e^{G_C - G}, eta
-  __shared__ float sums[4][4][C], energy[4], yu[C];
+  __shared__ float energy[kGradThreads / 64], yu[C];
+  float(*sums)[4][C] = reinterpret_cast<float(*)[4][C]>(B);  // [wave], once the slabs are done with
+  static_assert(sizeof(float) * NW * 4 * C <= sizeof(B));
   const int chunk = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.H / a.Hk;
   const Where w = locate<C>(a, chunk);
   if (w.len < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const bool wq = a.wide_q, wk = a.wide_k, wo = a.wide_do;
+  const int ch0 = wave * 16 * NJ;  // a wave's first channel
+  const bool busy = wave < NW;
   stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
   stage<E, C, DKP, kGradThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
   f32x4_t dq_sum[SHARED ? NT : 1][NJ], dk_sum[SHARED ? NT : 1][NJ];
@@ -211,8 +216,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
       for (int j = 0; j < NJ; ++j) dq_sum[mt][j] = dk_sum[mt][j] = zero4();
   }
   auto store = [&](const f32x4_t& dq, const f32x4_t& dk, int mt, int j) {
-    const int col = wave * (DKP / 4) + 16 * j + i;
-    if (col >= a.dk) return;
+    const int col = ch0 + 16 * j + i;
+    if (!busy || col >= a.dk) return;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * mt + 4 * g + r;
@@ -222,6 +227,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
       }
     }
   };
+  // wave w < NT has row tile w of X, wave NT + w that of M
+  const int rt = wave % NT;
+  const bool tri = wave < 2 * NT, second = wave >= NT;
   for (int hs = 0; hs < (SHARED ? share : 1); ++hs) {
     const int h = hk * share + hs;
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
@@ -239,79 +247,76 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
         vec[2][lane] = eta;
       }
     }
-    f32x4_t xs[NT], ms[NT], dq[NT][NJ], dkr[NT][NJ], dks[NT][NJ];
+    f32x4_t xm[NT], dq[NT][NJ], dkr[NT][NJ], dks[NT][NJ];
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      xs[mt] = ms[mt] = zero4();
+      xm[mt] = zero4();
 #pragma unroll
       for (int j = 0; j < NJ; ++j) dq[mt][j] = dkr[mt][j] = dks[mt][j] = zero4();
     }
     float en = 0.0f;
     for (int c0 = 0; c0 < a.dvp; c0 += kSlab) {
-      const int width = min(kSlab, a.dvp - c0);
       if (c0 > 0) __syncthreads();
       stage<E, C, kSlab, kGradThreads>(dO, static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv + c0, static_cast<int64_t>(a.H) * a.dv,
-                                       w.len, min(width, a.dv - c0), wo, width);
-      stage<E, C, kSlab, kGradThreads>(U, static_cast<const E*>(a.u) + item * C * a.dvp + c0, a.dvp, C, width, true, width);
-      stage<E, C, kSlab, kGradThreads>(Y, static_cast<const E*>(a.y) + item * C * a.dvp + c0, a.dvp, C, width, true, width);
+                                       w.len, a.dv - c0, wo);
+      stage<E, kSlab, C, kGradThreads>(U, static_cast<const E*>(a.u) + (item * a.dvp + c0) * C, C, kSlab, C, true);
+      stage<E, kSlab, C, kGradThreads>(Y, static_cast<const E*>(a.y) + (item * a.dvp + c0) * C, C, kSlab, C, true);
+      stage<E, kSlab, DKP, kGradThreads>(B, static_cast<const E*>(a.before) + (item * a.dvp + c0) * DKP, DKP, kSlab, DKP, true);
+      stage<E, kSlab, DKP, kGradThreads>(A, static_cast<const E*>(a.after) + (item * a.dvp + c0) * DKP, DKP, kSlab, DKP, true);
       __syncthreads();
-      if (wave < NT) {
-        for (int kp = 0; kp < width / 32; ++kp) {
-          const auto ox = row_frag<kSlab>(dO, 16 * wave + i, 32 * kp + 8 * g), yx = row_frag<kSlab>(Y, 16 * wave + i, 32 * kp + 8 * g);
+      typename Frag<E>::Raw ox[NT], ux[NT], yx[NT];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (nt <= wave) {
-              const auto ux = row_frag<kSlab>(U, 16 * nt + i, 32 * kp + 8 * g);
-              xs[nt] = mma(ox, ux, xs[nt]);
-              ms[nt] = mma(yx, ux, ms[nt]);
-            }
-          }
-        }
+      for (int mt = 0; mt < NT; ++mt) {
+        ox[mt] = row_frag<kSlab>(dO, 16 * mt + i, 8 * g);
+        ux[mt] = token_col<C>(U, mt);
+        yx[mt] = token_col<C>(Y, mt);
       }
-      for (int kp = 0; kp < width / 32; ++kp) {
-        typename Frag<E>::Raw sb[NJ], sa[NJ];
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt)
+        if (tri && rt == mt) {
+#pragma unroll
+          for (int nt = 0; nt <= mt; ++nt) xm[nt] = mma(second ? yx[mt] : ox[mt], ux[nt], xm[nt]);
+        }
+      if (busy) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const int64_t at = (item * DKP + wave * (DKP / 4) + 16 * j + i) * a.dvp + c0 + 32 * kp + 8 * g;
-          sb[j] = *reinterpret_cast<const typename Frag<E>::Raw*>(static_cast<const E*>(a.before) + at);
-          sa[j] = *reinterpret_cast<const typename Frag<E>::Raw*>(static_cast<const E*>(a.after) + at);
-          en += dot8<E>(sb[j], sa[j]);
-        }
+          const auto sb = plain_col<DKP>(B, 0, ch0 + 16 * j), sa = plain_col<DKP>(A, 0, ch0 + 16 * j);
+          en += dot8<E>(sb, sa);
 #pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-          const auto ox = row_frag<kSlab>(dO, 16 * mt + i, 32 * kp + 8 * g), yx = row_frag<kSlab>(Y, 16 * mt + i, 32 * kp + 8 * g);
-          const auto ux = row_frag<kSlab>(U, 16 * mt + i, 32 * kp + 8 * g);
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            dq[mt][j] = mma(ox, sb[j], dq[mt][j]);
-            dkr[mt][j] = mma(yx, sb[j], dkr[mt][j]);
-            dks[mt][j] = mma(ux, sa[j], dks[mt][j]);
+          for (int mt = 0; mt < NT; ++mt) {
+            dq[mt][j] = mma(ox[mt], sb, dq[mt][j]);
+            dkr[mt][j] = mma(yx[mt], sb, dkr[mt][j]);
+            dks[mt][j] = mma(ux[mt], sa, dks[mt][j]);
           }
         }
       }
     }
-    if (wave < NT) {
+    if (tri) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * wave + 4 * g + r, col = 16 * nt + i;
+          const int row = 16 * rt + 4 * g + r, col = 16 * nt + i;
           const float d = row >= col ? exp2_(static_cast<float>(G[row] - G[col])) : 0.0f;
-          Elem<E>::st(X, Sq::at(row, col), row >= col ? a.scale * d * xs[nt][r] : 0.0f);
-          Elem<E>::st(M, Sq::at(row, col), row > col ? -vec[2][row] * d * ms[nt][r] : 0.0f);
-          if (row == col) yu[row] = ms[nt][r];
+          if (second) {
+            Elem<E>::st(M, Sq::at(row, col), row > col ? -vec[2][row] * d * xm[nt][r] : 0.0f);
+            if (row == col) yu[row] = xm[nt][r];
+          } else {
+            Elem<E>::st(X, Sq::at(row, col), row >= col ? a.scale * d * xm[nt][r] : 0.0f);
+          }
         }
     }
     __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
+      if (!busy) break;
       const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
       const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
       const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
       f32x4_t d1 = zero4(), d2 = zero4(), d3 = zero4(), d4 = zero4();
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int c0 = wave * (DKP / 4) + 16 * j;
+        const int c0 = ch0 + 16 * j;
         dq[mt][j] *= gm * a.scale;
         dkr[mt][j] *= -(gm * et);
         dks[mt][j] *= rest;
@@ -358,7 +363,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
     if (wave == 0) {
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, all = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
+      for (int v = 0; v < NW; ++v) {
         all += energy[v];
 #pragma unroll
         for (int s = 0; s < 4; ++s) x[s] += lane < C ? sums[v][s][lane] : 0.0f;
@@ -397,11 +402,11 @@ template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t 
   hipError_t e = launch_prep<E, DKP, true>(a, s);
   if (e != hipSuccess) return e;
   {
-    constexpr int W = 4;
-    const int groups = (a.dvp / 16 + W - 1) / W;
     KernelScope scope(TTT_KERNEL_DELTA_BWD, s);
-    bwd_kernel<E, DKP, W><<<static_cast<uint32_t>(a.B) * a.H * groups, W * 64, 0, s>>>(a, groups);
-    e = hipGetLastError();
+    e = by_waves<DKP>(a, [&](auto waves, int groups) {
+      bwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(a.B) * a.H * groups, waves() * 64, 0, s>>>(a, groups);
+      return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
   }
   KernelScope scope(TTT_KERNEL_DELTA_GRAD, s);

@@ -29,6 +29,7 @@ struct Args {
   int B, T, H, Hk, dk, dv, dvp;  // dvp: dv rounded up to 32, the width of U, Y and the kept states
   int packed, gate_kind;
   int wide_q, wide_k, wide_do;   // whether every row of a head starts on 16 bytes
+  int dense;                     // both q and k are wide: the walks read them where they are
   float scale, lr_max, lr_bias;
   int64_t n;                     // tokens
   int64_t ldq, ldk, ldv, ldg, ldb;
@@ -44,10 +45,11 @@ struct Args {
   void* o;
   float* s_final;
   float* vec;                    // [chunks][H][3][C]: e^G, e^{G_C - G}, eta
+  void* kq;                      // else [chunks][Hk][2][C][dkp]: keys and queries, padded with zeros
   char* t;                       // [chunks][H] T, or its transpose, in operand order
   char* p;                       // the same of the scores
-  void* u;                       // [chunks][H][C][dvp]
-  void* before;                  // [chunks][H][dkp][dvp]: the state that enters the chunk
+  void* u;                       // [chunks][H][dvp][C], tokens in operand order (see token_col)
+  void* before;                  // [chunks][H][dvp][dkp]: the state that enters the chunk
   void* y;                       // as u: T^T dU
   void* after;                   // as before: the gradient of the state that leaves it
   const void* d_o;
@@ -160,6 +162,9 @@ __device__ __forceinline__ f32x4_t mma(bf16x8_t a, bf16x8_t b, f32x4_t c) { retu
 // a is exact in its type; b in two terms
 __device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Split<bf16_t>& b, f32x4_t c) { return mfma16(a, b.hi, mfma16(a, b.lo, c)); }
 __device__ __forceinline__ f32x4_t mma(f32x8 a, const Split<float>& b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
+// the first in two terms, the second exact
+__device__ __forceinline__ f32x4_t mma(const Split<bf16_t>& a, bf16x8_t b, f32x4_t c) { return mfma16(a.hi, b, mfma16(a.lo, b, c)); }
+__device__ __forceinline__ f32x4_t mma(const Split<float>& a, f32x8 b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
 // both in two terms
 __device__ __forceinline__ f32x4_t mma(const Split<bf16_t>& a, const Split<bf16_t>& b, f32x4_t c) {
   return mfma16(a.hi, b.hi, mfma16(a.hi, b.lo, mfma16(a.lo, b.hi, c)));
@@ -218,6 +223,15 @@ __device__ __forceinline__ typename Frag<E>::Raw plain_col(const E* lds, int row
   return col_frag<NCOL>(lds, row0 + 8 * g, row0 + 8 * g + 4, col0 + 4 * (i & 3), col0 + i);
 }
 
+// U and Y are kept as [column][C] with the tokens of a pair of tiles in the order of the operand that they
+// were: 8 g + j is token 4 g + j, or for j >= 4 token 16 + 4 g + j - 4.  This is the operand of token tile mt
+// over 32 columns (rows), in the tokens' own order.
+template <int NCOL, typename E>
+__device__ __forceinline__ typename Frag<E>::Raw token_col(const E* lds, int mt) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  return col_frag<NCOL>(lds, 8 * g, 8 * g + 4, state_row(mt, i & 3), state_row(mt, i >> 2) + (i & 3));
+}
+
 // ---- T and P in operand order ----
 //
 // An A operand of row tile mt over the pair kp of token tiles: lane (i, g) row 16 mt + i, columns
@@ -235,7 +249,7 @@ template <typename E> struct Tri {
   }
   static __device__ __forceinline__ int at_t(int mt, int kp) { return at(2 * (NP - 1 - (mt >> 1)) + (mt & 1), NP - 1 - kp); }
 };
-template <typename E> __device__ __forceinline__ typename Frag<E>::Raw tri_load(const char* base, int place) {
+template <typename E> __device__ __forceinline__ typename Frag<E>::Raw tri_load(const char* base, int place) {  // base: in LDS
   using R = typename Frag<E>::Raw;
   return *reinterpret_cast<const R*>(base + place * Tri<E>::kFragBytes + (threadIdx.x & 63) * sizeof(R));
 }
@@ -250,6 +264,148 @@ template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* 
     s.lo = tri_load<bf16_t>(base + Tri<bf16_t>::kHalfBytes, place);
   }
   return s;
+}
+
+// ---- what a walk reads of a chunk, one chunk ahead ----
+
+// A walk's LDS for one chunk.
+template <typename E, int DKP, bool BWD> struct WalkTile {
+  static constexpr int C = Chunk<E>::C;
+  static constexpr int kPBytes = BWD ? Tri<E>::kBytes : Tri<E>::kHalfBytes;  // the backward's scores have two terms
+  E K[C * Tile<E, DKP>::kRow];
+  E Q[C * Tile<E, DKP>::kRow];
+  char T[Tri<E>::kBytes];
+  char P[kPBytes];
+  float vec[3 * C];
+};
+
+// Two of them where they fit the 160 KB, so that one is filled while the other is read.
+template <typename E, int DKP, bool BWD> constexpr int kWalkBuffers = 2 * sizeof(WalkTile<E, DKP, BWD>) <= 160 * 1024 ? 2 : 1;
+
+// The next chunk's keys, queries, T, P and factors on their way through registers into the other buffer.
+template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
+  using W = WalkTile<E, DKP, BWD>;
+  static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V;
+  static constexpr int kRows = (C * kPieces + THREADS - 1) / THREADS;
+  static constexpr int kT = (Tri<E>::kBytes / 16 + THREADS - 1) / THREADS, kP = (W::kPBytes / 16 + THREADS - 1) / THREADS;
+  static_assert(C * kPieces % THREADS == 0 && 3 * C / 4 <= THREADS);
+  uint4 k[kRows], q[kRows], t[kT], p[kP], vec;
+
+  __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len) {
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    const int hk = h / (a.H / a.Hk);
+    const E *kp, *qp;
+    int64_t lk, lq;
+    int cols = DKP;
+    if (a.dense) {
+      kp = static_cast<const E*>(a.k) + token * a.ldk + hk * a.dk;
+      qp = static_cast<const E*>(a.q) + token * a.ldq + hk * a.dk;
+      lk = a.ldk;
+      lq = a.ldq;
+      cols = a.dk;
+    } else {
+      kp = static_cast<const E*>(a.kq) + (static_cast<int64_t>(chunk) * a.Hk + hk) * 2 * C * DKP;
+      qp = kp + C * DKP;
+      lk = lq = DKP;
+      len = C;
+    }
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      const int i = threadIdx.x + n * THREADS, row = i / kPieces, col = (i % kPieces) * V;
+      k[n] = q[n] = uint4{0, 0, 0, 0};
+      if (row < len && col < cols) {
+        k[n] = *reinterpret_cast<const uint4*>(kp + row * lk + col);
+        q[n] = *reinterpret_cast<const uint4*>(qp + row * lq + col);
+      }
+    }
+    const uint4* tp = reinterpret_cast<const uint4*>(a.t + item * Tri<E>::kBytes);
+    const uint4* pp = reinterpret_cast<const uint4*>(a.p + item * Tri<E>::kBytes);
+#pragma unroll
+    for (int n = 0; n < kT; ++n) {
+      const int i = threadIdx.x + n * THREADS;
+      if (i < Tri<E>::kBytes / 16) t[n] = tp[i];
+    }
+#pragma unroll
+    for (int n = 0; n < kP; ++n) {
+      const int i = threadIdx.x + n * THREADS;
+      if (i < W::kPBytes / 16) p[n] = pp[i];
+    }
+    if (threadIdx.x < 3 * C / 4) vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[threadIdx.x];
+  }
+  __device__ __forceinline__ void store(W& w) const {
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      const int i = threadIdx.x + n * THREADS, at = Tile<E, DKP>::at(i / kPieces, (i % kPieces) * V);
+      *reinterpret_cast<uint4*>(w.K + at) = k[n];
+      *reinterpret_cast<uint4*>(w.Q + at) = q[n];
+    }
+#pragma unroll
+    for (int n = 0; n < kT; ++n) {
+      const int i = threadIdx.x + n * THREADS;
+      if (i < Tri<E>::kBytes / 16) reinterpret_cast<uint4*>(w.T)[i] = t[n];
+    }
+#pragma unroll
+    for (int n = 0; n < kP; ++n) {
+      const int i = threadIdx.x + n * THREADS;
+      if (i < W::kPBytes / 16) reinterpret_cast<uint4*>(w.P)[i] = p[n];
+    }
+    if (threadIdx.x < 3 * C / 4) reinterpret_cast<uint4*>(w.vec)[threadIdx.x] = vec;
+  }
+};
+
+// A walk's chunks: those of one sequence, and its tokens.
+struct Span {
+  int first, end;   // chunks
+  int64_t token0, tokens;
+  __device__ __forceinline__ int len(int chunk, int C) const {
+    return static_cast<int>(min(static_cast<int64_t>(C), tokens - static_cast<int64_t>(chunk - first) * C));
+  }
+  __device__ __forceinline__ int64_t token(int chunk, int C) const { return token0 + static_cast<int64_t>(chunk - first) * C; }
+};
+__device__ __forceinline__ Span span_of(const Args& a, int seq) {
+  Span s;
+  if (a.packed) {
+    s.first = a.base[seq];
+    s.end = a.base[seq + 1];
+    s.token0 = s.tokens = 0;
+    if (s.first < s.end) {
+      const int4 head = a.table[s.first], tail = a.table[s.end - 1];
+      s.token0 = head.x;
+      s.tokens = tail.x + tail.y - head.x;
+    }
+  } else {
+    s.first = seq * a.chunks_per_seq;
+    s.end = s.first + a.chunks_per_seq;
+    s.token0 = static_cast<int64_t>(seq) * a.T;
+    s.tokens = a.T;
+  }
+  return s;
+}
+
+// A lane's column of 16-row result tiles, in the tensor's type: rows 4 g + r of tile mt are its tokens.
+template <typename E, int NT> struct Column {
+  E x[NT][4];
+  __device__ __forceinline__ void load(const E* p, int64_t ld, int len, bool in) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * g + r;
+        x[mt][r] = E{};
+        if (in && t < len) x[mt][r] = p[t * ld];
+      }
+  }
+  __device__ __forceinline__ f32x4_t tile(int mt) const {
+    f32x4_t f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = Elem<E>::ld(x[mt], r);
+    return f;
+  }
+};
+template <typename E> __device__ __forceinline__ typename Frag<E>::Raw high(const Split<E>& s) {
+  if constexpr (std::is_same_v<E, float>) return f32x8{s.a, s.b};
+  else return s.hi;
 }
 
 // ---- gates ----
@@ -285,6 +441,15 @@ __device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, 
     if ((threadIdx.x & 63) >= d) l += o;
   }
   G = l;
+}
+
+// The waves of a walk's workgroup, and the workgroups that share a head's columns: four waves where that
+// leaves a workgroup for every CU, else two.  Of 256 channels, four: two would have no registers for the next chunk.
+template <int DKP, typename F> hipError_t by_waves(const Args& a, F&& f) {
+  const int64_t columns = a.dvp / 16;
+  if constexpr (DKP == 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));
+  else if (static_cast<int64_t>(a.B) * a.H * ((columns + 3) / 4) >= 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));
+  else return f(std::integral_constant<int, 2>{}, static_cast<int>((columns + 1) / 2));
 }
 
 // The chunks' T and P into the workspace (ttt_delta.hip; BWD: the transposes), and the backward's three

@@ -246,18 +246,19 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks; the WAVES of a
 // workgroup share what they read of a chunk in LDS, filled one chunk ahead.  The state and what is added to
-// it are products of two-term operands: its error does not grow with the length.
-template <typename E, int DKP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, kBuf = kWalkBuffers<E, DKP, false>;
+// it are products of two-term operands: its error does not grow with the length.  KEEP: what a backward
+// needs is written.
+template <typename E, int DKP, int WAVES, bool KEEP>
+__global__ __launch_bounds__(WAVES * 64, 1) void fwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false>;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false> tiles[kWalkBuffers<E, DKP, false>];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false> tiles[kBuf];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
   const int h = chain % a.H, seq = chain / a.H;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
-  const bool in = col < a.dv, live = col < a.dvp;
+  const bool in = col < a.dv;
   const Span span = span_of(a, seq);
   const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   f32x4_t S[ND];
@@ -268,14 +269,20 @@ __global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
       const int row = state_row(t, g) + r;
       S[t][r] = a.s0 && in && row < a.dk ? a.s0[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
     }
+  const uint32_t sv = static_cast<uint32_t>(a.ldv * sizeof(E)), so = static_cast<uint32_t>(a.H * a.dv * sizeof(E));
+  const uint32_t v_at = in ? 4 * g * sv + col * sizeof(E) : kNowhere, o_at = in ? 4 * g * so + col * sizeof(E) : kNowhere;
+  const bool live = col < a.dvp;
+  const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
   Stager<E, DKP, false, WAVES * 64> next;
   Column<E, NT> v;
-  auto fetch_v = [&](int chunk) {
-    v.load(static_cast<const E*>(a.v) + span.token(chunk, C) * a.ldv + static_cast<int64_t>(h) * a.dv + col, a.ldv, span.len(chunk, C), in);
+  auto fetch = [&](int chunk) {
+    const int64_t token = span.token(chunk, C);
+    const int len = span.len(chunk, C);
+    next.load(a, chunk, h, token, len);
+    v.load(Buffer(static_cast<const E*>(a.v) + token * a.ldv + static_cast<int64_t>(h) * a.dv, rows_bytes(len, a.ldv, a.dv, sizeof(E))), v_at, sv);
   };
   if (span.first < span.end) {
-    next.load(a, span.first, h, span.token0, span.len(span.first, C));
-    fetch_v(span.first);
+    fetch(span.first);
     next.store(tiles[0]);
   }
   __syncthreads();
@@ -284,71 +291,98 @@ __global__ __launch_bounds__(WAVES * 64) void fwd_kernel(Args a, int groups) {
     const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
     const int len = span.len(chunk, C);
     const bool more = chunk + 1 < span.end;
-    if (more) next.load(a, chunk + 1, h, span.token(chunk + 1, C), span.len(chunk + 1, C));
-    // K S and Q S
-    f32x4_t ks[NT], o[NT];
+    f32x4_t vt[NT];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) ks[mt] = o[mt] = zero4();
-#pragma unroll
-    for (int kp = 0; kp < DKP / 32; ++kp) {
-      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
-      if (a.before && live)
-        *reinterpret_cast<Raw*>(static_cast<E*>(a.before) + (item * a.dvp + col) * DKP + 32 * kp + 8 * g) = high(s);
+    for (int mt = 0; mt < NT; ++mt) vt[mt] = v.tile(mt);
+    fetch(more ? chunk + 1 : chunk);
+    // K S and Q S: rows of the next 32 channels are read while these are multiplied
+    f32x4_t ko[2 * NT];
+    Raw rows[2][2 * NT];
+    auto read_rows = [&](int kp) {
 #pragma unroll
       for (int mt = 0; mt < NT; ++mt) {
-        ks[mt] = mma(row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g), s, ks[mt]);
-        o[mt] = mma(row_frag<DKP>(w.Q, 16 * mt + i, 32 * kp + 8 * g), s, o[mt]);
+        rows[kp & 1][mt] = row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g);
+        rows[kp & 1][NT + mt] = row_frag<DKP>(w.Q, 16 * mt + i, 32 * kp + 8 * g);
       }
+    };
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) ko[n] = zero4();
+    read_rows(0);
+    Split<E> tri[TR::kFrags];
+    f32x4_t gm[NT], et[NT], rest[NT];
+    const Buffer kept(KEEP ? static_cast<E*>(a.before) + item * a.dvp * DKP : nullptr, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      if (kp + 1 < NK) {
+        read_rows(kp + 1);
+      } else {
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+          et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+        }
+      }
+      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+      if constexpr (KEEP) kept.store(b_at + 32 * kp * sizeof(E), high(s));
+      in_order();
+      mma_all(ko, rows[kp & 1], s);
+      in_order();
     }
-    // eta (V - e^G K S)
+    // eta (V - e^G K S), U = T (that)
+    const float decay = w.vec[C - 1];
+    Raw cols[2][ND];
+    auto read_cols = [&](int kp) {
+#pragma unroll
+      for (int t = 0; t < ND; ++t) cols[kp & 1][t] = state_col<DKP>(w.K, 32 * kp, t);
+    };
+    read_cols(0);
+    f32x4_t o[NT], u[NT];
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
-      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
-      ks[mt] = et * (v.tile(mt) - gm * ks[mt]);
-      o[mt] *= a.scale * gm;
+      rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+      ko[mt] = et[mt] * (vt[mt] - gm[mt] * ko[mt]);
+      o[mt] = ko[NT + mt] * (a.scale * gm[mt]);
+      u[mt] = zero4();
     }
-    if (more) fetch_v(chunk + 1);
-    // U = T (that), then O += P U
-    f32x4_t u[NT];
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt) u[mt] = zero4();
+    in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
+      const Split<E> rhs(ko[2 * kp], ko[2 * kp + 1]);
 #pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri_load2<E>(w.T, TR::at(mt, kp)), rhs, u[mt]);
+      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri[TR::at(mt, kp)], rhs, u[mt]);
     }
-    // S = e^{G_C} S + K^T (e^{G_C - G} U)
-    const float decay = w.vec[C - 1];
+    in_order();
+    // S = e^{G_C} S + K^T (e^{G_C - G} U);  O += P U
+    Raw scores[TR::kFrags];
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
+    const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      f32x4_t x[2];
+      if (kp + 1 < NP) {
+        read_cols(kp + 1);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[j] = u[2 * kp + j] * *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * (2 * kp + j) + 4 * g);
-      const Split<E> us(x[0], x[1]);
-#pragma unroll
-      for (int t = 0; t < ND; ++t) S[t] = mma(state_col<DKP>(w.K, 32 * kp, t), us, S[t]);
+        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load<E>(w.P, f);
+      }
+      const Split<E> us(u[2 * kp] * rest[2 * kp], u[2 * kp + 1] * rest[2 * kp + 1]);
+      in_order();
+      mma_all(S, cols[kp & 1], us);
+      in_order();
     }
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       const Split<E> us(u[2 * kp], u[2 * kp + 1]);
-      if (a.u && live) *reinterpret_cast<Raw*>(static_cast<E*>(a.u) + (item * a.dvp + col) * C + 32 * kp + 8 * g) = high(us);
+      if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(us));
 #pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(tri_load<E>(w.P, TR::at(mt, kp)), us, o[mt]);
+      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], us, o[mt]);
     }
-    E* op = static_cast<E*>(a.o) + (token * a.H + h) * a.dv + col;
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * g + r;
-        if (in && t < len) Elem<E>::st(op, static_cast<int64_t>(t) * a.H * a.dv, o[mt][r]);
-      }
     if constexpr (kBuf == 1) __syncthreads();
     if (more) next.store(tiles[(chunk + 1 - span.first) & (kBuf - 1)]);
+    const Buffer ob(static_cast<E*>(a.o) + (token * a.H + h) * a.dv, rows_bytes(len, static_cast<int64_t>(a.H) * a.dv, a.dv, sizeof(E)));
+    store_column<E>(ob, o_at, so, o);
     __syncthreads();
   }
   if (a.s_final && in) {
@@ -628,7 +662,9 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     if (e != hipSuccess) return e;
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
     return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
-      delta::fwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(d.B) * d.H * groups, waves() * 64, 0, s>>>(a, groups);
+      const uint32_t grid = static_cast<uint32_t>(d.B) * d.H * groups;
+      if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, waves() * 64, 0, s>>>(a, groups);
+      else delta::fwd_kernel<E, DKP, waves(), false><<<grid, waves() * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
   };

@@ -19,16 +19,16 @@ namespace delta {
 namespace {
 
 template <typename E, int DKP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, kBuf = kWalkBuffers<E, DKP, true>;
+__global__ __launch_bounds__(WAVES * 64, 1) void bwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, true>;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true> tiles[kWalkBuffers<E, DKP, true>];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true> tiles[kBuf];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
   const int h = chain % a.H, seq = chain / a.H;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
-  const bool in = col < a.dv, live = col < a.dvp;
+  const bool in = col < a.dv;
   const Span span = span_of(a, seq);
   const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   f32x4_t S[ND];  // dS
@@ -39,16 +39,22 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
       const int row = state_row(t, g) + r;
       S[t][r] = a.d_sfinal && in && row < a.dk ? a.d_sfinal[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
     }
+  const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
+  const uint32_t sv = static_cast<uint32_t>(a.ldv * sizeof(E)), so = static_cast<uint32_t>(ldo * sizeof(E));
+  const uint32_t v_at = in ? 4 * g * sv + col * sizeof(E) : kNowhere, o_at = in ? 4 * g * so + col * sizeof(E) : kNowhere;
+  const bool live = col < a.dvp;
+  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
   Stager<E, DKP, true, WAVES * 64> next;
   Column<E, NT> d_o;
-  auto fetch_o = [&](int chunk) {
-    const int64_t ld = static_cast<int64_t>(a.H) * a.dv;
-    d_o.load(static_cast<const E*>(a.d_o) + span.token(chunk, C) * ld + static_cast<int64_t>(h) * a.dv + col, ld, span.len(chunk, C), in);
+  auto fetch = [&](int chunk) {
+    const int64_t token = span.token(chunk, C);
+    const int len = span.len(chunk, C);
+    next.load(a, chunk, h, token, len);
+    d_o.load(Buffer(static_cast<const E*>(a.d_o) + (token * a.H + h) * a.dv, rows_bytes(len, ldo, a.dv, sizeof(E))), o_at, so);
   };
   const int last = span.end - 1;
   if (span.first < span.end) {
-    next.load(a, last, h, span.token(last, C), span.len(last, C));
-    fetch_o(last);
+    fetch(last);
     next.store(tiles[0]);
   }
   __syncthreads();
@@ -57,72 +63,102 @@ __global__ __launch_bounds__(WAVES * 64) void bwd_kernel(Args a, int groups) {
     const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
     const int len = span.len(chunk, C);
     const bool more = chunk > span.first;
-    if (more) next.load(a, chunk - 1, h, span.token(chunk - 1, C), span.len(chunk - 1, C));
-    // e^{G_C - G} K dS', then + P^T dO
-    f32x4_t du[NT], go[NT];
+    f32x4_t go[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) go[mt] = d_o.tile(mt);
+    fetch(more ? chunk - 1 : chunk);
+    // e^{G_C - G} K dS'
+    f32x4_t du[NT];
+    Raw rows[2][NT];
+    auto read_rows = [&](int kp) {
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) rows[kp & 1][mt] = row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g);
+    };
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) du[mt] = zero4();
+    read_rows(0);
+    Split<E> scores[TR::kFrags], tri[TR::kFrags];
+    f32x4_t gm[NT], rest[NT], et[NT];
+    const Buffer kept(static_cast<E*>(a.after) + item * a.dvp * DKP, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      if (kp + 1 < NK) {
+        read_rows(kp + 1);
+      } else {
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+      }
+      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
+      kept.store(a_at + 32 * kp * sizeof(E), high(s));
+      in_order();
+      mma_all(du, rows[kp & 1], s);
+      in_order();
+    }
+    // + P^T dO (dO is exact in its type)
+#pragma unroll
+    for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      du[mt] = zero4();
-      go[mt] = d_o.tile(mt);
+      gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+      et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+      du[mt] *= rest[mt];
     }
-    if (more) fetch_o(chunk - 1);
-#pragma unroll
-    for (int kp = 0; kp < DKP / 32; ++kp) {
-      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
-      if (live) *reinterpret_cast<Raw*>(static_cast<E*>(a.after) + (item * a.dvp + col) * DKP + 32 * kp + 8 * g) = high(s);
-#pragma unroll
-      for (int mt = 0; mt < NT; ++mt) du[mt] = mma(row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g), s, du[mt]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt) du[mt] *= *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+    in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Raw s = high(Split<E>(go[2 * kp], go[2 * kp + 1]));  // dO is exact in its type
+      const Raw s = high(Split<E>(go[2 * kp], go[2 * kp + 1]));
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(tri_load2<E>(w.P, TR::at_t(mt, kp)), s, du[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(scores[TR::at_t(mt, kp)], s, du[mt]);
     }
-    // Y = T^T dU
+    in_order();
+    // dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y), the first while Y = T^T dU is under way
+    const float decay = w.vec[C - 1];
+    Raw cols[2][ND];
+    auto read_cols = [&](int n) {  // Q's and K's pairs of token tiles in turn
+#pragma unroll
+      for (int t = 0; t < ND; ++t) cols[n & 1][t] = state_col<DKP>(n < NP ? w.Q : w.K, 32 * (n % NP), t);
+    };
+    read_cols(0);
+    in_order();
     f32x4_t y[NT];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) y[mt] = zero4();
+    for (int mt = 0; mt < NT; ++mt) {
+      y[mt] = zero4();
+      go[mt] *= gm[mt] * a.scale;
+    }
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       const Split<E> s(du[2 * kp], du[2 * kp + 1]);
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri_load2<E>(w.T, TR::at_t(mt, kp)), s, y[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri[TR::at_t(mt, kp)], s, y[mt]);
     }
-    const float decay = w.vec[C - 1];
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
-    f32x4_t ey[NT];
+    const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) {
-      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
-      ey[mt] = y[mt] * *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
-      go[mt] *= gm * a.scale;
-      du[mt] = -(gm * ey[mt]);
+    for (int n = 0; n < 2 * NP; ++n) {
+      if (n + 1 < 2 * NP) read_cols(n + 1);
+      const int kp = n % NP;
+      if (n == NP) {
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          et[mt] *= y[mt];          // dV
+          go[mt] = -(gm[mt] * et[mt]);
+        }
+      }
+      const Split<E> s(go[2 * kp], go[2 * kp + 1]);
+      in_order();
+      mma_all(S, cols[n & 1], s);
+      in_order();
     }
 #pragma unroll
-    for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> s(go[2 * kp], go[2 * kp + 1]), n(du[2 * kp], du[2 * kp + 1]);
-#pragma unroll
-      for (int t = 0; t < ND; ++t) {
-        S[t] = mma(state_col<DKP>(w.Q, 32 * kp, t), s, S[t]);
-        S[t] = mma(state_col<DKP>(w.K, 32 * kp, t), n, S[t]);
-      }
-      if (live)
-        *reinterpret_cast<Raw*>(static_cast<E*>(a.y) + (item * a.dvp + col) * C + 32 * kp + 8 * g) = high(Split<E>(y[2 * kp], y[2 * kp + 1]));
-    }
-    E* vp = static_cast<E*>(a.dv_out) + token * a.ldv + static_cast<int64_t>(h) * a.dv + col;
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * g + r;
-        if (in && t < len) Elem<E>::st(vp, t * a.ldv, ey[mt][r]);
-      }
+    for (int kp = 0; kp < NP; ++kp) yb.store(y_at + 32 * kp * sizeof(E), high(Split<E>(y[2 * kp], y[2 * kp + 1])));
     if constexpr (kBuf == 1) __syncthreads();
     if (more) next.store(tiles[(last - chunk + 1) & (kBuf - 1)]);
+    const Buffer vb(static_cast<E*>(a.dv_out) + token * a.ldv + static_cast<int64_t>(h) * a.dv, rows_bytes(len, a.ldv, a.dv, sizeof(E)));
+    store_column<E>(vb, v_at, sv, et);
     __syncthreads();
   }
   if (a.ds0 && in) {

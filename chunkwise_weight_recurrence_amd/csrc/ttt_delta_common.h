@@ -282,14 +282,58 @@ template <typename E, int DKP, bool BWD> struct WalkTile {
 // Two of them where they fit the 160 KB, so that one is filled while the other is read.
 template <typename E, int DKP, bool BWD> constexpr int kWalkBuffers = 2 * sizeof(WalkTile<E, DKP, BWD>) <= 160 * 1024 ? 2 : 1;
 
+// A buffer resource over `bytes` bytes from p on (both the same for the wave): a load past them reads zero and
+// a store past them does nothing, so short chunks and narrow heads need no branch.  A chunk's rows lie within
+// 2^29 bytes; kNowhere, as a lane's offset, stays behind them for every row.
+constexpr uint32_t kNowhere = 0x40000000u;
+struct Buffer {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ Buffer(const void* p, int64_t bytes) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes > 0 ? bytes : 0));
+    rs = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0, n, 0x00020000);
+  }
+  template <typename R> __device__ __forceinline__ R load(uint32_t off) const {
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    const int o = static_cast<int>(off);
+    if constexpr (sizeof(R) == 2) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0));
+    else if constexpr (sizeof(R) == 4) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0));
+    else return __builtin_bit_cast(R, static_cast<u32x4_t>(__builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0)));
+  }
+  __device__ __forceinline__ void store(uint32_t off, uint16_t x) const { __builtin_amdgcn_raw_buffer_store_b16(x, rs, static_cast<int>(off), 0, 0); }
+  __device__ __forceinline__ void store(uint32_t off, float x) const {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), rs, static_cast<int>(off), 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t off, bf16x8_t x) const { store16(off, __builtin_bit_cast(uint4, x)); }
+  __device__ __forceinline__ void store(uint32_t off, f32x8 x) const {
+    store16(off, __builtin_bit_cast(uint4, x.a));
+    store16(off + 16, __builtin_bit_cast(uint4, x.b));
+  }
+  __device__ __forceinline__ void store16(uint32_t off, uint4 x) const {
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x.x, x.y, x.z, x.w}, rs, static_cast<int>(off), 0, 0);
+  }
+};
+// Bytes from the first element of `rows` rows of `cols` elements, ld apart, to the last one's end.
+__device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ld, int cols, int elem) {
+  return rows > 0 ? ((rows - 1) * ld + cols) * elem : 0;
+}
+
 // The next chunk's keys, queries, T, P and factors on their way through registers into the other buffer.
 template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
   using W = WalkTile<E, DKP, BWD>;
-  static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V;
-  static constexpr int kRows = (C * kPieces + THREADS - 1) / THREADS;
+  static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = THREADS / kPieces;
+  static constexpr int kRows = C / kStep;
   static constexpr int kT = (Tri<E>::kBytes / 16 + THREADS - 1) / THREADS, kP = (W::kPBytes / 16 + THREADS - 1) / THREADS;
-  static_assert(C * kPieces % THREADS == 0 && 3 * C / 4 <= THREADS);
+  static_assert(THREADS % kPieces == 0 && C % kStep == 0 && 3 * C / 4 <= THREADS);
   uint4 k[kRows], q[kRows], t[kT], p[kP], vec;
+  int row, col;  // of a thread's first piece
+
+  __device__ __forceinline__ Stager() : row(threadIdx.x / kPieces), col(threadIdx.x % kPieces * V) {}
+  // Pieces past the end are some thread's twice: both write the same.
+  static __device__ __forceinline__ int piece(int n, int all) { return min(static_cast<int>(threadIdx.x) + n * THREADS, all - 1); }
 
   __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len) {
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
@@ -309,49 +353,57 @@ template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
       lk = lq = DKP;
       len = C;
     }
+    const Buffer kb(kp, rows_bytes(len, lk, cols, sizeof(E))), qb(qp, rows_bytes(len, lq, cols, sizeof(E)));
+    const uint32_t sk = static_cast<uint32_t>(lk * sizeof(E)), sq = static_cast<uint32_t>(lq * sizeof(E));
+    const uint32_t at = col < cols ? col * sizeof(E) : kNowhere;
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-      const int i = threadIdx.x + n * THREADS, row = i / kPieces, col = (i % kPieces) * V;
-      k[n] = q[n] = uint4{0, 0, 0, 0};
-      if (row < len && col < cols) {
-        k[n] = *reinterpret_cast<const uint4*>(kp + row * lk + col);
-        q[n] = *reinterpret_cast<const uint4*>(qp + row * lq + col);
-      }
+      k[n] = kb.template load<uint4>(at + (row + n * kStep) * sk);
+      q[n] = qb.template load<uint4>(at + (row + n * kStep) * sq);
     }
     const uint4* tp = reinterpret_cast<const uint4*>(a.t + item * Tri<E>::kBytes);
     const uint4* pp = reinterpret_cast<const uint4*>(a.p + item * Tri<E>::kBytes);
 #pragma unroll
-    for (int n = 0; n < kT; ++n) {
-      const int i = threadIdx.x + n * THREADS;
-      if (i < Tri<E>::kBytes / 16) t[n] = tp[i];
-    }
+    for (int n = 0; n < kT; ++n) t[n] = tp[piece(n, Tri<E>::kBytes / 16)];
 #pragma unroll
-    for (int n = 0; n < kP; ++n) {
-      const int i = threadIdx.x + n * THREADS;
-      if (i < W::kPBytes / 16) p[n] = pp[i];
-    }
-    if (threadIdx.x < 3 * C / 4) vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[threadIdx.x];
+    for (int n = 0; n < kP; ++n) p[n] = pp[piece(n, W::kPBytes / 16)];
+    vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
   }
   __device__ __forceinline__ void store(W& w) const {
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-      const int i = threadIdx.x + n * THREADS, at = Tile<E, DKP>::at(i / kPieces, (i % kPieces) * V);
+      const int at = Tile<E, DKP>::at(row + n * kStep, col);
       *reinterpret_cast<uint4*>(w.K + at) = k[n];
       *reinterpret_cast<uint4*>(w.Q + at) = q[n];
     }
 #pragma unroll
-    for (int n = 0; n < kT; ++n) {
-      const int i = threadIdx.x + n * THREADS;
-      if (i < Tri<E>::kBytes / 16) reinterpret_cast<uint4*>(w.T)[i] = t[n];
-    }
+    for (int n = 0; n < kT; ++n) reinterpret_cast<uint4*>(w.T)[piece(n, Tri<E>::kBytes / 16)] = t[n];
 #pragma unroll
-    for (int n = 0; n < kP; ++n) {
-      const int i = threadIdx.x + n * THREADS;
-      if (i < W::kPBytes / 16) reinterpret_cast<uint4*>(w.P)[i] = p[n];
-    }
-    if (threadIdx.x < 3 * C / 4) reinterpret_cast<uint4*>(w.vec)[threadIdx.x] = vec;
+    for (int n = 0; n < kP; ++n) reinterpret_cast<uint4*>(w.P)[piece(n, W::kPBytes / 16)] = p[n];
+    reinterpret_cast<uint4*>(w.vec)[piece(0, 3 * C / 4)] = vec;
   }
 };
+
+// What is written above stays above: the reads of a stage are under way while the one before is computed.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// c[n] += a[n] b over N tiles, the terms of b one after the other so that a tile's sums are far apart.
+template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const bf16x8_t (&a)[N], const Split<bf16_t>& b) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.lo, c[n]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.hi, c[n]);
+}
+template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const f32x8 (&a)[N], const Split<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[n].a[j], b.a[j], c[n], 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[n].b[j], b.b[j], c[n], 0, 0, 0);
+}
 
 // A walk's chunks: those of one sequence, and its tokens.
 struct Span {
@@ -382,19 +434,15 @@ __device__ __forceinline__ Span span_of(const Args& a, int seq) {
   return s;
 }
 
-// A lane's column of 16-row result tiles, in the tensor's type: rows 4 g + r of tile mt are its tokens.
+// A lane's column of 16-row result tiles, in the tensor's type: rows 4 g + r of tile mt are its tokens.  `at`:
+// the byte offset of row 4 g, kNowhere for a column that is not there.
 template <typename E, int NT> struct Column {
   E x[NT][4];
-  __device__ __forceinline__ void load(const E* p, int64_t ld, int len, bool in) {
-    const int g = (threadIdx.x & 63) >> 4;
+  __device__ __forceinline__ void load(const Buffer& b, uint32_t at, uint32_t stride) {
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * g + r;
-        x[mt][r] = E{};
-        if (in && t < len) x[mt][r] = p[t * ld];
-      }
+      for (int r = 0; r < 4; ++r) x[mt][r] = b.template load<E>(at + (16 * mt + r) * stride);
   }
   __device__ __forceinline__ f32x4_t tile(int mt) const {
     f32x4_t f;
@@ -403,6 +451,17 @@ template <typename E, int NT> struct Column {
     return f;
   }
 };
+template <typename E> __device__ __forceinline__ E narrow(float x) {
+  if constexpr (std::is_same_v<E, float>) return x;
+  else return f32_to_bf16(x);
+}
+template <typename E, int NT>
+__device__ __forceinline__ void store_column(const Buffer& b, uint32_t at, uint32_t stride, const f32x4_t (&x)[NT]) {
+#pragma unroll
+  for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) b.store(at + (16 * mt + r) * stride, narrow<E>(x[mt][r]));
+}
 template <typename E> __device__ __forceinline__ typename Frag<E>::Raw high(const Split<E>& s) {
   if constexpr (std::is_same_v<E, float>) return f32x8{s.a, s.b};
   else return s.hi;

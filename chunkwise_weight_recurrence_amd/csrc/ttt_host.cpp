@@ -781,7 +781,7 @@ int check_delta_desc(const ttt_delta_desc* d) {
   if ((d->ldq != 0 && d->ldq < wk) || (d->ldk != 0 && d->ldk < wk) || (d->ldv != 0 && d->ldv < wv) ||
       (d->ldg != 0 && d->ldg < d->H) || (d->ldb != 0 && d->ldb < d->H))
     return fail(TTT_ERR_INVALID_ARG, "ldq, ldk, ldv, ldg, ldb must be 0 or at least a token's elements");
-  constexpr int64_t kMaxLd = 1 << 23;
+  constexpr int64_t kMaxLd = 1 << 22;  // a chunk's rows lie within 2^29 bytes
   const int64_t n = d->packed ? d->T : static_cast<int64_t>(d->B) * d->T;
   // Tokens are counted in 32 bits, rounded up to whole chunks; a launch has fewer than 2^32 threads.
   if (wk > kMaxLd || wv > kMaxLd || d->ldq > kMaxLd || d->ldk > kMaxLd || d->ldv > kMaxLd || d->ldg > kMaxLd || d->ldb > kMaxLd ||

@@ -620,7 +620,7 @@ typedef struct {
   float lr_max;   /* eta's upper end: 1, or 2 as the fast-weight layer has it        */
   float lr_bias;
   int64_t ldq, ldk, ldv; /* elements from one token's q (k, v) to the next, the heads of a
-                     token side by side; 0 means dense; up to 2^23                   */
+                     token side by side; 0 means dense; up to 2^22                   */
   int64_t ldg, ldb; /* the same for gate and beta, [..,H]                            */
 } ttt_delta_desc;
 

@@ -244,58 +244,41 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
 
 // ---- forward walk ----
 
-// A wave holds 16 columns of a head's state in its result registers and walks the chunks; the WAVES of a
-// workgroup share what they read of a chunk in LDS, filled one chunk ahead.  The state and what is added to
-// it are products of two-term operands: its error does not grow with the length.  KEEP: what a backward
-// needs is written.
+// A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
+// is added to it are products of two-term operands: its error does not grow with the length.  KEEP: what a
+// backward needs is written.
 template <typename E, int DKP, int WAVES, bool KEEP>
-__global__ __launch_bounds__(WAVES * 64, 1) void fwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false>;
+__global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void fwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false, WAVES>;
+  constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
   const int h = chain % a.H, seq = chain / a.H;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
-  const bool in = col < a.dv;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
-  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
-  f32x4_t S[ND];
-#pragma unroll
-  for (int t = 0; t < ND; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = state_row(t, g) + r;
-      S[t][r] = a.s0 && in && row < a.dk ? a.s0[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
-    }
-  const uint32_t sv = static_cast<uint32_t>(a.ldv * sizeof(E)), so = static_cast<uint32_t>(a.H * a.dv * sizeof(E));
-  const uint32_t v_at = in ? 4 * g * sv + col * sizeof(E) : kNowhere, o_at = in ? 4 * g * so + col * sizeof(E) : kNowhere;
-  const bool live = col < a.dvp;
-  const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
-  Stager<E, DKP, false, WAVES * 64> next;
-  Column<E, NT> v;
-  auto fetch = [&](int chunk) {
-    const int64_t token = span.token(chunk, C);
-    const int len = span.len(chunk, C);
-    next.load(a, chunk, h, token, len);
-    v.load(Buffer(static_cast<const E*>(a.v) + token * a.ldv + static_cast<int64_t>(h) * a.dv, rows_bytes(len, a.ldv, a.dv, sizeof(E))), v_at, sv);
-  };
-  if (span.first < span.end) {
-    fetch(span.first);
-    next.store(tiles[0]);
+  if (wave >= WAVES) {
+    load_walk<E, DKP, false, WAVES, kBuf>(a, span, h, grp * WAVES * 16, tiles, outs, static_cast<const E*>(a.v) + static_cast<int64_t>(h) * a.dv,
+                                          a.ldv, a.wide_v, static_cast<E*>(a.o) + static_cast<int64_t>(h) * a.dv, static_cast<int64_t>(a.H) * a.dv,
+                                          a.wide_o);
+    return;
   }
+  const int col = (grp * WAVES + wave) * 16 + i;
+  const bool live = col < a.dvp;
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
+  f32x4_t S[ND];
+  state_load(a.s0 ? a.s0 + state : nullptr, a.dk, a.dv, s_at, S);
+  __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
+  const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
   __syncthreads();
   for (int chunk = span.first; chunk < span.end; ++chunk) {
-    const WalkTile<E, DKP, false>& w = tiles[(chunk - span.first) & (kBuf - 1)];
-    const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
-    const int len = span.len(chunk, C);
-    const bool more = chunk + 1 < span.end;
-    f32x4_t vt[NT];
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt) vt[mt] = v.tile(mt);
-    fetch(more ? chunk + 1 : chunk);
-    // K S and Q S: rows of the next 32 channels are read while these are multiplied
+    const WalkTile<E, DKP, false, WAVES>& w = tiles[(chunk - span.first) & (kBuf - 1)];
+    OutTile<E, WAVES>& out = outs[(chunk - span.first) & (kBuf - 1)];
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    // K S and Q S: rows of the next 32 channels are read, and their part of the state split, while these are multiplied
     f32x4_t ko[2 * NT];
     Raw rows[2][2 * NT];
     auto read_rows = [&](int kp) {
@@ -309,25 +292,30 @@ __global__ __launch_bounds__(WAVES * 64, 1) void fwd_kernel(Args a, int groups) 
     for (int n = 0; n < 2 * NT; ++n) ko[n] = zero4();
     read_rows(0);
     Split<E> tri[TR::kFrags];
-    f32x4_t gm[NT], et[NT], rest[NT];
+    f32x4_t gm[NT], et[NT], rest[NT], vt[NT];
     const Buffer kept(KEEP ? static_cast<E*>(a.before) + item * a.dvp * DKP : nullptr, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    Split<E> s(S[0], S[1]);
 #pragma unroll
     for (int kp = 0; kp < NK; ++kp) {
       if (kp + 1 < NK) {
         read_rows(kp + 1);
       } else {
 #pragma unroll
-        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
-#pragma unroll
         for (int mt = 0; mt < NT; ++mt) {
           gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
           et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+          vt[mt] = four_of<16 * WAVES>(w.V, 16 * mt + 4 * g, 16 * wave);
         }
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
       }
-      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
       if constexpr (KEEP) kept.store(b_at + 32 * kp * sizeof(E), high(s));
       in_order();
       mma_all(ko, rows[kp & 1], s);
+      if (kp + 1 < NK) {
+        s = Split<E>(S[2 * kp + 2], S[2 * kp + 3]);
+        interleave<4 * NT * kMma, 2>();
+      }
       in_order();
     }
     // eta (V - e^G K S), U = T (that)
@@ -343,22 +331,26 @@ __global__ __launch_bounds__(WAVES * 64, 1) void fwd_kernel(Args a, int groups) 
     for (int mt = 0; mt < NT; ++mt) {
       rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
       ko[mt] = et[mt] * (vt[mt] - gm[mt] * ko[mt]);
-      o[mt] = ko[NT + mt] * (a.scale * gm[mt]);
       u[mt] = zero4();
     }
     in_order();
+    // the products with T leave room for what the next stages need
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       const Split<E> rhs(ko[2 * kp], ko[2 * kp + 1]);
 #pragma unroll
       for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri[TR::at(mt, kp)], rhs, u[mt]);
     }
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) o[mt] = ko[NT + mt] * (a.scale * gm[mt]);
     in_order();
     // S = e^{G_C} S + K^T (e^{G_C - G} U);  O += P U
     Raw scores[TR::kFrags];
-#pragma unroll
-    for (int t = 0; t < ND; ++t) S[t] *= decay;
     const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+    Split<E> us[NP];
+    Split<E> x(u[0] * rest[0], u[1] * rest[1]);
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       if (kp + 1 < NP) {
@@ -367,33 +359,25 @@ __global__ __launch_bounds__(WAVES * 64, 1) void fwd_kernel(Args a, int groups) 
 #pragma unroll
         for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load<E>(w.P, f);
       }
-      const Split<E> us(u[2 * kp] * rest[2 * kp], u[2 * kp + 1] * rest[2 * kp + 1]);
       in_order();
-      mma_all(S, cols[kp & 1], us);
+      mma_all(S, cols[kp & 1], x);
+      us[kp] = Split<E>(u[2 * kp], u[2 * kp + 1]);
+      if (kp + 1 < NP) x = Split<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
+      interleave<2 * ND * kMma, 3>();
       in_order();
     }
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> us(u[2 * kp], u[2 * kp + 1]);
-      if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(us));
+      if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(us[kp]));
 #pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], us, o[mt]);
+      for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], us[kp], o[mt]);
     }
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) out_tile(out, wave, mt, o[mt]);
     if constexpr (kBuf == 1) __syncthreads();
-    if (more) next.store(tiles[(chunk + 1 - span.first) & (kBuf - 1)]);
-    const Buffer ob(static_cast<E*>(a.o) + (token * a.H + h) * a.dv, rows_bytes(len, static_cast<int64_t>(a.H) * a.dv, a.dv, sizeof(E)));
-    store_column<E>(ob, o_at, so, o);
     __syncthreads();
   }
-  if (a.s_final && in) {
-#pragma unroll
-    for (int t = 0; t < ND; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = state_row(t, g) + r;
-        if (row < a.dk) a.s_final[state + static_cast<int64_t>(row) * a.dv + col] = S[t][r];
-      }
-  }
+  if (a.s_final) state_store(a.s_final + state, a.dk, a.dv, s_at, S);
 }
 
 // ---- one token ----
@@ -591,7 +575,8 @@ Args make_args(const ttt_delta_desc& d, const void* q, const void* k, const void
   a.q = q; a.k = k; a.v = v; a.gate = gate; a.beta = beta; a.d_o = d_o;
   a.wide_q = wide(q, d.dk, a.ldq);
   a.wide_k = wide(k, d.dk, a.ldk);
-  a.wide_do = wide(d_o, d.dv, 0);
+  a.wide_v = wide(v, d.dv, a.ldv);
+  a.wide_o = a.wide_do = d.dv % V == 0;  // dense, on 16 bytes
   a.dense = a.wide_q && a.wide_k;
   a.chunks = static_cast<int>(delta_chunks(d));
   a.chunks_per_seq = d.packed ? 0 : (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype);
@@ -663,8 +648,8 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
     return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
       const uint32_t grid = static_cast<uint32_t>(d.B) * d.H * groups;
-      if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, waves() * 64, 0, s>>>(a, groups);
-      else delta::fwd_kernel<E, DKP, waves(), false><<<grid, waves() * 64, 0, s>>>(a, groups);
+      if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
+      else delta::fwd_kernel<E, DKP, waves(), false><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
   };
@@ -677,6 +662,7 @@ hipError_t delta_bwd_launch(const ttt_delta_desc& d, const void* q, const void* 
   Args a = make_args(d, q, k, v, gate, beta, d_o);
   if (a.n == 0) return pass_states(d, d_sfinal, ds0, s);
   a.d_sfinal = d_sfinal;
+  a.wide_dv = d.dv % (16 / static_cast<int>(elem_bytes(d))) == 0 && a.ldv % (16 / static_cast<int>(elem_bytes(d))) == 0 && reinterpret_cast<uintptr_t>(dv) % 16 == 0;
   a.dq = dq; a.dk_out = dk; a.dv_out = dv; a.dgate = dgate; a.dbeta = dbeta; a.ds0 = ds0;
   const Layout l = ws_layout(d, true);
   place(a, d, l, ws, saved);

@@ -19,56 +19,39 @@ namespace delta {
 namespace {
 
 template <typename E, int DKP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 1) void bwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, true>;
+__global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void bwd_kernel(Args a, int groups) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, true, WAVES>;
+  constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true, WAVES> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
   const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
   const int h = chain % a.H, seq = chain / a.H;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const int col = (grp * WAVES + static_cast<int>(threadIdx.x >> 6)) * 16 + i;
-  const bool in = col < a.dv;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
-  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
-  f32x4_t S[ND];  // dS
-#pragma unroll
-  for (int t = 0; t < ND; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = state_row(t, g) + r;
-      S[t][r] = a.d_sfinal && in && row < a.dk ? a.d_sfinal[state + static_cast<int64_t>(row) * a.dv + col] : 0.0f;
-    }
-  const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
-  const uint32_t sv = static_cast<uint32_t>(a.ldv * sizeof(E)), so = static_cast<uint32_t>(ldo * sizeof(E));
-  const uint32_t v_at = in ? 4 * g * sv + col * sizeof(E) : kNowhere, o_at = in ? 4 * g * so + col * sizeof(E) : kNowhere;
-  const bool live = col < a.dvp;
-  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
-  Stager<E, DKP, true, WAVES * 64> next;
-  Column<E, NT> d_o;
-  auto fetch = [&](int chunk) {
-    const int64_t token = span.token(chunk, C);
-    const int len = span.len(chunk, C);
-    next.load(a, chunk, h, token, len);
-    d_o.load(Buffer(static_cast<const E*>(a.d_o) + (token * a.H + h) * a.dv, rows_bytes(len, ldo, a.dv, sizeof(E))), o_at, so);
-  };
-  const int last = span.end - 1;
-  if (span.first < span.end) {
-    fetch(last);
-    next.store(tiles[0]);
+  if (wave >= WAVES) {
+    load_walk<E, DKP, true, WAVES, kBuf>(a, span, h, grp * WAVES * 16, tiles, outs, static_cast<const E*>(a.d_o) + static_cast<int64_t>(h) * a.dv,
+                                         static_cast<int64_t>(a.H) * a.dv, a.wide_do, static_cast<E*>(a.dv_out) + static_cast<int64_t>(h) * a.dv,
+                                         a.ldv, a.wide_dv);
+    return;
   }
+  const int col = (grp * WAVES + wave) * 16 + i;
+  const bool live = col < a.dvp;
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
+  f32x4_t S[ND];  // dS
+  state_load(a.d_sfinal ? a.d_sfinal + state : nullptr, a.dk, a.dv, s_at, S);
+  __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
+  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+  const int last = span.end - 1;
   __syncthreads();
   for (int chunk = last; chunk >= span.first; --chunk) {
-    const WalkTile<E, DKP, true>& w = tiles[(last - chunk) & (kBuf - 1)];
-    const int64_t token = span.token(chunk, C), item = static_cast<int64_t>(chunk) * a.H + h;
-    const int len = span.len(chunk, C);
-    const bool more = chunk > span.first;
-    f32x4_t go[NT];
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt) go[mt] = d_o.tile(mt);
-    fetch(more ? chunk - 1 : chunk);
+    const WalkTile<E, DKP, true, WAVES>& w = tiles[(last - chunk) & (kBuf - 1)];
+    OutTile<E, WAVES>& out = outs[(last - chunk) & (kBuf - 1)];
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
     // e^{G_C - G} K dS'
-    f32x4_t du[NT];
+    f32x4_t du[NT], go[NT];
     Raw rows[2][NT];
     auto read_rows = [&](int kp) {
 #pragma unroll
@@ -80,20 +63,27 @@ __global__ __launch_bounds__(WAVES * 64, 1) void bwd_kernel(Args a, int groups) 
     Split<E> scores[TR::kFrags], tri[TR::kFrags];
     f32x4_t gm[NT], rest[NT], et[NT];
     const Buffer kept(static_cast<E*>(a.after) + item * a.dvp * DKP, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    Split<E> s(S[0], S[1]);
 #pragma unroll
     for (int kp = 0; kp < NK; ++kp) {
       if (kp + 1 < NK) {
         read_rows(kp + 1);
       } else {
 #pragma unroll
-        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
+        for (int mt = 0; mt < NT; ++mt) {
+          rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+          go[mt] = four_of<16 * WAVES>(w.V, 16 * mt + 4 * g, 16 * wave);
+        }
 #pragma unroll
-        for (int mt = 0; mt < NT; ++mt) rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
       }
-      const Split<E> s(S[2 * kp], S[2 * kp + 1]);
       kept.store(a_at + 32 * kp * sizeof(E), high(s));
       in_order();
       mma_all(du, rows[kp & 1], s);
+      if (kp + 1 < NK) {
+        s = Split<E>(S[2 * kp + 2], S[2 * kp + 3]);
+        interleave<2 * NT * kMma, 3>();
+      }
       in_order();
     }
     // + P^T dO (dO is exact in its type)
@@ -105,16 +95,18 @@ __global__ __launch_bounds__(WAVES * 64, 1) void bwd_kernel(Args a, int groups) 
       et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
       du[mt] *= rest[mt];
     }
+    const float decay = w.vec[C - 1];
     in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Raw s = high(Split<E>(go[2 * kp], go[2 * kp + 1]));
+      const Raw e = high(Split<E>(go[2 * kp], go[2 * kp + 1]));
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(scores[TR::at_t(mt, kp)], s, du[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) du[mt] = mma(scores[TR::at_t(mt, kp)], e, du[mt]);
     }
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
     in_order();
-    // dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y), the first while Y = T^T dU is under way
-    const float decay = w.vec[C - 1];
+    // dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y), with Y = T^T dU
     Raw cols[2][ND];
     auto read_cols = [&](int n) {  // Q's and K's pairs of token tiles in turn
 #pragma unroll
@@ -124,52 +116,45 @@ __global__ __launch_bounds__(WAVES * 64, 1) void bwd_kernel(Args a, int groups) 
     in_order();
     f32x4_t y[NT];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) {
-      y[mt] = zero4();
-      go[mt] *= gm[mt] * a.scale;
-    }
+    for (int mt = 0; mt < NT; ++mt) y[mt] = zero4();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> s(du[2 * kp], du[2 * kp + 1]);
+      const Split<E> e(du[2 * kp], du[2 * kp + 1]);
 #pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri[TR::at_t(mt, kp)], s, y[mt]);
+      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri[TR::at_t(mt, kp)], e, y[mt]);
     }
 #pragma unroll
-    for (int t = 0; t < ND; ++t) S[t] *= decay;
+    for (int mt = 0; mt < NT; ++mt) go[mt] *= gm[mt] * a.scale;
+    s = Split<E>(go[0], go[1]);
+    in_order();
     const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+    Split<E> ys[NP];
 #pragma unroll
     for (int n = 0; n < 2 * NP; ++n) {
       if (n + 1 < 2 * NP) read_cols(n + 1);
-      const int kp = n % NP;
-      if (n == NP) {
-#pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-          et[mt] *= y[mt];          // dV
-          go[mt] = -(gm[mt] * et[mt]);
-        }
-      }
-      const Split<E> s(go[2 * kp], go[2 * kp + 1]);
       in_order();
       mma_all(S, cols[n & 1], s);
+      if (n < NP) {
+        ys[n] = Split<E>(y[2 * n], y[2 * n + 1]);
+#pragma unroll
+        for (int mt = 2 * n; mt < 2 * n + 2; ++mt) {
+          et[mt] *= y[mt];          // dV
+          y[mt] = -(gm[mt] * et[mt]);
+        }
+      }
+      if (n + 1 < NP) s = Split<E>(go[2 * n + 2], go[2 * n + 3]);
+      else if (n + 1 < 2 * NP) s = Split<E>(y[2 * (n + 1 - NP)], y[2 * (n + 1 - NP) + 1]);
+      interleave<2 * ND * kMma, 3>();
       in_order();
     }
 #pragma unroll
-    for (int kp = 0; kp < NP; ++kp) yb.store(y_at + 32 * kp * sizeof(E), high(Split<E>(y[2 * kp], y[2 * kp + 1])));
+    for (int kp = 0; kp < NP; ++kp) yb.store(y_at + 32 * kp * sizeof(E), high(ys[kp]));
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) out_tile(out, wave, mt, et[mt]);
     if constexpr (kBuf == 1) __syncthreads();
-    if (more) next.store(tiles[(last - chunk + 1) & (kBuf - 1)]);
-    const Buffer vb(static_cast<E*>(a.dv_out) + token * a.ldv + static_cast<int64_t>(h) * a.dv, rows_bytes(len, a.ldv, a.dv, sizeof(E)));
-    store_column<E>(vb, v_at, sv, et);
     __syncthreads();
   }
-  if (a.ds0 && in) {
-#pragma unroll
-    for (int t = 0; t < ND; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = state_row(t, g) + r;
-        if (row < a.dk) a.ds0[state + static_cast<int64_t>(row) * a.dv + col] = S[t][r];
-      }
-  }
+  if (a.ds0) state_store(a.ds0 + state, a.dk, a.dv, s_at, S);
 }
 
 // ---- what does not depend on the walk ----
@@ -440,7 +425,7 @@ template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t 
   {
     KernelScope scope(TTT_KERNEL_DELTA_BWD, s);
     e = by_waves<DKP>(a, [&](auto waves, int groups) {
-      bwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(a.B) * a.H * groups, waves() * 64, 0, s>>>(a, groups);
+      bwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(a.B) * a.H * groups, (waves() + kLoaders) * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

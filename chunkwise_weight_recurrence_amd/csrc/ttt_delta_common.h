@@ -28,7 +28,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 struct Args {
   int B, T, H, Hk, dk, dv, dvp;  // dvp: dv rounded up to 32, the width of U, Y and the kept states
   int packed, gate_kind;
-  int wide_q, wide_k, wide_do;   // whether every row of a head starts on 16 bytes
+  int wide_q, wide_k, wide_v, wide_o, wide_do, wide_dv;  // whether every row of a head starts on 16 bytes
   int dense;                     // both q and k are wide: the walks read them where they are
   float scale, lr_max, lr_bias;
   int64_t n;                     // tokens
@@ -266,10 +266,16 @@ template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* 
   return s;
 }
 
-// ---- what a walk reads of a chunk, one chunk ahead ----
+// ---- the walks' workgroups ----
+//
+// WAVES waves hold 16 columns of a state each and do nothing but the chain of products; kLoaders more bring
+// what a chunk needs from memory into LDS, two chunks ahead (one in registers, one in the other buffer), and
+// carry the result columns away.  So the chain has no wait for memory in it and no registers go to loads.
+
+constexpr int kLoaders = 2, kLoadThreads = kLoaders * 64;
 
 // A walk's LDS for one chunk.
-template <typename E, int DKP, bool BWD> struct WalkTile {
+template <typename E, int DKP, bool BWD, int WAVES> struct WalkTile {
   static constexpr int C = Chunk<E>::C;
   static constexpr int kPBytes = BWD ? Tri<E>::kBytes : Tri<E>::kHalfBytes;  // the backward's scores have two terms
   E K[C * Tile<E, DKP>::kRow];
@@ -277,10 +283,16 @@ template <typename E, int DKP, bool BWD> struct WalkTile {
   char T[Tri<E>::kBytes];
   char P[kPBytes];
   float vec[3 * C];
+  E V[C * 16 * WAVES];  // [token][column]: v, or the gradient of o
 };
-
-// Two of them where they fit the 160 KB, so that one is filled while the other is read.
-template <typename E, int DKP, bool BWD> constexpr int kWalkBuffers = 2 * sizeof(WalkTile<E, DKP, BWD>) <= 160 * 1024 ? 2 : 1;
+// The result columns of a chunk: bf16 as [column][token], fp32 as [token][column].
+template <typename E, int WAVES> struct OutTile {
+  static constexpr int C = Chunk<E>::C, kRow = sizeof(E) == 2 ? C + 4 : 16 * WAVES;
+  E x[(sizeof(E) == 2 ? 16 * WAVES : C) * kRow];
+};
+// Two chunks where they fit the 160 KB, so that one is filled while the other is read.
+template <typename E, int DKP, bool BWD, int WAVES>
+constexpr int kWalkBuffers = 2 * (sizeof(WalkTile<E, DKP, BWD, WAVES>) + sizeof(OutTile<E, WAVES>)) <= 160 * 1024 ? 2 : 1;
 
 // A buffer resource over `bytes` bytes from p on (both the same for the wave): a load past them reads zero and
 // a store past them does nothing, so short chunks and narrow heads need no branch.  A chunk's rows lie within
@@ -321,39 +333,41 @@ __device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ld, int cols, in
   return rows > 0 ? ((rows - 1) * ld + cols) * elem : 0;
 }
 
-// The next chunk's keys, queries, T, P and factors on their way through registers into the other buffer.
-template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
-  using W = WalkTile<E, DKP, BWD>;
-  static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = THREADS / kPieces;
-  static constexpr int kRows = C / kStep;
-  static constexpr int kT = (Tri<E>::kBytes / 16 + THREADS - 1) / THREADS, kP = (W::kPBytes / 16 + THREADS - 1) / THREADS;
-  static_assert(THREADS % kPieces == 0 && C % kStep == 0 && 3 * C / 4 <= THREADS);
-  uint4 k[kRows], q[kRows], t[kT], p[kP], vec;
-  int row, col;  // of a thread's first piece
+// The loaders' part: the next chunk's pieces in registers.
+template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
+  using W = WalkTile<E, DKP, BWD, WAVES>;
+  static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = kLoadThreads / kPieces, kRows = C / kStep;
+  static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads, kP = (W::kPBytes / 16 + kLoadThreads - 1) / kLoadThreads;
+  static constexpr int kCols = 16 * WAVES, kVPieces = kCols / V, kVStep = kLoadThreads / kVPieces, kVRows = C / kVStep;
+  static_assert(kLoadThreads % kPieces == 0 && C % kStep == 0 && 3 * C / 4 <= kLoadThreads && C % kVStep == 0);
+  uint4 k[kRows], q[kRows], t[kT], p[kP], vec, v[kVRows];
+  int tid, row, col, vrow, vcol;  // of a thread's first pieces
 
-  __device__ __forceinline__ Stager() : row(threadIdx.x / kPieces), col(threadIdx.x % kPieces * V) {}
+  __device__ __forceinline__ Loader(int tid_)
+      : tid(tid_), row(tid_ / kPieces), col(tid_ % kPieces * V), vrow(tid_ / kVPieces), vcol(tid_ % kVPieces * V) {}
   // Pieces past the end are some thread's twice: both write the same.
-  static __device__ __forceinline__ int piece(int n, int all) { return min(static_cast<int>(threadIdx.x) + n * THREADS, all - 1); }
+  __device__ __forceinline__ int piece(int n, int all) const { return min(tid + n * kLoadThreads, all - 1); }
 
-  __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len) {
+  // cp: the first of the chunk's rows of v (or of the gradient of o), from this workgroup's column c0 on
+  __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len, const E* cp, int64_t ldc, int c0, bool wide) {
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
     const int hk = h / (a.H / a.Hk);
     const E *kp, *qp;
     int64_t lk, lq;
-    int cols = DKP;
+    int cols = DKP, krows = C;
     if (a.dense) {
       kp = static_cast<const E*>(a.k) + token * a.ldk + hk * a.dk;
       qp = static_cast<const E*>(a.q) + token * a.ldq + hk * a.dk;
       lk = a.ldk;
       lq = a.ldq;
       cols = a.dk;
+      krows = len;
     } else {
       kp = static_cast<const E*>(a.kq) + (static_cast<int64_t>(chunk) * a.Hk + hk) * 2 * C * DKP;
       qp = kp + C * DKP;
       lk = lq = DKP;
-      len = C;
     }
-    const Buffer kb(kp, rows_bytes(len, lk, cols, sizeof(E))), qb(qp, rows_bytes(len, lq, cols, sizeof(E)));
+    const Buffer kb(kp, rows_bytes(krows, lk, cols, sizeof(E))), qb(qp, rows_bytes(krows, lq, cols, sizeof(E)));
     const uint32_t sk = static_cast<uint32_t>(lk * sizeof(E)), sq = static_cast<uint32_t>(lq * sizeof(E));
     const uint32_t at = col < cols ? col * sizeof(E) : kNowhere;
 #pragma unroll
@@ -368,6 +382,22 @@ template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
 #pragma unroll
     for (int n = 0; n < kP; ++n) p[n] = pp[piece(n, W::kPBytes / 16)];
     vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
+    const int vcols = a.dv - c0;  // may be none
+    const Buffer vb(cp, vcols > 0 ? rows_bytes(len, ldc, vcols, sizeof(E)) : 0);
+    const uint32_t sv = static_cast<uint32_t>(ldc * sizeof(E));
+    if (wide) {
+      const uint32_t vat = vcol < vcols ? vcol * sizeof(E) : kNowhere;
+#pragma unroll
+      for (int n = 0; n < kVRows; ++n) v[n] = vb.template load<uint4>(vat + (vrow + n * kVStep) * sv);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kVRows; ++n) {
+        E x[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = vb.template load<E>(vcol + j < vcols ? (vcol + j) * sizeof(E) + (vrow + n * kVStep) * sv : kNowhere);
+        __builtin_memcpy(&v[n], x, 16);
+      }
+    }
   }
   __device__ __forceinline__ void store(W& w) const {
 #pragma unroll
@@ -381,11 +411,98 @@ template <typename E, int DKP, bool BWD, int THREADS> struct Stager {
 #pragma unroll
     for (int n = 0; n < kP; ++n) reinterpret_cast<uint4*>(w.P)[piece(n, W::kPBytes / 16)] = p[n];
     reinterpret_cast<uint4*>(w.vec)[piece(0, 3 * C / 4)] = vec;
+#pragma unroll
+    for (int n = 0; n < kVRows; ++n) *reinterpret_cast<uint4*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
+  }
+  // A chunk's result columns to memory (op: as cp).
+  __device__ __forceinline__ void put(const Args& a, const OutTile<E, WAVES>& out, E* op, int64_t ldo, int len, int c0, bool wide) const {
+    const int cols = a.dv - c0;
+    const Buffer ob(op, cols > 0 ? rows_bytes(len, ldo, cols, sizeof(E)) : 0);
+    const uint32_t so = static_cast<uint32_t>(ldo * sizeof(E));
+#pragma unroll
+    for (int n = 0; n < kVRows; ++n) {
+      int r, c;
+      uint4 x;
+      if constexpr (sizeof(E) == 2) {
+        // 16 lanes: 16 tokens of eight columns
+        typedef short v4s __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) const v4s lds_v4s;
+        const int unit = tid / 16 + n * (kLoadThreads / 16), i = tid & 15;
+        r = unit / kVPieces * 16;
+        c = unit % kVPieces * 8;
+        const auto p0 = (lds_v4s*)(out.x + (c + (i >> 2)) * out.kRow + r + 4 * (i & 3));
+        const auto p1 = (lds_v4s*)(out.x + (c + 4 + (i >> 2)) * out.kRow + r + 4 * (i & 3));
+        const v4s y[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p0),
+                          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p1)};
+        x = __builtin_bit_cast(uint4, y);
+        r += i;
+      } else {
+        r = vrow + n * kVStep;
+        c = vcol;
+        x = *reinterpret_cast<const uint4*>(out.x + r * out.kRow + c);
+      }
+      if (wide) {
+        ob.store16(c < cols ? c * sizeof(E) + r * so : kNowhere, x);
+      } else {
+        E e[V];
+        __builtin_memcpy(e, &x, 16);
+#pragma unroll
+        for (int j = 0; j < V; ++j) ob.store(c + j < cols ? (c + j) * sizeof(E) + r * so : kNowhere, e[j]);
+      }
+    }
   }
 };
 
+// The loaders' walk beside the others': FORWARD from the first chunk on, else from the last back.  `in` and `out` are the
+// head's first row of v (or of the gradient of o) and of the result.
+template <typename E, int DKP, bool BWD, int WAVES, int BUF, typename Tiles, typename Outs, typename S>
+__device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, int c0, Tiles& tiles, Outs& outs, const E* in, int64_t ld_in,
+                                          bool wide_in, E* out, int64_t ld_out, bool wide_out) {
+  constexpr int C = Chunk<E>::C;
+  Loader<E, DKP, BWD, WAVES> l(threadIdx.x - WAVES * 64);
+  const int count = span.end - span.first;
+  auto chunk_of = [&](int n) { return BWD ? span.end - 1 - min(n, count - 1) : span.first + min(n, count - 1); };
+  auto load = [&](int n) {
+    const int chunk = chunk_of(n);
+    const int64_t token = span.token(chunk, C);
+    l.load(a, chunk, h, token, span.len(chunk, C), in + token * ld_in + c0, ld_in, c0, wide_in);
+  };
+  auto put = [&](int n) {
+    const int chunk = chunk_of(n);
+    l.put(a, outs[n & (BUF - 1)], out + span.token(chunk, C) * ld_out + c0, ld_out, span.len(chunk, C), c0, wide_out);
+  };
+  if (count > 0) {
+    load(0);
+    l.store(tiles[0]);
+    load(1);
+  }
+  __syncthreads();
+  for (int n = 0; n < count; ++n) {
+    if constexpr (BUF == 2) {
+      l.store(tiles[(n + 1) & 1]);
+      load(n + 2);
+      if (n > 0) put(n - 1);
+    } else {
+      __syncthreads();  // the others are done with the chunk
+      l.store(tiles[0]);
+      load(n + 2);
+      put(n);
+    }
+    __syncthreads();
+  }
+  if (BUF == 2 && count > 0) put(count - 1);
+}
+
 // What is written above stays above: the reads of a stage are under way while the one before is computed.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+// N times a matrix instruction and then K others of the vector unit, which run while it does.
+template <int N, int K> __device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, K, 0);
+  }
+}
 
 // c[n] += a[n] b over N tiles, the terms of b one after the other so that a tile's sums are far apart.
 template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const bf16x8_t (&a)[N], const Split<bf16_t>& b) {
@@ -434,33 +551,49 @@ __device__ __forceinline__ Span span_of(const Args& a, int seq) {
   return s;
 }
 
-// A lane's column of 16-row result tiles, in the tensor's type: rows 4 g + r of tile mt are its tokens.  `at`:
-// the byte offset of row 4 g, kNowhere for a column that is not there.
-template <typename E, int NT> struct Column {
-  E x[NT][4];
-  __device__ __forceinline__ void load(const Buffer& b, uint32_t at, uint32_t stride) {
+// Four rows r0 .. r0 + 3 of column col0 + i of a [..][LD] array, as a result tile has them.
+template <int LD> __device__ __forceinline__ f32x4_t four_of(const bf16_t* lds, int r0, int col0) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  const int i = threadIdx.x & 15;
+  const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + (r0 + (i >> 2)) * LD + col0 + 4 * (i & 3)));
+  f32x4_t f;
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[mt][r] = b.template load<E>(at + (16 * mt + r) * stride);
-  }
-  __device__ __forceinline__ f32x4_t tile(int mt) const {
-    f32x4_t f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = Elem<E>::ld(x[mt], r);
-    return f;
-  }
-};
-template <typename E> __device__ __forceinline__ E narrow(float x) {
-  if constexpr (std::is_same_v<E, float>) return x;
-  else return f32_to_bf16(x);
+  for (int j = 0; j < 4; ++j) f[j] = bf16_to_f32(static_cast<uint16_t>(x[j]));
+  return f;
 }
-template <typename E, int NT>
-__device__ __forceinline__ void store_column(const Buffer& b, uint32_t at, uint32_t stride, const f32x4_t (&x)[NT]) {
+template <int LD> __device__ __forceinline__ f32x4_t four_of(const float* lds, int r0, int col0) {
+  f32x4_t f;
 #pragma unroll
-  for (int mt = 0; mt < NT; ++mt)
+  for (int j = 0; j < 4; ++j) f[j] = lds[(r0 + j) * LD + col0 + (threadIdx.x & 15)];
+  return f;
+}
+// A wave's 16 result columns of row tile mt.
+template <int WAVES> __device__ __forceinline__ void out_tile(OutTile<bf16_t, WAVES>& o, int wave, int mt, f32x4_t x) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  *reinterpret_cast<uint2*>(o.x + (16 * wave + i) * o.kRow + 16 * mt + 4 * g) = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+}
+template <int WAVES> __device__ __forceinline__ void out_tile(OutTile<float, WAVES>& o, int wave, int mt, f32x4_t x) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) b.store(at + (16 * mt + r) * stride, narrow<E>(x[mt][r]));
+  for (int r = 0; r < 4; ++r) o.x[(16 * mt + 4 * g + r) * o.kRow + 16 * wave + i] = x[r];
+}
+// A wave's 16 columns of a [dk][dv] state to and from its result tiles.
+template <int ND> __device__ __forceinline__ void state_load(const float* p, int dk, int dv, uint32_t at, f32x4_t (&S)[ND]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const Buffer b(p, p ? static_cast<int64_t>(dk) * dv * 4 : 0);
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[t][r] = b.load<float>(at + (state_row(t, g) + r) * dv * 4);
+}
+template <int ND> __device__ __forceinline__ void state_store(float* p, int dk, int dv, uint32_t at, const f32x4_t (&S)[ND]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const Buffer b(p, static_cast<int64_t>(dk) * dv * 4);
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) b.store(at + (state_row(t, g) + r) * dv * 4, S[t][r]);
 }
 template <typename E> __device__ __forceinline__ typename Frag<E>::Raw high(const Split<E>& s) {
   if constexpr (std::is_same_v<E, float>) return f32x8{s.a, s.b};

@@ -255,7 +255,8 @@ __global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void fwd_kernel(Args a,
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
-  const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
+  const int grp = walk_group(groups), chain = walk_chain(groups);
+  if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
@@ -647,7 +648,7 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     if (e != hipSuccess) return e;
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
     return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
-      const uint32_t grid = static_cast<uint32_t>(d.B) * d.H * groups;
+      const uint32_t grid = delta::walk_grid(a, groups);
       if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
       else delta::fwd_kernel<E, DKP, waves(), false><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
       return hipGetLastError();

@@ -26,7 +26,8 @@ __global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void bwd_kernel(Args a,
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
-  const int grp = blockIdx.x % groups, chain = blockIdx.x / groups;
+  const int grp = walk_group(groups), chain = walk_chain(groups);
+  if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
@@ -425,7 +426,7 @@ template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t 
   {
     KernelScope scope(TTT_KERNEL_DELTA_BWD, s);
     e = by_waves<DKP>(a, [&](auto waves, int groups) {
-      bwd_kernel<E, DKP, waves()><<<static_cast<uint32_t>(a.B) * a.H * groups, (waves() + kLoaders) * 64, 0, s>>>(a, groups);
+      bwd_kernel<E, DKP, waves()><<<walk_grid(a, groups), (waves() + kLoaders) * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

@@ -644,6 +644,12 @@ template <int DKP, typename F> hipError_t by_waves(const Args& a, F&& f) {
   else return f(std::integral_constant<int, 2>{}, static_cast<int>((columns + 1) / 2));
 }
 
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own.  Those that share a head's keys and
+// queries are put on one, the heads (chains) on all in turn: in long runs they are a sequence's.
+inline uint32_t walk_grid(const Args& a, int groups) { return static_cast<uint32_t>((static_cast<int64_t>(a.B) * a.H + 7) / 8 * 8 * groups); }
+__device__ __forceinline__ int walk_chain(int groups) { return static_cast<int>(blockIdx.x / 8 / groups * 8 + blockIdx.x % 8); }
+__device__ __forceinline__ int walk_group(int groups) { return static_cast<int>(blockIdx.x / 8 % groups); }
+
 // The chunks' T and P into the workspace (ttt_delta.hip; BWD: the transposes), and the backward's three
 // kernels (ttt_delta_bwd.hip).
 template <typename E, int DKP, bool BWD> hipError_t launch_prep(const Args& a, hipStream_t s);

@@ -244,26 +244,186 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
 
 // ---- forward walk ----
 
+// The chain (waves 0 .. WAVES - 1) and its helpers (the next WAVES) where there are few heads.  First half of a
+// chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.
+template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
+__device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
+                                                  Exchange<E, DKP, WAVES>& exchange) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kMma = sizeof(E) == 2 ? 1 : 4;
+  using TR = Tri<E>;
+  using Raw = typename Frag<E>::Raw;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const bool helper = threadIdx.x >= WAVES * 64;
+  const int wave = (threadIdx.x >> 6) % WAVES, col = (grp * WAVES + wave) * 16 + i;
+  char* states = exchange.state[wave];
+  char* us = exchange.rows[wave];
+  if (helper) {
+    const bool live = col < a.dvp;
+    const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+    __syncthreads();
+    for (int chunk = span.first; chunk < span.end; ++chunk) {
+      const auto& w = tiles[(chunk - span.first) & 1];
+      const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+      const Buffer kept(KEEP ? static_cast<E*>(a.before) + item * a.dvp * DKP : nullptr, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+      f32x4_t o[NT];
+      Raw rows[2][NT];
+      Split<E> s[2];
+      auto read = [&](int kp) {
+        s[kp & 1] = take<E>(states, kp);
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) rows[kp & 1][mt] = row_frag<DKP>(w.Q, 16 * mt + i, 32 * kp + 8 * g);
+      };
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) o[mt] = zero4();
+      read(0);
+#pragma unroll
+      for (int kp = 0; kp < NK; ++kp) {
+        if (kp + 1 < NK) read(kp + 1);
+        in_order();
+        if constexpr (KEEP) kept.store(b_at + 32 * kp * sizeof(E), high(s[kp & 1]));
+        mma_all(o, rows[kp & 1], s[kp & 1]);
+        in_order();
+      }
+      Raw scores[TR::kFrags];
+#pragma unroll
+      for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load<E>(w.P, f);
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) o[mt] *= *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g) * a.scale;
+      __syncthreads();
+      const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+#pragma unroll
+      for (int kp = 0; kp < NP; ++kp) {
+        const Split<E> u = take<E>(us, kp);
+        if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(u));
+#pragma unroll
+        for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], u, o[mt]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) out_tile(outs[(chunk - span.first) & 1], wave, mt, o[mt]);
+      __syncthreads();
+    }
+    return;
+  }
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
+  f32x4_t S[ND];
+  state_load(a.s0 ? a.s0 + state : nullptr, a.dk, a.dv, s_at, S);
+  Split<E> s[NK];
+#pragma unroll
+  for (int kp = 0; kp < NK; ++kp) {
+    s[kp] = Split<E>(S[2 * kp], S[2 * kp + 1]);
+    give(states, kp, s[kp]);
+  }
+  __syncthreads();
+  for (int chunk = span.first; chunk < span.end; ++chunk) {
+    const auto& w = tiles[(chunk - span.first) & 1];
+    f32x4_t ks[NT], gm[NT], et[NT], vt[NT], rest[NT];
+    Raw rows[2][NT];
+    auto read_rows = [&](int kp) {
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) rows[kp & 1][mt] = row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g);
+    };
+    Split<E> tri[TR::kFrags];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) ks[mt] = zero4();
+    read_rows(0);
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      if (kp + 1 < NK) {
+        read_rows(kp + 1);
+      }
+      if (kp + 2 == NK || NK == 1) {
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+          et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+          vt[mt] = four_of<16 * WAVES>(w.V, 16 * mt + 4 * g, 16 * wave);
+        }
+      }
+      if (kp + 1 == NK) {
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
+      }
+      in_order();
+      mma_all(ks, rows[kp & 1], s[kp]);
+      in_order();
+    }
+    const float decay = w.vec[C - 1];
+    Raw cols[2][ND];
+    auto read_cols = [&](int kp) {
+#pragma unroll
+      for (int t = 0; t < ND; ++t) cols[kp & 1][t] = state_col<DKP>(w.K, 32 * kp, t);
+    };
+    f32x4_t u[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+      ks[mt] = et[mt] * (vt[mt] - gm[mt] * ks[mt]);
+      u[mt] = zero4();
+    }
+    read_cols(0);
+    in_order();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
+      tri_mul<E>(u, tri, rhs, kp);
+    }
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
+    in_order();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) give(us, kp, Split<E>(u[2 * kp], u[2 * kp + 1]));
+    __syncthreads();
+    Split<E> x(u[0] * rest[0], u[1] * rest[1]);
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      if (kp + 1 < NP) read_cols(kp + 1);
+      in_order();
+      mma_all(S, cols[kp & 1], x);
+      if (kp + 1 < NP) {
+        x = Split<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
+        interleave<2 * ND * kMma, 2>();
+      }
+      in_order();
+    }
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      s[kp] = Split<E>(S[2 * kp], S[2 * kp + 1]);
+      give(states, kp, s[kp]);
+    }
+    __syncthreads();
+  }
+  if (a.s_final) state_store(a.s_final + state, a.dk, a.dv, s_at, S);
+}
+
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
 // is added to it are products of two-term operands: its error does not grow with the length.  KEEP: what a
 // backward needs is written.
 template <typename E, int DKP, int WAVES, bool KEEP>
-__global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void fwd_kernel(Args a, int groups) {
+__global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
+  __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
-  if (wave >= WAVES) {
-    load_walk<E, DKP, false, WAVES, kBuf>(a, span, h, grp * WAVES * 16, tiles, outs, static_cast<const E*>(a.v) + static_cast<int64_t>(h) * a.dv,
-                                          a.ldv, a.wide_v, static_cast<E*>(a.o) + static_cast<int64_t>(h) * a.dv, static_cast<int64_t>(a.H) * a.dv,
-                                          a.wide_o);
+  constexpr bool HELP = WAVES == 2;
+  if (wave >= WAVES + (HELP ? WAVES : 0)) {
+    const E* in = static_cast<const E*>(a.v) + static_cast<int64_t>(h) * a.dv;
+    E* out = static_cast<E*>(a.o) + static_cast<int64_t>(h) * a.dv;
+    const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
+    if (a.wide_v && a.wide_o) load_walk<E, DKP, false, WAVES, kBuf, HELP, true>(a, span, h, grp * WAVES * 16, tiles, outs, in, a.ldv, out, ldo);
+    else load_walk<E, DKP, false, WAVES, kBuf, HELP, false>(a, span, h, grp * WAVES * 16, tiles, outs, in, a.ldv, out, ldo);
+    return;
+  }
+  if constexpr (HELP) {
+    help_fwd_or_chain<E, DKP, WAVES, KEEP>(a, span, seq, h, grp, tiles, outs, exchange);
     return;
   }
   const int col = (grp * WAVES + wave) * 16 + i;
@@ -649,8 +809,8 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
     return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
       const uint32_t grid = delta::walk_grid(a, groups);
-      if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
-      else delta::fwd_kernel<E, DKP, waves(), false><<<grid, (waves() + delta::kLoaders) * 64, 0, s>>>(a, groups);
+      if (saved) delta::fwd_kernel<E, DKP, waves(), true><<<grid, delta::walk_waves(waves()) * 64, 0, s>>>(a, groups);
+      else delta::fwd_kernel<E, DKP, waves(), false><<<grid, delta::walk_waves(waves()) * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
   };

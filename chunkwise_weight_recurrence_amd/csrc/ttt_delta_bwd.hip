@@ -18,23 +18,193 @@ namespace ttt {
 namespace delta {
 namespace {
 
+// The chain and its helpers where there are few heads, as in the forward.  First half of a chunk: K dS', and by
+// the helper P^T dO and scale Q^T e^G dO; second half: Y and the gradient of the state before.
+template <typename E, int DKP, int WAVES, typename Tiles, typename Outs>
+__device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
+                                                  Exchange<E, DKP, WAVES>& exchange) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kMma = sizeof(E) == 2 ? 1 : 4;
+  using TR = Tri<E>;
+  using Raw = typename Frag<E>::Raw;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const bool helper = threadIdx.x >= WAVES * 64;
+  const int wave = (threadIdx.x >> 6) % WAVES, col = (grp * WAVES + wave) * 16 + i;
+  char* from_q = exchange.state[wave];
+  char* from_p = exchange.rows[wave];
+  const int last = span.end - 1;
+  if (helper) {
+    __syncthreads();
+    for (int chunk = last; chunk >= span.first; --chunk) {
+      const auto& w = tiles[(last - chunk) & 1];
+      Split<E> scores[TR::kFrags];
+      f32x4_t go[NT], x[NT], qg[ND], gm[NT];
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) {
+        go[mt] = four_of<16 * WAVES>(w.V, 16 * mt + 4 * g, 16 * wave);
+        gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+        x[mt] = zero4();
+      }
+#pragma unroll
+      for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
+      Raw cols[2][ND];
+      auto read_cols = [&](int n) {
+#pragma unroll
+        for (int t = 0; t < ND; ++t) cols[n & 1][t] = state_col<DKP>(w.Q, 32 * n, t);
+      };
+      read_cols(0);
+      in_order();
+#pragma unroll
+      for (int kp = 0; kp < NP; ++kp) {
+        const Raw e = high(Split<E>(go[2 * kp], go[2 * kp + 1]));  // dO is exact in its type
+#pragma unroll
+        for (int mt = 0; mt < 2 * kp + 2; ++mt) x[mt] = mma(scores[TR::at_t(mt, kp)], e, x[mt]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) go[mt] *= gm[mt] * a.scale;
+#pragma unroll
+      for (int t = 0; t < ND; ++t) qg[t] = zero4();
+      Split<E> s(go[0], go[1]);
+      in_order();
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) give(from_p, mt, x[mt]);
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        if (n + 1 < NP) read_cols(n + 1);
+        in_order();
+        mma_all(qg, cols[n & 1], s);
+        if (n + 1 < NP) s = Split<E>(go[2 * n + 2], go[2 * n + 3]);
+        in_order();
+      }
+#pragma unroll
+      for (int t = 0; t < ND; ++t) give(from_q, t, qg[t]);
+      __syncthreads();
+      __syncthreads();
+    }
+    return;
+  }
+  const bool live = col < a.dvp;
+  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
+  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+  f32x4_t S[ND];  // dS
+  state_load(a.d_sfinal ? a.d_sfinal + state : nullptr, a.dk, a.dv, s_at, S);
+  __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
+  __syncthreads();
+  for (int chunk = last; chunk >= span.first; --chunk) {
+    const auto& w = tiles[(last - chunk) & 1];
+    const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+    const Buffer kept(static_cast<E*>(a.after) + item * a.dvp * DKP, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    f32x4_t du[NT], gm[NT], rest[NT], et[NT];
+    Raw rows[2][NT];
+    auto read_rows = [&](int kp) {
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) rows[kp & 1][mt] = row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g);
+    };
+    Split<E> tri[TR::kFrags];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) du[mt] = zero4();
+    read_rows(0);
+    Split<E> s(S[0], S[1]);
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      if (kp + 1 < NK) {
+        read_rows(kp + 1);
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+          rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+          et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+        }
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
+      }
+      kept.store(a_at + 32 * kp * sizeof(E), high(s));
+      in_order();
+      mma_all(du, rows[kp & 1], s);
+      if (kp + 1 < NK) {
+        s = Split<E>(S[2 * kp + 2], S[2 * kp + 3]);
+        interleave<2 * NT * kMma, 3>();
+      }
+      in_order();
+    }
+    const float decay = w.vec[C - 1];
+    __syncthreads();
+    Raw cols[2][ND];
+    auto read_cols = [&](int n) {
+#pragma unroll
+      for (int t = 0; t < ND; ++t) cols[n & 1][t] = state_col<DKP>(w.K, 32 * n, t);
+    };
+    f32x4_t y[NT];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      du[mt] = du[mt] * rest[mt] + take(from_p, mt);
+      y[mt] = zero4();
+    }
+    f32x4_t qg[ND];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) qg[t] = take(from_q, t);
+    in_order();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> e(du[2 * kp], du[2 * kp + 1]);
+      tri_mul<E, true>(y, tri, e, kp);
+    }
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] = S[t] * decay + qg[t];
+    in_order();
+    read_cols(0);
+    const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      yb.store(y_at + 32 * kp * sizeof(E), high(Split<E>(y[2 * kp], y[2 * kp + 1])));
+#pragma unroll
+      for (int mt = 2 * kp; mt < 2 * kp + 2; ++mt) {
+        et[mt] *= y[mt];          // dV
+        y[mt] = -(gm[mt] * et[mt]);
+      }
+    }
+    s = Split<E>(y[0], y[1]);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      if (n + 1 < NP) read_cols(n + 1);
+      in_order();
+      mma_all(S, cols[n & 1], s);
+      if (n + 1 < NP) s = Split<E>(y[2 * n + 2], y[2 * n + 3]);
+      in_order();
+    }
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) out_tile(outs[(last - chunk) & 1], wave, mt, et[mt]);
+    __syncthreads();
+  }
+  if (a.ds0) state_store(a.ds0 + state, a.dk, a.dv, s_at, S);
+}
+
 template <typename E, int DKP, int WAVES>
-__global__ __launch_bounds__((WAVES + kLoaders) * 64, 1) void bwd_kernel(Args a, int groups) {
+__global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, true, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
+  __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
-  if (wave >= WAVES) {
-    load_walk<E, DKP, true, WAVES, kBuf>(a, span, h, grp * WAVES * 16, tiles, outs, static_cast<const E*>(a.d_o) + static_cast<int64_t>(h) * a.dv,
-                                         static_cast<int64_t>(a.H) * a.dv, a.wide_do, static_cast<E*>(a.dv_out) + static_cast<int64_t>(h) * a.dv,
-                                         a.ldv, a.wide_dv);
+  constexpr bool HELP = WAVES == 2;
+  if (wave >= WAVES + (HELP ? WAVES : 0)) {
+    const E* in = static_cast<const E*>(a.d_o) + static_cast<int64_t>(h) * a.dv;
+    E* out = static_cast<E*>(a.dv_out) + static_cast<int64_t>(h) * a.dv;
+    const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
+    if (a.wide_do && a.wide_dv) load_walk<E, DKP, true, WAVES, kBuf, HELP, true>(a, span, h, grp * WAVES * 16, tiles, outs, in, ldo, out, a.ldv);
+    else load_walk<E, DKP, true, WAVES, kBuf, HELP, false>(a, span, h, grp * WAVES * 16, tiles, outs, in, ldo, out, a.ldv);
+    return;
+  }
+  if constexpr (HELP) {
+    help_bwd_or_chain<E, DKP, WAVES>(a, span, seq, h, grp, tiles, outs, exchange);
     return;
   }
   const int col = (grp * WAVES + wave) * 16 + i;
@@ -426,7 +596,7 @@ template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t 
   {
     KernelScope scope(TTT_KERNEL_DELTA_BWD, s);
     e = by_waves<DKP>(a, [&](auto waves, int groups) {
-      bwd_kernel<E, DKP, waves()><<<walk_grid(a, groups), (waves() + kLoaders) * 64, 0, s>>>(a, groups);
+      bwd_kernel<E, DKP, waves()><<<walk_grid(a, groups), walk_waves(waves()) * 64, 0, s>>>(a, groups);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

@@ -153,6 +153,14 @@ template <> struct Split<float> {
   __device__ __forceinline__ Split(f32x4_t x, f32x4_t y) : a(x), b(y) {}
 };
 
+// A split's two 16-byte parts.
+__device__ __forceinline__ bf16x8_t first_half(const Split<bf16_t>& s) { return s.hi; }
+__device__ __forceinline__ bf16x8_t second_half(const Split<bf16_t>& s) { return s.lo; }
+__device__ __forceinline__ f32x4_t first_half(const Split<float>& s) { return s.a; }
+__device__ __forceinline__ f32x4_t second_half(const Split<float>& s) { return s.b; }
+__device__ __forceinline__ void set_halves(Split<bf16_t>& s, bf16x8_t a, bf16x8_t b) { s.hi = a; s.lo = b; }
+__device__ __forceinline__ void set_halves(Split<float>& s, f32x4_t a, f32x4_t b) { s.a = a; s.b = b; }
+
 __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -273,10 +281,12 @@ template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* 
 // ---- the walks' workgroups ----
 //
 // WAVES waves hold 16 columns of a state each and do nothing but the chain of products; kLoaders more bring
-// what a chunk needs from memory into LDS, two chunks ahead (one in registers, one in the other buffer), and
+// what a chunk needs from memory into LDS, three chunks ahead (two in registers, one in the other buffer), and
 // carry the result columns away.  So the chain has no wait for memory in it and no registers go to loads.
+// With few heads (WAVES = 2) each of these waves has a helper beside it, on a SIMD that would be idle, which
+// takes over what is not part of the chain: of 126 matrix instructions a chunk 44.  They meet twice a chunk.
 
-constexpr int kLoaders = 2, kLoadThreads = kLoaders * 64;
+constexpr int kLoaders = 4, kLoadThreads = kLoaders * 64;
 
 // A walk's LDS for one chunk.
 template <typename E, int DKP, bool BWD, int WAVES> struct WalkTile {
@@ -294,9 +304,32 @@ template <typename E, int WAVES> struct OutTile {
   static constexpr int C = Chunk<E>::C, kRow = sizeof(E) == 2 ? C + 4 : 16 * WAVES;
   E x[(sizeof(E) == 2 ? 16 * WAVES : C) * kRow];
 };
+// What a wave and its helper give each other.  Forward: the state and U as operands; backward: the tiles of
+// P^T dO and of Q^T e^G dO.
+template <typename E, int DKP, int WAVES> struct Exchange {
+  static constexpr int C = Chunk<E>::C;
+  static constexpr int kState = DKP * 16 * 4, kRows = C * 16 * 4;  // two bf16 terms or one fp32: four bytes a value
+  char state[WAVES][kState];
+  char rows[WAVES][kRows];
+};
+struct NoExchange {};
+template <typename E> __device__ __forceinline__ void give(char* p, int n, const Split<E>& s) {
+  reinterpret_cast<uint4*>(p)[2 * n * 64 + (threadIdx.x & 63)] = __builtin_bit_cast(uint4, first_half(s));
+  reinterpret_cast<uint4*>(p)[(2 * n + 1) * 64 + (threadIdx.x & 63)] = __builtin_bit_cast(uint4, second_half(s));
+}
+template <typename E> __device__ __forceinline__ Split<E> take(const char* p, int n) {
+  Split<E> s;
+  const auto* q = reinterpret_cast<const decltype(first_half(s))*>(p);
+  set_halves(s, q[2 * n * 64 + (threadIdx.x & 63)], q[(2 * n + 1) * 64 + (threadIdx.x & 63)]);
+  return s;
+}
+__device__ __forceinline__ void give(char* p, int n, f32x4_t x) { reinterpret_cast<f32x4_t*>(p)[n * 64 + (threadIdx.x & 63)] = x; }
+__device__ __forceinline__ f32x4_t take(const char* p, int n) { return reinterpret_cast<const f32x4_t*>(p)[n * 64 + (threadIdx.x & 63)]; }
+
 // Two chunks where they fit the 160 KB, so that one is filled while the other is read.
 template <typename E, int DKP, bool BWD, int WAVES>
 constexpr int kWalkBuffers = 2 * (sizeof(WalkTile<E, DKP, BWD, WAVES>) + sizeof(OutTile<E, WAVES>)) <= 160 * 1024 ? 2 : 1;
+constexpr int walk_waves(int waves) { return waves + (waves == 2 ? 2 : 0) + kLoaders; }  // of a workgroup
 
 // A buffer resource over `bytes` bytes from p on (both the same for the wave): a load past them reads zero and
 // a store past them does nothing, so short chunks and narrow heads need no branch.  A chunk's rows lie within
@@ -338,7 +371,7 @@ __device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ld, int cols, in
 }
 
 // The loaders' part: the next chunk's pieces in registers.
-template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
+template <typename E, int DKP, bool BWD, int WAVES, bool WIDE> struct Loader {
   using W = WalkTile<E, DKP, BWD, WAVES>;
   static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = kLoadThreads / kPieces, kRows = C / kStep;
   static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads, kP = (W::kPBytes / 16 + kLoadThreads - 1) / kLoadThreads;
@@ -353,7 +386,7 @@ template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
   __device__ __forceinline__ int piece(int n, int all) const { return min(tid + n * kLoadThreads, all - 1); }
 
   // cp: the first of the chunk's rows of v (or of the gradient of o), from this workgroup's column c0 on
-  __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len, const E* cp, int64_t ldc, int c0, bool wide) {
+  __device__ __forceinline__ void load(const Args& a, int chunk, int h, int64_t token, int len, const E* cp, int64_t ldc, int c0) {
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
     const int hk = h / (a.H / a.Hk);
     const E *kp, *qp;
@@ -389,7 +422,7 @@ template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
     const int vcols = a.dv - c0;  // may be none
     const Buffer vb(cp, vcols > 0 ? rows_bytes(len, ldc, vcols, sizeof(E)) : 0);
     const uint32_t sv = static_cast<uint32_t>(ldc * sizeof(E));
-    if (wide) {
+    if constexpr (WIDE) {
       const uint32_t vat = vcol < vcols ? vcol * sizeof(E) : kNowhere;
 #pragma unroll
       for (int n = 0; n < kVRows; ++n) v[n] = vb.template load<uint4>(vat + (vrow + n * kVStep) * sv);
@@ -419,7 +452,7 @@ template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
     for (int n = 0; n < kVRows; ++n) *reinterpret_cast<uint4*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
   }
   // A chunk's result columns to memory (op: as cp).
-  __device__ __forceinline__ void put(const Args& a, const OutTile<E, WAVES>& out, E* op, int64_t ldo, int len, int c0, bool wide) const {
+  __device__ __forceinline__ void put(const Args& a, const OutTile<E, WAVES>& out, E* op, int64_t ldo, int len, int c0) const {
     const int cols = a.dv - c0;
     const Buffer ob(op, cols > 0 ? rows_bytes(len, ldo, cols, sizeof(E)) : 0);
     const uint32_t so = static_cast<uint32_t>(ldo * sizeof(E));
@@ -445,7 +478,7 @@ template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
         c = vcol;
         x = *reinterpret_cast<const uint4*>(out.x + r * out.kRow + c);
       }
-      if (wide) {
+      if constexpr (WIDE) {
         ob.store16(c < cols ? c * sizeof(E) + r * so : kNowhere, x);
       } else {
         E e[V];
@@ -457,42 +490,50 @@ template <typename E, int DKP, bool BWD, int WAVES> struct Loader {
   }
 };
 
-// The loaders' walk beside the others': FORWARD from the first chunk on, else from the last back.  `in` and `out` are the
-// head's first row of v (or of the gradient of o) and of the result.
-template <typename E, int DKP, bool BWD, int WAVES, int BUF, typename Tiles, typename Outs, typename S>
+// The loaders' walk beside the others': from the first chunk on, BWD from the last back.  `in` and `out` are the
+// head's first row of v (or of the gradient of o) and of the result; WIDE: both in 16-byte pieces.
+template <typename E, int DKP, bool BWD, int WAVES, int BUF, bool MID, bool WIDE, typename Tiles, typename Outs, typename S>
 __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, int c0, Tiles& tiles, Outs& outs, const E* in, int64_t ld_in,
-                                          bool wide_in, E* out, int64_t ld_out, bool wide_out) {
+                                          E* out, int64_t ld_out) {
   constexpr int C = Chunk<E>::C;
-  Loader<E, DKP, BWD, WAVES> l(threadIdx.x - WAVES * 64);
+  using L = Loader<E, DKP, BWD, WAVES, WIDE>;
+  const int tid = threadIdx.x - static_cast<int>(blockDim.x - kLoadThreads);
+  L even(tid), odd(tid);  // the chunks' pieces on their way, in turn
   const int count = span.end - span.first;
   auto chunk_of = [&](int n) { return BWD ? span.end - 1 - min(n, count - 1) : span.first + min(n, count - 1); };
-  auto load = [&](int n) {
+  auto load = [&](L& l, int n) {
     const int chunk = chunk_of(n);
     const int64_t token = span.token(chunk, C);
-    l.load(a, chunk, h, token, span.len(chunk, C), in + token * ld_in + c0, ld_in, c0, wide_in);
+    l.load(a, chunk, h, token, span.len(chunk, C), in + token * ld_in + c0, ld_in, c0);
   };
   auto put = [&](int n) {
     const int chunk = chunk_of(n);
-    l.put(a, outs[n & (BUF - 1)], out + span.token(chunk, C) * ld_out + c0, ld_out, span.len(chunk, C), c0, wide_out);
+    even.put(a, outs[n & (BUF - 1)], out + span.token(chunk, C) * ld_out + c0, ld_out, span.len(chunk, C), c0);
   };
-  if (count > 0) {
-    load(0);
-    l.store(tiles[0]);
-    load(1);
-  }
-  __syncthreads();
-  for (int n = 0; n < count; ++n) {
+  auto step = [&](L& l, int n) {  // l has chunk n + 1
     if constexpr (BUF == 2) {
       l.store(tiles[(n + 1) & 1]);
-      load(n + 2);
+      load(l, n + 3);
+      if constexpr (MID) __syncthreads();
       if (n > 0) put(n - 1);
     } else {
       __syncthreads();  // the others are done with the chunk
       l.store(tiles[0]);
-      load(n + 2);
+      load(l, n + 3);
       put(n);
     }
     __syncthreads();
+  };
+  if (count > 0) {
+    load(even, 0);
+    load(odd, 1);
+    even.store(tiles[0]);
+    load(even, 2);
+  }
+  __syncthreads();
+  for (int n = 0; n < count; n += 2) {
+    step(odd, n);
+    if (n + 1 < count) step(even, n + 1);
   }
   if (BUF == 2 && count > 0) put(count - 1);
 }
@@ -514,6 +555,24 @@ template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const 
   for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.lo, c[n]);
 #pragma unroll
   for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.hi, c[n]);
+}
+// u += T x over the pair kp of token tiles; T lower triangular, TRANS its transpose.
+template <typename E, bool TRANS = false, int NT>
+__device__ __forceinline__ void tri_mul(f32x4_t (&u)[NT], const Split<E> (&t)[Tri<E>::kFrags], const Split<E>& x, int kp) {
+  using TR = Tri<E>;
+  const int first = TRANS ? 0 : 2 * kp, end = TRANS ? 2 * kp + 2 : NT;
+  if constexpr (std::is_same_v<E, float>) {
+#pragma unroll
+    for (int mt = first; mt < end; ++mt) u[mt] = mma(t[TRANS ? TR::at_t(mt, kp) : TR::at(mt, kp)], x, u[mt]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+      for (int mt = first; mt < end; ++mt) {
+        const Split<E>& f = t[TRANS ? TR::at_t(mt, kp) : TR::at(mt, kp)];
+        u[mt] = mfma16(n == 0 ? f.lo : f.hi, n == 1 ? x.lo : x.hi, u[mt]);
+      }
+  }
 }
 template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const f32x8 (&a)[N], const Split<float>& b) {
 #pragma unroll

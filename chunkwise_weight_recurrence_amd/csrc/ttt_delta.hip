@@ -157,19 +157,19 @@ template <int C, int LD> __device__ __forceinline__ void invert(const float* A, 
 }
 
 // A chunk and head a workgroup: its gates' sums, K K^T and Q K^T (row tile w by wave w), the inverse.
-// BWD writes the transposes, the scores in two terms.
+// BWD writes the transposes, the scores in two terms.  It is bound by the latency of its stages, so LDS is
+// used over and over: 36 KB let four workgroups share a CU.
 template <typename E, int DKP, bool BWD>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
-  constexpr int C = Chunk<E>::C, LD = C + 4;
+  constexpr int C = Chunk<E>::C, NT = C / 16, LD = C + 4, V = 16 / sizeof(E), kPieces = DKP / V, kRows = C * kPieces / kPrepThreads;
   using Lds = Tile<E, DKP>;
-  // T and P take the place of the keys and queries
+  // A and T take the place of the keys and queries, the scores that of A
   constexpr size_t kRowsBytes = 2 * C * Lds::kRow * sizeof(E), kSquares = 2 * C * LD * sizeof(float);
   __shared__ __attribute__((aligned(16))) char pool[kRowsBytes > kSquares ? kRowsBytes : kSquares];
   E* K = reinterpret_cast<E*>(pool);
   E* Q = K + C * Lds::kRow;
-  float* T = reinterpret_cast<float*>(pool);
-  float* P = T + C * LD;
-  __shared__ __attribute__((aligned(16))) float A[C * LD];
+  float* A = reinterpret_cast<float*>(pool);
+  float* T = A + C * LD;
   __shared__ double G[C];
   __shared__ float eta[C];
   const int chunk = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -177,8 +177,19 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   if (w.len < 0) return;
   const int hk = h / (a.H / a.Hk);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const bool wq = a.wide_q, wk = a.wide_k;
   const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
+  const E* kp = static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk;
+  const E* qp = static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk;
+  uint4 kr[kRows], qr[kRows];
+  if (a.dense) {  // on their way while the gates are summed
+    const Buffer kb(kp, rows_bytes(w.len, a.ldk, a.dk, sizeof(E))), qb(qp, rows_bytes(w.len, a.ldq, a.dk, sizeof(E)));
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      const int x = threadIdx.x + n * kPrepThreads, row = x / kPieces, col = x % kPieces * V;
+      kr[n] = kb.template load<uint4>(col < a.dk ? (row * static_cast<uint32_t>(a.ldk) + col) * sizeof(E) : kNowhere);
+      qr[n] = qb.template load<uint4>(col < a.dk ? (row * static_cast<uint32_t>(a.ldq) + col) * sizeof(E) : kNowhere);
+    }
+  }
   if (wave == 0) {
     double Gt;
     float et, rs, z;
@@ -193,53 +204,69 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
       vec[2 * C] = et;
     }
   }
-  stage<E, C, DKP, kPrepThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
-  stage<E, C, DKP, kPrepThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+  if (a.dense) {
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      const int x = threadIdx.x + n * kPrepThreads, at = Lds::at(x / kPieces, x % kPieces * V);
+      *reinterpret_cast<uint4*>(K + at) = kr[n];
+      *reinterpret_cast<uint4*>(Q + at) = qr[n];
+    }
+  } else {
+    stage<E, C, DKP, kPrepThreads>(K, kp, a.ldk, w.len, a.dk, a.wide_k);
+    stage<E, C, DKP, kPrepThreads>(Q, qp, a.ldq, w.len, a.dk, a.wide_q);
+  }
   __syncthreads();
   if (!a.dense && h % (a.H / a.Hk) == 0) {  // the walks' copy
     E* dst = static_cast<E*>(a.kq) + (static_cast<int64_t>(chunk) * a.Hk + hk) * 2 * C * DKP;
-    constexpr int V = 16 / sizeof(E), kPieces = DKP / V;
     for (int x = threadIdx.x; x < 2 * C * kPieces; x += kPrepThreads) {
       const int row = x / kPieces, col = (x % kPieces) * V;
       const E* src = row < C ? K + Lds::at(row, col) : Q + Lds::at(row - C, col);
       *reinterpret_cast<uint4*>(dst + row * DKP + col) = *reinterpret_cast<const uint4*>(src);
     }
   }
-  const int mt = wave;  // row tile; C / 16 waves have one
-  f32x4_t kk[C / 16], qk[C / 16];
+  const int mt = wave;  // row tile; NT waves have one
+  f32x4_t kk[NT], qk[NT];
 #pragma unroll
-  for (int nt = 0; nt < C / 16; ++nt) kk[nt] = qk[nt] = zero4();
-  if (mt < C / 16) {
+  for (int nt = 0; nt < NT; ++nt) kk[nt] = qk[nt] = zero4();
+  if (mt < NT) {
+    // all column tiles, those above the diagonal too: no branch between the products
 #pragma unroll
-    for (int kp = 0; kp < DKP / 32; ++kp) {
-      const auto ka = row_frag<DKP>(K, 16 * mt + i, 32 * kp + 8 * g), qa = row_frag<DKP>(Q, 16 * mt + i, 32 * kp + 8 * g);
+    for (int p = 0; p < DKP / 32; ++p) {
+      typename Frag<E>::Raw b[NT];
 #pragma unroll
-      for (int nt = 0; nt < C / 16; ++nt) {
-        if (nt <= mt) {
-          const auto b = row_frag<DKP>(K, 16 * nt + i, 32 * kp + 8 * g);
-          kk[nt] = mma(ka, b, kk[nt]);
-          qk[nt] = mma(qa, b, qk[nt]);
-        }
+      for (int nt = 0; nt < NT; ++nt) b[nt] = row_frag<DKP>(K, 16 * nt + i, 32 * p + 8 * g);
+      const auto ka = row_frag<DKP>(K, 16 * mt + i, 32 * p + 8 * g), qa = row_frag<DKP>(Q, 16 * mt + i, 32 * p + 8 * g);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        kk[nt] = mma(ka, b[nt], kk[nt]);
+        qk[nt] = mma(qa, b[nt], qk[nt]);
       }
     }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < C * LD; x += kPrepThreads) T[x] = 0.0f;
-  if (mt < C / 16) {
+  if (mt < NT) {
 #pragma unroll
-    for (int nt = 0; nt < C / 16; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * mt + 4 * g + r, col = 16 * nt + i;
         const float d = row >= col ? exp2_(static_cast<float>(G[row] - G[col])) : 0.0f;
         A[row * LD + col] = row > col ? eta[row] * d * kk[nt][r] : 0.0f;
-        P[row * LD + col] = row >= col ? a.scale * d * qk[nt][r] : 0.0f;
+        T[row * LD + col] = 0.0f;
+        qk[nt][r] = row >= col ? a.scale * d * qk[nt][r] : 0.0f;
       }
   }
   __syncthreads();
   invert<C, LD>(A, T);
   tri_store<E, LD, BWD, 2>(T, a.t + item * Tri<E>::kBytes);
-  tri_store<E, LD, BWD, BWD ? 2 : 1>(P, a.p + item * Tri<E>::kBytes);
+  if (mt < NT) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) A[(16 * mt + 4 * g + r) * LD + 16 * nt + i] = qk[nt][r];
+  }
+  __syncthreads();
+  tri_store<E, LD, BWD, BWD ? 2 : 1>(A, a.p + item * Tri<E>::kBytes);
 }
 
 // ---- forward walk ----

@@ -344,6 +344,11 @@ template <typename E> __device__ __forceinline__ float dot8(typename Frag<E>::Ra
   return s;
 }
 
+template <typename E> __device__ __forceinline__ E narrow(float x) {
+  if constexpr (std::is_same_v<E, float>) return x;
+  else return f32_to_bf16(x);
+}
+
 // Four rows r0 .. r0 + 3 of column col0 + i, as a result tile has them.
 template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const bf16_t* lds, int r0, int col0) {
   typedef short v4s __attribute__((ext_vector_type(4)));
@@ -362,11 +367,70 @@ template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const float* ld
   return f;
 }
 
+// The sum over 16 lanes, in all of them (rotations within them, without LDS).
 __device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d, 64);
+#define ROTATED(n) __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + n, 0xf, 0xf, true))
+  x += ROTATED(8);
+  x += ROTATED(4);
+  x += ROTATED(2);
+  x += ROTATED(1);
+#undef ROTATED
   return x;
 }
+
+// The next slab of the values' columns on its way through registers.
+template <typename E, int DKP> struct SlabLoader {
+  static constexpr int C = Chunk<E>::C, V = 16 / sizeof(E);
+  static constexpr int kO = C * kSlab / V, kS = kSlab * DKP / V;  // pieces of dO (and of U, Y); of a state
+  static constexpr int nO = (kO + kGradThreads - 1) / kGradThreads, nS = (kS + kGradThreads - 1) / kGradThreads;
+  uint4 o[nO], u[nO], y[nO], b[nS], a[nS];
+  // Pieces past the end are some thread's twice: both write the same.
+  static __device__ __forceinline__ int piece(int n, int all) { return min(static_cast<int>(threadIdx.x) + n * kGradThreads, all - 1); }
+  __device__ __forceinline__ void load(const Args& g, int64_t item, const E* dO, int64_t ld, int len, int c0) {
+    const int cols = g.dv - c0;  // may be none
+    const Buffer ob(dO + c0, cols > 0 ? rows_bytes(len, ld, cols, sizeof(E)) : 0);
+    const uint32_t stride = static_cast<uint32_t>(ld * sizeof(E));
+    const uint4* up = reinterpret_cast<const uint4*>(static_cast<const E*>(g.u) + (item * g.dvp + c0) * C);
+    const uint4* yp = reinterpret_cast<const uint4*>(static_cast<const E*>(g.y) + (item * g.dvp + c0) * C);
+    const uint4* bp = reinterpret_cast<const uint4*>(static_cast<const E*>(g.before) + (item * g.dvp + c0) * DKP);
+    const uint4* ap = reinterpret_cast<const uint4*>(static_cast<const E*>(g.after) + (item * g.dvp + c0) * DKP);
+#pragma unroll
+    for (int n = 0; n < nO; ++n) {
+      const int x = piece(n, kO), row = x / (kSlab / V), col = x % (kSlab / V) * V;
+      if (g.wide_do) {
+        o[n] = ob.template load<uint4>(col < cols ? row * stride + col * sizeof(E) : kNowhere);
+      } else {
+        E e[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = ob.template load<E>(col + j < cols ? row * stride + (col + j) * sizeof(E) : kNowhere);
+        __builtin_memcpy(&o[n], e, 16);
+      }
+      u[n] = up[x];
+      y[n] = yp[x];
+    }
+#pragma unroll
+    for (int n = 0; n < nS; ++n) {
+      b[n] = bp[piece(n, kS)];
+      a[n] = ap[piece(n, kS)];
+    }
+  }
+  __device__ __forceinline__ void store(E* dO, E* U, E* Y, E* B, E* A) const {
+#pragma unroll
+    for (int n = 0; n < nO; ++n) {
+      const int x = piece(n, kO);
+      *reinterpret_cast<uint4*>(dO + Tile<E, kSlab>::at(x / (kSlab / V), x % (kSlab / V) * V)) = o[n];
+      const int at = Tile<E, C>::at(x / (C / V), x % (C / V) * V);
+      *reinterpret_cast<uint4*>(U + at) = u[n];
+      *reinterpret_cast<uint4*>(Y + at) = y[n];
+    }
+#pragma unroll
+    for (int n = 0; n < nS; ++n) {
+      const int x = piece(n, kS), at = Tile<E, DKP>::at(x / (DKP / V), x % (DKP / V) * V);
+      *reinterpret_cast<uint4*>(B + at) = b[n];
+      *reinterpret_cast<uint4*>(A + at) = a[n];
+    }
+  }
+};
 
 // A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
 // dK summed in registers.  Of the triangular products a wave has a row tile of X or of M, of the others an
@@ -395,11 +459,10 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
   const Where w = locate<C>(a, chunk);
   if (w.len < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const bool wq = a.wide_q, wk = a.wide_k, wo = a.wide_do;
   const int ch0 = wave * 16 * NJ;  // a wave's first channel
   const bool busy = wave < NW;
-  stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, wk);
-  stage<E, C, DKP, kGradThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, wq);
+  stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, a.wide_k);
+  stage<E, C, DKP, kGradThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, a.wide_q);
   f32x4_t dq_sum[SHARED ? NT : 1][NJ], dk_sum[SHARED ? NT : 1][NJ];
   if constexpr (SHARED) {
 #pragma unroll
@@ -407,16 +470,17 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) dq_sum[mt][j] = dk_sum[mt][j] = zero4();
   }
+  const Buffer qb(static_cast<E*>(a.dq) + w.token * a.ldq + hk * a.dk, rows_bytes(w.len, a.ldq, a.dk, sizeof(E)));
+  const Buffer kb(static_cast<E*>(a.dk_out) + w.token * a.ldk + hk * a.dk, rows_bytes(w.len, a.ldk, a.dk, sizeof(E)));
+  const uint32_t sq = static_cast<uint32_t>(a.ldq * sizeof(E)), sk = static_cast<uint32_t>(a.ldk * sizeof(E));
   auto store = [&](const f32x4_t& dq, const f32x4_t& dk, int mt, int j) {
     const int col = ch0 + 16 * j + i;
-    if (!busy || col >= a.dk) return;
+    const uint32_t at = busy && col < a.dk ? col * sizeof(E) : kNowhere;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * mt + 4 * g + r;
-      if (t < w.len) {
-        Elem<E>::st(static_cast<E*>(a.dq) + w.token * a.ldq + hk * a.dk + col, t * a.ldq, dq[r]);
-        Elem<E>::st(static_cast<E*>(a.dk_out) + w.token * a.ldk + hk * a.dk + col, t * a.ldk, dk[r]);
-      }
+      qb.store(at + t * sq, narrow<E>(dq[r]));
+      kb.store(at + t * sk, narrow<E>(dk[r]));
     }
   };
   // wave w < NT has row tile w of X, wave NT + w that of M
@@ -447,14 +511,14 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
       for (int j = 0; j < NJ; ++j) dq[mt][j] = dkr[mt][j] = dks[mt][j] = zero4();
     }
     float en = 0.0f;
+    SlabLoader<E, DKP> slab;
+    const E* dop = static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv;
+    const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
+    slab.load(a, item, dop, ldo, w.len, 0);
     for (int c0 = 0; c0 < a.dvp; c0 += kSlab) {
       if (c0 > 0) __syncthreads();
-      stage<E, C, kSlab, kGradThreads>(dO, static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv + c0, static_cast<int64_t>(a.H) * a.dv,
-                                       w.len, a.dv - c0, wo);
-      stage<E, kSlab, C, kGradThreads>(U, static_cast<const E*>(a.u) + (item * a.dvp + c0) * C, C, kSlab, C, true);
-      stage<E, kSlab, C, kGradThreads>(Y, static_cast<const E*>(a.y) + (item * a.dvp + c0) * C, C, kSlab, C, true);
-      stage<E, kSlab, DKP, kGradThreads>(B, static_cast<const E*>(a.before) + (item * a.dvp + c0) * DKP, DKP, kSlab, DKP, true);
-      stage<E, kSlab, DKP, kGradThreads>(A, static_cast<const E*>(a.after) + (item * a.dvp + c0) * DKP, DKP, kSlab, DKP, true);
+      slab.store(dO, U, Y, B, A);
+      if (c0 + kSlab < a.dvp) slab.load(a, item, dop, ldo, w.len, c0 + kSlab);
       __syncthreads();
       typename Frag<E>::Raw ox[NT], ux[NT], yx[NT];
 #pragma unroll
@@ -499,54 +563,64 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
         }
     }
     __syncthreads();
+    if (busy) {
+      f32x4_t d1[NT], d2[NT], d3[NT], d4[NT];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) {
-      if (!busy) break;
-      const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
-      const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
-      const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
-      f32x4_t d1 = zero4(), d2 = zero4(), d3 = zero4(), d4 = zero4();
+      for (int mt = 0; mt < NT; ++mt) d1[mt] = d2[mt] = d3[mt] = d4[mt] = zero4();
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int c0 = ch0 + 16 * j;
-        dq[mt][j] *= gm * a.scale;
-        dkr[mt][j] *= -(gm * et);
-        dks[mt][j] *= rest;
+        typename Frag<E>::Raw kc[NP], qc[NP];
 #pragma unroll
-        for (int p = 0; p <= mt / 2; ++p) {
-          const auto kc = plain_col<DKP>(K, 32 * p, c0);
-          dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc, dq[mt][j]);
-          dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc, dkr[mt][j]);
+        for (int p = 0; p < NP; ++p) {
+          kc[p] = plain_col<DKP>(K, 32 * p, c0);
+          qc[p] = plain_col<DKP>(Q, 32 * p, c0);
         }
-        const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0);
-        d1 += qv * dq[mt][j];
-        d3 += kv * dkr[mt][j];
-        d4 += kv * dks[mt][j];
-        f32x4_t dk = dkr[mt][j] + dks[mt][j];
 #pragma unroll
-        for (int p = mt / 2; p < NP; ++p) {
-          dk = mma(plain_col<C>(X, 32 * p, 16 * mt), plain_col<DKP>(Q, 32 * p, c0), dk);
-          dk = mma(plain_col<C>(M, 32 * p, 16 * mt), plain_col<DKP>(K, 32 * p, c0), dk);
-        }
-        d2 += kv * dk;
-        if constexpr (SHARED) {
-          dq_sum[mt][j] += dq[mt][j];
-          dk_sum[mt][j] += dk;
-        } else {
-          store(dq[mt][j], dk, mt, j);
+        for (int mt = 0; mt < NT; ++mt) {
+          const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
+          const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
+          const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
+          dq[mt][j] *= gm * a.scale;
+          dkr[mt][j] *= -(gm * et);
+          dks[mt][j] *= rest;
+#pragma unroll
+          for (int p = 0; p <= mt / 2; ++p) {
+            dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc[p], dq[mt][j]);
+            dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc[p], dkr[mt][j]);
+          }
+          const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0);
+          d1[mt] += qv * dq[mt][j];
+          d3[mt] += kv * dkr[mt][j];
+          d4[mt] += kv * dks[mt][j];
+          f32x4_t dk = dkr[mt][j] + dks[mt][j];
+#pragma unroll
+          for (int p = mt / 2; p < NP; ++p) {
+            dk = mma(plain_col<C>(X, 32 * p, 16 * mt), qc[p], dk);
+            dk = mma(plain_col<C>(M, 32 * p, 16 * mt), kc[p], dk);
+          }
+          d2[mt] += kv * dk;
+          if constexpr (SHARED) {
+            dq_sum[mt][j] += dq[mt][j];
+            dk_sum[mt][j] += dk;
+          } else {
+            store(dq[mt][j], dk, mt, j);
+          }
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float s1 = sum16(d1[r]), s2 = sum16(d2[r]), s3 = sum16(d3[r]), s4 = sum16(d4[r]);
-        if (i == 0) {
-          const int t = 16 * mt + 4 * g + r;
-          sums[wave][0][t] = s1;
-          sums[wave][1][t] = s2;
-          sums[wave][2][t] = s3;
-          sums[wave][3][t] = s4;
+      for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float s1 = sum16(d1[mt][r]), s2 = sum16(d2[mt][r]), s3 = sum16(d3[mt][r]), s4 = sum16(d4[mt][r]);
+          if (i == 0) {
+            const int t = 16 * mt + 4 * g + r;
+            sums[wave][0][t] = s1;
+            sums[wave][1][t] = s2;
+            sums[wave][2][t] = s3;
+            sums[wave][3][t] = s4;
+          }
         }
-      }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) en += __shfl_xor(en, d, 64);

@@ -88,6 +88,7 @@ template <int C> __device__ __forceinline__ Where locate(const Args& a, int chun
 // A [rows][NCOL] tile: bf16 with swizzled 16-byte granules, fp32 with rows 16 bytes longer.
 template <typename E, int NCOL> struct Tile;
 template <int NCOL> struct Tile<bf16_t, NCOL> {
+  static_assert(NCOL >= 32);
   static constexpr int kRow = NCOL;
   static __device__ __forceinline__ int at(int row, int col) { return swz<NCOL>(row, col); }
 };

@@ -438,7 +438,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
   constexpr bool HELP = WAVES == 2;
   if (wave >= WAVES + (HELP ? WAVES : 0)) {

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of(a, seq);
   constexpr bool HELP = WAVES == 2;
   if (wave >= WAVES + (HELP ? WAVES : 0)) {
@@ -350,20 +350,20 @@ template <typename E> __device__ __forceinline__ E narrow(float x) {
 }
 
 // Four rows r0 .. r0 + 3 of column col0 + i, as a result tile has them.
-template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const bf16_t* lds, int r0, int col0) {
+template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const bf16_t* lds, int r0, int col0, int tid) {
   typedef short v4s __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4s lds_v4s;
-  const int i = threadIdx.x & 15;
+  const int i = tid & 15;
   const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r0 + (i >> 2), col0 + 4 * (i & 3))));
   f32x4_t f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) f[j] = bf16_to_f32(static_cast<uint16_t>(x[j]));
   return f;
 }
-template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const float* lds, int r0, int col0) {
+template <int NCOL> __device__ __forceinline__ f32x4_t four_rows(const float* lds, int r0, int col0, int tid) {
   f32x4_t f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = lds[Tile<float, NCOL>::at(r0 + j, col0 + (threadIdx.x & 15))];
+  for (int j = 0; j < 4; ++j) f[j] = lds[Tile<float, NCOL>::at(r0 + j, col0 + (tid & 15))];
   return f;
 }
 
@@ -435,8 +435,9 @@ template <typename E, int DKP> struct SlabLoader {
 // A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
 // dK summed in registers.  Of the triangular products a wave has a row tile of X or of M, of the others an
 // eighth of the key channels.  The value columns come 32 at a time.
+// Up to 128 bf16 channels two workgroups share a CU (128 registers, 80 KB).
 template <typename E, int DKP, bool SHARED>
-__global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
+__global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHARED ? 4 : 2) void grad_kernel(Args a) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = (DKP + 127) / 128, NW = DKP / 16 / NJ;  // NW waves have channels
   using Lds = Tile<E, DKP>;
   using Slab = Tile<E, kSlab>;
@@ -458,7 +459,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
   const int chunk = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.H / a.Hk;
   const Where w = locate<C>(a, chunk);
   if (w.len < 0) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  // lanes are named anew in each stage, so that a stage's LDS addresses do not take registers in the others
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int ch0 = wave * 16 * NJ;  // a wave's first channel
   const bool busy = wave < NW;
   stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, a.wide_k);
@@ -474,7 +476,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
   const Buffer kb(static_cast<E*>(a.dk_out) + w.token * a.ldk + hk * a.dk, rows_bytes(w.len, a.ldk, a.dk, sizeof(E)));
   const uint32_t sq = static_cast<uint32_t>(a.ldq * sizeof(E)), sk = static_cast<uint32_t>(a.ldk * sizeof(E));
   auto store = [&](const f32x4_t& dq, const f32x4_t& dk, int mt, int j) {
-    const int col = ch0 + 16 * j + i;
+    const int i = lane & 15, g = lane >> 4, col = ch0 + 16 * j + i;
     const uint32_t at = busy && col < a.dk ? col * sizeof(E) : kNowhere;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -520,34 +522,35 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
       slab.store(dO, U, Y, B, A);
       if (c0 + kSlab < a.dvp) slab.load(a, item, dop, ldo, w.len, c0 + kSlab);
       __syncthreads();
-      typename Frag<E>::Raw ox[NT], ux[NT], yx[NT];
+      const int tid = opaque(threadIdx.x), i = tid & 15, g = (tid & 63) >> 4;
+      if (tri) {
+        const auto x = second ? token_col<C>(Y, rt, tid) : row_frag<kSlab>(dO, 16 * rt + i, 8 * g);
 #pragma unroll
-      for (int mt = 0; mt < NT; ++mt) {
-        ox[mt] = row_frag<kSlab>(dO, 16 * mt + i, 8 * g);
-        ux[mt] = token_col<C>(U, mt);
-        yx[mt] = token_col<C>(Y, mt);
+        for (int nt = 0; nt < NT; ++nt) xm[nt] = mma(x, token_col<C>(U, nt, tid), xm[nt]);  // those above the diagonal too
       }
-#pragma unroll
-      for (int mt = 0; mt < NT; ++mt)
-        if (tri && rt == mt) {
-#pragma unroll
-          for (int nt = 0; nt <= mt; ++nt) xm[nt] = mma(second ? yx[mt] : ox[mt], ux[nt], xm[nt]);
-        }
       if (busy) {
+        typename Frag<E>::Raw sb[NJ], sa[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const auto sb = plain_col<DKP>(B, 0, ch0 + 16 * j), sa = plain_col<DKP>(A, 0, ch0 + 16 * j);
-          en += dot8<E>(sb, sa);
+          sb[j] = plain_col<DKP>(B, 0, ch0 + 16 * j, tid);
+          sa[j] = plain_col<DKP>(A, 0, ch0 + 16 * j, tid);
+          en += dot8<E>(sb[j], sa[j]);
+        }
 #pragma unroll
-          for (int mt = 0; mt < NT; ++mt) {
-            dq[mt][j] = mma(ox[mt], sb, dq[mt][j]);
-            dkr[mt][j] = mma(yx[mt], sb, dkr[mt][j]);
-            dks[mt][j] = mma(ux[mt], sa, dks[mt][j]);
+        for (int mt = 0; mt < NT; ++mt) {
+          const auto ox = row_frag<kSlab>(dO, 16 * mt + i, 8 * g), ux = token_col<C>(U, mt, tid), yx = token_col<C>(Y, mt, tid);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            dq[mt][j] = mma(ox, sb[j], dq[mt][j]);
+            dkr[mt][j] = mma(yx, sb[j], dkr[mt][j]);
+            dks[mt][j] = mma(ux, sa[j], dks[mt][j]);
           }
+          if (mt % 2) in_order();
         }
       }
     }
     if (tri) {
+      const int i = lane & 15, g = lane >> 4;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -564,42 +567,43 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
     }
     __syncthreads();
     if (busy) {
-      f32x4_t d1[NT], d2[NT], d3[NT], d4[NT];
+      const int tid = opaque(threadIdx.x), i = tid & 15, g = (tid & 63) >> 4;
+      typename Frag<E>::Raw kc[NJ][NP], qc[NJ][NP];
 #pragma unroll
-      for (int mt = 0; mt < NT; ++mt) d1[mt] = d2[mt] = d3[mt] = d4[mt] = zero4();
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int c0 = ch0 + 16 * j;
-        typename Frag<E>::Raw kc[NP], qc[NP];
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          kc[p] = plain_col<DKP>(K, 32 * p, c0);
-          qc[p] = plain_col<DKP>(Q, 32 * p, c0);
+          kc[j][p] = plain_col<DKP>(K, 32 * p, ch0 + 16 * j, tid);
+          qc[j][p] = plain_col<DKP>(Q, 32 * p, ch0 + 16 * j, tid);
         }
 #pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-          const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
-          const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
-          const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
+      for (int mt = 0; mt < NT; ++mt) {
+        f32x4_t d1 = zero4(), d2 = zero4(), d3 = zero4(), d4 = zero4();
+        const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
+        const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
+        const f32x4_t et = *reinterpret_cast<const f32x4_t*>(&vec[2][16 * mt + 4 * g]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int c0 = ch0 + 16 * j;
           dq[mt][j] *= gm * a.scale;
           dkr[mt][j] *= -(gm * et);
           dks[mt][j] *= rest;
 #pragma unroll
           for (int p = 0; p <= mt / 2; ++p) {
-            dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc[p], dq[mt][j]);
-            dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc[p], dkr[mt][j]);
+            dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc[j][p], dq[mt][j]);
+            dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc[j][p], dkr[mt][j]);
           }
-          const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0);
-          d1[mt] += qv * dq[mt][j];
-          d3[mt] += kv * dkr[mt][j];
-          d4[mt] += kv * dks[mt][j];
+          const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0, tid), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0, tid);
+          d1 += qv * dq[mt][j];
+          d3 += kv * dkr[mt][j];
+          d4 += kv * dks[mt][j];
           f32x4_t dk = dkr[mt][j] + dks[mt][j];
 #pragma unroll
           for (int p = mt / 2; p < NP; ++p) {
-            dk = mma(plain_col<C>(X, 32 * p, 16 * mt), qc[p], dk);
-            dk = mma(plain_col<C>(M, 32 * p, 16 * mt), kc[p], dk);
+            dk = mma(plain_col<C>(X, 32 * p, 16 * mt, tid), qc[j][p], dk);
+            dk = mma(plain_col<C>(M, 32 * p, 16 * mt, tid), kc[j][p], dk);
           }
-          d2[mt] += kv * dk;
+          d2 += kv * dk;
           if constexpr (SHARED) {
             dq_sum[mt][j] += dq[mt][j];
             dk_sum[mt][j] += dk;
@@ -607,12 +611,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
             store(dq[mt][j], dk, mt, j);
           }
         }
-      }
-#pragma unroll
-      for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float s1 = sum16(d1[mt][r]), s2 = sum16(d2[mt][r]), s3 = sum16(d3[mt][r]), s4 = sum16(d4[mt][r]);
+          const float s1 = sum16(d1[r]), s2 = sum16(d2[r]), s3 = sum16(d3[r]), s4 = sum16(d4[r]);
           if (i == 0) {
             const int t = 16 * mt + 4 * g + r;
             sums[wave][0][t] = s1;
@@ -621,6 +622,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(Args a) {
             sums[wave][3][t] = s4;
           }
         }
+        in_order();
+      }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) en += __shfl_xor(en, d, 64);

@@ -199,10 +199,10 @@ template <int NCOL> __device__ __forceinline__ f32x8 row_frag(const float* lds, 
 // col4 is what the lane i' with i' % 4 = i / 4 gave as `piece`: ds_read_b64_tr_b16 hands lane
 // 4 a + b of each 16 lanes element b of the 8-byte pieces that lanes a, a + 4, a + 8, a + 12 name.
 template <int NCOL>
-__device__ __forceinline__ bf16x8_t col_frag(const bf16_t* lds, int r0, int r1, int piece, int /*col*/) {
+__device__ __forceinline__ bf16x8_t col_frag(const bf16_t* lds, int r0, int r1, int piece, int /*col*/, int tid) {
   typedef short v4s __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4s lds_v4s;
-  const int i4 = (threadIdx.x & 15) >> 2;
+  const int i4 = (tid & 15) >> 2;
   const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r0 + i4, piece)));
   const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + Tile<bf16_t, NCOL>::at(r1 + i4, piece)));
   typedef short v8s __attribute__((ext_vector_type(8)));
@@ -210,7 +210,7 @@ __device__ __forceinline__ bf16x8_t col_frag(const bf16_t* lds, int r0, int r1, 
   return __builtin_bit_cast(bf16x8_t, z);
 }
 template <int NCOL>
-__device__ __forceinline__ f32x8 col_frag(const float* lds, int r0, int r1, int /*piece*/, int col) {
+__device__ __forceinline__ f32x8 col_frag(const float* lds, int r0, int r1, int /*piece*/, int col, int /*tid*/) {
   f32x8 f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -225,24 +225,24 @@ __device__ __forceinline__ f32x8 col_frag(const float* lds, int r0, int r1, int 
 __device__ __forceinline__ int state_row(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
 // Column operand of tile t's rows over the tokens of a pair of token tiles (row 0 = token `tok`).
 template <int NCOL, typename E>
-__device__ __forceinline__ typename Frag<E>::Raw state_col(const E* lds, int tok, int t) {
-  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  return col_frag<NCOL>(lds, tok + 4 * g, tok + 16 + 4 * g, state_row(t, i & 3), state_row(t, i >> 2) + (i & 3));
+__device__ __forceinline__ typename Frag<E>::Raw state_col(const E* lds, int tok, int t, int tid = threadIdx.x) {
+  const int i = tid & 15, g = (tid & 63) >> 4;
+  return col_frag<NCOL>(lds, tok + 4 * g, tok + 16 + 4 * g, state_row(t, i & 3), state_row(t, i >> 2) + (i & 3), tid);
 }
 // Column operand of columns col0 + i over rows row0 + 8 g + 0..7.
 template <int NCOL, typename E>
-__device__ __forceinline__ typename Frag<E>::Raw plain_col(const E* lds, int row0, int col0) {
-  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  return col_frag<NCOL>(lds, row0 + 8 * g, row0 + 8 * g + 4, col0 + 4 * (i & 3), col0 + i);
+__device__ __forceinline__ typename Frag<E>::Raw plain_col(const E* lds, int row0, int col0, int tid = threadIdx.x) {
+  const int i = tid & 15, g = (tid & 63) >> 4;
+  return col_frag<NCOL>(lds, row0 + 8 * g, row0 + 8 * g + 4, col0 + 4 * (i & 3), col0 + i, tid);
 }
 
 // U and Y are kept as [column][C] with the tokens of a pair of tiles in the order of the operand that they
 // were: 8 g + j is token 4 g + j, or for j >= 4 token 16 + 4 g + j - 4.  This is the operand of token tile mt
 // over 32 columns (rows), in the tokens' own order.
 template <int NCOL, typename E>
-__device__ __forceinline__ typename Frag<E>::Raw token_col(const E* lds, int mt) {
-  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  return col_frag<NCOL>(lds, 8 * g, 8 * g + 4, state_row(mt, i & 3), state_row(mt, i >> 2) + (i & 3));
+__device__ __forceinline__ typename Frag<E>::Raw token_col(const E* lds, int mt, int tid = threadIdx.x) {
+  const int i = tid & 15, g = (tid & 63) >> 4;
+  return col_frag<NCOL>(lds, 8 * g, 8 * g + 4, state_row(mt, i & 3), state_row(mt, i >> 2) + (i & 3), tid);
 }
 
 // ---- T and P in operand order ----

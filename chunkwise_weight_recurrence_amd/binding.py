@@ -126,6 +126,7 @@ class Kernel(IntEnum):
     QK_FWD = 39
     QK_BWD = 40
     QK_REDUCE = 41
+    DELTA_MAP = 42
 
 
 ENTRY_FWD = 0

@@ -271,6 +271,16 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
 
 // ---- forward walk ----
 
+// The state that enters a sequence or a piece of one (NULL: zero), and where the one that leaves it goes.
+__device__ __forceinline__ const float* entering(const Args& a, int seq, int h) {
+  const int64_t at = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
+  return a.nseg > 1 ? a.seg_states + at : a.s0 ? a.s0 + at : nullptr;
+}
+__device__ __forceinline__ float* leaving(const Args& a, int seq, int h) {
+  if (!a.s_final || seq % a.nseg != a.nseg - 1) return nullptr;
+  return a.s_final + (static_cast<int64_t>(seq / a.nseg) * a.H + h) * a.dk * a.dv;
+}
+
 // The chain (waves 0 .. WAVES - 1) and its helpers (the next WAVES) where there are few heads.  First half of a
 // chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.
 template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
@@ -331,10 +341,9 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
     }
     return;
   }
-  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
   f32x4_t S[ND];
-  state_load(a.s0 ? a.s0 + state : nullptr, a.dk, a.dv, s_at, S);
+  state_load(entering(a, seq, h), a.dk, a.dv, s_at, S);
   Split<E> s[NK];
 #pragma unroll
   for (int kp = 0; kp < NK; ++kp) {
@@ -420,7 +429,7 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
     }
     __syncthreads();
   }
-  if (a.s_final) state_store(a.s_final + state, a.dk, a.dv, s_at, S);
+  if (float* to = leaving(a, seq, h)) state_store(to, a.dk, a.dv, s_at, S);
 }
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
@@ -436,10 +445,10 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
   __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
-  if (chain >= a.B * a.H) return;
+  if (chain >= a.B * a.nseg * a.H) return;
   const int h = chain % a.H, seq = chain / a.H;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const Span span = span_of(a, seq);
+  const Span span = span_of<C>(a, seq);
   constexpr bool HELP = WAVES == 2;
   if (wave >= WAVES + (HELP ? WAVES : 0)) {
     const E* in = static_cast<const E*>(a.v) + static_cast<int64_t>(h) * a.dv;
@@ -455,10 +464,9 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   }
   const int col = (grp * WAVES + wave) * 16 + i;
   const bool live = col < a.dvp;
-  const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
   f32x4_t S[ND];
-  state_load(a.s0 ? a.s0 + state : nullptr, a.dk, a.dv, s_at, S);
+  state_load(entering(a, seq, h), a.dk, a.dv, s_at, S);
   __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
   const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
   __syncthreads();
@@ -565,7 +573,149 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     if constexpr (kBuf == 1) __syncthreads();
     __syncthreads();
   }
-  if (a.s_final) state_store(a.s_final + state, a.dk, a.dv, s_at, S);
+  if (float* to = leaving(a, seq, h)) state_store(to, a.dk, a.dv, s_at, S);
+}
+
+// ---- pieces of a long sequence ----
+//
+// Over some chunks the state maps to M S + N: M is where they take the columns of the identity without any
+// values, N where they take a zero state.  So where there are few heads the pieces of a sequence are walked at
+// the same time twice, first for their maps (dk + dv columns, no outputs), then from the states that the maps give.
+
+constexpr int kMapWaves = 4;
+
+// The maps: [piece][H][dkp][dvp + dkp], N before M.  The last piece's is not needed.
+template <typename E, int DKP>
+__global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Args a, int groups, float* maps) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, WAVES = kMapWaves;
+  constexpr int kBuf = kWalkBuffers<E, DKP, false, WAVES>;
+  using TR = Tri<E>;
+  using Raw = typename Frag<E>::Raw;
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
+  const int grp = walk_group(groups), chain = walk_chain(groups);
+  if (chain >= a.B * a.nseg * a.H) return;
+  const int h = chain % a.H, seq = chain / a.H;
+  if (seq % a.nseg == a.nseg - 1) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const Span span = span_of<C>(a, seq);
+  if (wave >= WAVES) {
+    const E* in = static_cast<const E*>(a.v) + static_cast<int64_t>(h) * a.dv;
+    if (a.wide_v) load_walk<E, DKP, false, WAVES, kBuf, false, true, true>(a, span, h, grp * WAVES * 16, tiles, tiles, in, a.ldv, static_cast<E*>(nullptr), 0);
+    else load_walk<E, DKP, false, WAVES, kBuf, false, false, true>(a, span, h, grp * WAVES * 16, tiles, tiles, in, a.ldv, static_cast<E*>(nullptr), 0);
+    return;
+  }
+  const int col = (grp * WAVES + wave) * 16 + i, width = a.dvp + DKP;
+  f32x4_t S[ND];
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[t][r] = state_row(t, g) + r == col - a.dvp ? 1.0f : 0.0f;
+  __syncthreads();
+  for (int chunk = span.first; chunk < span.end; ++chunk) {
+    const auto& w = tiles[(chunk - span.first) & (kBuf - 1)];
+    f32x4_t ks[NT], u[NT], gm[NT], et[NT], vt[NT], rest[NT];
+    Raw rows[2][NT];
+    auto read_rows = [&](int kp) {
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt) rows[kp & 1][mt] = row_frag<DKP>(w.K, 16 * mt + i, 32 * kp + 8 * g);
+    };
+    Split<E> tri[TR::kFrags];
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) ks[mt] = u[mt] = zero4();
+    read_rows(0);
+    Split<E> s(S[0], S[1]);
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp) {
+      if (kp + 1 < NK) {
+        read_rows(kp + 1);
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < NT; ++mt) {
+          gm[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g);
+          et[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + 2 * C + 16 * mt + 4 * g);
+          vt[mt] = four_of<16 * WAVES>(w.V, 16 * mt + 4 * g, 16 * wave);
+        }
+#pragma unroll
+        for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
+      }
+      in_order();
+      mma_all(ks, rows[kp & 1], s);
+      if (kp + 1 < NK) s = Split<E>(S[2 * kp + 2], S[2 * kp + 3]);
+      in_order();
+    }
+    const float decay = w.vec[C - 1];
+    Raw cols[ND];
+    auto read_cols = [&](int kp) {
+#pragma unroll
+      for (int t = 0; t < ND; ++t) cols[t] = state_col<DKP>(w.K, 32 * kp, t);
+    };
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      rest[mt] = *reinterpret_cast<const f32x4_t*>(w.vec + C + 16 * mt + 4 * g);
+      ks[mt] = et[mt] * (vt[mt] - gm[mt] * ks[mt]);
+    }
+    read_cols(0);
+    in_order();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) tri_mul<E>(u, tri, Split<E>(ks[2 * kp], ks[2 * kp + 1]), kp);
+#pragma unroll
+    for (int t = 0; t < ND; ++t) S[t] *= decay;
+    in_order();
+#pragma unroll
+    for (int kp = 0; kp < NP; ++kp) {
+      const Split<E> x(u[2 * kp] * rest[2 * kp], u[2 * kp + 1] * rest[2 * kp + 1]);
+      mma_all(S, cols, x);
+      if (kp + 1 < NP) read_cols(kp + 1);
+    }
+    if constexpr (kBuf == 1) __syncthreads();
+    __syncthreads();
+  }
+  if (col < width) {
+    float* to = maps + (static_cast<int64_t>(seq) * a.H + h) * DKP * width + col;
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[static_cast<int64_t>(state_row(t, g) + r) * width] = S[t][r];
+  }
+}
+
+// The states that enter the pieces, one after the other: 16 columns of a head a workgroup, 16 rows a wave.
+template <typename E, int DKP>
+__global__ __launch_bounds__(DKP * 4) void join_kernel(Args a, const float* maps, float* states) {
+  constexpr int NK = DKP / 32;
+  __shared__ f32x4_t S[DKP / 16][64];
+  const int groups = a.dvp / 16, grp = blockIdx.x % groups, h = blockIdx.x / groups % a.H, seq = blockIdx.x / groups / a.H;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int col = 16 * grp + i, width = a.dvp + DKP;
+  f32x4_t x;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = 16 * wave + 4 * g + r;
+    x[r] = a.s0 && row < a.dk && col < a.dv ? a.s0[((static_cast<int64_t>(seq) * a.H + h) * a.dk + row) * a.dv + col] : 0.0f;
+  }
+  for (int n = 0; n < a.nseg; ++n) {
+    const int64_t piece = (static_cast<int64_t>(seq) * a.nseg + n) * a.H + h;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * wave + 4 * g + r;
+      if (row < a.dk && col < a.dv) states[(piece * a.dk + row) * a.dv + col] = x[r];
+    }
+    if (n + 1 == a.nseg) return;
+    S[wave][lane] = x;
+    const float* m = maps + piece * DKP * width;
+    f32x4_t c, row[2 * NK];
+#pragma unroll
+    for (int kp = 0; kp < 2 * NK; ++kp)
+      row[kp] = *reinterpret_cast<const f32x4_t*>(m + static_cast<int64_t>(16 * wave + i) * width + a.dvp + 16 * kp + 4 * g);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[r] = m[static_cast<int64_t>(16 * wave + 4 * g + r) * width + col];
+    __syncthreads();
+#pragma unroll
+    for (int kp = 0; kp < NK; ++kp)
+      c = mma(Split<E>(row[2 * kp], row[2 * kp + 1]), Split<E>(S[2 * kp][lane], S[2 * kp + 1][lane]), c);
+    __syncthreads();
+    x = c;
+  }
 }
 
 // ---- one token ----
@@ -714,8 +864,31 @@ int64_t delta_chunks(const ttt_delta_desc& d) {
 
 namespace {
 
+int padded_dv(int dv) { return (dv + 31) / 32 * 32; }
+
+// The pieces of a dense sequence's forward walk.  A chunk of a walk takes about 2 us with helpers, 2.5 us with four
+// waves' columns in a workgroup on every CU, 2.2 us without outputs; a piece costs 2 us more where the maps
+// are joined.  131072 tokens of 16 heads of 128: one piece 4.3 ms, eight 1.7 ms.
+int pieces(const ttt_delta_desc& d) {
+  if (d.packed || d.T == 0 || d.B == 0) return 1;
+  const int64_t chunks = (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype), heads = static_cast<int64_t>(d.B) * d.H;
+  const int64_t gv = (padded_dv(d.dv) + 63) / 64, gm = (padded_dv(d.dv) + padded_dk(d.dk) + 63) / 64;
+  if (heads * gv * 2 >= 256) return 1;  // every CU has a walk with helpers
+  double best = chunks * 2.0;
+  int n = 1;
+  for (int64_t k = 2; k <= 64 && 4 * k <= chunks; ++k) {
+    const int64_t each = (chunks + k - 1) / k, k1 = (chunks + each - 1) / each;
+    const double t = (heads * (k1 - 1) * gm + 255) / 256 * each * 2.2 + k1 * 2.0 + 20.0 + (heads * k1 * gv + 255) / 256 * each * 2.5;
+    if (t < (n == 1 ? 0.8 : 1.0) * best) {
+      best = t;
+      n = static_cast<int>(k1);
+    }
+  }
+  return n;
+}
+
 struct Layout {
-  size_t edge, base, table, vec, t, p, kq, y, after, bytes;
+  size_t edge, base, table, vec, t, p, kq, y, after, maps, states, bytes;
 };
 Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, C = chunk_tokens(d.dtype), e = elem_bytes(d);
@@ -736,6 +909,11 @@ Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   l.t = take(items * tri_bytes(d));
   l.p = take(items * tri_bytes(d));
   l.kq = take(static_cast<size_t>(delta_chunks(d)) * d.Hk * 2 * C * padded_dk(d.dk) * e);
+  if (!bwd && pieces(d) > 1) {
+    const size_t all = static_cast<size_t>(d.B) * pieces(d) * d.H * sizeof(float);
+    l.maps = take(all * padded_dk(d.dk) * (dvp + padded_dk(d.dk)));
+    l.states = take(all * d.dk * d.dv);
+  }
   if (bwd) {
     l.y = take(items * C * dvp * e);
     l.after = take(items * padded_dk(d.dk) * dvp * e);
@@ -767,6 +945,8 @@ Args make_args(const ttt_delta_desc& d, const void* q, const void* k, const void
   a.wide_o = a.wide_do = d.dv % V == 0;  // dense, on 16 bytes
   a.dense = a.wide_q && a.wide_k;
   a.chunks = static_cast<int>(delta_chunks(d));
+  a.nseg = 1;
+  a.seg_chunks = d.packed ? 0 : (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype);
   a.chunks_per_seq = d.packed ? 0 : (d.T + chunk_tokens(d.dtype) - 1) / chunk_tokens(d.dtype);
   return a;
 }
@@ -833,6 +1013,21 @@ hipError_t delta_fwd_launch(const ttt_delta_desc& d, const void* q, const void* 
     constexpr int DKP = width();
     hipError_t e = delta::launch_prep<E, DKP, false>(a, s);
     if (e != hipSuccess) return e;
+    if (const int n = pieces(d); n > 1) {
+      a.nseg = n;
+      a.seg_chunks = (a.chunks_per_seq + n - 1) / n;
+      float* maps = reinterpret_cast<float*>(static_cast<char*>(ws) + l.maps);
+      float* states = reinterpret_cast<float*>(static_cast<char*>(ws) + l.states);
+      a.seg_states = states;
+      KernelScope scope(TTT_KERNEL_DELTA_MAP, s);
+      const int groups = (a.dvp + DKP + 16 * delta::kMapWaves - 1) / (16 * delta::kMapWaves);
+      delta::map_kernel<E, DKP><<<delta::walk_grid(a, groups), (delta::kMapWaves + delta::kLoaders) * 64, 0, s>>>(a, groups, maps);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      delta::join_kernel<E, DKP><<<static_cast<uint32_t>(d.B) * d.H * (a.dvp / 16), DKP * 4, 0, s>>>(a, maps, states);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     KernelScope scope(TTT_KERNEL_DELTA_FWD, s);
     return delta::by_waves<DKP>(a, [&](auto waves, int groups) {
       const uint32_t grid = delta::walk_grid(a, groups);

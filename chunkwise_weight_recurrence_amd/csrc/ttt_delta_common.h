@@ -34,6 +34,8 @@ struct Args {
   int64_t n;                     // tokens
   int64_t ldq, ldk, ldv, ldg, ldb;
   int chunks, chunks_per_seq;    // chunk slots; of a sequence (dense)
+  int nseg, seg_chunks;          // dense: the pieces that a sequence is walked in at the same time; a piece's chunks
+  const float* seg_states;       // [B * nseg][H][dk][dv]: the states that enter them, where nseg > 1
   const int* base;               // packed: [B + 1] the sequences' first chunks
   const int4* table;             // packed: [chunks] first token, tokens, sequence
   const void* q;
@@ -372,7 +374,7 @@ __device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ld, int cols, in
 }
 
 // The loaders' part: the next chunk's pieces in registers.
-template <typename E, int DKP, bool BWD, int WAVES, bool WIDE> struct Loader {
+template <typename E, int DKP, bool BWD, int WAVES, bool WIDE, bool LEAN = false> struct Loader {  // LEAN: no queries, no scores
   using W = WalkTile<E, DKP, BWD, WAVES>;
   static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = kLoadThreads / kPieces, kRows = C / kStep;
   static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads, kP = (W::kPBytes / 16 + kLoadThreads - 1) / kLoadThreads;
@@ -411,14 +413,14 @@ template <typename E, int DKP, bool BWD, int WAVES, bool WIDE> struct Loader {
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
       k[n] = kb.template load<uint4>(at + (row + n * kStep) * sk);
-      q[n] = qb.template load<uint4>(at + (row + n * kStep) * sq);
+      if constexpr (!LEAN) q[n] = qb.template load<uint4>(at + (row + n * kStep) * sq);
     }
     const uint4* tp = reinterpret_cast<const uint4*>(a.t + item * Tri<E>::kBytes);
     const uint4* pp = reinterpret_cast<const uint4*>(a.p + item * Tri<E>::kBytes);
 #pragma unroll
     for (int n = 0; n < kT; ++n) t[n] = tp[piece(n, Tri<E>::kBytes / 16)];
 #pragma unroll
-    for (int n = 0; n < kP; ++n) p[n] = pp[piece(n, W::kPBytes / 16)];
+    for (int n = 0; n < (LEAN ? 0 : kP); ++n) p[n] = pp[piece(n, W::kPBytes / 16)];
     vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
     const int vcols = a.dv - c0;  // may be none
     const Buffer vb(cp, vcols > 0 ? rows_bytes(len, ldc, vcols, sizeof(E)) : 0);
@@ -442,12 +444,12 @@ template <typename E, int DKP, bool BWD, int WAVES, bool WIDE> struct Loader {
     for (int n = 0; n < kRows; ++n) {
       const int at = Tile<E, DKP>::at(row + n * kStep, col);
       *reinterpret_cast<uint4*>(w.K + at) = k[n];
-      *reinterpret_cast<uint4*>(w.Q + at) = q[n];
+      if constexpr (!LEAN) *reinterpret_cast<uint4*>(w.Q + at) = q[n];
     }
 #pragma unroll
     for (int n = 0; n < kT; ++n) reinterpret_cast<uint4*>(w.T)[piece(n, Tri<E>::kBytes / 16)] = t[n];
 #pragma unroll
-    for (int n = 0; n < kP; ++n) reinterpret_cast<uint4*>(w.P)[piece(n, W::kPBytes / 16)] = p[n];
+    for (int n = 0; n < (LEAN ? 0 : kP); ++n) reinterpret_cast<uint4*>(w.P)[piece(n, W::kPBytes / 16)] = p[n];
     reinterpret_cast<uint4*>(w.vec)[piece(0, 3 * C / 4)] = vec;
 #pragma unroll
     for (int n = 0; n < kVRows; ++n) *reinterpret_cast<uint4*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
@@ -492,12 +494,12 @@ template <typename E, int DKP, bool BWD, int WAVES, bool WIDE> struct Loader {
 };
 
 // The loaders' walk beside the others': from the first chunk on, BWD from the last back.  `in` and `out` are the
-// head's first row of v (or of the gradient of o) and of the result; WIDE: both in 16-byte pieces.
-template <typename E, int DKP, bool BWD, int WAVES, int BUF, bool MID, bool WIDE, typename Tiles, typename Outs, typename S>
+// head's first row of v (or of the gradient of o) and of the result; WIDE: both in 16-byte pieces; LEAN: there is no result.
+template <typename E, int DKP, bool BWD, int WAVES, int BUF, bool MID, bool WIDE, bool LEAN = false, typename Tiles, typename Outs, typename S>
 __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, int c0, Tiles& tiles, Outs& outs, const E* in, int64_t ld_in,
                                           E* out, int64_t ld_out) {
   constexpr int C = Chunk<E>::C;
-  using L = Loader<E, DKP, BWD, WAVES, WIDE>;
+  using L = Loader<E, DKP, BWD, WAVES, WIDE, LEAN>;
   const int tid = threadIdx.x - static_cast<int>(blockDim.x - kLoadThreads);
   L even(tid), odd(tid);  // the chunks' pieces on their way, in turn
   const int count = span.end - span.first;
@@ -508,8 +510,10 @@ __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, i
     l.load(a, chunk, h, token, span.len(chunk, C), in + token * ld_in + c0, ld_in, c0);
   };
   auto put = [&](int n) {
-    const int chunk = chunk_of(n);
-    even.put(a, outs[n & (BUF - 1)], out + span.token(chunk, C) * ld_out + c0, ld_out, span.len(chunk, C), c0);
+    if constexpr (!LEAN) {
+      const int chunk = chunk_of(n);
+      even.put(a, outs[n & (BUF - 1)], out + span.token(chunk, C) * ld_out + c0, ld_out, span.len(chunk, C), c0);
+    }
   };
   auto step = [&](L& l, int n) {  // l has chunk n + 1
     if constexpr (BUF == 2) {
@@ -595,7 +599,7 @@ struct Span {
   }
   __device__ __forceinline__ int64_t token(int chunk, int C) const { return token0 + static_cast<int64_t>(chunk - first) * C; }
 };
-__device__ __forceinline__ Span span_of(const Args& a, int seq) {
+template <int C> __device__ __forceinline__ Span span_of(const Args& a, int seq) {
   Span s;
   if (a.packed) {
     s.first = a.base[seq];
@@ -606,11 +610,12 @@ __device__ __forceinline__ Span span_of(const Args& a, int seq) {
       s.token0 = head.x;
       s.tokens = tail.x + tail.y - head.x;
     }
-  } else {
-    s.first = seq * a.chunks_per_seq;
-    s.end = s.first + a.chunks_per_seq;
-    s.token0 = static_cast<int64_t>(seq) * a.T;
-    s.tokens = a.T;
+  } else {  // seq: a piece of one
+    const int n = seq % a.nseg * a.seg_chunks, whole = seq / a.nseg;
+    s.first = whole * a.chunks_per_seq + n;
+    s.end = whole * a.chunks_per_seq + min(n + a.seg_chunks, a.chunks_per_seq);
+    s.token0 = static_cast<int64_t>(whole) * a.T + static_cast<int64_t>(n) * C;
+    s.tokens = min(static_cast<int64_t>(a.T) - static_cast<int64_t>(n) * C, static_cast<int64_t>(a.seg_chunks) * C);
   }
   return s;
 }
@@ -704,13 +709,13 @@ __device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, 
 template <int DKP, typename F> hipError_t by_waves(const Args& a, F&& f) {
   const int64_t columns = a.dvp / 16;
   if constexpr (DKP == 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));
-  else if (static_cast<int64_t>(a.B) * a.H * ((columns + 3) / 4) >= 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));
+  else if (static_cast<int64_t>(a.B) * a.nseg * a.H * ((columns + 3) / 4) >= 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));
   else return f(std::integral_constant<int, 2>{}, static_cast<int>((columns + 1) / 2));
 }
 
 // Workgroups go to the eight XCDs in turn, each with an L2 of its own.  Those that share a head's keys and
 // queries are put on one, the heads (chains) on all in turn: in long runs they are a sequence's.
-inline uint32_t walk_grid(const Args& a, int groups) { return static_cast<uint32_t>((static_cast<int64_t>(a.B) * a.H + 7) / 8 * 8 * groups); }
+inline uint32_t walk_grid(const Args& a, int groups) { return static_cast<uint32_t>((static_cast<int64_t>(a.B) * a.nseg * a.H + 7) / 8 * 8 * groups); }
 __device__ __forceinline__ int walk_chain(int groups) { return static_cast<int>(blockIdx.x / 8 / groups * 8 + blockIdx.x % 8); }
 __device__ __forceinline__ int walk_group(int groups) { return static_cast<int>(blockIdx.x / 8 % groups); }
 

@@ -812,7 +812,8 @@ typedef enum {
   TTT_KERNEL_QK_FWD = 39,        /* norm and rotation of queries and keys */
   TTT_KERNEL_QK_BWD = 40,        /* its backward: dq, dk and partial dwq, dwk */
   TTT_KERNEL_QK_REDUCE = 41,     /* its backward: sum of the partial dwq, dwk */
-  TTT_KERNEL_COUNT = 42
+  TTT_KERNEL_DELTA_MAP = 42,     /* gated delta rule forward: maps of a long sequence's pieces, joined */
+  TTT_KERNEL_COUNT = 43
 } ttt_kernel;
 
 TTT_API int ttt_timing_enable(int on);

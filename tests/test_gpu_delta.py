@@ -153,6 +153,20 @@ def test_many_chunks(dtype, T, Bn):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,dk,dv,chunks,tail", [(1, 64, 64, 40, 1), (1, 128, 40, 67, 0), (2, 33, 96, 50, 17), (1, 256, 32, 36, 5)])
+def test_long_sequences_walked_in_pieces(dtype, H, dk, dv, chunks, tail):
+    """Few heads and many chunks: the forward walks pieces at the same time and joins their maps.  A map's own error,
+    two-term operands as everywhere, comes to that of the states once more for each piece that is joined, passed on
+    with what is left of the decay: twice the states' tolerance."""
+    C = 64 if dtype == "bf16" else 32
+    T, Bn = chunks * C + tail, 2 if dv == 96 else 1
+    inp = _make(chunks, Bn * T, Bn, H, 1, dk, dv, dtype, "sigmoid", z_mean=5.0)
+    out = _train(inp, "sigmoid", dtype, B_=Bn, T=T)
+    _check(out, _oracle(inp, list(range(0, Bn * T + 1, T)), "sigmoid", dk ** -0.5), dtype,
+           state_tol=4 * STATE_TOL if dtype == "bf16" else 4 * TOL["f32"], tol=4 * TOL["f32"] if dtype == "f32" else None, what=f"{dtype} pieces")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_gates_at_their_ends(dtype):
     """Tokens that forget everything (a = 0) or nothing (a = 1), and steps of 0 and 1."""
     import torch

@@ -744,12 +744,24 @@ struct StepArgs {
 
 template <typename E, int NR>  // NR: rows of the state a thread holds
 __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a) {
-  __shared__ float part[2][kStepRuns][kStepCols];
+  __shared__ float part[2][kStepRuns][kStepCols], kq_part[kStepRuns];
   __shared__ float ks[kStepRuns * NR], qs[kStepRuns * NR];
   __shared__ uint64_t same[kStepThreads / 64];
+  static_assert(kStepRuns * NR <= kStepThreads);
   const int cb = blockIdx.x % a.ncb, h = blockIdx.x / a.ncb % a.H, b = blockIdx.x / a.ncb / a.H;
   const int hk = h / (a.H / a.Hk);
   const int c = threadIdx.x % kStepCols, run = threadIdx.x / kStepCols, col = cb * kStepCols + c;
+  // a token's values; the first one's are on their way while its slot is looked for
+  float kx, qx, vt, z, bt;
+  auto fetch = [&](int64_t row) {
+    const int x = threadIdx.x;
+    kx = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.k), row * a.ldk + hk * a.dk + x) : 0.0f;
+    qx = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.q), row * a.ldq + hk * a.dk + x) : 0.0f;
+    vt = col < a.dv ? Elem<E>::ld(static_cast<const E*>(a.v), row * a.ldv + static_cast<int64_t>(h) * a.dv + col) : 0.0f;
+    z = a.gate ? Elem<E>::ld(static_cast<const E*>(a.gate), row * a.ldg + h) : 0.0f;
+    bt = Elem<E>::ld(static_cast<const E*>(a.beta), row * a.ldb + h);
+  };
+  fetch(b);
   int slot = b;
   if (a.slots) {
     slot = __builtin_amdgcn_readfirstlane(a.slots[b]);
@@ -765,15 +777,13 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a) {
     const int row = r * kStepRuns + run;
     S[r] = row < a.dk && col < a.dv ? a.s[at + static_cast<int64_t>(row) * a.dv] : 0.0f;
   }
-  auto token = [&](int row) {
-    const int64_t rr = row;
-    for (int x = threadIdx.x; x < kStepRuns * NR; x += kStepThreads) {
-      ks[x] = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.k), rr * a.ldk + hk * a.dk + x) : 0.0f;
-      qs[x] = x < a.dk ? Elem<E>::ld(static_cast<const E*>(a.q), rr * a.ldq + hk * a.dk + x) : 0.0f;
+  auto token = [&](int64_t row) {
+    if (threadIdx.x < kStepRuns * NR) {
+      ks[threadIdx.x] = kx;
+      qs[threadIdx.x] = qx;
     }
-    const float vt = col < a.dv ? Elem<E>::ld(static_cast<const E*>(a.v), rr * a.ldv + static_cast<int64_t>(h) * a.dv + col) : 0.0f;
-    const float decay = a.gate ? exp2_(log2_decay(Elem<E>::ld(static_cast<const E*>(a.gate), rr * a.ldg + h), a.gate_kind)) : 1.0f;
-    const float eta = a.lr_max / (1.0f + __expf(-(Elem<E>::ld(static_cast<const E*>(a.beta), rr * a.ldb + h) + a.lr_bias)));
+    const float decay = a.gate ? exp2_(log2_decay(z, a.gate_kind)) : 1.0f;
+    const float eta = a.lr_max / (1.0f + __expf(-(bt + a.lr_bias))), v = vt;
     __syncthreads();
     float e = 0.0f, kq = 0.0f, o = 0.0f;
 #pragma unroll
@@ -782,23 +792,25 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a) {
       S[r] *= decay;
       e += kr * S[r];
       o += qr * S[r];
+      kq += kr * qr;
     }
     part[0][run][c] = e;
     part[1][run][c] = o;
+    if (c == 0) kq_part[run] = kq;
     __syncthreads();
-    e = vt;
-    o = 0.0f;
+    e = v;
+    o = kq = 0.0f;
 #pragma unroll
     for (int j = 0; j < kStepRuns; ++j) {
       e -= part[0][j][c];
       o += part[1][j][c];
+      kq += kq_part[j];
     }
     const float u = eta * e;
 #pragma unroll
     for (int r = 0; r < NR; ++r) S[r] += ks[r * kStepRuns + run] * u;
     // o = S^T q = (the decayed state)^T q + (k.q) u
-    for (int x = 0; x < a.dk; ++x) kq += ks[x] * qs[x];
-    if (run == 0 && col < a.dv) Elem<E>::st(static_cast<E*>(a.o), (rr * a.H + h) * a.dv + col, a.scale * (o + kq * u));
+    if (run == 0 && col < a.dv) Elem<E>::st(static_cast<E*>(a.o), (row * a.H + h) * a.dv + col, a.scale * (o + kq * u));
     __syncthreads();
   };
   token(b);
@@ -809,7 +821,11 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepArgs a) {
       if ((threadIdx.x & 63) == 0) same[threadIdx.x >> 6] = hit;
       __syncthreads();
       for (int w = 0; w < kStepThreads / 64; ++w)
-        for (uint64_t left = same[w]; left; left &= left - 1) token(j0 + w * 64 + __builtin_ctzll(left));
+        for (uint64_t left = same[w]; left; left &= left - 1) {
+          const int row = j0 + w * 64 + __builtin_ctzll(left);
+          fetch(row);
+          token(row);
+        }
       __syncthreads();
     }
   }

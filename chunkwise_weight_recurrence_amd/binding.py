@@ -678,6 +678,9 @@ def _tokens(name, x, dev, dtype, n, H, d, ld):
     of one side by side: [..,H,d] or [..,H * d].  The checks are _arg's."""
     if x is None or type(x) is int:
         return x
+    if ld and ld != H * d and hasattr(x, "stride") and x.dim() == 3 and x.shape[1:] == (H, d) and x.shape[0] == n and \
+            x.stride() == (ld, d, 1) and x.dtype is dtype and x.get_device() == dev and dev >= 0:
+        return x.data_ptr()
     if ld and ld != H * d and hasattr(x, "stride") and x.dim() >= 2 and x.shape[-1] == d and x.shape[-2] == H:
         if H > 1 and x.stride(-2) != d or d > 1 and x.stride(-1) != 1:
             raise ValueError(f"{name} must have {H} heads of {d} elements side by side (got shape {tuple(x.shape)}, "

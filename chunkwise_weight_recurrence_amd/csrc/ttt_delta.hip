@@ -13,7 +13,7 @@ constexpr int kPlanThreads = 1024;
 // so whatever they are, the chunks fit the table and the tokens the buffers.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, int B, int n, int C, int slots, int* edge, int* base,
                                                             int4* table) {
-  __shared__ int part[kPlanThreads / 64];
+  __shared__ int part[kPlanThreads / 64], near_base[kPlanThreads];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // running maximum of the starts
   int carry = 0;
@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, i
       all += part[j];
     }
     if (i <= B) base[i] = before + c - own;
+    if (i < kPlanThreads) near_base[i] = before + c - own;  // for the search below
     carry = all;
     __syncthreads();
   }
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, i
       int lo = 0, hi = B;  // the last sequence whose base is <= c
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (base[mid] <= c) lo = mid;
+        if ((B < kPlanThreads ? near_base[mid] : base[mid]) <= c) lo = mid;
         else hi = mid;
       }
       const int first = edge[lo] + (c - base[lo]) * C;

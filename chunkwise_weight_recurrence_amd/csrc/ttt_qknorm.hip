@@ -159,10 +159,14 @@ template <typename E, int V, int LANES, int N, bool HALF>
 struct Rows {
   using P = Piece<E, V>;
   using Raw = typename P::Raw;
-  static __device__ __forceinline__ void load(const E* row, const Unit<V, HALF>& u, int d, float (&x)[2][V]) {
-    Raw r[2] = {};
+  static __device__ __forceinline__ void fetch(const E* row, const Unit<V, HALF>& u, int d, Raw (&r)[2]) {
+    r[0] = r[1] = Raw{};
     if (u.a < d) r[0] = *reinterpret_cast<const Raw*>(row + u.a);
     if (u.b < d) r[1] = *reinterpret_cast<const Raw*>(row + u.b);
+  }
+  static __device__ __forceinline__ void load(const E* row, const Unit<V, HALF>& u, int d, float (&x)[2][V]) {
+    Raw r[2];
+    fetch(row, u, d, r);
     P::get(r[0], x[0]);
     P::get(r[1], x[1]);
   }
@@ -179,48 +183,60 @@ struct Rows {
   }
 };
 
+// A slot's rows go over the queries' and the keys' heads of the workgroup's tokens; a row is on its way while the
+// one before it (or the table) is computed.
 template <typename E, int V, int LANES, int N, bool HALF>
 __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkArgs a) {
   using R = Rows<E, V, LANES, N, HALF>;
   extern __shared__ float2 table[];
   constexpr int kSlots = kThreads / LANES;
-  const int slot = threadIdx.x / LANES, lane = threadIdx.x % LANES, entries = (a.d + 1) / 2;
+  const int slot = threadIdx.x / LANES, lane = threadIdx.x % LANES, entries = (a.d + 1) / 2, heads = a.Hq + a.Hk;
+  float* weights = reinterpret_cast<float*>(table + a.tok * entries);  // [2][d]
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tok; t0 < a.tokens; t0 += static_cast<int64_t>(gridDim.x) * a.tok) {
-    const int count = static_cast<int>(min(static_cast<int64_t>(a.tok), a.tokens - t0));
+    const int count = static_cast<int>(min(static_cast<int64_t>(a.tok), a.tokens - t0)), rows = count * heads;
+    typename R::Raw raw[N][2];
+    auto fetch = [&](int row) {
+      const int t = row / heads, h = row % heads;
+      const E* src = h < a.Hq ? static_cast<const E*>(a.q) + (t0 + t) * a.ldq + h * a.d : static_cast<const E*>(a.k) + (t0 + t) * a.ldk + (h - a.Hq) * a.d;
+#pragma unroll
+      for (int n = 0; n < N; ++n) R::fetch(src, Unit<V, HALF>(lane + n * LANES, a.d, a.rot), a.d, raw[n]);
+    };
+    if (slot < rows) fetch(slot);
     __syncthreads();
     fill_table(table, a, t0, count);
+    for (int x = threadIdx.x; x < 2 * a.d; x += kThreads) {
+      const float* w = x < a.d ? a.wq : a.wk;
+      weights[x] = w ? w[x < a.d ? x : x - a.d] : 1.0f;
+    }
     __syncthreads();
-    auto part = [&](const E* x, int64_t ld, int H, const float* w, E* y) {
-      if (H == 0) return;
-      float wv[N][2][V];
-  #pragma unroll
-      for (int n = 0; n < N; ++n) R::weights(w, Unit<V, HALF>(lane + n * LANES, a.d, a.rot), a.d, wv[n]);
-      for (int row = slot; row < count * H; row += kSlots) {
-        const int t = row / H, h = row % H;
-        const E* src = x + (t0 + t) * ld + h * a.d;
-        float v[N][2][V], ss = 0.0f;
-  #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          R::load(src, Unit<V, HALF>(lane + n * LANES, a.d, a.rot), a.d, v[n]);
-  #pragma unroll
-          for (int j = 0; j < V; ++j) ss += v[n][0][j] * v[n][0][j] + v[n][1][j] * v[n][1][j];
-        }
-        const float r = scale_of(a, slot_sum<LANES>(ss));
-  #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const Unit<V, HALF> u(lane + n * LANES, a.d, a.rot);
-  #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            v[n][0][j] *= r * wv[n][0][j];
-            v[n][1][j] *= r * wv[n][1][j];
-          }
-          if (u.a < a.d) turn<V, HALF, false>(v[n], table + t * entries, u);
-          R::store(y + ((t0 + t) * H + h) * a.d, u, a.d, v[n]);
-        }
+    for (int row = slot; row < rows; row += kSlots) {
+      const int t = row / heads, h = row % heads;
+      const bool is_q = h < a.Hq;
+      const float* w = weights + (is_q ? 0 : a.d);
+      float v[N][2][V], ss = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        R::P::get(raw[n][0], v[n][0]);
+        R::P::get(raw[n][1], v[n][1]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss += v[n][0][j] * v[n][0][j] + v[n][1][j] * v[n][1][j];
       }
-    };
-    part(static_cast<const E*>(a.q), a.ldq, a.Hq, a.wq, static_cast<E*>(a.yq));
-    part(static_cast<const E*>(a.k), a.ldk, a.Hk, a.wk, static_cast<E*>(a.yk));
+      if (row + kSlots < rows) fetch(row + kSlots);
+      const float r = scale_of(a, slot_sum<LANES>(ss));
+      E* dst = is_q ? static_cast<E*>(a.yq) + ((t0 + t) * a.Hq + h) * a.d : static_cast<E*>(a.yk) + ((t0 + t) * a.Hk + h - a.Hq) * a.d;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const Unit<V, HALF> u(lane + n * LANES, a.d, a.rot);
+        const int pa = min(u.a, a.d - V), pb = min(u.b, a.d - V);  // a piece that is not there takes the last one's
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[n][0][j] *= r * w[pa + j];
+          v[n][1][j] *= r * w[pb + j];
+        }
+        if (u.a < a.d) turn<V, HALF, false>(v[n], table + t * entries, u);
+        R::store(dst, u, a.d, v[n]);
+      }
+    }
   }
 }
 
@@ -397,7 +413,7 @@ hipError_t qknorm_fwd_launch(const ttt_qknorm_desc& d, const void* q, const void
     KernelScope scope(TTT_KERNEL_QK_FWD, s);
     const int64_t groups = (d.tokens + a.tok - 1) / a.tok;
     const uint32_t grid = static_cast<uint32_t>(groups < kFwdGroups ? groups : kFwdGroups);
-    qk_fwd_kernel<decltype(e), v(), lanes(), n(), half()><<<grid, kThreads, table_bytes(a), s>>>(a);
+    qk_fwd_kernel<decltype(e), v(), lanes(), n(), half()><<<grid, kThreads, table_bytes(a) + 2 * d.d * sizeof(float), s>>>(a);
     return hipGetLastError();
   });
 }

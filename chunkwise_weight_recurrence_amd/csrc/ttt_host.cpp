@@ -783,10 +783,11 @@ int check_delta_desc(const ttt_delta_desc* d) {
     return fail(TTT_ERR_INVALID_ARG, "ldq, ldk, ldv, ldg, ldb must be 0 or at least a token's elements");
   constexpr int64_t kMaxLd = 1 << 22;  // a chunk's rows lie within 2^29 bytes
   const int64_t n = d->packed ? d->T : static_cast<int64_t>(d->B) * d->T;
-  // Tokens are counted in 32 bits, rounded up to whole chunks; a launch has fewer than 2^32 threads.
+  // Tokens are counted in 32 bits, rounded up to whole chunks; a launch has fewer than 2^32 threads, 512 of them
+  // for a chunk and head or for the columns of a sequence's head.
   if (wk > kMaxLd || wv > kMaxLd || d->ldq > kMaxLd || d->ldk > kMaxLd || d->ldv > kMaxLd || d->ldg > kMaxLd || d->ldb > kMaxLd ||
       n > INT32_MAX - 4095 || d->B > INT32_MAX - 4095 || static_cast<double>(d->B) * wv * d->dk > 4.0e12 ||
-      static_cast<double>(ttt::delta_chunks(*d)) * d->H >= 1 << 24 || static_cast<double>(d->B) * d->H * ((d->dv + 15) / 16) >= 1 << 24)
+      static_cast<double>(ttt::delta_chunks(*d)) * d->H >= 1 << 23 || static_cast<double>(d->B) * d->H * ((d->dv + 15) / 16) >= 1 << 22)
     return fail(TTT_ERR_UNSUPPORTED, "problem too large (%lld tokens, %d sequences of %d heads)", static_cast<long long>(n), d->B, d->H);
   return TTT_OK;
 }

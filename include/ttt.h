@@ -605,11 +605,14 @@ TTT_API int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const floa
  * S is kept in float32.  In bf16 the products that make it take their operands in
  * two bf16 terms (2^-17 of a value is lost), and those that only read it to form
  * o or a gradient one.  A decay below 2^-150 counts as 2^-150, with no gradient.
- * An infinity may go on as NaN in its own sequence; no value reaches another one.
+ * An infinity or NaN may go on as NaN in its own sequence and head, to the tokens
+ * before it in its chunk too; no value reaches another sequence.
  */
 typedef struct {
-  int32_t B;      /* sequences (rows of one token each for ttt_delta_step)           */
-  int32_t T;      /* tokens of each; packed: token rows of the buffers               */
+  int32_t B;      /* sequences (rows of one token each for ttt_delta_step); B * H *
+                     ceil(dv / 16) below 2^22                                        */
+  int32_t T;      /* tokens of each; packed: token rows of the buffers.  Chunks (see the
+                     saved context) times H below 2^23                               */
   int32_t H;      /* value heads                                                     */
   int32_t Hk;     /* query and key heads, a divisor of H                             */
   int32_t dk, dv; /* 1 .. 256; S is dk x dv                                          */

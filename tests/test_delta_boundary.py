@@ -78,6 +78,9 @@ def test_structs_and_enums_match_the_header():
     (dict(B=1 << 16, T=1 << 15), -2, "too large"), (dict(T=(1 << 30), B=1), -2, "too large"),
     (dict(B=1 << 23, T=1), -2, "too large"), (dict(B=(1 << 31) - 1, T=0, packed=True), -2, "too large"),
     (dict(H=1 << 18, Hk=1, dv=64), -2, "too large"),
+    # a launch has fewer than 2^32 threads, 512 of them for a chunk and head or a sequence's columns
+    (dict(B=1, T=1 << 27, H=4), -2, "too large"), (dict(B=1 << 20, T=1, H=4, dv=1), -2, "too large"),
+    (dict(B=1 << 19, T=1, H=4, dv=32), -2, "too large"), (dict(ldq=(1 << 22) + 1), -2, "too large"),
 ])
 def test_delta_desc(kw, code, msg):
     d = _desc(**kw)

@@ -159,7 +159,8 @@ template <int C, int LD> __device__ __forceinline__ void invert(const float* A, 
 
 // A chunk and head a workgroup: its gates' sums, K K^T and Q K^T (row tile w by wave w), the inverse.
 // BWD writes the transposes, the scores in two terms.  It is bound by the latency of its stages, so LDS is
-// used over and over: 36 KB let four workgroups share a CU.
+// used over and over: 36 KB let four workgroups share a CU.  4096 chunks and heads of 128 bf16 59 us (93 with 53 KB,
+// three workgroups and the loads behind the gates' sums).
 template <typename E, int DKP, bool BWD>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   constexpr int C = Chunk<E>::C, NT = C / 16, LD = C + 4, V = 16 / sizeof(E), kPieces = DKP / V, kRows = C * kPieces / kPrepThreads;
@@ -283,7 +284,9 @@ __device__ __forceinline__ float* leaving(const Args& a, int seq, int h) {
 }
 
 // The chain (waves 0 .. WAVES - 1) and its helpers (the next WAVES) where there are few heads.  First half of a
-// chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.
+// chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.  A chunk of 64 x 128
+// bf16 takes 1.9 us, which is the chain's own: 82 matrix instructions and about 400 vector instructions, one in 5.5
+// cycles from one wave.  64 chunks of 64 heads with what a backward needs 174 us, 208 without helpers.
 template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
@@ -435,7 +438,8 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
 // is added to it are products of two-term operands: its error does not grow with the length.  KEEP: what a
-// backward needs is written.
+// backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 334 us, 4.4 us a chunk of a workgroup: four
+// chains share LDS and the loads of 256 workgroups the memory.
 template <typename E, int DKP, int WAVES, bool KEEP>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false, WAVES>;
@@ -585,7 +589,8 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
 
 constexpr int kMapWaves = 4;
 
-// The maps: [piece][H][dkp][dvp + dkp], N before M.  The last piece's is not needed.
+// The maps: [piece][H][dkp][dvp + dkp], N before M.  The last piece's is not needed.  Seven of eight pieces of 131072
+// tokens, 16 heads of 128 bf16, 904 us; the whole walk after it 687, in one piece 4300.
 template <typename E, int DKP>
 __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Args a, int groups, float* maps) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, WAVES = kMapWaves;
@@ -724,7 +729,8 @@ __global__ __launch_bounds__(DKP * 4) void join_kernel(Args a, const float* maps
 constexpr int kStepThreads = 256;
 
 // A workgroup has kStepCols columns of one head's state of one row, a thread a run of the dk rows of one
-// column; the two products over dk meet in LDS.  Rows that name one slot are consecutive tokens of it, in
+// column; the three sums over dk meet in LDS.  256 rows of 16 heads of 128 x 128 (537 MB) 114 us, 4.7 TB/s; 8 rows
+// 7.2 us, the latency of slot, state and sums.  Rows that name one slot are consecutive tokens of it, in
 // row order: the first of them does them all.
 constexpr int kStepCols = 32, kStepRuns = kStepThreads / kStepCols;
 

@@ -705,7 +705,9 @@ __device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, 
 }
 
 // The waves of a walk's workgroup, and the workgroups that share a head's columns: four waves where that
-// leaves a workgroup for every CU, else two.  Of 256 channels, four: two would have no registers for the next chunk.
+// leaves a workgroup for every CU, else two with helpers.  30011 packed tokens of 20 heads of 128 (740 heads of
+// sequences) take 335 us with four and 485 with two; 4 x 4096 tokens of 16 heads (64) 176 with two and helpers, 258 with
+// four.  Of 256 channels, four: helpers' part would not fit beside two chunks.
 template <int DKP, typename F> hipError_t by_waves(const Args& a, F&& f) {
   const int64_t columns = a.dvp / 16;
   if constexpr (DKP == 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));

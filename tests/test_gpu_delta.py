@@ -297,7 +297,45 @@ def test_gradients_against_differences_on_the_gpu():
         assert abs(got - want) <= 2e-3 * np.linalg.norm(grad), (name, got, want)
 
 
+def test_offsets_past_32_bits():
+    """Rows of 2^15 elements: the last token's lies behind 2^31 elements.  The same values close together give the same bits."""
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import DeltaBuffers
+    n, dk = 66000, 64
+    inp = _make(3, n, 1, 1, 1, dk, dk, "bf16", "sigmoid")
+    x = {k: inp[k].cuda()[None] for k in ("q", "k", "v", "gate", "beta", "d_o")}
+    wide = torch.empty(1, n, 1 << 15, dtype=torch.bfloat16, device="cuda")
+    for j, m in enumerate("qkv"):
+        wide[..., dk * j:dk * (j + 1)] = x[m][..., 0, :]
+    far = [wide[..., dk * j:dk * (j + 1)].unflatten(-1, (1, dk)) for j in range(3)]
+    near = DeltaBuffers(x["q"], x["k"], x["v"], x["gate"], x["beta"], with_bwd=True)
+    b = DeltaBuffers(*far, x["gate"], x["beta"], with_bwd=True)
+    for buf in (near, b):
+        buf.forward()
+        buf.backward(x["d_o"])
+    torch.cuda.synchronize()
+    for m in ("o", "s_final", "dq", "dk", "dv", "dgate", "dbeta", "ds0"):
+        assert torch.isfinite(getattr(near, m)).all() and torch.equal(getattr(near, m), getattr(b, m)), m
+
+
 # ---- one token ----
+
+
+def test_step_in_a_pool_past_32_bits():
+    """8200 states of 16 heads of 128 x 128: the last one's lies behind 2^31 elements."""
+    import torch
+    H, d, states = 16, 128, 8200
+    x, inp = _step_inputs(5, 2, 2, H, H, d, d, "bf16")
+    pool = torch.empty(states, H, d, d, device="cuda")
+    pool[-1], pool[0] = x["s0"][0], x["s0"][1]
+    slots = torch.tensor([states - 1, 0], dtype=torch.int32, device="cuda")
+    desc = B.make_delta_desc(2, 1, H, d, d)
+    o, want = torch.empty(2, H, d, dtype=torch.bfloat16, device="cuda"), torch.empty(2, H, d, dtype=torch.bfloat16, device="cuda")
+    B.ttt_delta_step(desc, x["q"], x["k"], x["v"], x["gate"], x["beta"], slots, pool, pool, o)
+    small = x["s0"].clone()
+    B.ttt_delta_step(desc, x["q"], x["k"], x["v"], x["gate"], x["beta"], None, small, small, want)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(pool[-1], small[0]) and torch.equal(pool[0], small[1])
 
 
 def _step_inputs(seed, rows, states, H, Hk, dk, dv, dtype):

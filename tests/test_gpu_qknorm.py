@@ -207,3 +207,23 @@ def test_captured_and_on_two_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(getattr(b, m), want[m]) for m in names), k
         work[1][0].forward()
+
+
+def test_offsets_past_32_bits():
+    """Rows of 2^15 elements: the last token's lies behind 2^31 elements.  The same values close together give the same bits."""
+    import torch
+    from chunkwise_weight_recurrence_amd.layer import QkNormBuffers
+    n, d = 66000, 64
+    inp = _make(9, n, 1, 1, d, d, "bf16", True, False)
+    x = {m: v.cuda() for m, v in inp.items()}
+    wide = torch.empty(n, 1 << 15, dtype=torch.bfloat16, device="cuda")
+    wide[:, :d], wide[:, d:2 * d] = x["q"][:, 0], x["k"][:, 0]
+    rest = (x["wq"], x["wk"], x["pos"], x["freq"])
+    near = QkNormBuffers(x["q"], x["k"], *rest, with_bwd=True)
+    far = QkNormBuffers(wide[:, None, :d], wide[:, None, d:2 * d], *rest, with_bwd=True)
+    for b in (near, far):
+        b.forward()
+        b.backward(x["dyq"], x["dyk"])
+    torch.cuda.synchronize()
+    for m in ("yq", "yk", "dq", "dk", "dwq", "dwk"):
+        assert torch.isfinite(getattr(near, m)).all() and torch.equal(getattr(near, m), getattr(far, m)), m

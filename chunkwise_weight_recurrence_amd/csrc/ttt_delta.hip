@@ -12,7 +12,7 @@ constexpr int kPlanThreads = 1024;
 // The chunk table of packed sequences: entries of seq_starts are held to 0 .. n and to ascend,
 // so whatever they are, the chunks fit the table and the tokens the buffers.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, int B, int n, int C, int slots, int* edge, int* base,
-                                                            int4* table) {
+                                                            int4* table, int* order) {
   __shared__ int part[kPlanThreads / 64], near_base[kPlanThreads];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // running maximum of the starts
@@ -58,6 +58,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* starts, i
     if (i < kPlanThreads) near_base[i] = before + c - own;  // for the search below
     carry = all;
     __syncthreads();
+  }
+  // the sequences by their chunks, the most first, of up to 1023; more keep their own order, which fills the chip anyway
+  for (int i = threadIdx.x; i < B; i += kPlanThreads) {
+    int rank = i;
+    if (B < kPlanThreads) {
+      const int own = near_base[i + 1] - near_base[i];
+      rank = 0;
+      for (int j = 0; j < B; ++j) {
+        const int c = near_base[j + 1] - near_base[j];
+        rank += c > own || (c == own && j < i);
+      }
+    }
+    order[rank] = i;
   }
   const int total = carry;
   for (int c = threadIdx.x; c < slots; c += kPlanThreads) {
@@ -451,7 +464,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.nseg * a.H) return;
-  const int h = chain % a.H, seq = chain / a.H;
+  const int h = chain % a.H, seq = walk_sequence(a, chain);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of<C>(a, seq);
   constexpr bool HELP = WAVES == 2;
@@ -600,7 +613,7 @@ __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Arg
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.nseg * a.H) return;
-  const int h = chain % a.H, seq = chain / a.H;
+  const int h = chain % a.H, seq = walk_sequence(a, chain);
   if (seq % a.nseg == a.nseg - 1) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of<C>(a, seq);
@@ -911,7 +924,7 @@ int pieces(const ttt_delta_desc& d) {
 }
 
 struct Layout {
-  size_t edge, base, table, vec, t, p, kq, y, after, maps, states, bytes;
+  size_t edge, base, order, table, vec, t, p, kq, y, after, maps, states, bytes;
 };
 Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, C = chunk_tokens(d.dtype), e = elem_bytes(d);
@@ -926,6 +939,7 @@ Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
   if (d.packed && items > 0) {
     l.edge = take(sizeof(int) * (static_cast<size_t>(d.B) + 1));
     l.base = take(sizeof(int) * (static_cast<size_t>(d.B) + 1));
+    l.order = take(sizeof(int) * (static_cast<size_t>(d.B) + 1));
     l.table = take(sizeof(int4) * static_cast<size_t>(delta_chunks(d)));
   }
   l.vec = take(items * 3 * C * sizeof(float));
@@ -982,6 +996,7 @@ void place(Args& a, const ttt_delta_desc& d, const Layout& l, void* ws, const vo
   a.kq = w + l.kq;
   a.base = reinterpret_cast<const int*>(w + l.base);
   a.table = reinterpret_cast<const int4*>(w + l.table);
+  a.order = reinterpret_cast<const int*>(w + l.order);
   if (saved) {
     const size_t items = static_cast<size_t>(a.chunks) * a.H;
     a.u = const_cast<char*>(static_cast<const char*>(saved));
@@ -994,7 +1009,7 @@ hipError_t plan(const ttt_delta_desc& d, const Layout& l, const int32_t* starts,
   KernelScope scope(TTT_KERNEL_DELTA_PLAN, s);
   delta::plan_kernel<<<1, delta::kPlanThreads, 0, s>>>(starts, d.B, d.T, chunk_tokens(d.dtype), static_cast<int>(delta_chunks(d)),
                                                        reinterpret_cast<int*>(w + l.edge), reinterpret_cast<int*>(w + l.base),
-                                                       reinterpret_cast<int4*>(w + l.table));
+                                                       reinterpret_cast<int4*>(w + l.table), reinterpret_cast<int*>(w + l.order));
   return hipGetLastError();
 }
 

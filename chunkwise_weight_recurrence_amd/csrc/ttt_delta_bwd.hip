@@ -193,7 +193,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
   __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.nseg * a.H) return;
-  const int h = chain % a.H, seq = chain / a.H;
+  const int h = chain % a.H, seq = walk_sequence(a, chain);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const Span span = span_of<C>(a, seq);
   constexpr bool HELP = WAVES == 2;

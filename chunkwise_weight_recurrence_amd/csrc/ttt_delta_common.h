@@ -38,6 +38,7 @@ struct Args {
   const float* seg_states;       // [B * nseg][H][dk][dv]: the states that enter them, where nseg > 1
   const int* base;               // packed: [B + 1] the sequences' first chunks
   const int4* table;             // packed: [chunks] first token, tokens, sequence
+  const int* order;              // packed: [B] the sequences, the longest first
   const void* q;
   const void* k;
   const void* v;
@@ -703,6 +704,9 @@ __device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, 
   }
   G = l;
 }
+
+// Workgroups start in their order, so the longest sequences' walks are put first.
+__device__ __forceinline__ int walk_sequence(const Args& a, int chain) { return a.packed ? a.order[chain / a.H] : chain / a.H; }
 
 // The waves of a walk's workgroup, and the workgroups that share a head's columns: four waves where that
 // leaves a workgroup for every CU, else two with helpers.  30011 packed tokens of 20 heads of 128 (740 heads of

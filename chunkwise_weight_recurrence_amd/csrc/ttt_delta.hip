@@ -298,8 +298,8 @@ __device__ __forceinline__ float* leaving(const Args& a, int seq, int h) {
 
 // The chain (waves 0 .. WAVES - 1) and its helpers (the next WAVES) where there are few heads.  First half of a
 // chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.  A chunk of 64 x 128
-// bf16 takes 1.9 us, which is the chain's own: 82 matrix instructions and about 400 vector instructions, one in 5.5
-// cycles from one wave.  64 chunks of 64 heads with what a backward needs 174 us, 208 without helpers.
+// bf16 takes 1.9 us (2.7 where every CU has one), which is the chain's own: 82 matrix instructions and about 400 vector instructions, one in 5.5
+// cycles from one wave.  64 chunks of 64 heads with what a backward needs 177 us, 208 without helpers.
 template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
@@ -451,8 +451,8 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
 // is added to it are products of two-term operands: its error does not grow with the length.  KEEP: what a
-// backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 334 us, 4.4 us a chunk of a workgroup: four
-// chains share LDS and the loads of 256 workgroups the memory.
+// backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 288 us, 3.8 us a chunk of a workgroup: four
+// chains share LDS, and the loads of 256 workgroups the memory.
 template <typename E, int DKP, int WAVES, bool KEEP>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false, WAVES>;
@@ -603,7 +603,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
 constexpr int kMapWaves = 4;
 
 // The maps: [piece][H][dkp][dvp + dkp], N before M.  The last piece's is not needed.  Seven of eight pieces of 131072
-// tokens, 16 heads of 128 bf16, 904 us; the whole walk after it 687, in one piece 4300.
+// tokens, 16 heads of 128 bf16, 958 us; the whole walk after it 727, in one piece 4300.
 template <typename E, int DKP>
 __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Args a, int groups, float* maps) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, WAVES = kMapWaves;

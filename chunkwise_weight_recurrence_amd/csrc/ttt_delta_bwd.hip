@@ -20,7 +20,7 @@ namespace {
 
 // The chain and its helpers where there are few heads, as in the forward.  First half of a chunk: K dS', and by
 // the helper P^T dO and scale Q^T e^G dO; second half: Y and the gradient of the state before.  64 chunks of 64 heads
-// of 128 bf16 188 us, 208 without helpers.
+// of 128 bf16 191 us, 208 without helpers.
 template <typename E, int DKP, int WAVES, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
@@ -437,7 +437,7 @@ template <typename E, int DKP> struct SlabLoader {
 // A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
 // dK summed in registers.  Of the triangular products a wave has a row tile of X or of M, of the others an
 // eighth of the key channels.  The value columns come 32 at a time.
-// Up to 128 bf16 channels two workgroups share a CU (128 registers, 80 KB): 4096 chunks and heads of 128 take 263 us
+// Up to 128 bf16 channels two workgroups share a CU (128 registers, 80 KB): 4096 chunks and heads of 128 take 267 us
 // so, 317 with one and all in registers.
 template <typename E, int DKP, bool SHARED>
 __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHARED ? 4 : 2) void grad_kernel(Args a) {

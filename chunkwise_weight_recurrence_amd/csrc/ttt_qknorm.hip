@@ -16,6 +16,7 @@
 
 #include "ttt_device.h"
 #include "ttt_internal.h"
+#include "ttt_qknorm_unit.h"
 
 namespace ttt {
 namespace {
@@ -77,25 +78,6 @@ template <> struct Piece<bf16_t, 1> {
   static __device__ __forceinline__ Raw put(const float* f) { return f32_to_bf16(f[0]); }
 };
 
-// Where a lane's unit u lies: pieces at a and b (d: none), their pairs from table entry t on.
-// HALF: pair (j, j + rot / 2); the columns behind rot, and interleaved pairs, are pieces side by side.
-template <int V, bool HALF> struct Unit {
-  int a, b, t;
-  bool turn;
-  __device__ __forceinline__ Unit(int u, int d, int rot) {
-    const int nr = HALF ? rot / 2 / V : 0;
-    turn = HALF ? u < nr : true;
-    if (HALF && u < nr) {
-      a = t = u * V;
-      b = a + rot / 2;
-    } else {
-      a = min(d, (HALF ? rot : 0) + (u - nr) * 2 * V);
-      b = min(d, a + V);
-      t = a / 2;
-    }
-  }
-};
-
 // The cosines and sines (times m) of `count` tokens, (d + 1) / 2 entries a token; (1, 0) behind rot / 2.
 __device__ __forceinline__ void fill_table(float2* table, const QkArgs& a, int64_t t0, int count) {
   const int entries = (a.d + 1) / 2;
@@ -115,30 +97,31 @@ __device__ __forceinline__ void fill_table(float2* table, const QkArgs& a, int64
   }
 }
 
-// One row's pieces of a lane, NV values each, turned (BACK: back).
+// One row's pieces of a lane, turned (BACK: back).  A pair that is not there is left alone: its entries would be
+// another token's, or words that nobody wrote, and an infinity or NaN of theirs would reach the row's sums.
 template <int V, bool HALF, bool BACK>
 __device__ __forceinline__ void turn(float (&x)[2][V], const float2* table, const Unit<V, HALF>& u) {
   if constexpr (HALF || V == 1) {
     // V == 1: a pair lies in the two pieces in either order of columns
-    if (u.turn) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v)
+      if (v < u.pairs) {
         const float2 cs = table[u.t + v];
         const float s = BACK ? -cs.y : cs.y, p = x[0][v], q = x[1][v];
         x[0][v] = p * cs.x - q * s;
         x[1][v] = p * s + q * cs.x;
       }
-    }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        const float2 cs = table[u.t + (h * V + v) / 2];
-        const float s = BACK ? -cs.y : cs.y, p = x[h][v], q = x[h][v + 1];
-        x[h][v] = p * cs.x - q * s;
-        x[h][v + 1] = p * s + q * cs.x;
-      }
+      for (int v = 0; v < V; v += 2)
+        if ((h * V + v) / 2 < u.pairs) {
+          const float2 cs = table[u.t + (h * V + v) / 2];
+          const float s = BACK ? -cs.y : cs.y, p = x[h][v], q = x[h][v + 1];
+          x[h][v] = p * cs.x - q * s;
+          x[h][v + 1] = p * s + q * cs.x;
+        }
   }
 }
 
@@ -234,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkArgs a) {
           v[n][0][j] *= r * w[pa + j];
           v[n][1][j] *= r * w[pb + j];
         }
-        if (u.a < a.d) turn<V, HALF, false>(v[n], table + t * entries, u);
+        turn<V, HALF, false>(v[n], table + t * entries, u);
         R::store(dst, u, a.d, v[n]);
       }
     }
@@ -276,7 +259,7 @@ __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkArgs a) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const Unit<V, HALF> u(lane + n * LANES, a.d, a.rot);
-          if (u.a < a.d) turn<V, HALF, true>(g[n], table + t * entries, u);
+          turn<V, HALF, true>(g[n], table + t * entries, u);
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll

@@ -4,9 +4,9 @@
 
 namespace ttt {
 
-// Where a lane's unit u lies: pieces of V columns at a and b (d: none), their pairs' table entries t .. t + pairs - 1.
-// HALF: pair (j, j + rot / 2); the columns behind rot, and interleaved pairs, are pieces side by side, and a row of an
-// odd number of pieces ends in a unit that has a piece at a only.
+// Where a lane's unit u lies: pieces of V columns at a and b (d: none), and its turned pairs' table entries
+// t .. t + pairs - 1.  HALF: pair (j, j + rot / 2); the columns behind rot, and interleaved pairs, are pieces side by
+// side, and a row of an odd number of pieces ends in a unit that has a piece at a only.
 template <int V, bool HALF> struct Unit {
   int a, b, t, pairs;
   __device__ __forceinline__ Unit(int u, int d, int rot) {
@@ -20,7 +20,8 @@ template <int V, bool HALF> struct Unit {
       a = a < d ? a : d;
       b = a + V < d ? a + V : d;
       t = a / 2;
-      pairs = HALF ? 0 : ((b + V < d ? b + V : d) - a) / 2;
+      const int left = HALF || rot / 2 < t ? 0 : rot / 2 - t;
+      pairs = left < V ? left : V;
     }
   }
 };

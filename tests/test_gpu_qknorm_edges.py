@@ -1,5 +1,5 @@
-"""GPU tests of the query and key norm at the ends of its rows: widths that are an odd number of 16-byte pieces, after
-other work has left NaN in LDS.  Tolerances are those of test_gpu_qknorm."""
+"""GPU tests of the query and key norm at the ends of its rows and its turned columns: widths that are an odd number of
+16-byte pieces, after other work has left NaN in LDS, and infinities where nothing is turned.  Tolerances are those of test_gpu_qknorm."""
 import pytest
 
 from chunkwise_weight_recurrence_amd import binding as B
@@ -37,3 +37,27 @@ def test_rows_that_end_in_half_a_unit(dtype, d, rot, norm):
         for m in outs[0]:
             assert torch.equal(outs[0][m], outs[1][m]), m
         _check(inp, outs[1], dtype, norm, "interleaved", 1e-6, 1.0)
+
+
+@pytest.mark.parametrize("dtype,d,rot", [("bf16", 64, 32), ("bf16", 64, 0), ("bf16", 40, 4), ("bf16", 70, 34), ("f32", 12, 2), ("f32", 33, 6)])
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+def test_columns_that_are_not_turned_do_not_meet(dtype, d, rot, pairing):
+    """An infinity or NaN behind the turned columns stays in its own, in both directions."""
+    import torch
+    inp = _make(d, 6, 2, 1, d, rot, dtype, True, False)
+    clean = _run(inp, dtype, "none", pairing, 1e-6, 1.0)
+    for bad in (float("inf"), float("nan")):
+        for c in sorted({rot, rot + 1, d - 2, d - 1}):
+            for x, m in (("q", "yq"), ("dyq", "dq")):
+                dirty = {**inp, x: inp[x].clone()}
+                dirty[x][3, 1, c] = bad
+                got = _run(dirty, dtype, "none", pairing, 1e-6, 1.0)[m]
+                assert not torch.isfinite(got[3, 1, c]) and torch.isnan(got[3, 1, c]).item() == (bad != bad), (m, bad, c)
+                want = clean[m].clone()
+                want[3, 1, c] = got[3, 1, c] = 0
+                assert (got == want).all(), (m, bad, c)
+    # a row with an infinity has the norm's factor 0: the other columns are zero
+    dirty = {**inp, "q": inp["q"].clone()}
+    dirty["q"][3, 1, d - 1] = float("inf")
+    y = _run(dirty, dtype, "rms", pairing, 1e-6, 1.0)["yq"][3, 1]
+    assert torch.isnan(y[d - 1]) and (y[:d - 1] == 0).all()

@@ -30,7 +30,7 @@ template <int V, bool HALF> void check(int d, int rot) {
       // the columns that the kernel turns by entry t + p: of one piece each, or neighbours in piece 2 p / V
       int first = HALF ? x.a + p : x.a + 2 * p, second = HALF ? x.b + p : x.a + 2 * p + 1;
       const int j = x.t + p;
-      ok = ok && j >= 0 && j < (d + 1) / 2 && second < d && ++of_pair[j] == 1;
+      ok = ok && j >= 0 && j < rot / 2 && second < d && ++of_pair[j] == 1;  // no column behind rot is turned
       ok = ok && first == (HALF ? j : 2 * j) && second == (HALF ? j + rot / 2 : 2 * j + 1);
     }
     if (!ok) { std::printf("V %d half %d d %d rot %d unit %d\n", V, HALF, d, rot, u); std::exit(1); }

@@ -271,14 +271,15 @@ __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkArgs a) {
         }
         dot = slot_sum<LANES>(dot);
         if (a.norm == TTT_HEADNORM_RMS) dot /= a.d;
-        if (a.norm == TTT_HEADNORM_NONE) dot = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const Unit<V, HALF> u(lane + n * LANES, a.d, a.rot);
+          if (a.norm != TTT_HEADNORM_NONE) {  // without a norm dx is dh, whatever x is
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2)
+            for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-            for (int j = 0; j < V; ++j) g[n][h2][j] = r * (g[n][h2][j] - v[n][h2][j] * dot);
+              for (int j = 0; j < V; ++j) g[n][h2][j] = r * (g[n][h2][j] - v[n][h2][j] * dot);
+          }
           R::store(dx + at, u, a.d, g[n]);
         }
       }

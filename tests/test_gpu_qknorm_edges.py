@@ -61,3 +61,14 @@ def test_columns_that_are_not_turned_do_not_meet(dtype, d, rot, pairing):
     dirty["q"][3, 1, d - 1] = float("inf")
     y = _run(dirty, dtype, "rms", pairing, 1e-6, 1.0)["yq"][3, 1]
     assert torch.isnan(y[d - 1]) and (y[:d - 1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,d,rot", [("bf16", 64, 32), ("bf16", 70, 34), ("f32", 64, 64), ("f32", 33, 6)])
+def test_without_a_norm_the_gradient_does_not_know_the_values(dtype, d, rot):
+    import torch
+    inp = _make(d, 6, 2, 1, d, rot, dtype, True, False)
+    clean = _run(inp, dtype, "none", "half", 1e-6, 1.0)
+    for bad in (float("inf"), float("nan")):
+        dirty = {**inp, "q": inp["q"].clone()}
+        dirty["q"][3, 1, 2] = dirty["q"][4, 0, d - 1] = bad
+        assert (_run(dirty, dtype, "none", "half", 1e-6, 1.0)["dq"] == clean["dq"]).all(), bad

@@ -349,6 +349,8 @@ class DeltaBuffers:
         H, dv = v.shape[-2:]
         Bn, T = (seq_starts.numel() - 1, q.shape[0]) if packed else q.shape[:2]
         f32, d = torch.float32, q.device
+        self._state_shape = (Bn, H, dk, dv)
+        self._check_state("s0", s0)
         self.q, self.k, self.v, self.gate, self.beta, self.s0, self.seq_starts = q, k, v, gate, beta, s0, seq_starts
         self.desc = B.make_delta_desc(Bn, T, H, dk, dv, Hk=Hk, dtype="bf16" if q.dtype == torch.bfloat16 else "f32", gate=kind,
                                       packed=packed, scale=scale, lr_max=lr_max, lr_bias=lr_bias, ldq=_token_distance(q),
@@ -367,12 +369,17 @@ class DeltaBuffers:
             self.ds0 = torch.empty((Bn, H, dk, dv), dtype=f32, device=d)
         self.ws = torch.empty(max(size, 1), dtype=torch.uint8, device=d)
 
+    def _check_state(self, name, x):
+        if x is not None and x.shape != self._state_shape:
+            raise ValueError(f"{name} must have shape {self._state_shape} (got {tuple(x.shape)})")
+
     def forward(self, stream=None):
         B.ttt_delta_fwd(self.desc, self.q, self.k, self.v, self.gate, self.beta, self.s0, self.seq_starts, self.o, self.s_final,
                         self.saved, self.ws, stream=stream)
 
     def backward(self, d_o, d_sfinal=None, stream=None):
         """Fills dq, dk, dv, dgate and dbeta (with the strides of q, k, v, gate and beta) and ds0."""
+        self._check_state("d_sfinal", d_sfinal)
         B.ttt_delta_bwd(self.desc, self.q, self.k, self.v, self.gate, self.beta, self.seq_starts, self.saved, d_o, d_sfinal,
                         self.dq, self.dk, self.dv, self.dgate, self.dbeta, self.ds0, self.ws, stream=stream)
 

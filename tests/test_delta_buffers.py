@@ -1,0 +1,23 @@
+"""Which states and weights the delta rule's and the query and key norm's buffers take (CPU: nothing is launched)."""
+import pytest
+import torch
+
+from chunkwise_weight_recurrence_amd.layer import DeltaBuffers
+
+
+def _z(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_delta_states_have_the_rule_s_shape(packed):
+    lead, st = ((10,), torch.tensor([0, 4, 10], dtype=torch.int32)) if packed else ((2, 5), None)
+    args = (_z(*lead, 2, 8), _z(*lead, 2, 8), _z(*lead, 4, 16), None, _z(*lead, 4))
+    f32 = dict(dtype=torch.float32)
+    DeltaBuffers(*args, s0=_z(2, 4, 8, 16, **f32), seq_starts=st)
+    # as many elements, or more, with the keys' and values' channels, the heads or the sequences elsewhere
+    for shape in ((2, 4, 16, 8), (4, 2, 8, 16), (3, 4, 8, 16), (2, 4, 128), (1, 4, 8, 16)):
+        with pytest.raises(ValueError, match="s0 must have shape"):
+            DeltaBuffers(*args, s0=_z(*shape, **f32), seq_starts=st)
+        with pytest.raises(ValueError, match="d_sfinal must have shape"):
+            DeltaBuffers(*args, seq_starts=st, with_bwd=True).backward(_z(*lead, 4, 16), _z(*shape, **f32))

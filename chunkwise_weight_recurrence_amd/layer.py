@@ -395,6 +395,11 @@ class QkNormBuffers:
         torch = _torch()
         if q.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
             raise ValueError(f"q and k must be [..,Hq,d] and [..,Hk,d] (got shapes {tuple(q.shape)}, {tuple(k.shape)})")
+        for name, w in (("wq", wq), ("wk", wk)):
+            if w is not None and w.shape != q.shape[-1:]:
+                raise ValueError(f"{name} must have shape {tuple(q.shape[-1:])} (got {tuple(w.shape)})")
+        if positions is not None and positions.numel() != math.prod(q.shape[:-2]):
+            raise ValueError(f"positions must be one a token (got shape {tuple(positions.shape)} for {math.prod(q.shape[:-2])})")
         f32, d = torch.float32, q.device
         self.q, self.k, self.wq, self.wk, self.positions, self.inv_freq = q, k, wq, wk, positions, inv_freq
         rot = 0 if inv_freq is None else 2 * inv_freq.numel()

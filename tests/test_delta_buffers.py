@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from chunkwise_weight_recurrence_amd.layer import DeltaBuffers
+from chunkwise_weight_recurrence_amd.layer import DeltaBuffers, QkNormBuffers
 
 
 def _z(*shape, dtype=torch.bfloat16):
@@ -21,3 +21,22 @@ def test_delta_states_have_the_rule_s_shape(packed):
             DeltaBuffers(*args, s0=_z(*shape, **f32), seq_starts=st)
         with pytest.raises(ValueError, match="d_sfinal must have shape"):
             DeltaBuffers(*args, seq_starts=st, with_bwd=True).backward(_z(*lead, 4, 16), _z(*shape, **f32))
+
+
+def test_query_and_key_weights_have_a_head_s_columns():
+    """A weight per head, [H,d], has enough elements too: its first head's would be taken for all."""
+    q, k = _z(2, 5, 4, 16), _z(2, 5, 2, 16)
+    w = lambda *s: _z(*s, dtype=torch.float32)  # noqa: E731
+    QkNormBuffers(q, k, w(16), w(16), with_bwd=True)
+    for shape in ((4, 16), (17,), (1, 16), (64,)):
+        with pytest.raises(ValueError, match="wq must have shape"):
+            QkNormBuffers(q, k, wq=w(*shape))
+        with pytest.raises(ValueError, match="wk must have shape"):
+            QkNormBuffers(q, k, wk=w(*shape))
+    # and one position a token
+    pos = lambda *s: _z(*s, dtype=torch.int32)  # noqa: E731
+    for ok in (pos(10), pos(2, 5)):
+        QkNormBuffers(q, k, positions=ok)
+    for bad in (pos(5), pos(11), pos(2, 10)):
+        with pytest.raises(ValueError, match="positions must be"):
+            QkNormBuffers(q, k, positions=bad)

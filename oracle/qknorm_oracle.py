@@ -29,10 +29,13 @@ def turn(x, pos, freq, pairing, scale=1.0, back=False):
 
 
 def _hat(x, norm, eps):
+    """x / size and 1 / size; a row of zeros is 0 / 0 where eps is zero."""
     ss = (x * x).sum(-1, keepdims=True)
-    r = {"none": np.ones_like(ss), "rms": 1.0 / np.sqrt(ss / x.shape[-1] + eps), "l2": 1.0 / np.sqrt(ss + eps)}[norm] \
-        if eps > 0 or ss.all() else np.ones_like(ss)
-    return x * r, r
+    if norm == "none":
+        return x, np.ones_like(ss)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        r = 1.0 / np.sqrt((ss / x.shape[-1] if norm == "rms" else ss) + eps)
+        return x * r, r
 
 
 def forward(x, w, pos, freq, norm, pairing, eps=1e-6, scale=1.0):

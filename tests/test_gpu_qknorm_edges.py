@@ -72,3 +72,23 @@ def test_without_a_norm_the_gradient_does_not_know_the_values(dtype, d, rot):
         dirty = {**inp, "q": inp["q"].clone()}
         dirty["q"][3, 1, 2] = dirty["q"][4, 0, d - 1] = bad
         assert (_run(dirty, dtype, "none", "half", 1e-6, 1.0)["dq"] == clean["dq"]).all(), bad
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_a_row_of_zeros_without_eps(norm):
+    """0 / 0 in its own row; the others as the oracle has them."""
+    import torch
+    inp = _make(2, 9, 3, 2, 64, 32, "f32", False, False)
+    keep = torch.ones(9, 3, dtype=torch.bool)
+    keep[4, 1] = False
+    inp["q"][4, 1] = 0
+    out = _run(inp, "f32", norm, "half", 0.0, 1.0)
+    assert torch.isnan(out["yq"][4, 1]).all() and torch.isnan(out["dq"][4, 1]).all() and torch.isnan(out["dwq"]).all()
+    # the same rows without that one
+    rest = {**inp, "q": inp["q"][keep][:, None], "dyq": inp["dyq"][keep][:, None], "k": torch.ones(26, 1, 64), "dyk": torch.ones(26, 1, 64),
+            "pos": inp["pos"][:, None].expand(9, 3)[keep].contiguous()}
+    got = dict(yq=out["yq"].cpu()[keep], dq=out["dq"].cpu()[keep])
+    alone = _run(rest, "f32", norm, "half", 0.0, 1.0)
+    _check(rest, alone, "f32", norm, "half", 0.0, 1.0)
+    for m in got:
+        assert torch.equal(got[m], alone[m].cpu()[:, 0]), m

@@ -348,15 +348,16 @@ template <typename F> hipError_t dispatch(const ttt_qknorm_desc& d, bool w, F&& 
   };
   using std::integral_constant;
   auto lanes = [&](auto e, auto v) {
-    // rotated units and the others are counted apart: each may end in half a unit
+    // the halves' units and the others are counted apart: these may end in half a unit
     const int V = v, nr = d.pairing == TTT_ROPE_HALF ? d.rot / 2 / V : 0;
     const int units = nr + (d.d - 2 * nr * V + 2 * V - 1) / (2 * V);
     if constexpr (v() > 1) {
       if (units <= 4) return with(e, v, integral_constant<int, 4>{}, integral_constant<int, 1>{});
       if (units <= 8) return with(e, v, integral_constant<int, 8>{}, integral_constant<int, 1>{});
       if (units <= 16) return with(e, v, integral_constant<int, 16>{}, integral_constant<int, 1>{});
-      if (units <= 32) return with(e, v, integral_constant<int, 32>{}, integral_constant<int, 1>{});
-      return with(e, v, integral_constant<int, 64>{}, integral_constant<int, 1>{});
+      // 512 columns are 32 units of 16
+      if (v() == 8 || units <= 32) return with(e, v, integral_constant<int, 32>{}, integral_constant<int, 1>{});
+      if constexpr (v() < 8) return with(e, v, integral_constant<int, 64>{}, integral_constant<int, 1>{});
     } else {
       if (units <= 64) return with(e, v, integral_constant<int, 64>{}, integral_constant<int, 1>{});
       return with(e, v, integral_constant<int, 64>{}, integral_constant<int, 4>{});

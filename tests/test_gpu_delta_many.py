@@ -1,11 +1,12 @@
 """GPU tests of the gated delta rule where many heads' walks fill the chip (four chain waves a workgroup, chunks in turn
-through two LDS buffers), against the fp64 token loop.  Tolerances are those of test_gpu_delta."""
+through two LDS buffers), and where few heads' long sequences are walked in pieces, against the fp64 token loop.
+Tolerances are those of test_gpu_delta."""
 import numpy as np
 import pytest
 
 from chunkwise_weight_recurrence_amd import binding as B
 from tests.block_utils import f64
-from tests.test_gpu_delta import _check, _make, _oracle, _train
+from tests.test_gpu_delta import CHUNK_TOL, _check, _make, _oracle, _train
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,26 @@ def test_many_heads(dtype, packed):
                     assert np.array_equal(f64(part[m]), f64(first[m])), (m, r)
                 for m, k in (("o", n), ("s_final", 5)):
                     assert np.array_equal(f64(alone[m][r * k:(r + 1) * k]), f64(first_alone[m][:k])), (m, r)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,dk,dv,chunks,tail", [(1, 256, 32, 60, 5), (1, 200, 96, 64, 9), (3, 64, 64, 48, 0), (1, 128, 128, 72, 31)])
+def test_pieces_are_walked_and_joined(dtype, H, dk, dv, chunks, tail):
+    """Slow decays, so that what enters a piece still counts when it leaves.  A token keeps e^-0.0025 on average, a chunk
+    0.86 (bf16) or 0.92: a state's error a chunk, CHUNK_TOL in bf16 and three sums of 128 terms in fp32, adds up to 7 or
+    13 of it, once more for the maps, and twice that for sums of 256 terms.  bf16 outputs and gradients as elsewhere."""
+    C = 64 if dtype == "bf16" else 32
+    T = chunks * C + tail
+    inp = _make(chunks, T, 1, H, 1, dk, dv, dtype, "log")
+    inp["gate"] = inp["gate"] * (1.0 / 64)   # the mean of |N(3, 1.5)| is 3.05: 3.05 x 0.05 / 64 a token
+    inp["s0"] *= 0.3
+    B.ttt_timing_enable(True)
+    try:
+        out = _train(inp, "log", dtype, B_=1, T=T)
+        launches = B.ttt_timing_read(B.Kernel.DELTA_MAP)[1]
+    finally:
+        B.ttt_timing_enable(False)
+    assert launches > 0, "the forward was not walked in pieces"
+    state_tol = 2 * 2 * 7 * CHUNK_TOL if dtype == "bf16" else 2 * 2 * 13 * 3 * 128 * 2.0 ** -24
+    _check(out, _oracle(inp, [0, T], "log", dk ** -0.5), dtype, state_tol=state_tol, tol=state_tol if dtype == "f32" else None,
+           what=f"{dtype} pieces {H} x {dk} x {dv}")

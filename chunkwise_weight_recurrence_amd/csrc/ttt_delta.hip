@@ -106,8 +106,8 @@ template <int LD> __device__ __forceinline__ f32x4_t block_col(const float* m, i
   return f;
 }
 
-// A [C][C] fp32 matrix in operand order; TRANS: its transpose.  TERMS: 2 writes hi and lo for bf16.
-template <typename E, int LD, bool TRANS, int TERMS>
+// A [C][C] fp32 matrix in operand order, hi and lo for bf16; TRANS: its transpose.
+template <typename E, int LD, bool TRANS>
 __device__ __forceinline__ void tri_store(const float* m, char* dst) {
   using T = Tri<E>;
   constexpr int kThreads = kPrepThreads;
@@ -131,7 +131,7 @@ __device__ __forceinline__ void tri_store(const float* m, char* dst) {
     } else {
       const Split<bf16_t> s(x[0], x[1]);
       *reinterpret_cast<bf16x8_t*>(dst + place * T::kFragBytes + lane * 16) = s.hi;
-      if (TERMS == 2) *reinterpret_cast<bf16x8_t*>(dst + T::kHalfBytes + place * T::kFragBytes + lane * 16) = s.lo;
+      *reinterpret_cast<bf16x8_t*>(dst + T::kHalfBytes + place * T::kFragBytes + lane * 16) = s.lo;
     }
   }
 }
@@ -171,7 +171,8 @@ template <int C, int LD> __device__ __forceinline__ void invert(const float* A, 
 }
 
 // A chunk and head a workgroup: its gates' sums, K K^T and Q K^T (row tile w by wave w), the inverse.
-// BWD writes the transposes, the scores in two terms.  It is bound by the latency of its stages, so LDS is
+// BWD writes the transposes.  Both in two terms: with the scores in one, O was 2.2e-3 off and not a rounding's 1.66e-3
+// (the walk of 30011 packed tokens of 20 heads takes 5 % longer so).  It is bound by the latency of its stages, so LDS is
 // used over and over: 36 KB let four workgroups share a CU.  4096 chunks and heads of 128 bf16 59 us (93 with 53 KB,
 // three workgroups and the loads behind the gates' sums).
 template <typename E, int DKP, bool BWD>
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
   }
   __syncthreads();
   invert<C, LD>(A, T);
-  tri_store<E, LD, BWD, 2>(T, a.t + item * Tri<E>::kBytes);
+  tri_store<E, LD, BWD>(T, a.t + item * Tri<E>::kBytes);
   if (mt < NT) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
       for (int r = 0; r < 4; ++r) A[(16 * mt + 4 * g + r) * LD + 16 * nt + i] = qk[nt][r];
   }
   __syncthreads();
-  tri_store<E, LD, BWD, BWD ? 2 : 1>(A, a.p + item * Tri<E>::kBytes);
+  tri_store<E, LD, BWD>(A, a.p + item * Tri<E>::kBytes);
 }
 
 // ---- forward walk ----
@@ -338,9 +339,9 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
         mma_all(o, rows[kp & 1], s[kp & 1]);
         in_order();
       }
-      Raw scores[TR::kFrags];
+      Split<E> scores[TR::kFrags];
 #pragma unroll
-      for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load<E>(w.P, f);
+      for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
 #pragma unroll
       for (int mt = 0; mt < NT; ++mt) o[mt] *= *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g) * a.scale;
       __syncthreads();
@@ -455,11 +456,11 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 // chains share LDS, and the loads of 256 workgroups the memory.
 template <typename E, int DKP, int WAVES, bool KEEP>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, false, WAVES>;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
   __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
@@ -489,7 +490,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
   __syncthreads();
   for (int chunk = span.first; chunk < span.end; ++chunk) {
-    const WalkTile<E, DKP, false, WAVES>& w = tiles[(chunk - span.first) & (kBuf - 1)];
+    const WalkTile<E, DKP, WAVES>& w = tiles[(chunk - span.first) & (kBuf - 1)];
     OutTile<E, WAVES>& out = outs[(chunk - span.first) & (kBuf - 1)];
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
     // K S and Q S: rows of the next 32 channels are read, and their part of the state split, while these are multiplied
@@ -561,7 +562,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     for (int mt = 0; mt < NT; ++mt) o[mt] = ko[NT + mt] * (a.scale * gm[mt]);
     in_order();
     // S = e^{G_C} S + K^T (e^{G_C - G} U);  O += P U
-    Raw scores[TR::kFrags];
+    Split<E> scores[TR::kFrags];
     const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
     Split<E> us[NP];
     Split<E> x(u[0] * rest[0], u[1] * rest[1]);
@@ -571,7 +572,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
         read_cols(kp + 1);
       } else {
 #pragma unroll
-        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load<E>(w.P, f);
+        for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
       }
       in_order();
       mma_all(S, cols[kp & 1], x);
@@ -607,10 +608,10 @@ constexpr int kMapWaves = 4;
 template <typename E, int DKP>
 __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Args a, int groups, float* maps) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, WAVES = kMapWaves;
-  constexpr int kBuf = kWalkBuffers<E, DKP, false, WAVES>;
+  constexpr int kBuf = kWalkBuffers<E, DKP, WAVES>;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, false, WAVES> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, WAVES> tiles[kBuf];
   const int grp = walk_group(groups), chain = walk_chain(groups);
   if (chain >= a.B * a.nseg * a.H) return;
   const int h = chain % a.H, seq = walk_sequence(a, chain);

@@ -184,11 +184,11 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
 // The walk from the last chunk back, in the forward's way.
 template <typename E, int DKP, int WAVES>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, int groups) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, true, WAVES>;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
-  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, true, WAVES> tiles[kBuf];
+  __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, WAVES> tiles[kBuf];
   __shared__ __attribute__((aligned(16))) OutTile<E, WAVES> outs[kBuf];
   __shared__ __attribute__((aligned(16))) std::conditional_t<WAVES == 2, Exchange<E, DKP, WAVES>, NoExchange> exchange;
   const int grp = walk_group(groups), chain = walk_chain(groups);
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
   const int last = span.end - 1;
   __syncthreads();
   for (int chunk = last; chunk >= span.first; --chunk) {
-    const WalkTile<E, DKP, true, WAVES>& w = tiles[(last - chunk) & (kBuf - 1)];
+    const WalkTile<E, DKP, WAVES>& w = tiles[(last - chunk) & (kBuf - 1)];
     OutTile<E, WAVES>& out = outs[(last - chunk) & (kBuf - 1)];
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
     // e^{G_C - G} K dS'

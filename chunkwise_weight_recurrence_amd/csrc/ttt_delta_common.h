@@ -293,13 +293,12 @@ template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* 
 constexpr int kLoaders = 4, kLoadThreads = kLoaders * 64;
 
 // A walk's LDS for one chunk.
-template <typename E, int DKP, bool BWD, int WAVES> struct WalkTile {
+template <typename E, int DKP, int WAVES> struct WalkTile {
   static constexpr int C = Chunk<E>::C;
-  static constexpr int kPBytes = BWD ? Tri<E>::kBytes : Tri<E>::kHalfBytes;  // the backward's scores have two terms
   E K[C * Tile<E, DKP>::kRow];
   E Q[C * Tile<E, DKP>::kRow];
   char T[Tri<E>::kBytes];
-  char P[kPBytes];
+  char P[Tri<E>::kBytes];
   float vec[3 * C];
   E V[C * 16 * WAVES];  // [token][column]: v, or the gradient of o
 };
@@ -331,8 +330,8 @@ __device__ __forceinline__ void give(char* p, int n, f32x4_t x) { reinterpret_ca
 __device__ __forceinline__ f32x4_t take(const char* p, int n) { return reinterpret_cast<const f32x4_t*>(p)[n * 64 + (threadIdx.x & 63)]; }
 
 // Two chunks where they fit the 160 KB, so that one is filled while the other is read.
-template <typename E, int DKP, bool BWD, int WAVES>
-constexpr int kWalkBuffers = 2 * (sizeof(WalkTile<E, DKP, BWD, WAVES>) + sizeof(OutTile<E, WAVES>)) <= 160 * 1024 ? 2 : 1;
+template <typename E, int DKP, int WAVES>
+constexpr int kWalkBuffers = 2 * (sizeof(WalkTile<E, DKP, WAVES>) + sizeof(OutTile<E, WAVES>)) <= 160 * 1024 ? 2 : 1;
 constexpr int walk_waves(int waves) { return waves + (waves == 2 ? 2 : 0) + kLoaders; }  // of a workgroup
 
 // A buffer resource over `bytes` bytes from p on (both the same for the wave): a load past them reads zero and
@@ -375,13 +374,13 @@ __device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ld, int cols, in
 }
 
 // The loaders' part: the next chunk's pieces in registers.
-template <typename E, int DKP, bool BWD, int WAVES, bool WIDE, bool LEAN = false> struct Loader {  // LEAN: no queries, no scores
-  using W = WalkTile<E, DKP, BWD, WAVES>;
+template <typename E, int DKP, int WAVES, bool WIDE, bool LEAN = false> struct Loader {  // LEAN: no queries, no scores
+  using W = WalkTile<E, DKP, WAVES>;
   static constexpr int C = W::C, V = 16 / sizeof(E), kPieces = DKP / V, kStep = kLoadThreads / kPieces, kRows = C / kStep;
-  static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads, kP = (W::kPBytes / 16 + kLoadThreads - 1) / kLoadThreads;
+  static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads;
   static constexpr int kCols = 16 * WAVES, kVPieces = kCols / V, kVStep = kLoadThreads / kVPieces, kVRows = C / kVStep;
   static_assert(kLoadThreads % kPieces == 0 && C % kStep == 0 && 3 * C / 4 <= kLoadThreads && C % kVStep == 0);
-  uint4 k[kRows], q[kRows], t[kT], p[kP], vec, v[kVRows];
+  uint4 k[kRows], q[kRows], t[kT], p[kT], vec, v[kVRows];
   int tid, row, col, vrow, vcol;  // of a thread's first pieces
 
   __device__ __forceinline__ Loader(int tid_)
@@ -421,7 +420,7 @@ template <typename E, int DKP, bool BWD, int WAVES, bool WIDE, bool LEAN = false
 #pragma unroll
     for (int n = 0; n < kT; ++n) t[n] = tp[piece(n, Tri<E>::kBytes / 16)];
 #pragma unroll
-    for (int n = 0; n < (LEAN ? 0 : kP); ++n) p[n] = pp[piece(n, W::kPBytes / 16)];
+    for (int n = 0; n < (LEAN ? 0 : kT); ++n) p[n] = pp[piece(n, Tri<E>::kBytes / 16)];
     vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
     const int vcols = a.dv - c0;  // may be none
     const Buffer vb(cp, vcols > 0 ? rows_bytes(len, ldc, vcols, sizeof(E)) : 0);
@@ -450,7 +449,7 @@ template <typename E, int DKP, bool BWD, int WAVES, bool WIDE, bool LEAN = false
 #pragma unroll
     for (int n = 0; n < kT; ++n) reinterpret_cast<uint4*>(w.T)[piece(n, Tri<E>::kBytes / 16)] = t[n];
 #pragma unroll
-    for (int n = 0; n < (LEAN ? 0 : kP); ++n) reinterpret_cast<uint4*>(w.P)[piece(n, W::kPBytes / 16)] = p[n];
+    for (int n = 0; n < (LEAN ? 0 : kT); ++n) reinterpret_cast<uint4*>(w.P)[piece(n, Tri<E>::kBytes / 16)] = p[n];
     reinterpret_cast<uint4*>(w.vec)[piece(0, 3 * C / 4)] = vec;
 #pragma unroll
     for (int n = 0; n < kVRows; ++n) *reinterpret_cast<uint4*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
@@ -500,7 +499,7 @@ template <typename E, int DKP, bool BWD, int WAVES, int BUF, bool MID, bool WIDE
 __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, int c0, Tiles& tiles, Outs& outs, const E* in, int64_t ld_in,
                                           E* out, int64_t ld_out) {
   constexpr int C = Chunk<E>::C;
-  using L = Loader<E, DKP, BWD, WAVES, WIDE, LEAN>;
+  using L = Loader<E, DKP, WAVES, WIDE, LEAN>;
   const int tid = threadIdx.x - static_cast<int>(blockDim.x - kLoadThreads);
   L even(tid), odd(tid);  // the chunks' pieces on their way, in turn
   const int count = span.end - span.first;

@@ -1,0 +1,39 @@
+"""GPU tests of how exact the gated delta rule is in bf16: beside the rounding of an output there is what fp32 loses.
+
+Errors are 2-norms over that of the fp64 result.  An output may be off by what the fp64 result is off when it is rounded
+once (2^-8 of a value at most), and by what operands of two bf16 terms lose: 2^-17 of an operand, of at most four on
+the way, in sums whose terms' magnitudes are together at most four times the result's: 2^-13."""
+import numpy as np
+import pytest
+
+from tests.block_utils import f64
+from tests.test_gpu_delta import _make, _oracle, _train
+
+pytestmark = pytest.mark.gpu
+
+# sequences, tokens, heads, key heads, dk, dv: one chunk and many, narrow and wide, walks of two waves and of four
+SHAPES = [(2, 7, 3, 3, 64, 64), (1, 64, 4, 4, 128, 128), (2, 300, 2, 1, 64, 64), (1, 300, 2, 2, 128, 96), (3, 200, 2, 2, 16, 16),
+          (70, 130, 4, 2, 32, 64), (1, 150, 2, 2, 256, 64), (1, 2700, 1, 1, 64, 64)]
+
+
+def _norm(x):
+    return float(np.linalg.norm(x))
+
+
+def _once(ref):
+    """What rounding the fp64 result to bf16 loses."""
+    import torch
+    return _norm(f64(torch.from_numpy(ref.astype(np.float32)).to(torch.bfloat16)) - ref) / _norm(ref)
+
+
+@pytest.mark.parametrize("j", range(len(SHAPES)))
+def test_bf16_outputs_are_rounded_once(j):
+    Bn, T, H, Hk, dk, dv = SHAPES[j]
+    kind = ["sigmoid", "log"][j % 2]
+    inp = _make(200 + j, Bn * T, Bn, H, Hk, dk, dv, "bf16", kind)
+    inp["s0"] *= 0.3
+    inp["d_sf"] *= 0.3
+    out, want = _train(inp, kind, "bf16", B_=Bn, T=T), _oracle(inp, list(range(0, Bn * T + 1, T)), kind, dk ** -0.5)
+    errs = {m: (_norm(f64(out[m]) - want[m]) / _norm(want[m]), _once(want[m])) for m in ("o",)}
+    print(f"[delta] {SHAPES[j]} " + " ".join(f"{m}={e:.2e}/{r:.2e}" for m, (e, r) in errs.items()), flush=True)
+    assert all(e <= r + 2.0 ** -13 for e, r in errs.values()), errs

@@ -304,7 +304,7 @@ __device__ __forceinline__ float* leaving(const Args& a, int seq, int h) {
 template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kMma = sizeof(E) == 2 ? 1 : 4;
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -419,7 +419,7 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
     in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
+      const Whole<E> rhs(ks[2 * kp], ks[2 * kp + 1]);
       tri_mul<E>(u, tri, rhs, kp);
     }
 #pragma unroll
@@ -428,15 +428,15 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) give(us, kp, Split<E>(u[2 * kp], u[2 * kp + 1]));
     __syncthreads();
-    Split<E> x(u[0] * rest[0], u[1] * rest[1]);
+    Whole<E> x(u[0] * rest[0], u[1] * rest[1]);
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       if (kp + 1 < NP) read_cols(kp + 1);
       in_order();
       mma_all(S, cols[kp & 1], x);
       if (kp + 1 < NP) {
-        x = Split<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
-        interleave<2 * ND * kMma, 2>();
+        x = Whole<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
+        interleave<kWhole<E> * ND, 2>();
       }
       in_order();
     }
@@ -451,7 +451,7 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 }
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
-// is added to it are products of two-term operands: its error does not grow with the length.  KEEP: what a
+// is added to it are products of operands of two and three terms: its error does not grow with the length.  KEEP: what a
 // backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 288 us, 3.8 us a chunk of a workgroup: four
 // chains share LDS, and the loads of 256 workgroups the memory.
 template <typename E, int DKP, int WAVES, bool KEEP>
@@ -552,9 +552,8 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     // the products with T leave room for what the next stages need
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> rhs(ko[2 * kp], ko[2 * kp + 1]);
-#pragma unroll
-      for (int mt = 2 * kp; mt < NT; ++mt) u[mt] = mma(tri[TR::at(mt, kp)], rhs, u[mt]);
+      const Whole<E> rhs(ko[2 * kp], ko[2 * kp + 1]);
+      tri_mul<E>(u, tri, rhs, kp);
     }
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
@@ -565,7 +564,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     Split<E> scores[TR::kFrags];
     const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
     Split<E> us[NP];
-    Split<E> x(u[0] * rest[0], u[1] * rest[1]);
+    Whole<E> x(u[0] * rest[0], u[1] * rest[1]);
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
       if (kp + 1 < NP) {
@@ -577,8 +576,8 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
       in_order();
       mma_all(S, cols[kp & 1], x);
       us[kp] = Split<E>(u[2 * kp], u[2 * kp + 1]);
-      if (kp + 1 < NP) x = Split<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
-      interleave<2 * ND * kMma, 3>();
+      if (kp + 1 < NP) x = Whole<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
+      interleave<kWhole<E> * ND, 3>();
       in_order();
     }
 #pragma unroll
@@ -677,13 +676,13 @@ __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Arg
     read_cols(0);
     in_order();
 #pragma unroll
-    for (int kp = 0; kp < NP; ++kp) tri_mul<E>(u, tri, Split<E>(ks[2 * kp], ks[2 * kp + 1]), kp);
+    for (int kp = 0; kp < NP; ++kp) tri_mul<E>(u, tri, Whole<E>(ks[2 * kp], ks[2 * kp + 1]), kp);
 #pragma unroll
     for (int t = 0; t < ND; ++t) S[t] *= decay;
     in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> x(u[2 * kp] * rest[2 * kp], u[2 * kp + 1] * rest[2 * kp + 1]);
+      const Whole<E> x(u[2 * kp] * rest[2 * kp], u[2 * kp + 1] * rest[2 * kp + 1]);
       mma_all(S, cols, x);
       if (kp + 1 < NP) read_cols(kp + 1);
     }
@@ -731,8 +730,7 @@ __global__ __launch_bounds__(DKP * 4) void join_kernel(Args a, const float* maps
     for (int r = 0; r < 4; ++r) c[r] = m[static_cast<int64_t>(16 * wave + 4 * g + r) * width + col];
     __syncthreads();
 #pragma unroll
-    for (int kp = 0; kp < NK; ++kp)
-      c = mma(Split<E>(row[2 * kp], row[2 * kp + 1]), Split<E>(S[2 * kp][lane], S[2 * kp + 1][lane]), c);
+    for (int kp = 0; kp < 2 * NK; ++kp) c = mfma16(row[kp], S[kp][lane], c);
     __syncthreads();
     x = c;
   }

@@ -64,7 +64,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
       for (int mt = 0; mt < NT; ++mt) go[mt] *= gm[mt] * a.scale;
 #pragma unroll
       for (int t = 0; t < ND; ++t) qg[t] = zero4();
-      Split<E> s(go[0], go[1]);
+      Whole<E> s(go[0], go[1]);
       in_order();
 #pragma unroll
       for (int mt = 0; mt < NT; ++mt) give(from_p, mt, x[mt]);
@@ -73,7 +73,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
         if (n + 1 < NP) read_cols(n + 1);
         in_order();
         mma_all(qg, cols[n & 1], s);
-        if (n + 1 < NP) s = Split<E>(go[2 * n + 2], go[2 * n + 3]);
+        if (n + 1 < NP) s = Whole<E>(go[2 * n + 2], go[2 * n + 3]);
         in_order();
       }
 #pragma unroll
@@ -148,7 +148,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
     in_order();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> e(du[2 * kp], du[2 * kp + 1]);
+      const Whole<E> e(du[2 * kp], du[2 * kp + 1]);
       tri_mul<E, true>(y, tri, e, kp);
     }
 #pragma unroll
@@ -165,13 +165,13 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
         y[mt] = -(gm[mt] * et[mt]);
       }
     }
-    s = Split<E>(y[0], y[1]);
+    Whole<E> x(y[0], y[1]);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       if (n + 1 < NP) read_cols(n + 1);
       in_order();
-      mma_all(S, cols[n & 1], s);
-      if (n + 1 < NP) s = Split<E>(y[2 * n + 2], y[2 * n + 3]);
+      mma_all(S, cols[n & 1], x);
+      if (n + 1 < NP) x = Whole<E>(y[2 * n + 2], y[2 * n + 3]);
       in_order();
     }
 #pragma unroll
@@ -292,13 +292,12 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
     for (int mt = 0; mt < NT; ++mt) y[mt] = zero4();
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      const Split<E> e(du[2 * kp], du[2 * kp + 1]);
-#pragma unroll
-      for (int mt = 0; mt < 2 * kp + 2; ++mt) y[mt] = mma(tri[TR::at_t(mt, kp)], e, y[mt]);
+      const Whole<E> e(du[2 * kp], du[2 * kp + 1]);
+      tri_mul<E, true>(y, tri, e, kp);
     }
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) go[mt] *= gm[mt] * a.scale;
-    s = Split<E>(go[0], go[1]);
+    Whole<E> x(go[0], go[1]);
     in_order();
     const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
     Split<E> ys[NP];
@@ -306,7 +305,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
     for (int n = 0; n < 2 * NP; ++n) {
       if (n + 1 < 2 * NP) read_cols(n + 1);
       in_order();
-      mma_all(S, cols[n & 1], s);
+      mma_all(S, cols[n & 1], x);
       if (n < NP) {
         ys[n] = Split<E>(y[2 * n], y[2 * n + 1]);
 #pragma unroll
@@ -315,9 +314,9 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
           y[mt] = -(gm[mt] * et[mt]);
         }
       }
-      if (n + 1 < NP) s = Split<E>(go[2 * n + 2], go[2 * n + 3]);
-      else if (n + 1 < 2 * NP) s = Split<E>(y[2 * (n + 1 - NP)], y[2 * (n + 1 - NP) + 1]);
-      interleave<2 * ND * kMma, 3>();
+      if (n + 1 < NP) x = Whole<E>(go[2 * n + 2], go[2 * n + 3]);
+      else if (n + 1 < 2 * NP) x = Whole<E>(y[2 * (n + 1 - NP)], y[2 * (n + 1 - NP) + 1]);
+      interleave<kWhole<E> * ND, 3>();
       in_order();
     }
 #pragma unroll

@@ -157,6 +157,33 @@ template <> struct Split<float> {
   __device__ __forceinline__ Split(f32x4_t x, f32x4_t y) : a(x), b(y) {}
 };
 
+// The same values in three terms (2^-25 is lost): what is added to a state, and the right-hand sides that it comes from.
+// In two, the state was 3.6e-6 off and not fp32's 1e-7; the state, K S and T in two terms leave it 5e-7 off.
+template <typename E> struct Whole;
+template <> struct Whole<bf16_t> {
+  bf16x8_t hi, mid, lo;
+  __device__ __forceinline__ Whole() {}
+  __device__ __forceinline__ Whole(f32x4_t x, f32x4_t y) {
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    u32x4_t h, m, l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a = j < 2 ? x[2 * j] : y[2 * j - 4], b = j < 2 ? x[2 * j + 1] : y[2 * j - 3];
+      h[j] = pack_bf16x2(a, b);
+      a -= __uint_as_float(h[j] << 16);
+      b -= __uint_as_float(h[j] & 0xffff0000u);
+      m[j] = pack_bf16x2(a, b);
+      l[j] = pack_bf16x2(a - __uint_as_float(m[j] << 16), b - __uint_as_float(m[j] & 0xffff0000u));
+    }
+    hi = __builtin_bit_cast(bf16x8_t, h);
+    mid = __builtin_bit_cast(bf16x8_t, m);
+    lo = __builtin_bit_cast(bf16x8_t, l);
+  }
+};
+template <> struct Whole<float> : Split<float> {
+  using Split<float>::Split;
+};
+
 // A split's two 16-byte parts.
 __device__ __forceinline__ bf16x8_t first_half(const Split<bf16_t>& s) { return s.hi; }
 __device__ __forceinline__ bf16x8_t second_half(const Split<bf16_t>& s) { return s.lo; }
@@ -380,7 +407,9 @@ template <typename E, int DKP, int WAVES, bool WIDE, bool LEAN = false> struct L
   static constexpr int kT = (Tri<E>::kBytes / 16 + kLoadThreads - 1) / kLoadThreads;
   static constexpr int kCols = 16 * WAVES, kVPieces = kCols / V, kVStep = kLoadThreads / kVPieces, kVRows = C / kVStep;
   static_assert(kLoadThreads % kPieces == 0 && C % kStep == 0 && 3 * C / 4 <= kLoadThreads && C % kVStep == 0);
-  uint4 k[kRows], q[kRows], t[kT], p[kT], vec, v[kVRows];
+  // as vectors: copies of uint4 alone, a structure, would leave the lean form's arrays in memory
+  typedef uint32_t Vec __attribute__((ext_vector_type(4)));
+  Vec k[kRows], q[LEAN ? 1 : kRows], t[kT], p[LEAN ? 1 : kT], vec, v[kVRows];
   int tid, row, col, vrow, vcol;  // of a thread's first pieces
 
   __device__ __forceinline__ Loader(int tid_)
@@ -412,23 +441,23 @@ template <typename E, int DKP, int WAVES, bool WIDE, bool LEAN = false> struct L
     const uint32_t at = col < cols ? col * sizeof(E) : kNowhere;
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
-      k[n] = kb.template load<uint4>(at + (row + n * kStep) * sk);
-      if constexpr (!LEAN) q[n] = qb.template load<uint4>(at + (row + n * kStep) * sq);
+      k[n] = kb.template load<Vec>(at + (row + n * kStep) * sk);
+      if constexpr (!LEAN) q[n] = qb.template load<Vec>(at + (row + n * kStep) * sq);
     }
-    const uint4* tp = reinterpret_cast<const uint4*>(a.t + item * Tri<E>::kBytes);
-    const uint4* pp = reinterpret_cast<const uint4*>(a.p + item * Tri<E>::kBytes);
+    const Vec* tp = reinterpret_cast<const Vec*>(a.t + item * Tri<E>::kBytes);
+    const Vec* pp = reinterpret_cast<const Vec*>(a.p + item * Tri<E>::kBytes);
 #pragma unroll
     for (int n = 0; n < kT; ++n) t[n] = tp[piece(n, Tri<E>::kBytes / 16)];
 #pragma unroll
     for (int n = 0; n < (LEAN ? 0 : kT); ++n) p[n] = pp[piece(n, Tri<E>::kBytes / 16)];
-    vec = reinterpret_cast<const uint4*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
+    vec = reinterpret_cast<const Vec*>(a.vec + item * 3 * C)[piece(0, 3 * C / 4)];
     const int vcols = a.dv - c0;  // may be none
     const Buffer vb(cp, vcols > 0 ? rows_bytes(len, ldc, vcols, sizeof(E)) : 0);
     const uint32_t sv = static_cast<uint32_t>(ldc * sizeof(E));
     if constexpr (WIDE) {
       const uint32_t vat = vcol < vcols ? vcol * sizeof(E) : kNowhere;
 #pragma unroll
-      for (int n = 0; n < kVRows; ++n) v[n] = vb.template load<uint4>(vat + (vrow + n * kVStep) * sv);
+      for (int n = 0; n < kVRows; ++n) v[n] = vb.template load<Vec>(vat + (vrow + n * kVStep) * sv);
     } else {
 #pragma unroll
       for (int n = 0; n < kVRows; ++n) {
@@ -443,16 +472,16 @@ template <typename E, int DKP, int WAVES, bool WIDE, bool LEAN = false> struct L
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
       const int at = Tile<E, DKP>::at(row + n * kStep, col);
-      *reinterpret_cast<uint4*>(w.K + at) = k[n];
-      if constexpr (!LEAN) *reinterpret_cast<uint4*>(w.Q + at) = q[n];
+      *reinterpret_cast<Vec*>(w.K + at) = k[n];
+      if constexpr (!LEAN) *reinterpret_cast<Vec*>(w.Q + at) = q[n];
     }
 #pragma unroll
-    for (int n = 0; n < kT; ++n) reinterpret_cast<uint4*>(w.T)[piece(n, Tri<E>::kBytes / 16)] = t[n];
+    for (int n = 0; n < kT; ++n) reinterpret_cast<Vec*>(w.T)[piece(n, Tri<E>::kBytes / 16)] = t[n];
 #pragma unroll
-    for (int n = 0; n < (LEAN ? 0 : kT); ++n) reinterpret_cast<uint4*>(w.P)[piece(n, Tri<E>::kBytes / 16)] = p[n];
-    reinterpret_cast<uint4*>(w.vec)[piece(0, 3 * C / 4)] = vec;
+    for (int n = 0; n < (LEAN ? 0 : kT); ++n) reinterpret_cast<Vec*>(w.P)[piece(n, Tri<E>::kBytes / 16)] = p[n];
+    reinterpret_cast<Vec*>(w.vec)[piece(0, 3 * C / 4)] = vec;
 #pragma unroll
-    for (int n = 0; n < kVRows; ++n) *reinterpret_cast<uint4*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
+    for (int n = 0; n < kVRows; ++n) *reinterpret_cast<Vec*>(w.V + (vrow + n * kVStep) * kCols + vcol) = v[n];
   }
   // A chunk's result columns to memory (op: as cp).
   __device__ __forceinline__ void put(const Args& a, const OutTile<E, WAVES>& out, E* op, int64_t ldo, int len, int c0) const {
@@ -545,6 +574,7 @@ __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, i
 
 // What is written above stays above: the reads of a stage are under way while the one before is computed.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+template <typename E> constexpr int kWhole = sizeof(E) == 2 ? 3 : 8;  // matrix instructions of a Whole operand and a tile
 // N times a matrix instruction and then K others of the vector unit, which run while it does.
 template <int N, int K> __device__ __forceinline__ void interleave() {
 #pragma unroll
@@ -561,9 +591,17 @@ template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const 
 #pragma unroll
   for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.hi, c[n]);
 }
+template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const bf16x8_t (&a)[N], const Whole<bf16_t>& b) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.lo, c[n]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.mid, c[n]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.hi, c[n]);
+}
 // u += T x over the pair kp of token tiles; T lower triangular, TRANS its transpose.
 template <typename E, bool TRANS = false, int NT>
-__device__ __forceinline__ void tri_mul(f32x4_t (&u)[NT], const Split<E> (&t)[Tri<E>::kFrags], const Split<E>& x, int kp) {
+__device__ __forceinline__ void tri_mul(f32x4_t (&u)[NT], const Split<E> (&t)[Tri<E>::kFrags], const Whole<E>& x, int kp) {
   using TR = Tri<E>;
   const int first = TRANS ? 0 : 2 * kp, end = TRANS ? 2 * kp + 2 : NT;
   if constexpr (std::is_same_v<E, float>) {
@@ -571,11 +609,11 @@ __device__ __forceinline__ void tri_mul(f32x4_t (&u)[NT], const Split<E> (&t)[Tr
     for (int mt = first; mt < end; ++mt) u[mt] = mma(t[TRANS ? TR::at_t(mt, kp) : TR::at(mt, kp)], x, u[mt]);
   } else {
 #pragma unroll
-    for (int n = 0; n < 3; ++n)
+    for (int n = 0; n < 5; ++n)  // the smallest products first
 #pragma unroll
       for (int mt = first; mt < end; ++mt) {
         const Split<E>& f = t[TRANS ? TR::at_t(mt, kp) : TR::at(mt, kp)];
-        u[mt] = mfma16(n == 0 ? f.lo : f.hi, n == 1 ? x.lo : x.hi, u[mt]);
+        u[mt] = mfma16(n == 0 || n == 2 ? f.lo : f.hi, n == 1 ? x.lo : n == 0 || n == 3 ? x.mid : x.hi, u[mt]);
       }
   }
 }

@@ -314,12 +314,12 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
   char* us = exchange.rows[wave];
   if (helper) {
     const bool live = col < a.dvp;
-    const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+    const uint32_t u_at = live ? (col * C + 8 * g) * kKept<E> : kNowhere, b_at = live ? (col * DKP + 8 * g) * kKept<E> : kNowhere;
     __syncthreads();
     for (int chunk = span.first; chunk < span.end; ++chunk) {
       const auto& w = tiles[(chunk - span.first) & 1];
       const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
-      const Buffer kept(KEEP ? static_cast<E*>(a.before) + item * a.dvp * DKP : nullptr, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+      const Buffer kept(KEEP ? static_cast<char*>(a.before) + item * a.dvp * DKP * kKept<E> : nullptr, static_cast<int64_t>(a.dvp) * DKP * kKept<E>);
       f32x4_t o[NT];
       Raw rows[2][NT];
       Split<E> s[2];
@@ -335,7 +335,7 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
       for (int kp = 0; kp < NK; ++kp) {
         if (kp + 1 < NK) read(kp + 1);
         in_order();
-        if constexpr (KEEP) kept.store(b_at + 32 * kp * sizeof(E), high(s[kp & 1]));
+        if constexpr (KEEP) keep<E>(kept, b_at + 32 * kp * kKept<E>, s[kp & 1]);
         mma_all(o, rows[kp & 1], s[kp & 1]);
         in_order();
       }
@@ -345,11 +345,11 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 #pragma unroll
       for (int mt = 0; mt < NT; ++mt) o[mt] *= *reinterpret_cast<const f32x4_t*>(w.vec + 16 * mt + 4 * g) * a.scale;
       __syncthreads();
-      const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+      const Buffer ub(KEEP ? static_cast<char*>(a.u) + item * a.dvp * C * kKept<E> : nullptr, static_cast<int64_t>(a.dvp) * C * kKept<E>);
 #pragma unroll
       for (int kp = 0; kp < NP; ++kp) {
         const Split<E> u = take<E>(us, kp);
-        if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(u));
+        if constexpr (KEEP) keep<E>(ub, u_at + 32 * kp * kKept<E>, u);
 #pragma unroll
         for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], u, o[mt]);
       }
@@ -458,6 +458,7 @@ template <typename E, int DKP, int WAVES, bool KEEP>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
+  constexpr int TG = kGroup<ND>, NG = ND / TG;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, WAVES> tiles[kBuf];
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
   f32x4_t S[ND];
   state_load(entering(a, seq, h), a.dk, a.dv, s_at, S);
   __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
-  const uint32_t u_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, b_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+  const uint32_t u_at = live ? (col * C + 8 * g) * kKept<E> : kNowhere, b_at = live ? (col * DKP + 8 * g) * kKept<E> : kNowhere;
   __syncthreads();
   for (int chunk = span.first; chunk < span.end; ++chunk) {
     const WalkTile<E, DKP, WAVES>& w = tiles[(chunk - span.first) & (kBuf - 1)];
@@ -508,7 +509,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     read_rows(0);
     Split<E> tri[TR::kFrags];
     f32x4_t gm[NT], et[NT], rest[NT], vt[NT];
-    const Buffer kept(KEEP ? static_cast<E*>(a.before) + item * a.dvp * DKP : nullptr, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    const Buffer kept(KEEP ? static_cast<char*>(a.before) + item * a.dvp * DKP * kKept<E> : nullptr, static_cast<int64_t>(a.dvp) * DKP * kKept<E>);
     Split<E> s(S[0], S[1]);
 #pragma unroll
     for (int kp = 0; kp < NK; ++kp) {
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
 #pragma unroll
         for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
       }
-      if constexpr (KEEP) kept.store(b_at + 32 * kp * sizeof(E), high(s));
+      if constexpr (KEEP) keep<E>(kept, b_at + 32 * kp * kKept<E>, s);
       in_order();
       mma_all(ko, rows[kp & 1], s);
       if (kp + 1 < NK) {
@@ -535,10 +536,10 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     }
     // eta (V - e^G K S), U = T (that)
     const float decay = w.vec[C - 1];
-    Raw cols[2][ND];
-    auto read_cols = [&](int kp) {
+    Raw cols[2][TG];
+    auto read_cols = [&](int n) {  // the pairs of token tiles, each by groups of the state's tiles
 #pragma unroll
-      for (int t = 0; t < ND; ++t) cols[kp & 1][t] = state_col<DKP>(w.K, 32 * kp, t);
+      for (int t = 0; t < TG; ++t) cols[n & 1][t] = state_col<DKP>(w.K, 32 * (n / NG), n % NG * TG + t);
     };
     read_cols(0);
     f32x4_t o[NT], u[NT];
@@ -562,27 +563,28 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
     in_order();
     // S = e^{G_C} S + K^T (e^{G_C - G} U);  O += P U
     Split<E> scores[TR::kFrags];
-    const Buffer ub(KEEP ? static_cast<E*>(a.u) + item * a.dvp * C : nullptr, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+    const Buffer ub(KEEP ? static_cast<char*>(a.u) + item * a.dvp * C * kKept<E> : nullptr, static_cast<int64_t>(a.dvp) * C * kKept<E>);
     Split<E> us[NP];
     Whole<E> x(u[0] * rest[0], u[1] * rest[1]);
 #pragma unroll
-    for (int kp = 0; kp < NP; ++kp) {
-      if (kp + 1 < NP) {
-        read_cols(kp + 1);
+    for (int n = 0; n < NP * NG; ++n) {
+      const int kp = n / NG;
+      if (n + 1 < NP * NG) {
+        read_cols(n + 1);
       } else {
 #pragma unroll
         for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
       }
       in_order();
-      mma_all(S, cols[kp & 1], x);
-      us[kp] = Split<E>(u[2 * kp], u[2 * kp + 1]);
-      if (kp + 1 < NP) x = Whole<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
-      interleave<kWhole<E> * ND, 3>();
+      mma_all(tiles_from<TG>(S, n % NG * TG), cols[n & 1], x);
+      if (n % NG == 0) us[kp] = Split<E>(u[2 * kp], u[2 * kp + 1]);
+      if (n % NG == NG - 1 && kp + 1 < NP) x = Whole<E>(u[2 * kp + 2] * rest[2 * kp + 2], u[2 * kp + 3] * rest[2 * kp + 3]);
+      interleave<kWhole<E> * TG, 3>();
       in_order();
     }
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      if constexpr (KEEP) ub.store(u_at + 32 * kp * sizeof(E), high(us[kp]));
+      if constexpr (KEEP) keep<E>(ub, u_at + 32 * kp * kKept<E>, us[kp]);
 #pragma unroll
       for (int mt = 2 * kp; mt < NT; ++mt) o[mt] = mma(scores[TR::at(mt, kp)], us[kp], o[mt]);
     }
@@ -884,6 +886,7 @@ using delta::Args;
 int chunk_tokens(int dtype) { return dtype == TTT_F32 ? delta::Chunk<float>::C : delta::Chunk<bf16_t>::C; }
 int64_t all_tokens(const ttt_delta_desc& d) { return d.packed ? d.T : static_cast<int64_t>(d.B) * d.T; }
 size_t elem_bytes(const ttt_delta_desc& d) { return d.dtype == TTT_F32 ? 4 : 2; }
+size_t kept_bytes(const ttt_delta_desc& d) { return d.dtype == TTT_F32 ? delta::kKept<float> : delta::kKept<bf16_t>; }  // of a value for the gradients
 int padded_dk(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
 size_t tri_bytes(const ttt_delta_desc& d) { return d.dtype == TTT_F32 ? delta::Tri<float>::kBytes : delta::Tri<bf16_t>::kBytes; }
 
@@ -951,8 +954,8 @@ Layout ws_layout(const ttt_delta_desc& d, bool bwd) {
     l.states = take(all * d.dk * d.dv);
   }
   if (bwd) {
-    l.y = take(items * C * dvp * e);
-    l.after = take(items * padded_dk(d.dk) * dvp * e);
+    l.y = take(items * C * dvp * kept_bytes(d));
+    l.after = take(items * padded_dk(d.dk) * dvp * kept_bytes(d));
   }
   l.bytes = at;
   return l;
@@ -999,7 +1002,7 @@ void place(Args& a, const ttt_delta_desc& d, const Layout& l, void* ws, const vo
   if (saved) {
     const size_t items = static_cast<size_t>(a.chunks) * a.H;
     a.u = const_cast<char*>(static_cast<const char*>(saved));
-    a.before = static_cast<char*>(a.u) + align256(items * chunk_tokens(d.dtype) * a.dvp * elem_bytes(d));
+    a.before = static_cast<char*>(a.u) + align256(items * chunk_tokens(d.dtype) * a.dvp * kept_bytes(d));
   }
 }
 
@@ -1030,7 +1033,7 @@ size_t delta_workspace(const ttt_delta_desc& d, int entry) {
   return delta_chunks(d) == 0 ? 0 : ws_layout(d, entry == TTT_ENTRY_BWD).bytes;
 }
 size_t delta_saved(const ttt_delta_desc& d) {
-  const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, e = elem_bytes(d), dvp = (d.dv + 31) / 32 * 32;
+  const size_t items = static_cast<size_t>(delta_chunks(d)) * d.H, e = kept_bytes(d), dvp = (d.dv + 31) / 32 * 32;
   return align256(items * chunk_tokens(d.dtype) * dvp * e) + align256(items * padded_dk(d.dk) * dvp * e);
 }
 

@@ -3,14 +3,13 @@
 //   dU = P^T dO + e^{G_C - G} K dS';   Y = T^T dU;   dV = eta Y;
 //   dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y).
 // That much is walked through, in the forward's way with everything transposed.  The rest
-// is free of it, a chunk a workgroup: with X = scale R o (dO U^T) and M_ij = -eta_i R_ij Y_i.U_j (j < i),
+// is free of it, a chunk a workgroup, every operand in two bf16 terms or in fp32: with X = scale R o (dO U^T) and M_ij = -eta_i R_ij Y_i.U_j (j < i),
 //   dQ = scale e^G dO S^T + X K;
 //   dK = [-e^G eta Y S^T + M K] + e^{G_C - G} U dS'^T + X^T Q + M^T K;
 //   deta_i = Y_i.e_i, so dbeta_i = (1 - sigmoid) Y_i.U_i.
 // Each G_i stands in R, e^G and e^{G_C - G}; what it gathers are row sums that are there already:
 //   dG_i = q_i.dq_i - k_i.dk_i + 2 k_i.[...]_i,  and dG_C also e^{G_C} <dS', S> + sum_i e^{G_C - G_i} k_i.(dS' u_i);
-// log a_t has the sum of dG_i over i >= t.  Terms that cancel in that sum come from the same rounded X, M, U
-// and dS', so they cancel to fp32.
+// log a_t has the sum of dG_i over i >= t.  Terms that cancel in that sum come from the same X, M, U and dS'.
 
 #include "ttt_delta_common.h"
 
@@ -86,7 +85,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
   const bool live = col < a.dvp;
   const int64_t state = (static_cast<int64_t>(seq) * a.H + h) * a.dk * a.dv;
   const uint32_t s_at = col < a.dv ? col * 4 : kNowhere;
-  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+  const uint32_t y_at = live ? (col * C + 8 * g) * kKept<E> : kNowhere, a_at = live ? (col * DKP + 8 * g) * kKept<E> : kNowhere;
   f32x4_t S[ND];  // dS
   state_load(a.d_sfinal ? a.d_sfinal + state : nullptr, a.dk, a.dv, s_at, S);
   __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
@@ -94,7 +93,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
   for (int chunk = last; chunk >= span.first; --chunk) {
     const auto& w = tiles[(last - chunk) & 1];
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
-    const Buffer kept(static_cast<E*>(a.after) + item * a.dvp * DKP, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    const Buffer kept(static_cast<char*>(a.after) + item * a.dvp * DKP * kKept<E>, static_cast<int64_t>(a.dvp) * DKP * kKept<E>);
     f32x4_t du[NT], gm[NT], rest[NT], et[NT];
     Raw rows[2][NT];
     auto read_rows = [&](int kp) {
@@ -120,7 +119,7 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
 #pragma unroll
         for (int f = 0; f < TR::kFrags; ++f) tri[f] = tri_load2<E>(w.T, f);
       }
-      kept.store(a_at + 32 * kp * sizeof(E), high(s));
+      keep<E>(kept, a_at + 32 * kp * kKept<E>, s);
       in_order();
       mma_all(du, rows[kp & 1], s);
       if (kp + 1 < NK) {
@@ -155,10 +154,10 @@ __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& spa
     for (int t = 0; t < ND; ++t) S[t] = S[t] * decay + qg[t];
     in_order();
     read_cols(0);
-    const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+    const Buffer yb(static_cast<char*>(a.y) + item * a.dvp * C * kKept<E>, static_cast<int64_t>(a.dvp) * C * kKept<E>);
 #pragma unroll
     for (int kp = 0; kp < NP; ++kp) {
-      yb.store(y_at + 32 * kp * sizeof(E), high(Split<E>(y[2 * kp], y[2 * kp + 1])));
+      keep<E>(yb, y_at + 32 * kp * kKept<E>, Split<E>(y[2 * kp], y[2 * kp + 1]));
 #pragma unroll
       for (int mt = 2 * kp; mt < 2 * kp + 2; ++mt) {
         et[mt] *= y[mt];          // dV
@@ -186,6 +185,7 @@ template <typename E, int DKP, int WAVES>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, int groups) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, kBuf = kWalkBuffers<E, DKP, WAVES>;
   constexpr int kMma = sizeof(E) == 2 ? 1 : 4;  // matrix instructions of an operand's term
+  constexpr int TG = kGroup<ND>, NG = ND / TG;
   using TR = Tri<E>;
   using Raw = typename Frag<E>::Raw;
   __shared__ __attribute__((aligned(16))) WalkTile<E, DKP, WAVES> tiles[kBuf];
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
   f32x4_t S[ND];  // dS
   state_load(a.d_sfinal ? a.d_sfinal + state : nullptr, a.dk, a.dv, s_at, S);
   __builtin_amdgcn_s_waitcnt(0);  // here, so that the loop has no wait for memory
-  const uint32_t y_at = live ? (col * C + 8 * g) * sizeof(E) : kNowhere, a_at = live ? (col * DKP + 8 * g) * sizeof(E) : kNowhere;
+  const uint32_t y_at = live ? (col * C + 8 * g) * kKept<E> : kNowhere, a_at = live ? (col * DKP + 8 * g) * kKept<E> : kNowhere;
   const int last = span.end - 1;
   __syncthreads();
   for (int chunk = last; chunk >= span.first; --chunk) {
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
     read_rows(0);
     Split<E> scores[TR::kFrags], tri[TR::kFrags];
     f32x4_t gm[NT], rest[NT], et[NT];
-    const Buffer kept(static_cast<E*>(a.after) + item * a.dvp * DKP, static_cast<int64_t>(a.dvp) * DKP * sizeof(E));
+    const Buffer kept(static_cast<char*>(a.after) + item * a.dvp * DKP * kKept<E>, static_cast<int64_t>(a.dvp) * DKP * kKept<E>);
     Split<E> s(S[0], S[1]);
 #pragma unroll
     for (int kp = 0; kp < NK; ++kp) {
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
 #pragma unroll
         for (int f = 0; f < TR::kFrags; ++f) scores[f] = tri_load2<E>(w.P, f);
       }
-      kept.store(a_at + 32 * kp * sizeof(E), high(s));
+      keep<E>(kept, a_at + 32 * kp * kKept<E>, s);
       in_order();
       mma_all(du, rows[kp & 1], s);
       if (kp + 1 < NK) {
@@ -280,10 +280,11 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
     for (int t = 0; t < ND; ++t) S[t] *= decay;
     in_order();
     // dS = e^{G_C} dS' + scale Q^T e^G dO - K^T (e^G eta Y), with Y = T^T dU
-    Raw cols[2][ND];
-    auto read_cols = [&](int n) {  // Q's and K's pairs of token tiles in turn
+    Raw cols[2][TG];
+    auto read_cols = [&](int n) {  // Q's and K's pairs of token tiles in turn, each by groups of the state's tiles
+      const int q = n / NG;
 #pragma unroll
-      for (int t = 0; t < ND; ++t) cols[n & 1][t] = state_col<DKP>(n < NP ? w.Q : w.K, 32 * (n % NP), t);
+      for (int t = 0; t < TG; ++t) cols[n & 1][t] = state_col<DKP>(q < NP ? w.Q : w.K, 32 * (q % NP), n % NG * TG + t);
     };
     read_cols(0);
     in_order();
@@ -299,28 +300,31 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
     for (int mt = 0; mt < NT; ++mt) go[mt] *= gm[mt] * a.scale;
     Whole<E> x(go[0], go[1]);
     in_order();
-    const Buffer yb(static_cast<E*>(a.y) + item * a.dvp * C, static_cast<int64_t>(a.dvp) * C * sizeof(E));
+    const Buffer yb(static_cast<char*>(a.y) + item * a.dvp * C * kKept<E>, static_cast<int64_t>(a.dvp) * C * kKept<E>);
     Split<E> ys[NP];
 #pragma unroll
-    for (int n = 0; n < 2 * NP; ++n) {
-      if (n + 1 < 2 * NP) read_cols(n + 1);
+    for (int n = 0; n < 2 * NP * NG; ++n) {
+      const int q = n / NG;
+      if (n + 1 < 2 * NP * NG) read_cols(n + 1);
       in_order();
-      mma_all(S, cols[n & 1], x);
-      if (n < NP) {
-        ys[n] = Split<E>(y[2 * n], y[2 * n + 1]);
+      mma_all(tiles_from<TG>(S, n % NG * TG), cols[n & 1], x);
+      if (q < NP && n % NG == 0) {
+        ys[q] = Split<E>(y[2 * q], y[2 * q + 1]);
 #pragma unroll
-        for (int mt = 2 * n; mt < 2 * n + 2; ++mt) {
+        for (int mt = 2 * q; mt < 2 * q + 2; ++mt) {
           et[mt] *= y[mt];          // dV
           y[mt] = -(gm[mt] * et[mt]);
         }
       }
-      if (n + 1 < NP) x = Whole<E>(go[2 * n + 2], go[2 * n + 3]);
-      else if (n + 1 < 2 * NP) x = Whole<E>(y[2 * (n + 1 - NP)], y[2 * (n + 1 - NP) + 1]);
-      interleave<kWhole<E> * ND, 3>();
+      if (n % NG == NG - 1) {
+        if (q + 1 < NP) x = Whole<E>(go[2 * q + 2], go[2 * q + 3]);
+        else if (q + 1 < 2 * NP) x = Whole<E>(y[2 * (q + 1 - NP)], y[2 * (q + 1 - NP) + 1]);
+      }
+      interleave<kWhole<E> * TG, 3>();
       in_order();
     }
 #pragma unroll
-    for (int kp = 0; kp < NP; ++kp) yb.store(y_at + 32 * kp * sizeof(E), high(ys[kp]));
+    for (int kp = 0; kp < NP; ++kp) keep<E>(yb, y_at + 32 * kp * kKept<E>, ys[kp]);
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) out_tile(out, wave, mt, et[mt]);
     if constexpr (kBuf == 1) __syncthreads();
@@ -331,18 +335,44 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
 
 // ---- what does not depend on the walk ----
 
-constexpr int kGradThreads = 512, kSlab = 32;  // columns of the values in LDS at a time
+constexpr int kSlab = 32;  // columns of the values in LDS at a time
+// Sixteen waves, two for each eighth of the key channels with half of the tokens' tiles each, where 128 registers do for
+// that (4 x 4096 tokens of 16 heads of 128 bf16, forward and backward, 929 us; with eight waves 964; heads of 64 632 and
+// 647); else eight with 256 registers: with sums of four shared heads 937 (sixteen: 1015), 8 heads of 256 2769 (3311).
+template <typename E, int DKP, bool SHARED> constexpr int kHalves = sizeof(E) == 2 && DKP <= 128 && !SHARED ? 2 : 1;
+template <typename E, int DKP, bool SHARED> constexpr int kGradThreads = 512 * kHalves<E, DKP, SHARED>;
 
-template <typename E> __device__ __forceinline__ float dot8(typename Frag<E>::Raw a, typename Frag<E>::Raw b) {
+// An operand in as many terms as are kept, and its products (the smallest first; the product of two second terms is 2^-16 of one).
+template <typename E> struct Kept { typename Frag<E>::Raw t[kTerms<E>]; };
+template <typename E> __device__ __forceinline__ f32x4_t mma_kept(const Kept<E>& a, typename Frag<E>::Raw b, f32x4_t c) {
+#pragma unroll
+  for (int n = kTerms<E> - 1; n >= 0; --n) c = mma(a.t[n], b, c);
+  return c;
+}
+template <typename E> __device__ __forceinline__ f32x4_t mma_kept(typename Frag<E>::Raw a, const Kept<E>& b, f32x4_t c) {
+#pragma unroll
+  for (int n = kTerms<E> - 1; n >= 0; --n) c = mma(a, b.t[n], c);
+  return c;
+}
+template <typename E> __device__ __forceinline__ f32x4_t mma_kept(const Kept<E>& a, const Kept<E>& b, f32x4_t c) {
+  if constexpr (kTerms<E> == 2) c = mma(a.t[0], b.t[1], mma(a.t[1], b.t[0], c));
+  return mma(a.t[0], b.t[0], c);
+}
+template <typename E> __device__ __forceinline__ float dot8(const Kept<E>& a, const Kept<E>& b) {
   float s = 0.0f;
   if constexpr (std::is_same_v<E, float>) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += a.a[j] * b.a[j] + a.b[j] * b.b[j];
+    for (int j = 0; j < 4; ++j) s += a.t[0].a[j] * b.t[0].a[j] + a.t[0].b[j] * b.t[0].b[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += from_bf(a[j]) * from_bf(b[j]);
+    for (int j = 0; j < 8; ++j) s += (from_bf(a.t[0][j]) + from_bf(a.t[1][j])) * (from_bf(b.t[0][j]) + from_bf(b.t[1][j]));
   }
   return s;
+}
+// A fp32 value's terms, `gap` elements apart.
+template <typename E> __device__ __forceinline__ void put_terms(E* p, int at, int gap, float x) {
+  Elem<E>::st(p, at, x);
+  if constexpr (kTerms<E> == 2) Elem<E>::st(p, at + gap, x - bf16_to_f32(f32_to_bf16(x)));
 }
 
 template <typename E> __device__ __forceinline__ E narrow(float x) {
@@ -379,117 +409,143 @@ __device__ __forceinline__ float sum16(float x) {
   return x;
 }
 
+// A workgroup's LDS while the slabs go by, and once they are done with.
+template <typename E, int DKP> struct SlabTiles {
+  static constexpr int C = Chunk<E>::C, kU = kSlab * Tile<E, C>::kRow, kB = kSlab * Tile<E, DKP>::kRow;  // elements of a term
+  E dO[C * Tile<E, kSlab>::kRow];  // [token][column]
+  E U[kTerms<E> * kU];             // [term][column][token]
+  E Y[kTerms<E> * kU];
+  E B[kTerms<E> * kB];             // [term][column][channel]: the state before
+  E A[kTerms<E> * kB];             // and the gradient of the one after
+};
+template <typename E, int NW> struct SquareTiles {
+  static constexpr int C = Chunk<E>::C, kX = C * Tile<E, C>::kRow;
+  E X[kTerms<E> * kX];
+  E M[kTerms<E> * kX];
+  float sums[NW][4][C];  // [wave]
+};
+
 // The next slab of the values' columns on its way through registers.
-template <typename E, int DKP> struct SlabLoader {
-  static constexpr int C = Chunk<E>::C, V = 16 / sizeof(E);
-  static constexpr int kO = C * kSlab / V, kS = kSlab * DKP / V;  // pieces of dO (and of U, Y); of a state
-  static constexpr int nO = (kO + kGradThreads - 1) / kGradThreads, nS = (kS + kGradThreads - 1) / kGradThreads;
-  uint4 o[nO], u[nO], y[nO], b[nS], a[nS];
+template <typename E, int DKP, int THREADS> struct SlabLoader {
+  static constexpr int C = Chunk<E>::C, V = 16 / sizeof(E), kThreads = THREADS;
+  static constexpr int kO = C * kSlab / V, kU = kTerms<E> * kO, kB = kTerms<E> * kSlab * DKP / V;  // pieces of dO, of U and Y, of the states
+  static constexpr int nO = (kO + kThreads - 1) / kThreads, nU = (kU + kThreads - 1) / kThreads, nB = (kB + kThreads - 1) / kThreads;
+  typedef uint32_t Vec __attribute__((ext_vector_type(4)));
+  Vec o[nO], u[nU], y[nU], b[nB], a[nB];
   // Pieces past the end are some thread's twice: both write the same.
-  static __device__ __forceinline__ int piece(int n, int all) { return min(static_cast<int>(threadIdx.x) + n * kGradThreads, all - 1); }
+  static __device__ __forceinline__ int piece(int n, int all) { return min(static_cast<int>(threadIdx.x) + n * kThreads, all - 1); }
   __device__ __forceinline__ void load(const Args& g, int64_t item, const E* dO, int64_t ld, int len, int c0) {
     const int cols = g.dv - c0;  // may be none
     const Buffer ob(dO + c0, cols > 0 ? rows_bytes(len, ld, cols, sizeof(E)) : 0);
     const uint32_t stride = static_cast<uint32_t>(ld * sizeof(E));
-    const uint4* up = reinterpret_cast<const uint4*>(static_cast<const E*>(g.u) + (item * g.dvp + c0) * C);
-    const uint4* yp = reinterpret_cast<const uint4*>(static_cast<const E*>(g.y) + (item * g.dvp + c0) * C);
-    const uint4* bp = reinterpret_cast<const uint4*>(static_cast<const E*>(g.before) + (item * g.dvp + c0) * DKP);
-    const uint4* ap = reinterpret_cast<const uint4*>(static_cast<const E*>(g.after) + (item * g.dvp + c0) * DKP);
+    const int64_t first = item * g.dvp + c0;  // column
+    const Vec* up = reinterpret_cast<const Vec*>(static_cast<const char*>(g.u) + first * C * kKept<E>);
+    const Vec* yp = reinterpret_cast<const Vec*>(static_cast<const char*>(g.y) + first * C * kKept<E>);
+    const Vec* bp = reinterpret_cast<const Vec*>(static_cast<const char*>(g.before) + first * DKP * kKept<E>);
+    const Vec* ap = reinterpret_cast<const Vec*>(static_cast<const char*>(g.after) + first * DKP * kKept<E>);
 #pragma unroll
     for (int n = 0; n < nO; ++n) {
       const int x = piece(n, kO), row = x / (kSlab / V), col = x % (kSlab / V) * V;
       if (g.wide_do) {
-        o[n] = ob.template load<uint4>(col < cols ? row * stride + col * sizeof(E) : kNowhere);
+        o[n] = ob.template load<Vec>(col < cols ? row * stride + col * sizeof(E) : kNowhere);
       } else {
         E e[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) e[j] = ob.template load<E>(col + j < cols ? row * stride + (col + j) * sizeof(E) : kNowhere);
         __builtin_memcpy(&o[n], e, 16);
       }
-      u[n] = up[x];
-      y[n] = yp[x];
     }
 #pragma unroll
-    for (int n = 0; n < nS; ++n) {
-      b[n] = bp[piece(n, kS)];
-      a[n] = ap[piece(n, kS)];
+    for (int n = 0; n < nU; ++n) {
+      u[n] = up[piece(n, kU)];
+      y[n] = yp[piece(n, kU)];
+    }
+#pragma unroll
+    for (int n = 0; n < nB; ++n) {
+      b[n] = bp[piece(n, kB)];
+      a[n] = ap[piece(n, kB)];
     }
   }
-  __device__ __forceinline__ void store(E* dO, E* U, E* Y, E* B, E* A) const {
+  __device__ __forceinline__ void store(SlabTiles<E, DKP>& s) const {
+    using S = SlabTiles<E, DKP>;
 #pragma unroll
     for (int n = 0; n < nO; ++n) {
       const int x = piece(n, kO);
-      *reinterpret_cast<uint4*>(dO + Tile<E, kSlab>::at(x / (kSlab / V), x % (kSlab / V) * V)) = o[n];
-      const int at = Tile<E, C>::at(x / (C / V), x % (C / V) * V);
-      *reinterpret_cast<uint4*>(U + at) = u[n];
-      *reinterpret_cast<uint4*>(Y + at) = y[n];
+      *reinterpret_cast<Vec*>(s.dO + Tile<E, kSlab>::at(x / (kSlab / V), x % (kSlab / V) * V)) = o[n];
     }
 #pragma unroll
-    for (int n = 0; n < nS; ++n) {
-      const int x = piece(n, kS), at = Tile<E, DKP>::at(x / (DKP / V), x % (DKP / V) * V);
-      *reinterpret_cast<uint4*>(B + at) = b[n];
-      *reinterpret_cast<uint4*>(A + at) = a[n];
+    for (int n = 0; n < nU; ++n) {
+      const int x = piece(n, kU), z = x / kTerms<E>, at = x % kTerms<E> * S::kU + Tile<E, C>::at(z / (C / V), z % (C / V) * V);
+      *reinterpret_cast<Vec*>(s.U + at) = u[n];
+      *reinterpret_cast<Vec*>(s.Y + at) = y[n];
+    }
+#pragma unroll
+    for (int n = 0; n < nB; ++n) {
+      const int x = piece(n, kB), z = x / kTerms<E>, at = x % kTerms<E> * S::kB + Tile<E, DKP>::at(z / (DKP / V), z % (DKP / V) * V);
+      *reinterpret_cast<Vec*>(s.B + at) = b[n];
+      *reinterpret_cast<Vec*>(s.A + at) = a[n];
     }
   }
 };
 
+// The terms of an operand that `read` reads from a tile.
+template <typename E, typename F> __device__ __forceinline__ Kept<E> kept(const E* tile, int term, F&& read) {
+  Kept<E> k;
+#pragma unroll
+  for (int n = 0; n < kTerms<E>; ++n) k.t[n] = read(tile + n * term);
+  return k;
+}
+
 // A chunk and key head a workgroup, the value heads that share it one after the other (SHARED) with dQ and
-// dK summed in registers.  Of the triangular products a wave has a row tile of X or of M, of the others an
-// eighth of the key channels.  The value columns come 32 at a time.
-// Up to 128 bf16 channels two workgroups share a CU (128 registers, 80 KB): 4096 chunks and heads of 128 take 267 us
-// so, 317 with one and all in registers.
-template <typename E, int DKP, bool SHARED>
-__global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHARED ? 4 : 2) void grad_kernel(Args a) {
-  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = (DKP + 127) / 128, NW = DKP / 16 / NJ;  // NW waves have channels
+// dK summed in registers.  Of the triangular products a wave has (half of) a row tile of X or of M, of the others an
+// eighth of the key channels, bf16 for half of the tokens.  The value columns come 32 at a time.
+template <typename E, int DKP, bool SHARED> __global__ __launch_bounds__((kGradThreads<E, DKP, SHARED>)) void grad_kernel(Args a, int chunk0) {
+  constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, NJ = (DKP + 127) / 128, NW = DKP / 16 / NJ;  // NW waves (of a half) have channels
+  constexpr int HALVES = kHalves<E, DKP, SHARED>, NH = NT / HALVES, kThreads = kGradThreads<E, DKP, SHARED>;  // token tiles of a wave
   using Lds = Tile<E, DKP>;
-  using Slab = Tile<E, kSlab>;
   using Sq = Tile<E, C>;
+  using Slabs = SlabTiles<E, DKP>;
+  using Squares = SquareTiles<E, NW>;
   __shared__ __attribute__((aligned(16))) E K[C * Lds::kRow];
   __shared__ __attribute__((aligned(16))) E Q[C * Lds::kRow];
-  __shared__ __attribute__((aligned(16))) E dO[C * Slab::kRow];     // [token][column]
-  __shared__ __attribute__((aligned(16))) E U[kSlab * Sq::kRow];    // [column][token]
-  __shared__ __attribute__((aligned(16))) E Y[kSlab * Sq::kRow];
-  __shared__ __attribute__((aligned(16))) E B[kSlab * Lds::kRow];   // [column][channel]: the state before
-  __shared__ __attribute__((aligned(16))) E A[kSlab * Lds::kRow];   // and the gradient of the one after
-  __shared__ __attribute__((aligned(16))) E X[C * Sq::kRow];
-  __shared__ __attribute__((aligned(16))) E M[C * Sq::kRow];
+  __shared__ __attribute__((aligned(16))) char pool[sizeof(Slabs) > sizeof(Squares) ? sizeof(Slabs) : sizeof(Squares)];
+  Slabs& s = *reinterpret_cast<Slabs*>(pool);
+  Squares& sq = *reinterpret_cast<Squares*>(pool);  // once the slabs are done with
   __shared__ double G[C];
   __shared__ __attribute__((aligned(16))) float vec[3][C];  // e^G, e^{G_C - G}, eta
-  __shared__ float energy[kGradThreads / 64], yu[C];
-  float(*sums)[4][C] = reinterpret_cast<float(*)[4][C]>(B);  // [wave], once the slabs are done with
-  static_assert(sizeof(float) * NW * 4 * C <= sizeof(B));
-  const int chunk = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.H / a.Hk;
+  __shared__ float energy[NW], yu[C];
+  const int chunk = chunk0 + blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk, share = a.H / a.Hk;
   const Where w = locate<C>(a, chunk);
   if (w.len < 0) return;
   // lanes are named anew in each stage, so that a stage's LDS addresses do not take registers in the others
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int ch0 = wave * 16 * NJ;  // a wave's first channel
-  const bool busy = wave < NW;
-  stage<E, C, DKP, kGradThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, a.wide_k);
-  stage<E, C, DKP, kGradThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, a.wide_q);
-  f32x4_t dq_sum[SHARED ? NT : 1][NJ], dk_sum[SHARED ? NT : 1][NJ];
+  const int ch0 = wave % 8 * 16 * NJ, m0 = wave / 8 * NH;  // a wave's first channel and token tile
+  const bool busy = wave % 8 < NW;
+  stage<E, C, DKP, kThreads>(K, static_cast<const E*>(a.k) + w.token * a.ldk + hk * a.dk, a.ldk, w.len, a.dk, a.wide_k);
+  stage<E, C, DKP, kThreads>(Q, static_cast<const E*>(a.q) + w.token * a.ldq + hk * a.dk, a.ldq, w.len, a.dk, a.wide_q);
+  f32x4_t dq_sum[SHARED ? NH : 1][NJ], dk_sum[SHARED ? NH : 1][NJ];
   if constexpr (SHARED) {
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
+    for (int m = 0; m < NH; ++m)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) dq_sum[mt][j] = dk_sum[mt][j] = zero4();
+      for (int j = 0; j < NJ; ++j) dq_sum[m][j] = dk_sum[m][j] = zero4();
   }
   const Buffer qb(static_cast<E*>(a.dq) + w.token * a.ldq + hk * a.dk, rows_bytes(w.len, a.ldq, a.dk, sizeof(E)));
   const Buffer kb(static_cast<E*>(a.dk_out) + w.token * a.ldk + hk * a.dk, rows_bytes(w.len, a.ldk, a.dk, sizeof(E)));
-  const uint32_t sq = static_cast<uint32_t>(a.ldq * sizeof(E)), sk = static_cast<uint32_t>(a.ldk * sizeof(E));
+  const uint32_t strideq = static_cast<uint32_t>(a.ldq * sizeof(E)), stridek = static_cast<uint32_t>(a.ldk * sizeof(E));
   auto store = [&](const f32x4_t& dq, const f32x4_t& dk, int mt, int j) {
     const int i = lane & 15, g = lane >> 4, col = ch0 + 16 * j + i;
     const uint32_t at = busy && col < a.dk ? col * sizeof(E) : kNowhere;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * mt + 4 * g + r;
-      qb.store(at + t * sq, narrow<E>(dq[r]));
-      kb.store(at + t * sk, narrow<E>(dk[r]));
+      qb.store(at + t * strideq, narrow<E>(dq[r]));
+      kb.store(at + t * stridek, narrow<E>(dk[r]));
     }
   };
-  // wave w < NT has row tile w of X, wave NT + w that of M
-  const int rt = wave % NT;
-  const bool tri = wave < 2 * NT, second = wave >= NT;
+  // of the triangular products: whose row tile, and which half of its columns (those above the diagonal are zero)
+  const int rt = wave % NT, n0 = wave / NT % HALVES * NH;
+  const bool tri = wave < 2 * NT * HALVES, second = wave >= NT * HALVES;
   for (int hs = 0; hs < (SHARED ? share : 1); ++hs) {
     const int h = hk * share + hs;
     const int64_t item = static_cast<int64_t>(chunk) * a.H + h;
@@ -507,63 +563,72 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
         vec[2][lane] = eta;
       }
     }
-    f32x4_t xm[NT], dq[NT][NJ], dkr[NT][NJ], dks[NT][NJ];
+    f32x4_t xm[NH], dq[NH][NJ], dkr[NH][NJ], dks[NH][NJ];
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) {
-      xm[mt] = zero4();
+    for (int m = 0; m < NH; ++m) {
+      xm[m] = zero4();
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) dq[mt][j] = dkr[mt][j] = dks[mt][j] = zero4();
+      for (int j = 0; j < NJ; ++j) dq[m][j] = dkr[m][j] = dks[m][j] = zero4();
     }
     float en = 0.0f;
-    SlabLoader<E, DKP> slab;
+    SlabLoader<E, DKP, kThreads> slab;
     const E* dop = static_cast<const E*>(a.d_o) + (w.token * a.H + h) * a.dv;
     const int64_t ldo = static_cast<int64_t>(a.H) * a.dv;
     slab.load(a, item, dop, ldo, w.len, 0);
     for (int c0 = 0; c0 < a.dvp; c0 += kSlab) {
       if (c0 > 0) __syncthreads();
-      slab.store(dO, U, Y, B, A);
+      slab.store(s);
       if (c0 + kSlab < a.dvp) slab.load(a, item, dop, ldo, w.len, c0 + kSlab);
       __syncthreads();
       const int tid = opaque(threadIdx.x), i = tid & 15, g = (tid & 63) >> 4;
-      if (tri) {
-        const auto x = second ? token_col<C>(Y, rt, tid) : row_frag<kSlab>(dO, 16 * rt + i, 8 * g);
+      auto tokens = [&](const E* tile, int mt) { return kept<E>(tile, Slabs::kU, [&](const E* t) { return token_col<C>(t, mt, tid); }); };
+      if (tri && n0 <= rt) {
+        if (second) {
+          const auto x = tokens(s.Y, rt);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xm[nt] = mma(x, token_col<C>(U, nt, tid), xm[nt]);  // those above the diagonal too
+          for (int n = 0; n < NH; ++n) xm[n] = mma_kept<E>(x, tokens(s.U, n0 + n), xm[n]);
+        } else {
+          const auto x = row_frag<kSlab>(s.dO, 16 * rt + i, 8 * g);
+#pragma unroll
+          for (int n = 0; n < NH; ++n) xm[n] = mma_kept<E>(x, tokens(s.U, n0 + n), xm[n]);
+        }
       }
       if (busy) {
-        typename Frag<E>::Raw sb[NJ], sa[NJ];
+        Kept<E> sb[NJ], sa[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          sb[j] = plain_col<DKP>(B, 0, ch0 + 16 * j, tid);
-          sa[j] = plain_col<DKP>(A, 0, ch0 + 16 * j, tid);
-          en += dot8<E>(sb[j], sa[j]);
+          auto channels = [&](const E* t) { return plain_col<DKP>(t, 0, ch0 + 16 * j, tid); };
+          sb[j] = kept<E>(s.B, Slabs::kB, channels);
+          sa[j] = kept<E>(s.A, Slabs::kB, channels);
+          if (wave < 8) en += dot8<E>(sb[j], sa[j]);
         }
 #pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-          const auto ox = row_frag<kSlab>(dO, 16 * mt + i, 8 * g), ux = token_col<C>(U, mt, tid), yx = token_col<C>(Y, mt, tid);
+        for (int m = 0; m < NH; ++m) {
+          const auto ox = row_frag<kSlab>(s.dO, 16 * (m0 + m) + i, 8 * g);
+          const auto ux = tokens(s.U, m0 + m), yx = tokens(s.Y, m0 + m);
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            dq[mt][j] = mma(ox, sb[j], dq[mt][j]);
-            dkr[mt][j] = mma(yx, sb[j], dkr[mt][j]);
-            dks[mt][j] = mma(ux, sa[j], dks[mt][j]);
+            dq[m][j] = mma_kept<E>(ox, sb[j], dq[m][j]);
+            dkr[m][j] = mma_kept<E>(yx, sb[j], dkr[m][j]);
+            dks[m][j] = mma_kept<E>(ux, sa[j], dks[m][j]);
           }
-          if (mt % 2) in_order();
         }
       }
     }
+    __syncthreads();
     if (tri) {
       const int i = lane & 15, g = lane >> 4;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int n = 0; n < NH; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * rt + 4 * g + r, col = 16 * nt + i;
+          const int row = 16 * rt + 4 * g + r, col = 16 * (n0 + n) + i;
           const float d = row >= col ? exp2_(static_cast<float>(G[row] - G[col])) : 0.0f;
           if (second) {
-            Elem<E>::st(M, Sq::at(row, col), row > col ? -vec[2][row] * d * xm[nt][r] : 0.0f);
-            if (row == col) yu[row] = xm[nt][r];
+            put_terms<E>(sq.M, Sq::at(row, col), Squares::kX, row > col ? -vec[2][row] * d * xm[n][r] : 0.0f);
+            if (row == col) yu[row] = xm[n][r];
           } else {
-            Elem<E>::st(X, Sq::at(row, col), row >= col ? a.scale * d * xm[nt][r] : 0.0f);
+            put_terms<E>(sq.X, Sq::at(row, col), Squares::kX, row >= col ? a.scale * d * xm[n][r] : 0.0f);
           }
         }
     }
@@ -579,7 +644,8 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
           qc[j][p] = plain_col<DKP>(Q, 32 * p, ch0 + 16 * j, tid);
         }
 #pragma unroll
-      for (int mt = 0; mt < NT; ++mt) {
+      for (int m = 0; m < NH; ++m) {
+        const int mt = m0 + m;
         f32x4_t d1 = zero4(), d2 = zero4(), d3 = zero4(), d4 = zero4();
         const f32x4_t gm = *reinterpret_cast<const f32x4_t*>(&vec[0][16 * mt + 4 * g]);
         const f32x4_t rest = *reinterpret_cast<const f32x4_t*>(&vec[1][16 * mt + 4 * g]);
@@ -587,30 +653,36 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const int c0 = ch0 + 16 * j;
-          dq[mt][j] *= gm * a.scale;
-          dkr[mt][j] *= -(gm * et);
-          dks[mt][j] *= rest;
+          dq[m][j] *= gm * a.scale;
+          dkr[m][j] *= -(gm * et);
+          dks[m][j] *= rest;
 #pragma unroll
-          for (int p = 0; p <= mt / 2; ++p) {
-            dq[mt][j] = mma(row_frag<C>(X, 16 * mt + i, 32 * p + 8 * g), kc[j][p], dq[mt][j]);
-            dkr[mt][j] = mma(row_frag<C>(M, 16 * mt + i, 32 * p + 8 * g), kc[j][p], dkr[mt][j]);
+          for (int p = 0; p < NP; ++p) {
+            if (p <= mt / 2) {
+              auto row = [&](const E* t) { return row_frag<C>(t, 16 * mt + i, 32 * p + 8 * g); };
+              dq[m][j] = mma_kept<E>(kept<E>(sq.X, Squares::kX, row), kc[j][p], dq[m][j]);
+              dkr[m][j] = mma_kept<E>(kept<E>(sq.M, Squares::kX, row), kc[j][p], dkr[m][j]);
+            }
           }
           const f32x4_t qv = four_rows<DKP>(Q, 16 * mt + 4 * g, c0, tid), kv = four_rows<DKP>(K, 16 * mt + 4 * g, c0, tid);
-          d1 += qv * dq[mt][j];
-          d3 += kv * dkr[mt][j];
-          d4 += kv * dks[mt][j];
-          f32x4_t dk = dkr[mt][j] + dks[mt][j];
+          d1 += qv * dq[m][j];
+          d3 += kv * dkr[m][j];
+          d4 += kv * dks[m][j];
+          f32x4_t dk = dkr[m][j] + dks[m][j];
 #pragma unroll
-          for (int p = mt / 2; p < NP; ++p) {
-            dk = mma(plain_col<C>(X, 32 * p, 16 * mt, tid), qc[j][p], dk);
-            dk = mma(plain_col<C>(M, 32 * p, 16 * mt, tid), kc[j][p], dk);
+          for (int p = 0; p < NP; ++p) {
+            if (p >= mt / 2) {
+              auto col = [&](const E* t) { return plain_col<C>(t, 32 * p, 16 * mt, tid); };
+              dk = mma_kept<E>(kept<E>(sq.X, Squares::kX, col), qc[j][p], dk);
+              dk = mma_kept<E>(kept<E>(sq.M, Squares::kX, col), kc[j][p], dk);
+            }
           }
           d2 += kv * dk;
           if constexpr (SHARED) {
-            dq_sum[mt][j] += dq[mt][j];
-            dk_sum[mt][j] += dk;
+            dq_sum[m][j] += dq[m][j];
+            dk_sum[m][j] += dk;
           } else {
-            store(dq[mt][j], dk, mt, j);
+            store(dq[m][j], dk, mt, j);
           }
         }
 #pragma unroll
@@ -618,18 +690,17 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
           const float s1 = sum16(d1[r]), s2 = sum16(d2[r]), s3 = sum16(d3[r]), s4 = sum16(d4[r]);
           if (i == 0) {
             const int t = 16 * mt + 4 * g + r;
-            sums[wave][0][t] = s1;
-            sums[wave][1][t] = s2;
-            sums[wave][2][t] = s3;
-            sums[wave][3][t] = s4;
+            sq.sums[wave % 8][0][t] = s1;
+            sq.sums[wave % 8][1][t] = s2;
+            sq.sums[wave % 8][2][t] = s3;
+            sq.sums[wave % 8][3][t] = s4;
           }
         }
-        in_order();
       }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) en += __shfl_xor(en, d, 64);
-    if (lane == 0) energy[wave] = en;
+    if (lane == 0 && wave < NW) energy[wave] = en;
     __syncthreads();
     if (wave == 0) {
       float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, all = 0.0f;
@@ -637,7 +708,7 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
       for (int v = 0; v < NW; ++v) {
         all += energy[v];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[s] += lane < C ? sums[v][s][lane] : 0.0f;
+        for (int n = 0; n < 4; ++n) x[n] += lane < C ? sq.sums[v][n][lane] : 0.0f;
       }
       float dG = x[0] - x[1] + 2.0f * x[2], H = x[3];
 #pragma unroll
@@ -661,9 +732,9 @@ __global__ __launch_bounds__(kGradThreads, sizeof(E) == 2 && DKP <= 128 && !SHAR
   }
   if constexpr (SHARED) {
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
+    for (int m = 0; m < NH; ++m)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) store(dq_sum[mt][j], dk_sum[mt][j], mt, j);
+      for (int j = 0; j < NJ; ++j) store(dq_sum[m][j], dk_sum[m][j], m0 + m, j);
   }
 }
 
@@ -681,10 +752,17 @@ template <typename E, int DKP> hipError_t launch_bwd(const Args& a, hipStream_t 
     if (e != hipSuccess) return e;
   }
   KernelScope scope(TTT_KERNEL_DELTA_GRAD, s);
-  const uint32_t grid = static_cast<uint32_t>(a.chunks) * a.Hk;
-  if (a.H == a.Hk) grad_kernel<E, DKP, false><<<grid, kGradThreads, 0, s>>>(a);
-  else grad_kernel<E, DKP, true><<<grid, kGradThreads, 0, s>>>(a);
-  return hipGetLastError();
+  auto run = [&](auto shared) {
+    constexpr int kThreads = kGradThreads<E, DKP, shared()>;
+    const int most = static_cast<int>((UINT32_MAX / kThreads) / a.Hk);  // chunks of a launch, which has fewer than 2^32 threads
+    for (int chunk0 = 0; chunk0 < a.chunks; chunk0 += most) {
+      const uint32_t grid = static_cast<uint32_t>(a.chunks - chunk0 < most ? a.chunks - chunk0 : most) * a.Hk;
+      grad_kernel<E, DKP, shared()><<<grid, kThreads, 0, s>>>(a, chunk0);
+      if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  };
+  return a.H == a.Hk ? run(std::false_type{}) : run(std::true_type{});
 }
 template hipError_t launch_bwd<bf16_t, 64>(const Args&, hipStream_t);
 template hipError_t launch_bwd<bf16_t, 128>(const Args&, hipStream_t);

@@ -51,8 +51,8 @@ struct Args {
   void* kq;                      // else [chunks][Hk][2][C][dkp]: keys and queries, padded with zeros
   char* t;                       // [chunks][H] T, or its transpose, in operand order
   char* p;                       // the same of the scores
-  void* u;                       // [chunks][H][dvp][C], tokens in operand order (see token_col)
-  void* before;                  // [chunks][H][dvp][dkp]: the state that enters the chunk
+  void* u;                       // [chunks][H][dvp][C], tokens in operand order (see token_col), in terms (see keep)
+  void* before;                  // [chunks][H][dvp][dkp]: the state that enters the chunk, in terms
   void* y;                       // as u: T^T dU
   void* after;                   // as before: the gradient of the state that leaves it
   const void* d_o;
@@ -530,7 +530,8 @@ __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, i
   constexpr int C = Chunk<E>::C;
   using L = Loader<E, DKP, WAVES, WIDE, LEAN>;
   const int tid = threadIdx.x - static_cast<int>(blockDim.x - kLoadThreads);
-  L even(tid), odd(tid);  // the chunks' pieces on their way, in turn
+  // the chunks' pieces on their way, in turn; with one buffer, whose chunks are so wide, one of them fills the registers
+  L even(tid), odd(tid);
   const int count = span.end - span.first;
   auto chunk_of = [&](int n) { return BWD ? span.end - 1 - min(n, count - 1) : span.first + min(n, count - 1); };
   auto load = [&](L& l, int n) {
@@ -553,21 +554,25 @@ __device__ __forceinline__ void load_walk(const Args& a, const S& span, int h, i
     } else {
       __syncthreads();  // the others are done with the chunk
       l.store(tiles[0]);
-      load(l, n + 3);
+      load(l, n + 2);
       put(n);
     }
     __syncthreads();
   };
   if (count > 0) {
     load(even, 0);
-    load(odd, 1);
+    if constexpr (BUF == 2) load(odd, 1);
     even.store(tiles[0]);
-    load(even, 2);
+    load(even, BUF);
   }
   __syncthreads();
-  for (int n = 0; n < count; n += 2) {
-    step(odd, n);
-    if (n + 1 < count) step(even, n + 1);
+  if constexpr (BUF == 2) {
+    for (int n = 0; n < count; n += 2) {
+      step(odd, n);
+      if (n + 1 < count) step(even, n + 1);
+    }
+  } else {
+    for (int n = 0; n < count; ++n) step(even, n);
   }
   if (BUF == 2 && count > 0) put(count - 1);
 }
@@ -598,6 +603,12 @@ template <int N> __device__ __forceinline__ void mma_all(f32x4_t (&c)[N], const 
   for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.mid, c[n]);
 #pragma unroll
   for (int n = 0; n < N; ++n) c[n] = mfma16(a[n], b.hi, c[n]);
+}
+// A walk's update of its state takes the state's tiles kGroup at a time: of 256 channels all at once, with the next
+// operands on their way, would be twice the registers there are.
+template <int ND> constexpr int kGroup = ND > 8 ? 8 : ND;
+template <int N, int ND> __device__ __forceinline__ f32x4_t (&tiles_from(f32x4_t (&S)[ND], int t))[N] {
+  return *reinterpret_cast<f32x4_t(*)[N]>(&S[t]);
 }
 // u += T x over the pair kp of token tiles; T lower triangular, TRANS its transpose.
 template <typename E, bool TRANS = false, int NT>
@@ -705,6 +716,17 @@ template <int ND> __device__ __forceinline__ void state_store(float* p, int dk, 
 template <typename E> __device__ __forceinline__ typename Frag<E>::Raw high(const Split<E>& s) {
   if constexpr (std::is_same_v<E, float>) return f32x8{s.a, s.b};
   else return s.hi;
+}
+
+// What the walks keep for the gradients (U, Y, the states before and the gradients of those after): fp32, or two terms of
+// bf16, eight values' first and then their second.  In one term the gradients were up to 4e-3 off and not a rounding's
+// 1.66e-3, and the gate's, in which large terms may cancel, up to 8e-2.
+template <typename E> constexpr int kTerms = sizeof(E) == 2 ? 2 : 1;
+template <typename E> constexpr uint32_t kKept = kTerms<E> * sizeof(E);  // bytes of a value
+// `at`: bytes in front of the operand, all terms counted.
+template <typename E> __device__ __forceinline__ void keep(const Buffer& b, uint32_t at, const Split<E>& s) {
+  b.store16(at, __builtin_bit_cast(uint4, first_half(s)));
+  b.store16(at + 16, __builtin_bit_cast(uint4, second_half(s)));
 }
 
 // ---- gates ----

@@ -602,9 +602,9 @@ TTT_API int ttt_layernorm_bwd(const ttt_ln_desc* desc, const void* x, const floa
  *   eta_t = lr_max Sigmoid(beta_t + lr_bias);
  *   S <- a_t S;  e_t = v_t - S^T k_t;  S <- S + eta_t k_t e_t^T;  o_t = scale S^T q_t.
  * Queries and keys may have fewer heads: value head h uses head h / (H / Hk).
- * S is kept in float32.  In bf16 the products that make it and o take their
- * operands in two bf16 terms (2^-17 of a value is lost), what is added to S in
- * three, and those that form a gradient one.  A decay below 2^-150 counts as 2^-150, with no gradient.
+ * S is kept in float32.  In bf16 products take operands that are not given in bf16
+ * in two bf16 terms (2^-17 of a value is lost), and what is added to S in three:
+ * results are rounded to bf16 once, at the end.  A decay below 2^-150 counts as 2^-150, with no gradient.
  * An infinity or NaN may go on as NaN in its own sequence and head, to the tokens
  * before it in its chunk too; no value reaches another sequence.
  */

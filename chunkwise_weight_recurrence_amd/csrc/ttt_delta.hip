@@ -173,8 +173,8 @@ template <int C, int LD> __device__ __forceinline__ void invert(const float* A, 
 
 // A chunk and head a workgroup: its gates' sums, K K^T and Q K^T (row tile w by wave w), the inverse.
 // BWD writes the transposes.  Both in two terms: with the scores in one, O was 2.2e-3 off and not a rounding's 1.66e-3
-// (the walk of 30011 packed tokens of 20 heads takes 5 % longer so).  It is bound by the latency of its stages, so LDS is
-// used over and over: 36 KB let four workgroups share a CU.  4096 chunks and heads of 128 bf16 59 us (93 with 53 KB,
+// (a forward over 30011 packed tokens of 20 heads takes 5 % longer so).  It is bound by the latency of its stages, so LDS is
+// used over and over: 36 KB let four workgroups share a CU.  4096 chunks and heads of 128 bf16 60 us (93 with 53 KB,
 // three workgroups and the loads behind the gates' sums).
 template <typename E, int DKP, bool BWD>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(Args a) {
@@ -300,8 +300,9 @@ __device__ __forceinline__ float* leaving(const Args& a, int seq, int h) {
 
 // The chain (waves 0 .. WAVES - 1) and its helpers (the next WAVES) where there are few heads.  First half of a
 // chunk: K S, U and, by the helper, Q S; second half: the next state and, by the helper, O += P U.  A chunk of 64 x 128
-// bf16 takes 1.9 us (2.7 where every CU has one), which is the chain's own: 82 matrix instructions and about 400 vector instructions, one in 5.5
-// cycles from one wave.  64 chunks of 64 heads with what a backward needs 177 us, 208 without helpers.
+// bf16 takes 2.3 us (3.4 where every CU has one and keeps what a backward needs), which is the chain's own: 110 matrix
+// instructions and about 450 vector instructions, one in 5.5 cycles from one wave.  64 chunks of 64 heads with what a
+// backward needs 221 us, with four chain waves a workgroup instead 295.
 template <typename E, int DKP, int WAVES, bool KEEP, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
@@ -453,7 +454,7 @@ __device__ __forceinline__ void help_fwd_or_chain(const Args& a, const Span& spa
 
 // A wave holds 16 columns of a head's state in its result registers and walks the chunks.  The state and what
 // is added to it are products of operands of two and three terms: its error does not grow with the length.  KEEP: what a
-// backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 288 us, 3.8 us a chunk of a workgroup: four
+// backward needs is written.  30011 packed tokens of 20 heads of 128 bf16 284 us (323 under the profiler), 3.8 us a chunk of a workgroup: four
 // chains share LDS, and the loads of 256 workgroups the memory.
 template <typename E, int DKP, int WAVES, bool KEEP>
 __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, int groups) {
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void fwd_kernel(Args a, 
 constexpr int kMapWaves = 4;
 
 // The maps: [piece][H][dkp][dvp + dkp], N before M.  The last piece's is not needed.  Seven of eight pieces of 131072
-// tokens, 16 heads of 128 bf16, 958 us; the whole walk after it 727, in one piece 4300.
+// tokens, 16 heads of 128 bf16, 1061 us; the whole walk after it 763, in one piece 4822.
 template <typename E, int DKP>
 __global__ __launch_bounds__((kMapWaves + kLoaders) * 64, 1) void map_kernel(Args a, int groups, float* maps) {
   constexpr int C = Chunk<E>::C, NT = C / 16, NP = C / 32, ND = DKP / 16, NK = DKP / 32, WAVES = kMapWaves;
@@ -745,7 +746,7 @@ constexpr int kStepThreads = 256;
 
 // A workgroup has kStepCols columns of one head's state of one row, a thread a run of the dk rows of one
 // column; the three sums over dk meet in LDS.  256 rows of 16 heads of 128 x 128 (537 MB) 114 us, 4.7 TB/s; 8 rows
-// 7.2 us, the latency of slot, state and sums.  Rows that name one slot are consecutive tokens of it, in
+// 7.1 us, the latency of slot, state and sums.  Rows that name one slot are consecutive tokens of it, in
 // row order: the first of them does them all.
 constexpr int kStepCols = 32, kStepRuns = kStepThreads / kStepCols;
 
@@ -905,9 +906,10 @@ namespace {
 
 int padded_dv(int dv) { return (dv + 31) / 32 * 32; }
 
-// The pieces of a dense sequence's forward walk.  A chunk of a walk takes about 2 us with helpers, 2.5 us with four
-// waves' columns in a workgroup on every CU, 2.2 us without outputs; a piece costs 2 us more where the maps
-// are joined: times of 128 bf16 channels, which stand for all.  131072 tokens of 16 heads of 128: one piece 4.5 ms, eight 2.2 ms.
+// The pieces of a dense sequence's forward walk, by what a chunk takes: about 2 us with helpers, 2.5 with four
+// waves' columns in a workgroup on every CU, 2.2 without outputs, and 2 us more a piece where the maps are joined: figures of
+// 128 bf16 channels (2.3, 3.0 and 2.1 at the last measurement) that stand for all widths and both types.  131072 tokens of 16 heads of
+// 128: one piece 5.21 ms, four 2.62, eight, which this takes, 2.19, sixteen 2.22.
 // Measured for 1, 4 and 16 heads of 64, 128 and 256 channels, bf16 and fp32, at 24, 64, 256 and 1024 chunks: where this cuts, the
 // forward takes 0.08 to 0.80 of one piece's time, and up to 1.17 times the best number's; where it does not, 24 chunks would
 // take down to 1/1.55 in eight pieces, and 16 heads of 256 at 64 and 256 chunks down to 1/1.6 in four.

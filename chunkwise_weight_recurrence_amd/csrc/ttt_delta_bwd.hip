@@ -19,7 +19,7 @@ namespace {
 
 // The chain and its helpers where there are few heads, as in the forward.  First half of a chunk: K dS', and by
 // the helper P^T dO and scale Q^T e^G dO; second half: Y and the gradient of the state before.  64 chunks of 64 heads
-// of 128 bf16 191 us, 208 without helpers.
+// of 128 bf16 243 us, with four chain waves a workgroup instead 294.
 template <typename E, int DKP, int WAVES, typename Tiles, typename Outs>
 __device__ __forceinline__ void help_bwd_or_chain(const Args& a, const Span& span, int seq, int h, int grp, Tiles& tiles, Outs& outs,
                                                   Exchange<E, DKP, WAVES>& exchange) {
@@ -337,8 +337,8 @@ __global__ __launch_bounds__(walk_waves(WAVES) * 64, 1) void bwd_kernel(Args a, 
 
 constexpr int kSlab = 32;  // columns of the values in LDS at a time
 // Sixteen waves, two for each eighth of the key channels with half of the tokens' tiles each, where 128 registers do for
-// that (4 x 4096 tokens of 16 heads of 128 bf16, forward and backward, 929 us; with eight waves 964; heads of 64 632 and
-// 647); else eight with 256 registers: with sums of four shared heads 937 (sixteen: 1015), 8 heads of 256 2769 (3311).
+// that (4 x 4096 tokens of 16 heads of 128 bf16, forward and backward, 929 us, 353 of them here; with eight waves 964; heads
+// of 64 632 and 647); else eight with 256 registers: with sums of four shared heads 937 (sixteen: 1015), 8 heads of 256 2769 (3311).
 template <typename E, int DKP, bool SHARED> constexpr int kHalves = sizeof(E) == 2 && DKP <= 128 && !SHARED ? 2 : 1;
 template <typename E, int DKP, bool SHARED> constexpr int kGradThreads = 512 * kHalves<E, DKP, SHARED>;
 

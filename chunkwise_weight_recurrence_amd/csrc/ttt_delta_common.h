@@ -315,7 +315,7 @@ template <typename E> __device__ __forceinline__ Split<E> tri_load2(const char* 
 // what a chunk needs from memory into LDS, three chunks ahead (two in registers, one in the other buffer), and
 // carry the result columns away.  So the chain has no wait for memory in it and no registers go to loads.
 // With few heads (WAVES = 2) each of these waves has a helper beside it, on a SIMD that would be idle, which
-// takes over what is not part of the chain: of 126 matrix instructions a chunk 44.  They meet twice a chunk.
+// takes over what is not part of the chain: of 160 matrix instructions a chunk 50.  They meet twice a chunk.
 
 constexpr int kLoaders = 4, kLoadThreads = kLoaders * 64;
 
@@ -765,13 +765,13 @@ __device__ __forceinline__ void gate_lane(const Args& a, const Where& w, int h, 
 }
 
 // Workgroups start in their order, so the longest sequences' walks are put first: 30011 tokens in 37 prompts, 20 heads,
-// 275 us, in the prompts' own order 345.
+// 284 us, in the prompts' own order 341.
 __device__ __forceinline__ int walk_sequence(const Args& a, int chain) { return a.packed ? a.order[chain / a.H] : chain / a.H; }
 
 // The waves of a walk's workgroup, and the workgroups that share a head's columns: four waves where that
-// leaves a workgroup for every CU, else two with helpers.  30011 packed tokens of 20 heads of 128 (740 heads of
-// sequences) take 345 us with four and 485 with two (288 with four and the longest first); 4 x 4096 tokens of 16 heads (64) 176 with two and helpers, 258 with
-// four.  Of 256 channels, four: helpers' part would not fit beside two chunks.
+// leaves a workgroup for every CU, else two with helpers.  30011 packed tokens of 20 heads of 128 bf16 (740 heads of
+// sequences) take 284 us with four and 440 with two, 16 x 1024 tokens of 16 heads (256) 183 and 232, 4 x 4096 (64) 295 and
+// 221.  Of 256 channels, four: helpers' part would not fit beside two chunks.
 template <int DKP, typename F> hipError_t by_waves(const Args& a, F&& f) {
   const int64_t columns = a.dvp / 16;
   if constexpr (DKP == 256) return f(std::integral_constant<int, 4>{}, static_cast<int>((columns + 3) / 4));

@@ -166,8 +166,8 @@ struct Rows {
 };
 
 // A slot's rows go over the queries' and the keys' heads of the workgroup's tokens; a row is on its way while the
-// one before it (or the table) is computed.  32768 tokens of 40 heads of 128 bf16 (671 MB) 138 us, a copy's rate; 8
-// tokens 4.7 us (10.6 with the queries' rows before the keys' and no load ahead).
+// one before it (or the table) is computed.  32768 tokens of 40 heads of 128 bf16 (671 MB) 137 us, a copy's rate; 8
+// tokens 4.3 us (10.6 with the queries' rows before the keys' and no load ahead).
 template <typename E, int V, int LANES, int N, bool HALF>
 __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkArgs a) {
   using R = Rows<E, V, LANES, N, HALF>;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkArgs a) {
 }
 
 // x is read again and its size formed again, which is free beside the reading.  16384 x 32 rows of 128 bf16 (402 MB)
-// 98 us.
+// 93 us.
 template <typename E, int V, int LANES, int N, bool HALF>
 __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkArgs a) {
   using R = Rows<E, V, LANES, N, HALF>;
@@ -375,8 +375,8 @@ QkArgs make_args(const ttt_qknorm_desc& d) {
   a.ldq = d.ldq ? d.ldq : static_cast<int64_t>(d.Hq) * d.d;
   a.ldk = d.ldk ? d.ldk : static_cast<int64_t>(d.Hk) * d.d;
   // Tokens a workgroup takes: about 256 rows of 128 columns, fewer where that leaves less than 1024 workgroups.  32768
-  // tokens of 40 heads of 128 take 138 us forward so, 156 with one token and 147 with four times as many; the
-  // backward of 16384 x 32 rows 99, 183 and 101, and 3001 x 6 fp32 rows 12, 14 and 22 forward.
+  // tokens of 40 heads of 128 take 139 us forward so, 146 with one token and 144 with four times as many; the
+  // backward of 16384 x 32 rows 88, 174 and 94, and 3001 x 6 fp32 rows 12, 13 and 22 forward.
   const int64_t row = static_cast<int64_t>(d.Hq + d.Hk) * d.d;
   int64_t tok = 32768 / row;
   const int64_t share = (d.tokens + 1023) / 1024;

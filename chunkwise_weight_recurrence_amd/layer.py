@@ -326,6 +326,12 @@ def _token_distance(x):
     return H * d
 
 
+def _check_heads(name, x, like):
+    """A tensor ``x`` has the tokens, heads and channels of ``like``, the tokens' axes as they may be."""
+    if hasattr(x, "shape") and (x.shape[-2:] != like.shape[-2:] or x.numel() != like.numel()):
+        raise ValueError(f"{name} must have the heads and channels of {tuple(like.shape)} (got {tuple(x.shape)})")
+
+
 class DeltaBuffers:
     """Outputs and workspace of the gated delta rule over q, k [B,T,Hk,dk] and v [B,T,H,dv], or packed [T,Hk,dk], [T,H,dv].
 
@@ -379,6 +385,7 @@ class DeltaBuffers:
 
     def backward(self, d_o, d_sfinal=None, stream=None):
         """Fills dq, dk, dv, dgate and dbeta (with the strides of q, k, v, gate and beta) and ds0."""
+        _check_heads("d_o", d_o, self.v)
         self._check_state("d_sfinal", d_sfinal)
         B.ttt_delta_bwd(self.desc, self.q, self.k, self.v, self.gate, self.beta, self.seq_starts, self.saved, d_o, d_sfinal,
                         self.dq, self.dk, self.dv, self.dgate, self.dbeta, self.ds0, self.ws, stream=stream)
@@ -418,5 +425,7 @@ class QkNormBuffers:
 
     def backward(self, dyq, dyk, stream=None):
         """Fills dq and dk (with the strides of q and k), dwq and dwk."""
+        _check_heads("dyq", dyq, self.q)
+        _check_heads("dyk", dyk, self.k)
         B.ttt_qknorm_bwd(self.desc, self.q, self.k, self.wq, self.wk, self.positions, self.inv_freq, dyq, dyk, self.dq, self.dk,
                          self.dwq, self.dwk, self.ws, stream=stream)

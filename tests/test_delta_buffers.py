@@ -40,3 +40,22 @@ def test_query_and_key_weights_have_a_head_s_columns():
     for bad in (pos(5), pos(11), pos(2, 10)):
         with pytest.raises(ValueError, match="positions must be"):
             QkNormBuffers(q, k, positions=bad)
+
+
+def test_gradients_of_the_outputs_have_their_heads_and_channels():
+    """Heads in front of the tokens, or channels of another tensor, have as many elements."""
+    q, v = _z(2, 5, 2, 8), _z(2, 5, 4, 16)
+    buf = DeltaBuffers(q, q, v, None, _z(2, 5, 4), with_bwd=True)
+    for shape in ((2, 4, 5, 16), (2, 5, 64), (2, 5, 16, 4), (2, 6, 4, 16)):
+        with pytest.raises(ValueError, match="d_o must have"):
+            buf.backward(_z(*shape))
+    norm = QkNormBuffers(_z(2, 5, 4, 16), _z(2, 5, 2, 16), with_bwd=True)
+    for dyq, dyk, name in (((2, 4, 5, 16), (2, 5, 2, 16), "dyq"), ((2, 5, 4, 16), (2, 2, 5, 16), "dyk"), ((2, 5, 64), (2, 5, 2, 16), "dyq"),
+                           ((2, 5, 4, 16), (1, 5, 4, 16), "dyk")):
+        with pytest.raises(ValueError, match=f"{name} must have"):
+            norm.backward(_z(*dyq), _z(*dyk))
+    # rows of all tokens one behind the other are the same rows: on to the check that they are on the GPU
+    with pytest.raises(ValueError, match="GPU"):
+        buf.backward(_z(10, 4, 16))
+    with pytest.raises(ValueError, match="GPU"):
+        norm.backward(_z(10, 4, 16), _z(10, 2, 16))

@@ -202,10 +202,7 @@ __device__ __forceinline__ f32x4_t mfma16(f32x4_t a, f32x4_t b, f32x4_t c) {
 }
 __device__ __forceinline__ f32x4_t mma(f32x8 a, f32x8 b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
 __device__ __forceinline__ f32x4_t mma(bf16x8_t a, bf16x8_t b, f32x4_t c) { return mfma16(a, b, c); }
-// a is exact in its type; b in two terms
-__device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Split<bf16_t>& b, f32x4_t c) { return mfma16(a, b.hi, mfma16(a, b.lo, c)); }
-__device__ __forceinline__ f32x4_t mma(f32x8 a, const Split<float>& b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
-// the first in two terms, the second exact
+// the first in two terms, the second exact in its type
 __device__ __forceinline__ f32x4_t mma(const Split<bf16_t>& a, bf16x8_t b, f32x4_t c) { return mfma16(a.hi, b, mfma16(a.lo, b, c)); }
 __device__ __forceinline__ f32x4_t mma(const Split<float>& a, f32x8 b, f32x4_t c) { return mfma16(a.b, b.b, mfma16(a.a, b.a, c)); }
 // both in two terms
@@ -384,11 +381,6 @@ struct Buffer {
   __device__ __forceinline__ void store(uint32_t off, uint16_t x) const { __builtin_amdgcn_raw_buffer_store_b16(x, rs, static_cast<int>(off), 0, 0); }
   __device__ __forceinline__ void store(uint32_t off, float x) const {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), rs, static_cast<int>(off), 0, 0);
-  }
-  __device__ __forceinline__ void store(uint32_t off, bf16x8_t x) const { store16(off, __builtin_bit_cast(uint4, x)); }
-  __device__ __forceinline__ void store(uint32_t off, f32x8 x) const {
-    store16(off, __builtin_bit_cast(uint4, x.a));
-    store16(off + 16, __builtin_bit_cast(uint4, x.b));
   }
   __device__ __forceinline__ void store16(uint32_t off, uint4 x) const {
     typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));

@@ -158,7 +158,8 @@ template <> struct Split<float> {
 };
 
 // The same values in three terms (2^-25 is lost): what is added to a state, and the right-hand sides that it comes from.
-// In two, the state was 3.6e-6 off and not fp32's 1e-7; the state, K S and T in two terms leave it 5e-7 off.
+// In two, the state was 3.6e-6 off and not fp32's 1e-7; the state in K S and T, in two terms, leave it 5e-7 off (128
+// channels; 1e-6 to 3e-6 below 32).
 template <typename E> struct Whole;
 template <> struct Whole<bf16_t> {
   bf16x8_t hi, mid, lo;
